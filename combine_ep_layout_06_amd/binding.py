@@ -35,7 +35,8 @@ EXPORTED = ("ep_layout", "ep_dispatch", "ep_dispatch_fp8", "ep_layout_dispatch",
             "ep_dispatch_packed_fp8", "ep_layout_dispatch_packed", "ep_layout_dispatch_packed_fp8",
             "ep_combine_packed", "ep_check_e4m3_conversion", "ep_last_launches",
             "ep_layout_workspace_bytes", "ep_layout_dispatch_ws", "ep_layout_dispatch_fp8_ws",
-            "ep_layout_dispatch_noalloc", "ep_error_string", "ep_last_error", "ep_version")
+            "ep_layout_dispatch_noalloc", "ep_expert_gemm_fp8", "ep_expert_gemm_fp8_packed",
+            "ep_expert_swiglu_fp8", "ep_expert_swiglu_fp8_packed", "ep_error_string", "ep_last_error", "ep_version")
 
 
 class EpShape(ctypes.Structure):
@@ -105,6 +106,10 @@ def load_library():
         L.ep_layout_dispatch_ws.argtypes = [sp] + [vp] * 10 + [ctypes.c_size_t, vp]
         L.ep_layout_dispatch_fp8_ws.argtypes = [sp] + [vp] * 11 + [ctypes.c_size_t, vp]
         L.ep_layout_dispatch_noalloc.argtypes = [sp] + [vp] * 10
+        L.ep_expert_gemm_fp8.argtypes = [sp, i32] + [vp] * 7
+        L.ep_expert_gemm_fp8_packed.argtypes = [sp, i32, i32] + [vp] * 8
+        L.ep_expert_swiglu_fp8.argtypes = [sp, i32] + [vp] * 8
+        L.ep_expert_swiglu_fp8_packed.argtypes = [sp, i32, i32] + [vp] * 9
         for fn in EXPORTED:
             if fn.startswith("ep_") and fn not in ("ep_error_string", "ep_last_error",
                                                    "ep_version", "ep_layout_workspace_bytes"):
@@ -859,6 +864,111 @@ def ep_combine_packed(y: torch.Tensor, topk_idx: torch.Tensor, slot: torch.Tenso
           stream=stream)
     return out
 
+
+# ------------------------------------------------------------------------------------------
+# the experts between dispatch and combine
+# ------------------------------------------------------------------------------------------
+
+def _e4m3(t: torch.Tensor) -> torch.dtype:
+    # FP8 codes may be passed as torch.float8_e4m3fn or as their uint8 bit patterns
+    return t.dtype if t.dtype in (torch.uint8, torch.float8_e4m3fn) else torch.uint8
+
+
+def _product_args(q, scale, expert_count, w_q, w_scale, lead):
+    """Checks of the rows and weights of an experts' product; returns (E, n, H)."""
+    if w_q.dim() != 3 or q.dim() != lead + 1:
+        raise ValueError(f"expected rows with {lead + 1} dimensions and w_q [E, N, H], got "
+                         f"{tuple(q.shape)} and {tuple(w_q.shape)}")
+    E, n, H = w_q.shape
+    if q.shape[-1] != H or (lead == 2 and q.shape[0] != E):
+        raise ValueError(f"rows {tuple(q.shape)} do not fit the weights {tuple(w_q.shape)}")
+    dev = q.device
+    nb = H // EP_FP8_BLOCK
+    _need(q, "recv_q", _e4m3(q), q.numel(), dev)
+    _need(scale, "recv_scale", torch.float32, q.numel() // H * nb if H else 0, dev)
+    _need(expert_count, "expert_count", torch.int32, E, dev)
+    _need(w_q, "w_q", _e4m3(w_q), E * n * H, dev)
+    _need(w_scale, "w_scale", torch.float32, E * -(-n // EP_FP8_BLOCK) * nb, dev)
+    return E, n, H
+
+
+def ep_expert_gemm_fp8(recv_q: torch.Tensor, recv_scale: torch.Tensor,
+                       expert_count: torch.Tensor, w_q: torch.Tensor, w_scale: torch.Tensor,
+                       pairs: int, *, y=None, stream=None):
+    """The experts' product on a padded receive buffer: ``recv_q`` [E, C, H] E4M3 codes and
+    ``recv_scale`` [E, C, H/128] float32 (as ep_dispatch_fp8 writes them), the first
+    ``expert_count[e]`` rows of each expert; weights ``w_q`` [E, N, H] codes and ``w_scale``
+    [E, ceil(N/128), H/128] -> ``y`` [E, C, N] bf16. Rows that hold no pair are neither read nor
+    written. ``pairs``: T * K, the pairs the layout placed (chooses the tile size)."""
+    E, N, H = _product_args(recv_q, recv_scale, expert_count, w_q, w_scale, 2)
+    C, dev = recv_q.shape[1], recv_q.device
+    y = torch.empty((E, C, N), dtype=torch.bfloat16, device=dev) if y is None else y
+    _need(y, "y", _bf16(y), E * C * N, dev)
+    sh = _shape(pairs, H, E, 1, C, 1)
+    _call("ep_expert_gemm_fp8", sh, N, recv_q, recv_scale, expert_count, w_q, w_scale, y,
+          stream=stream)
+    return y
+
+
+def ep_expert_gemm_fp8_packed(recv_q: torch.Tensor, recv_scale: torch.Tensor,
+                              expert_count: torch.Tensor, packed_offset: torch.Tensor,
+                              w_q: torch.Tensor, w_scale: torch.Tensor, pairs: int, *, y=None,
+                              stream=None):
+    """ep_expert_gemm_fp8 on a packed buffer: ``recv_q`` [rows, H], ``recv_scale`` [rows, H/128],
+    expert e's rows from ``packed_offset[e]`` on -> ``y`` [rows, N] bf16."""
+    E, N, H = _product_args(recv_q, recv_scale, expert_count, w_q, w_scale, 1)
+    rows, dev = recv_q.shape[0], recv_q.device
+    _need(packed_offset, "packed_offset", torch.int32, E + 1, dev)
+    y = torch.empty((rows, N), dtype=torch.bfloat16, device=dev) if y is None else y
+    _need(y, "y", _bf16(y), rows * N, dev)
+    sh = _shape(pairs, H, E, 1, 1, 1)
+    _call("ep_expert_gemm_fp8_packed", sh, rows, N, recv_q, recv_scale, expert_count,
+          packed_offset, w_q, w_scale, y, stream=stream)
+    return y
+
+
+def ep_expert_swiglu_fp8(recv_q: torch.Tensor, recv_scale: torch.Tensor,
+                         expert_count: torch.Tensor, w_q: torch.Tensor, w_scale: torch.Tensor,
+                         pairs: int, *, h_q=None, h_scale=None, stream=None):
+    """The gate and up products, SwiGLU and the FP8 cast on a padded receive buffer: the rows of
+    ep_expert_gemm_fp8, ``w_q`` [E, 2I, H] (the I gate rows, then the I up rows) and ``w_scale``
+    [E, 2I/128, H/128] -> ``h_q`` [E, C, I] E4M3 codes and ``h_scale`` [E, C, I/128] float32,
+    which ep_expert_gemm_fp8 takes as its rows."""
+    E, n, H = _product_args(recv_q, recv_scale, expert_count, w_q, w_scale, 2)
+    if n % 2:
+        raise ValueError(f"w_q: expected an even number of rows (gate, then up), got {n}")
+    C, I, dev = recv_q.shape[1], n // 2, recv_q.device
+    h_q = torch.empty((E, C, I), dtype=recv_q.dtype, device=dev) if h_q is None else h_q
+    h_scale = (torch.empty((E, C, I // EP_FP8_BLOCK), dtype=torch.float32, device=dev)
+               if h_scale is None else h_scale)
+    _need(h_q, "h_q", _e4m3(h_q), E * C * I, dev)
+    _need(h_scale, "h_scale", torch.float32, E * C * (I // EP_FP8_BLOCK), dev)
+    sh = _shape(pairs, H, E, 1, C, 1)
+    _call("ep_expert_swiglu_fp8", sh, I, recv_q, recv_scale, expert_count, w_q, w_scale, h_q,
+          h_scale, stream=stream)
+    return h_q, h_scale
+
+
+def ep_expert_swiglu_fp8_packed(recv_q: torch.Tensor, recv_scale: torch.Tensor,
+                                expert_count: torch.Tensor, packed_offset: torch.Tensor,
+                                w_q: torch.Tensor, w_scale: torch.Tensor, pairs: int, *,
+                                h_q=None, h_scale=None, stream=None):
+    """ep_expert_swiglu_fp8 on a packed buffer: ``recv_q`` [rows, H] -> ``h_q`` [rows, I] and
+    ``h_scale`` [rows, I/128]."""
+    E, n, H = _product_args(recv_q, recv_scale, expert_count, w_q, w_scale, 1)
+    if n % 2:
+        raise ValueError(f"w_q: expected an even number of rows (gate, then up), got {n}")
+    rows, I, dev = recv_q.shape[0], n // 2, recv_q.device
+    _need(packed_offset, "packed_offset", torch.int32, E + 1, dev)
+    h_q = torch.empty((rows, I), dtype=recv_q.dtype, device=dev) if h_q is None else h_q
+    h_scale = (torch.empty((rows, I // EP_FP8_BLOCK), dtype=torch.float32, device=dev)
+               if h_scale is None else h_scale)
+    _need(h_q, "h_q", _e4m3(h_q), rows * I, dev)
+    _need(h_scale, "h_scale", torch.float32, rows * (I // EP_FP8_BLOCK), dev)
+    sh = _shape(pairs, H, E, 1, 1, 1)
+    _call("ep_expert_swiglu_fp8_packed", sh, rows, I, recv_q, recv_scale, expert_count,
+          packed_offset, w_q, w_scale, h_q, h_scale, stream=stream)
+    return h_q, h_scale
 
 
 def ep_check_e4m3_conversion(first_pattern: int, count: int, *, device=None, stream=None):

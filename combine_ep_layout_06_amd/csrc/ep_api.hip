@@ -7,6 +7,7 @@
 #include <string>
 
 #include "ep.h"
+#include "ep_expert.h"
 #include "ep_internal.h"
 
 #ifndef EP_VERSION_STRING
@@ -678,6 +679,140 @@ int ep_combine_packed(const ep_shape_t *shape, int32_t rows, const uint16_t *y,
     return hip_status(ep::launch_combine(*shape, y, topk_idx, slot, topk_w, out, stream,
                                          ep::RowMap{packed_offset, rows}),
                       fn);
+}
+
+namespace {
+
+// Checks shared by the experts' FP8 products: `n` weight rows per expert (a multiple of
+// `n_multiple`), rows of H channels.
+int check_product(const ep_shape_t *shape, int32_t n, int n_multiple, const char *n_name,
+                  const uint8_t *q, const float *scale, const int32_t *expert_count,
+                  const uint8_t *w_q, const float *w_scale, const void *out, const char *fn)
+{
+    const std::string f(fn);
+    if (int rc = check_shape(shape, fn)) return rc;
+    if (n < 1) return fail(EP_ERR_INVALID, f + ": need " + n_name + " >= 1");
+    if (shape->E > EP_MAX_EXPERTS) return fail(EP_ERR_UNSUPPORTED, f + ": E exceeds EP_MAX_EXPERTS");
+    if (shape->H % EP_FP8_BLOCK != 0)
+        return fail(EP_ERR_UNSUPPORTED, f + ": H must be a multiple of 128");
+    if (n % n_multiple != 0)
+        return fail(EP_ERR_UNSUPPORTED, f + ": " + n_name + " must be a multiple of " +
+                                            std::to_string(n_multiple));
+    // lane offsets inside one expert's weights and inside one tile of rows are 32 bits wide
+    if ((int64_t)n * 2 * shape->H > INT32_MAX || (int64_t)shape->H * 256 > INT32_MAX)
+        return fail(EP_ERR_UNSUPPORTED, f + ": an expert's weights exceed 2^30 elements");
+    const bool empty = (int64_t)shape->T * shape->K == 0;
+    if (!empty && (!q || !scale || !expert_count || !w_q || !w_scale || !out))
+        return fail(EP_ERR_INVALID, f + ": NULL required pointer");
+    if (!aligned(q, 16) || !aligned(w_q, 16) || !aligned(out, 16))
+        return fail(EP_ERR_ALIGN, f + ": the row buffers and w_q must be 16-byte aligned");
+    if (!aligned(scale, 4) || !aligned(expert_count, 4) || !aligned(w_scale, 4))
+        return fail(EP_ERR_ALIGN, f + ": scales and counts must be 4-byte aligned");
+    return EP_OK;
+}
+
+int check_packed_rows(const ep_shape_t *shape, int32_t rows, const int32_t *packed_offset,
+                      const char *fn)
+{
+    const std::string f(fn);
+    if (rows < 0) return fail(EP_ERR_INVALID, f + ": need rows >= 0");
+    if ((int64_t)shape->T * shape->K > 0 && !packed_offset)
+        return fail(EP_ERR_INVALID, f + ": NULL required pointer");
+    if (!aligned(packed_offset, 4))
+        return fail(EP_ERR_ALIGN, f + ": packed_offset must be 4-byte aligned");
+    return EP_OK;
+}
+
+ep::ExpertProduct product(const ep_shape_t *s, int32_t n, const uint8_t *q, const float *scale,
+                          const int32_t *count, const uint8_t *w_q, const float *w_scale)
+{
+    ep::ExpertProduct p{};
+    p.q = q;
+    p.scale = scale;
+    p.count = count;
+    p.w_q = w_q;
+    p.w_scale = w_scale;
+    p.E = s->E;
+    p.C = s->C;
+    p.H = s->H;
+    p.n = n;
+    p.pairs = s->T * s->K;
+    return p;
+}
+
+}  // namespace
+
+int ep_expert_gemm_fp8(const ep_shape_t *shape, int32_t N, const uint8_t *recv_q,
+                       const float *recv_scale, const int32_t *expert_count, const uint8_t *w_q,
+                       const float *w_scale, uint16_t *y, hipStream_t stream)
+{
+    const char *fn = "ep_expert_gemm_fp8";
+    if (int rc = check_product(shape, N, 8, "N", recv_q, recv_scale, expert_count, w_q, w_scale, y,
+                               fn))
+        return rc;
+    ep::ExpertProduct p = product(shape, N, recv_q, recv_scale, expert_count, w_q, w_scale);
+    p.y = y;
+    return hip_status(ep::launch_expert_gemm_fp8(p, stream), fn);
+}
+
+int ep_expert_gemm_fp8_packed(const ep_shape_t *shape, int32_t rows, int32_t N,
+                              const uint8_t *recv_q, const float *recv_scale,
+                              const int32_t *expert_count, const int32_t *packed_offset,
+                              const uint8_t *w_q, const float *w_scale, uint16_t *y,
+                              hipStream_t stream)
+{
+    const char *fn = "ep_expert_gemm_fp8_packed";
+    if (int rc = check_product(shape, N, 8, "N", recv_q, recv_scale, expert_count, w_q, w_scale, y,
+                               fn))
+        return rc;
+    if (int rc = check_packed_rows(shape, rows, packed_offset, fn)) return rc;
+    ep::ExpertProduct p = product(shape, N, recv_q, recv_scale, expert_count, w_q, w_scale);
+    p.offset = packed_offset;
+    p.rows = p.C = rows;
+    p.y = y;
+    return hip_status(ep::launch_expert_gemm_fp8(p, stream), fn);
+}
+
+int ep_expert_swiglu_fp8(const ep_shape_t *shape, int32_t I, const uint8_t *recv_q,
+                         const float *recv_scale, const int32_t *expert_count,
+                         const uint8_t *w_q, const float *w_scale, uint8_t *h_q, float *h_scale,
+                         hipStream_t stream)
+{
+    const char *fn = "ep_expert_swiglu_fp8";
+    if (int rc = check_product(shape, I, EP_FP8_BLOCK, "I", recv_q, recv_scale, expert_count, w_q,
+                               w_scale, h_q, fn))
+        return rc;
+    if ((int64_t)shape->T * shape->K > 0 && !h_scale)
+        return fail(EP_ERR_INVALID, std::string(fn) + ": NULL required pointer");
+    if (!aligned(h_scale, 4))
+        return fail(EP_ERR_ALIGN, std::string(fn) + ": scales and counts must be 4-byte aligned");
+    ep::ExpertProduct p = product(shape, 2 * I, recv_q, recv_scale, expert_count, w_q, w_scale);
+    p.h_q = h_q;
+    p.h_scale = h_scale;
+    return hip_status(ep::launch_expert_swiglu_fp8(p, stream), fn);
+}
+
+int ep_expert_swiglu_fp8_packed(const ep_shape_t *shape, int32_t rows, int32_t I,
+                                const uint8_t *recv_q, const float *recv_scale,
+                                const int32_t *expert_count, const int32_t *packed_offset,
+                                const uint8_t *w_q, const float *w_scale, uint8_t *h_q,
+                                float *h_scale, hipStream_t stream)
+{
+    const char *fn = "ep_expert_swiglu_fp8_packed";
+    if (int rc = check_product(shape, I, EP_FP8_BLOCK, "I", recv_q, recv_scale, expert_count, w_q,
+                               w_scale, h_q, fn))
+        return rc;
+    if (int rc = check_packed_rows(shape, rows, packed_offset, fn)) return rc;
+    if ((int64_t)shape->T * shape->K > 0 && !h_scale)
+        return fail(EP_ERR_INVALID, std::string(fn) + ": NULL required pointer");
+    if (!aligned(h_scale, 4))
+        return fail(EP_ERR_ALIGN, std::string(fn) + ": scales and counts must be 4-byte aligned");
+    ep::ExpertProduct p = product(shape, 2 * I, recv_q, recv_scale, expert_count, w_q, w_scale);
+    p.offset = packed_offset;
+    p.rows = p.C = rows;
+    p.h_q = h_q;
+    p.h_scale = h_scale;
+    return hip_status(ep::launch_expert_swiglu_fp8(p, stream), fn);
 }
 
 int ep_check_e4m3_conversion(uint32_t first_pattern, uint32_t count, uint32_t *mismatches,

@@ -1,0 +1,315 @@
+// The experts' FP8 products on gfx950: each expert's rows (E4M3 codes with one fp32 scale per row
+// and 128 channels, as the FP8 dispatch writes them) times its weights (E4M3 codes with one fp32
+// scale per 128 x 128 block).
+//
+//   y[r][c] = bf16( sum_b xs[r][b] * ws[e][c / 128][b] * sum_{k in block b} xq[r][k] * wq[e][c][k] )
+//
+// One v_mfma_f32_16x16x128_f8f6f4 covers exactly one scale block of a 16 x 16 tile, so the inner
+// sum is one matrix instruction with a zero start and the outer sum one fmaf per element, in
+// ascending b. The SwiGLU form, whose scales are fp32 outputs, takes the exact product of the same
+// codes (mfma_exact). The weights are the A operand and the rows the B operand: a lane then holds one
+// row (its scale is one value) and four consecutive output channels.
+#include "ep_expert.h"
+
+namespace ep {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kTileN = 256;        // weight rows per workgroup: 64 per wavefront
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The experts' rows cut into tiles of `bm` rows: rows and first row of each expert, and the
+// running number of tiles. Built once per workgroup.
+struct TileTable {
+    int32_t end[EP_MAX_EXPERTS], base[EP_MAX_EXPERTS], n[EP_MAX_EXPERTS];
+    int32_t wave_sum[kWaves];
+};
+
+__device__ __forceinline__ int build_table(TileTable &t, const ExpertProduct &p, int bm)
+{
+    constexpr int kPer = EP_MAX_EXPERTS / kThreads;
+    const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
+    const int e0 = threadIdx.x * kPer;
+    int tiles[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        tiles[i] = 0;
+        if (e0 + i < p.E) {
+            int base, n;
+            expert_rows(p.count, p.offset, e0 + i, p.C, p.rows, base, n);
+            t.base[e0 + i] = base;
+            t.n[e0 + i] = n;
+            tiles[i] = (n + bm - 1) / bm;
+        }
+        sum += tiles[i];
+    }
+    const int incl = wave_inclusive_sum(sum);
+    if (lane == kWave - 1) t.wave_sum[wave] = incl;
+    __syncthreads();
+    int run = incl - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        const int s = t.wave_sum[w];
+        if (w < wave) run += s;
+        total += s;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        run += tiles[i];
+        if (e0 + i < p.E) t.end[e0 + i] = run;
+    }
+    __syncthreads();
+    return total;
+}
+
+// The expert whose tiles include row tile m (m < total).
+__device__ __forceinline__ int find_expert(const TileTable &t, int E, int m)
+{
+    int lo = 0, hi = E - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (t.end[mid] > m) hi = mid;
+        else lo = mid + 1;
+    }
+    return uniform(lo);
+}
+
+// h = silu(g) * u.
+__device__ __forceinline__ float swiglu(float g, float u)
+{
+    return g / (1.0f + __expf(-g)) * u;
+}
+
+// The scale of a block with this amax pattern (integer max of |h|): amax / 448, a NaN amax giving
+// the quiet NaN (the rules of the FP8 dispatch).
+__device__ __forceinline__ float block_scale(uint32_t amax)
+{
+    return amax > 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float(amax) / 448.0f;
+}
+
+// E4M3 codes of four values of a block: q = e4m3(h / scale), IEEE division; signed zeros where
+// the scale is 0, and every code carries its value's own sign.
+__device__ __forceinline__ uint32_t encode4_any(const float (&h)[4], float scale)
+{
+    uint32_t v = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t sign = (__float_as_uint(h[k]) >> 24) & 0x80u;
+        const uint32_t c = scale == 0.0f ? sign : sign | (e4m3_rne_sat(h[k] / scale) & 0x7Fu);
+        v |= c << (8 * k);
+    }
+    return v;
+}
+
+// SwiGLU: MT tiles of 16 rows, a wavefront's tiles 0, 1 (gate) and 2, 3 (up) of weight rows.
+template <int MT>
+struct SwigluShared {
+    uint32_t amax[kWaves][MT * 16];
+    float scale[MT * 16];
+    u32x4 code[MT * 16][8];
+};
+
+template <int MT>
+__device__ __forceinline__ void store_swiglu(SwigluShared<MT> &sh, f32x4 (&acc)[4][MT],
+                                             const ExpertProduct &p, int row0, int n, int nblk)
+{
+    const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
+    const int r16 = lane & 15, g4 = lane >> 4;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        uint32_t amax = 0;
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                acc[nt][mt][k] = swiglu(acc[nt][mt][k], acc[nt + 2][mt][k]);
+                amax = max(amax, __float_as_uint(acc[nt][mt][k]) & 0x7FFFFFFFu);
+            }
+        amax = max(amax, (uint32_t)__shfl_xor((int)amax, 16));
+        amax = max(amax, (uint32_t)__shfl_xor((int)amax, 32));
+        if (g4 == 0) sh.amax[wave][mt * 16 + r16] = amax;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const int r = mt * 16 + r16;
+        uint32_t amax = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) amax = max(amax, sh.amax[w][r]);
+        const float scale = block_scale(amax);
+        // 2^-60 <= amax < inf: the quotients lie where div_by_rcp and the conversion are exact
+        const bool plain = amax < 0x21800000u || amax >= 0x7F800000u;
+        const bool any_plain = __any(plain);
+        const float y = 1.0f / scale;
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+            const float h[4] = {acc[nt][mt][0], acc[nt][mt][1], acc[nt][mt][2], acc[nt][mt][3]};
+            uint32_t v;
+            if (any_plain)
+                v = encode4_any(h, scale);
+            else
+                v = e4m3_pack4(div_by_rcp(h[0], scale, y), div_by_rcp(h[1], scale, y),
+                               div_by_rcp(h[2], scale, y), div_by_rcp(h[3], scale, y));
+            // channel wave * 32 + nt * 16 + g4 * 4 of the row's block
+            reinterpret_cast<uint32_t *>(&sh.code[r][0])[wave * 8 + nt * 4 + g4] = v;
+        }
+        if (wave == 0 && g4 == 0) sh.scale[r] = scale;
+    }
+    __syncthreads();
+    const int I = p.n / 2;
+    for (int i = threadIdx.x; i < MT * 16 * 8; i += kThreads) {
+        const int r = i >> 3;
+        if (r < n)
+            *reinterpret_cast<u32x4 *>(p.h_q + (size_t)(row0 + r) * I + nblk * 128 + (i & 7) * 16) =
+                sh.code[r][i & 7];
+    }
+    for (int r = threadIdx.x; r < n; r += kThreads)
+        p.h_scale[(size_t)(row0 + r) * (I / 128) + nblk] = sh.scale[r];
+    __syncthreads();
+}
+
+// Few rows per expert: every operand straight from global memory to registers, no barrier in the
+// product. MT tiles of 16 rows; a wavefront takes 4 tiles of 16 weight rows (gemm: 64 consecutive
+// rows; SwiGLU: 32 gate rows and the same 32 up rows) and the whole of H, D blocks in flight.
+template <int MT, bool SWIGLU, int D>
+__global__ __launch_bounds__(kThreads) void expert_stream_kernel(ExpertProduct p)
+{
+    __shared__ TileTable table;
+    __shared__ SwigluShared<SWIGLU ? MT : 1> sh;
+    const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
+    const int r16 = lane & 15, g4 = lane >> 4;
+    const int nkb = p.H >> 7;
+    const int n_tiles = SWIGLU ? p.n / kTileN : (p.n + kTileN - 1) / kTileN;
+    const int ws_rows = (p.n + 127) >> 7;
+    const int total = build_table(table, p, MT * 16) * n_tiles;
+    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+        const int m = tile / n_tiles, nblk = tile - m * n_tiles;
+        const int e = find_expert(table, p.E, m);
+        const int n_e = uniform(table.n[e]);
+        const int m0 = (m - (uniform(table.end[e]) - (n_e + MT * 16 - 1) / (MT * 16))) * (MT * 16);
+        const int row0 = uniform(table.base[e]) + m0;
+        const int n = min(n_e - m0, MT * 16);        // rows of this tile
+
+        // lane offsets of the weight rows (clamped) and of the tile's rows (clamped)
+        uint32_t woff[4], xoff[MT], soff[MT];
+        int wrow[4];
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+            wrow[nt] = SWIGLU ? (nt >> 1) * (p.n / 2) + nblk * 128 + wave * 32 + (nt & 1) * 16
+                              : nblk * kTileN + wave * 64 + nt * 16;
+            woff[nt] = (uint32_t)min(wrow[nt] + r16, p.n - 1) * p.H + g4 * 16;
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int r = min(mt * 16 + r16, n - 1);
+            xoff[mt] = (uint32_t)r * p.H + g4 * 16;
+            soff[mt] = (uint32_t)r * nkb;
+        }
+        const uint8_t *w = p.w_q + (size_t)e * p.n * p.H;
+        const uint8_t *x = p.q + (size_t)row0 * p.H;
+        const float *xs = p.scale + (size_t)row0 * nkb;
+        const float *ws[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            ws[i] = p.w_scale + ((size_t)e * ws_rows + min(wrow[2 * i] >> 7, ws_rows - 1)) * nkb;
+
+        i32x8 wf[D][4], xf[D][MT];
+        float sx[D][MT], sw[D][2];
+        auto load = [&](int d, int kb) {
+            const uint8_t *wk = w + kb * 128, *xk = x + kb * 128;
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+                wf[d][nt] = join(*reinterpret_cast<const i32x4 *>(wk + woff[nt]),
+                                 *reinterpret_cast<const i32x4 *>(wk + woff[nt] + 64));
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                xf[d][mt] = join(*reinterpret_cast<const i32x4 *>(xk + xoff[mt]),
+                                 *reinterpret_cast<const i32x4 *>(xk + xoff[mt] + 64));
+                sx[d][mt] = xs[kb + soff[mt]];
+            }
+            sw[d][0] = ws[0][kb];
+            sw[d][1] = ws[1][kb];
+        };
+        f32x4 acc[4][MT];
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) acc[nt][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int d = 0; d < D; ++d) load(d, min(d, nkb - 1));
+        for (int kb = 0; kb < nkb; kb += D) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                if (kb + d < nkb) {
+                    Bf16Block xb[SWIGLU ? MT : 1];
+                    if constexpr (SWIGLU)
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) xb[mt] = bf16_block(xf[d][mt]);
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt) {
+                        Bf16Block wb;
+                        if constexpr (SWIGLU) wb = bf16_block(wf[d][nt]);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            f32x4 v;
+                            if constexpr (SWIGLU) v = mfma_exact(wb, xb[mt]);
+                            else v = mfma_e4m3(wf[d][nt], xf[d][mt]);
+                            const float s = sx[d][mt] * sw[d][nt >> 1];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                acc[nt][mt][k] = __builtin_fmaf(s, v[k], acc[nt][mt][k]);
+                        }
+                    }
+                }
+                load(d, min(kb + d + D, nkb - 1));
+            }
+        }
+
+        if constexpr (SWIGLU) {
+            store_swiglu<MT>(sh, acc, p, row0, n, nblk);
+        } else {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const int r = mt * 16 + r16;
+                uint16_t *y = p.y + (size_t)(row0 + r) * p.n;
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) {
+                    const int c = wrow[nt] + g4 * 4;
+                    if (r < n && c < p.n) {          // n % 8 == 0: the four channels together
+                        uint2 o;
+                        o.x = bf16_rne(acc[nt][mt][0]) | (bf16_rne(acc[nt][mt][1]) << 16);
+                        o.y = bf16_rne(acc[nt][mt][2]) | (bf16_rne(acc[nt][mt][3]) << 16);
+                        *reinterpret_cast<uint2 *>(y + c) = o;
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <bool SWIGLU>
+hipError_t launch_product(const ExpertProduct &p, hipStream_t stream)
+{
+    if (p.pairs == 0 || (p.offset && p.rows == 0)) return hipSuccess;
+    const int64_t n_tiles = (p.n + kTileN - 1) / kTileN;
+    const int64_t tiles = ((int64_t)p.pairs / 64 + p.E) * n_tiles;
+    const int grid = (int)(tiles < 512 ? tiles : 512);
+    return launch(expert_stream_kernel<4, SWIGLU, 1>, dim3(grid), dim3(kThreads), 0, stream, p);
+}
+
+}  // namespace
+
+hipError_t launch_expert_gemm_fp8(const ExpertProduct &p, hipStream_t stream)
+{
+    return launch_product<false>(p, stream);
+}
+
+hipError_t launch_expert_swiglu_fp8(const ExpertProduct &p, hipStream_t stream)
+{
+    return launch_product<true>(p, stream);
+}
+
+}  // namespace ep

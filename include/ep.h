@@ -443,6 +443,72 @@ int ep_combine_reduce(const ep_shape_t *shape, const uint16_t *part, const int32
                       uint16_t *out, hipStream_t stream);
 
 /*
+ * The experts between dispatch and combine: FP8 products over the rows of the receive buffer.
+ *
+ * Each expert e holds n = expert_count[e] rows from row e*C of a padded buffer [E][C] (n taken as
+ * min(max(n, 0), C)), or from row packed_offset[e] of a packed buffer of `rows` rows (rows outside
+ * the buffer are left out; C is not used). Only these rows are read and written; other rows of the
+ * outputs keep what they hold. shape->T * shape->K is the number of pairs laid out; it chooses
+ * the tile size and the grid, never the result, except that T = 0 means no rows: the call does
+ * nothing. R is not used. H is the width of the INPUT rows.
+ *
+ * Weights are row-major per expert, one row of H codes per output channel, with one fp32 scale
+ * per 128 x 128 block: w_q [E][N][H] uint8 (OCP E4M3), 16-byte aligned; w_scale
+ * [E][ceil(N/128)][H/128] float, the last row of blocks covering the N % 128 rows that are left.
+ *
+ * Common requirements (else EP_ERR_UNSUPPORTED): E <= EP_MAX_EXPERTS, H % 128 == 0, H and the
+ * weights of one expert within 2^30 elements (H <= 2^23).
+ */
+
+/*
+ * ep_expert_gemm_fp8 / ep_expert_gemm_fp8_packed -- y = rows * w^T with block scales, to bf16.
+ *
+ *   y[r][c] = bf16_rne(acc), acc = +0.0f, then for b = 0 .. H/128-1 ascending
+ *             acc = fmaf(recv_scale[r][b] * w_scale[e][c/128][b], dot_b, acc),
+ *             dot_b = sum over k in block b of recv_q[r][k] * w_q[e][c][k] in fp32
+ *   recv_q [E*C*H] (packed: [rows*H]) uint8, 16-byte aligned; recv_scale [.../128] float
+ *   y      [E*C*N] (packed: [rows*N]) uint16 (bf16) out, 16-byte aligned
+ * dot_b is one FP8 matrix instruction: it aligns each group of (at most 16 consecutive) products
+ * to the largest exponent among them and cuts what lies 14 or more binary places below it, which
+ * is about 2e-5 of the result's norm on real data, a hundredth of y's own rounding.
+ * Deterministic: the same inputs give the same bits.
+ * NaN codes and non-finite scales propagate to the elements they enter. N % 8 == 0.
+ */
+int ep_expert_gemm_fp8(const ep_shape_t *shape, int32_t N, const uint8_t *recv_q,
+                       const float *recv_scale, const int32_t *expert_count, const uint8_t *w_q,
+                       const float *w_scale, uint16_t *y, hipStream_t stream);
+
+int ep_expert_gemm_fp8_packed(const ep_shape_t *shape, int32_t rows, int32_t N,
+                              const uint8_t *recv_q, const float *recv_scale,
+                              const int32_t *expert_count, const int32_t *packed_offset,
+                              const uint8_t *w_q, const float *w_scale, uint16_t *y,
+                              hipStream_t stream);
+
+/*
+ * ep_expert_swiglu_fp8 / ep_expert_swiglu_fp8_packed -- the gate and up products, SwiGLU and the
+ * FP8 cast in one launch. The weights hold the I gate rows, then the I up rows: w_q [E][2I][H],
+ * w_scale [E][2I/128][H/128]. With g and u the same products (not rounded; here each dot_b is
+ * exact up to fp32's rounding, since h_scale is an fp32 output):
+ *   h = g / (1 + exp(-g)) * u   (fp32)
+ * and per row and block of 128 channels of h, the cast of ep_dispatch_fp8:
+ *   h_scale = amax|h| / 448, h_q = e4m3(h / h_scale); the same rules for zeros and non-finite
+ *   values (a NaN h makes its block's scale the quiet NaN).
+ *   h_q     [E*C*I] (packed: [rows*I]) uint8 out, 16-byte aligned
+ *   h_scale [E*C*(I/128)] (packed: [rows*(I/128)]) float out, 4-byte aligned
+ * h_q and h_scale are what ep_expert_gemm_fp8 takes as rows. I % 128 == 0. Deterministic.
+ */
+int ep_expert_swiglu_fp8(const ep_shape_t *shape, int32_t I, const uint8_t *recv_q,
+                         const float *recv_scale, const int32_t *expert_count,
+                         const uint8_t *w_q, const float *w_scale, uint8_t *h_q, float *h_scale,
+                         hipStream_t stream);
+
+int ep_expert_swiglu_fp8_packed(const ep_shape_t *shape, int32_t rows, int32_t I,
+                                const uint8_t *recv_q, const float *recv_scale,
+                                const int32_t *expert_count, const int32_t *packed_offset,
+                                const uint8_t *w_q, const float *w_scale, uint8_t *h_q,
+                                float *h_scale, hipStream_t stream);
+
+/*
  * ep_check_e4m3_conversion -- self-check of the two OCP E4M3 encoders of the FP8 dispatch on
  * the current device.
  *

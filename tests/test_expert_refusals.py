@@ -1,0 +1,113 @@
+"""Refusals of the experts' operators, on the CPU: the C ABI rejects bad arguments before any
+launch, and the Python wrappers reject tensors that do not fit."""
+import ctypes
+
+import pytest
+import torch
+
+from combine_ep_layout_06_amd import binding as B
+
+A16 = 1 << 20          # a fake aligned address: every call below fails its checks first
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return B.load_library()
+
+
+def shape(T=128, H=2048, E=128, K=8, C=512, R=1):
+    return ctypes.byref(B.EpShape(T, H, E, K, C, R))
+
+
+GEMM = dict(name="ep_expert_gemm_fp8", n=1000, ptrs=6)
+SWIGLU = dict(name="ep_expert_swiglu_fp8", n=256, ptrs=7)
+
+
+def call(lib, op, sh, *, n=None, packed=False, rows=100, at=None, value=None):
+    """The call with every pointer aligned but number `at`, which is `value`."""
+    args = [A16] * (op["ptrs"] + packed)
+    if at is not None:
+        args[at] = value
+    n = op["n"] if n is None else n
+    if packed:
+        return getattr(lib, op["name"] + "_packed")(sh, rows, n, *args, None)
+    return getattr(lib, op["name"])(sh, n, *args, None)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("op", [GEMM, SWIGLU], ids=lambda o: o["name"])
+def test_product_shapes_refused(lib, op, packed):
+    bad = lambda code, sh=None, **kw: call(lib, op, sh or shape(), packed=packed, **kw) == code  # noqa: E731
+    assert bad(B.EP_ERR_INVALID, shape(T=-1))
+    assert bad(B.EP_ERR_INVALID, shape(H=0))
+    assert bad(B.EP_ERR_INVALID, shape(T=1 << 30))
+    assert call(lib, op, None, packed=packed) == B.EP_ERR_INVALID
+    assert bad(B.EP_ERR_INVALID, n=0) and bad(B.EP_ERR_INVALID, n=-8)
+    assert bad(B.EP_ERR_UNSUPPORTED, shape(H=2000))
+    assert "multiple of 128" in lib.ep_last_error().decode()
+    assert bad(B.EP_ERR_UNSUPPORTED, shape(E=1025))
+    assert bad(B.EP_ERR_UNSUPPORTED, n=op["n"] + 4)
+    assert bad(B.EP_ERR_UNSUPPORTED, shape(H=1 << 20), n=1024)
+    assert "2^30" in lib.ep_last_error().decode()
+    assert bad(B.EP_ERR_UNSUPPORTED, shape(H=1 << 24, E=1), n=128)
+    if packed:
+        assert bad(B.EP_ERR_INVALID, rows=-1)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("op", [GEMM, SWIGLU], ids=lambda o: o["name"])
+def test_product_pointers_refused(lib, op, packed):
+    n = op["ptrs"] + packed
+    for at in range(n):
+        assert call(lib, op, shape(), packed=packed, at=at, value=None) == B.EP_ERR_INVALID, at
+        assert call(lib, op, shape(), packed=packed, at=at, value=A16 + 2) == B.EP_ERR_ALIGN, at
+    assert lib.ep_last_launches(None, 0) == 0
+    # rows, weights and row outputs need 16 bytes; scales, counts and offsets 4
+    wide = {0, 3 + packed, 5 + packed}
+    for at in wide:
+        assert call(lib, op, shape(), packed=packed, at=at, value=A16 + 8) == B.EP_ERR_ALIGN, at
+
+
+def tensors(E=4, C=8, H=256, N=256):
+    return dict(q=torch.zeros((E, C, H), dtype=torch.uint8), s=torch.zeros((E, C, H // 128)),
+                count=torch.zeros(E, dtype=torch.int32),
+                w=torch.zeros((E, N, H), dtype=torch.uint8),
+                ws=torch.zeros((E, -(-N // 128), H // 128)))
+
+
+@pytest.mark.parametrize("fn", [B.ep_expert_gemm_fp8, B.ep_expert_swiglu_fp8])
+@pytest.mark.parametrize("key,value,error", [
+    ("q", torch.zeros((4, 8, 256), dtype=torch.int16), TypeError),
+    ("q", torch.zeros((4, 8, 512), dtype=torch.uint8), ValueError),
+    ("q", torch.zeros((3, 8, 256), dtype=torch.uint8), ValueError),
+    ("q", torch.zeros((32, 256), dtype=torch.uint8), ValueError),
+    ("q", torch.zeros((4, 256, 8), dtype=torch.uint8).transpose(1, 2), ValueError),
+    ("s", torch.zeros((4, 8, 1)), ValueError),
+    ("s", torch.zeros((4, 8, 2), dtype=torch.float64), TypeError),
+    ("count", torch.zeros(4, dtype=torch.int64), TypeError),
+    ("count", torch.zeros(5, dtype=torch.int32), ValueError),
+    ("w", torch.zeros((4, 256, 256), dtype=torch.bfloat16), TypeError),
+    ("w", torch.zeros((256, 256), dtype=torch.uint8), ValueError),
+    ("ws", torch.zeros((4, 1, 2)), ValueError),
+])
+def test_product_tensors_refused(fn, key, value, error):
+    t = tensors()
+    t[key] = value
+    with pytest.raises(error):
+        fn(t["q"], t["s"], t["count"], t["w"], t["ws"], 32)
+
+
+def test_host_tensors_are_refused():
+    t = tensors()
+    for fn in (B.ep_expert_gemm_fp8, B.ep_expert_swiglu_fp8):
+        with pytest.raises(ValueError, match="current HIP device"):
+            fn(t["q"], t["s"], t["count"], t["w"], t["ws"], 32)
+    off = torch.zeros(5, dtype=torch.int32)
+    for fn in (B.ep_expert_gemm_fp8_packed, B.ep_expert_swiglu_fp8_packed):
+        with pytest.raises(ValueError, match="current HIP device"):
+            fn(t["q"].view(32, 256), t["s"].view(32, 2), t["count"], off, t["w"], t["ws"], 32)
+        with pytest.raises(ValueError):
+            fn(t["q"].view(32, 256), t["s"].view(32, 2), t["count"], off[:4], t["w"], t["ws"], 32)
+    with pytest.raises(ValueError, match="even"):
+        B.ep_expert_swiglu_fp8(t["q"], t["s"], t["count"],
+                               torch.zeros((4, 255, 256), dtype=torch.uint8), t["ws"], 32)
