@@ -24,6 +24,7 @@ EP_MAX_EXPERTS = 1024
 EP_MAX_TOPK = 256
 EP_FP8_BLOCK = 128
 EP_MAX_RANKS = 64
+EP_MOE_MAX_PAIRS = 2048
 
 #: every entry point the header declares
 EXPORTED = ("ep_layout", "ep_dispatch", "ep_dispatch_fp8", "ep_layout_dispatch",
@@ -36,7 +37,8 @@ EXPORTED = ("ep_layout", "ep_dispatch", "ep_dispatch_fp8", "ep_layout_dispatch",
             "ep_combine_packed", "ep_check_e4m3_conversion", "ep_last_launches",
             "ep_layout_workspace_bytes", "ep_layout_dispatch_ws", "ep_layout_dispatch_fp8_ws",
             "ep_layout_dispatch_noalloc", "ep_expert_gemm_fp8", "ep_expert_gemm_fp8_packed",
-            "ep_expert_swiglu_fp8", "ep_expert_swiglu_fp8_packed", "ep_error_string", "ep_last_error", "ep_version")
+            "ep_expert_swiglu_fp8", "ep_expert_swiglu_fp8_packed", "ep_moe_layer",
+            "ep_moe_layer_fp8", "ep_moe_layer_workspace_bytes", "ep_error_string", "ep_last_error", "ep_version")
 
 
 class EpShape(ctypes.Structure):
@@ -110,9 +112,14 @@ def load_library():
         L.ep_expert_gemm_fp8_packed.argtypes = [sp, i32, i32] + [vp] * 8
         L.ep_expert_swiglu_fp8.argtypes = [sp, i32] + [vp] * 8
         L.ep_expert_swiglu_fp8_packed.argtypes = [sp, i32, i32] + [vp] * 9
+        L.ep_moe_layer.argtypes = [sp, i32] + [vp] * 7 + [ctypes.c_size_t, vp]
+        L.ep_moe_layer_fp8.argtypes = [sp, i32] + [vp] * 9 + [ctypes.c_size_t, vp]
+        L.ep_moe_layer_workspace_bytes.argtypes = [sp, i32]
+        L.ep_moe_layer_workspace_bytes.restype = ctypes.c_size_t
         for fn in EXPORTED:
             if fn.startswith("ep_") and fn not in ("ep_error_string", "ep_last_error",
-                                                   "ep_version", "ep_layout_workspace_bytes"):
+                                                   "ep_version", "ep_layout_workspace_bytes",
+                                                   "ep_moe_layer_workspace_bytes"):
                 getattr(L, fn).restype = ctypes.c_int
         L.ep_layout_workspace_bytes.argtypes = [sp]
         L.ep_layout_workspace_bytes.restype = ctypes.c_size_t
@@ -969,6 +976,66 @@ def ep_expert_swiglu_fp8_packed(recv_q: torch.Tensor, recv_scale: torch.Tensor,
     _call("ep_expert_swiglu_fp8_packed", sh, rows, I, recv_q, recv_scale, expert_count,
           packed_offset, w_q, w_scale, h_q, h_scale, stream=stream)
     return h_q, h_scale
+
+def moe_layer_workspace_bytes(T: int, K: int, I: int) -> int:
+    """Bytes of workspace a whole-layer call needs for T tokens, top-K, intermediate size I."""
+    return int(load_library().ep_moe_layer_workspace_bytes(
+        ctypes.byref(_shape(T, 1, 1, K, 1, 1)), I))
+
+
+def _moe_layer(name, x, topk_idx, topk_w, w13, w2, dtype, out, workspace, stream):
+    """Checks shared by the whole-layer calls; returns what both C calls take."""
+    if x.dim() != 2 or topk_idx.dim() != 2 or w13.dim() != 3 or w2.dim() != 3:
+        raise ValueError(f"{name}: expected x [T, H], topk_idx [T, K], w13 [E, 2I, H] and "
+                         f"w2 [E, H, I]")
+    dev = x.device
+    (T, H), K, (E, n, _), I = x.shape, topk_idx.shape[1], w13.shape, w2.shape[2]
+    if n != 2 * I or topk_idx.shape[0] != T:
+        raise ValueError(f"{name}: x {tuple(x.shape)}, topk_idx {tuple(topk_idx.shape)}, w13 "
+                         f"{tuple(w13.shape)} and w2 {tuple(w2.shape)} do not fit together")
+    _need(x, "x", _bf16(x), T * H, dev)
+    _need(topk_idx, "topk_idx", torch.int32, T * K, dev)
+    _need(topk_w, "topk_w", torch.float32, T * K, dev)
+    _need(w13, "w13", dtype(w13), E * n * H, dev)
+    _need(w2, "w2", dtype(w2), E * H * I, dev)
+    out = torch.empty((T, H), dtype=_bf16(x), device=dev) if out is None else out
+    _need(out, "out", _bf16(out), T * H, dev)
+    if workspace is None:
+        workspace = torch.empty(max(4 * T * K * I, 16), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: must be a contiguous tensor on the tokens' device")
+    return (_shape(T, H, E, K, 1, 1), I, out, workspace,
+            workspace.numel() * workspace.element_size())
+
+
+def ep_moe_layer(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
+                 w13: torch.Tensor, w2: torch.Tensor, *, out=None, workspace=None, stream=None):
+    """A whole MoE layer for a few tokens (T * K <= EP_MOE_MAX_PAIRS), in two launches:
+    ``out[t] = sum_j topk_w[t, j] * W2[e_j] (silu(Wg[e_j] x[t]) * (Wu[e_j] x[t]))`` with bf16
+    weights ``w13`` [E, 2I, H] (gate rows, then up rows) and ``w2`` [E, H, I]; ``x`` and ``out``
+    [T, H] bf16. Pairs whose id is not a valid expert add nothing. ``workspace``: a device tensor
+    of at least moe_layer_workspace_bytes(T, K, I) bytes (allocated here if not given)."""
+    sh, I, out, ws, nbytes = _moe_layer("ep_moe_layer", x, topk_idx, topk_w, w13, w2, _bf16, out,
+                                        workspace, stream)
+    _call("ep_moe_layer", sh, I, x, topk_idx, topk_w, w13, w2, out, ws, nbytes, stream=stream)
+    return out
+
+
+def ep_moe_layer_fp8(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
+                     w13_q: torch.Tensor, w13_scale: torch.Tensor, w2_q: torch.Tensor,
+                     w2_scale: torch.Tensor, *, out=None, workspace=None, stream=None):
+    """ep_moe_layer with FP8 weights: E4M3 codes ``w13_q`` [E, 2I, H] and ``w2_q`` [E, H, I] and
+    one float32 scale per 128 x 128 block, ``w13_scale`` [E, 2I/128, H/128] and ``w2_scale``
+    [E, H/128, I/128]. Activations stay bf16."""
+    sh, I, out, ws, nbytes = _moe_layer("ep_moe_layer_fp8", x, topk_idx, topk_w, w13_q, w2_q,
+                                        _e4m3, out, workspace, stream)
+    E, (H, dev) = sh.E, (sh.H, x.device)
+    _need(w13_scale, "w13_scale", torch.float32,
+          E * (2 * I // EP_FP8_BLOCK) * (H // EP_FP8_BLOCK), dev)
+    _need(w2_scale, "w2_scale", torch.float32, E * (H // EP_FP8_BLOCK) * (I // EP_FP8_BLOCK), dev)
+    _call("ep_moe_layer_fp8", sh, I, x, topk_idx, topk_w, w13_q, w13_scale, w2_q, w2_scale, out,
+          ws, nbytes, stream=stream)
+    return out
 
 
 def ep_check_e4m3_conversion(first_pattern: int, count: int, *, device=None, stream=None):

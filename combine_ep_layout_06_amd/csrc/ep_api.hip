@@ -815,6 +815,93 @@ int ep_expert_swiglu_fp8_packed(const ep_shape_t *shape, int32_t rows, int32_t I
     return hip_status(ep::launch_expert_swiglu_fp8(p, stream), fn);
 }
 
+size_t ep_moe_layer_workspace_bytes(const ep_shape_t *shape, int32_t I)
+{
+    if (!shape || shape->T < 0 || shape->K < 1 || I < 1) return 0;
+    return (size_t)4 * shape->T * shape->K * I;
+}
+
+namespace {
+
+int moe_layer(const ep_shape_t *shape, int32_t I, ep::MoeLayer p, bool fp8, void *workspace,
+              size_t workspace_bytes, hipStream_t stream, const char *fn)
+{
+    const std::string f(fn);
+    if (int rc = check_shape(shape, fn)) return rc;
+    if (I < 1) return fail(EP_ERR_INVALID, f + ": need I >= 1");
+    if (shape->E > EP_MAX_EXPERTS) return fail(EP_ERR_UNSUPPORTED, f + ": E exceeds EP_MAX_EXPERTS");
+    if ((int64_t)shape->T * shape->K > EP_MOE_MAX_PAIRS)
+        return fail(EP_ERR_UNSUPPORTED, f + ": T*K exceeds EP_MOE_MAX_PAIRS");
+    const int step = fp8 ? 128 : 64;
+    if (shape->H % step != 0 || I % step != 0)
+        return fail(EP_ERR_UNSUPPORTED, f + ": H and I must be multiples of " +
+                                            std::to_string(step));
+    // byte offsets inside one expert's weights are 32 bits wide
+    if ((int64_t)2 * I * shape->H > (int64_t)1 << 29)
+        return fail(EP_ERR_UNSUPPORTED, f + ": 2*I*H exceeds 2^29");
+    if ((int64_t)shape->T * shape->H > (int64_t)1 << 30 ||
+        (int64_t)shape->T * shape->K * I > (int64_t)1 << 30)
+        return fail(EP_ERR_UNSUPPORTED, f + ": T*H or T*K*I exceeds 2^30");
+    if (shape->T == 0) return hip_status(hipSuccess, fn);
+    if (!p.x || !p.idx || !p.topk_w || !p.w13 || !p.w2 || !p.out ||
+        (fp8 && (!p.w13_scale || !p.w2_scale)))
+        return fail(EP_ERR_INVALID, f + ": NULL required pointer");
+    if (!aligned(p.x, 16) || !aligned(p.w13, 16) || !aligned(p.w2, 16) || !aligned(p.out, 16))
+        return fail(EP_ERR_ALIGN, f + ": x, the weights and out must be 16-byte aligned");
+    if (!aligned(p.idx, 4) || !aligned(p.topk_w, 4) || !aligned(p.w13_scale, 4) ||
+        !aligned(p.w2_scale, 4))
+        return fail(EP_ERR_ALIGN, f + ": ids, weights and scales must be 4-byte aligned");
+    const size_t need = ep_moe_layer_workspace_bytes(shape, I);
+    if (!workspace) return fail(EP_ERR_INVALID, f + ": workspace is NULL");
+    if (workspace_bytes < need)
+        return fail(EP_ERR_INVALID, f + ": workspace_bytes " + std::to_string(workspace_bytes) +
+                                        " below the " + std::to_string(need) +
+                                        " this shape needs");
+    if (!aligned(workspace, 16))
+        return fail(EP_ERR_ALIGN, f + ": workspace must be 16-byte aligned");
+    p.T = shape->T;
+    p.E = shape->E;
+    p.K = shape->K;
+    p.H = shape->H;
+    p.I = I;
+    p.h_hi = static_cast<uint16_t *>(workspace);
+    p.h_lo = p.h_hi + (size_t)shape->T * shape->K * I;
+    return hip_status(ep::launch_moe_layer(p, fp8, stream), fn);
+}
+
+}  // namespace
+
+int ep_moe_layer(const ep_shape_t *shape, int32_t I, const uint16_t *x, const int32_t *topk_idx,
+                 const float *topk_w, const uint16_t *w13, const uint16_t *w2, uint16_t *out,
+                 void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    ep::MoeLayer p{};
+    p.x = x;
+    p.idx = topk_idx;
+    p.topk_w = topk_w;
+    p.w13 = w13;
+    p.w2 = w2;
+    p.out = out;
+    return moe_layer(shape, I, p, false, workspace, workspace_bytes, stream, "ep_moe_layer");
+}
+
+int ep_moe_layer_fp8(const ep_shape_t *shape, int32_t I, const uint16_t *x,
+                     const int32_t *topk_idx, const float *topk_w, const uint8_t *w13_q,
+                     const float *w13_scale, const uint8_t *w2_q, const float *w2_scale,
+                     uint16_t *out, void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    ep::MoeLayer p{};
+    p.x = x;
+    p.idx = topk_idx;
+    p.topk_w = topk_w;
+    p.w13 = w13_q;
+    p.w13_scale = w13_scale;
+    p.w2 = w2_q;
+    p.w2_scale = w2_scale;
+    p.out = out;
+    return moe_layer(shape, I, p, true, workspace, workspace_bytes, stream, "ep_moe_layer_fp8");
+}
+
 int ep_check_e4m3_conversion(uint32_t first_pattern, uint32_t count, uint32_t *mismatches,
                              uint32_t *first_mismatch, hipStream_t stream)
 {

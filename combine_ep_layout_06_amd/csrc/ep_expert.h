@@ -27,6 +27,24 @@ struct ExpertProduct {
 hipError_t launch_expert_gemm_fp8(const ExpertProduct &p, hipStream_t stream);
 hipError_t launch_expert_swiglu_fp8(const ExpertProduct &p, hipStream_t stream);
 
+// A whole MoE layer for a few tokens; weights bf16 (scales null) or E4M3 with 128 x 128 scales.
+struct MoeLayer {
+    const uint16_t *x;        // [T][H] bf16
+    const int32_t *idx;       // [T][K]
+    const float *topk_w;      // [T][K]
+    const void *w13;          // [E][2I][H]: gate rows, then up rows
+    const float *w13_scale;   // [E][2I/128][H/128]
+    const void *w2;           // [E][H][I]
+    const float *w2_scale;    // [E][H/128][I/128]
+    uint16_t *h_hi, *h_lo;    // workspace: [T*K][I] each, h = hi + lo
+    uint16_t *out;            // [T][H] bf16
+    int T, E, K, H, I;
+};
+
+constexpr int kMoePairs = EP_MOE_MAX_PAIRS;
+
+hipError_t launch_moe_layer(const MoeLayer &p, bool fp8, hipStream_t stream);
+
 #if defined(__HIPCC__)
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));

@@ -61,6 +61,7 @@ enum {
 #define EP_MAX_TOPK 256        /* largest K dispatch and combine support */
 #define EP_FP8_BLOCK 128       /* channels per FP8 scale */
 #define EP_MAX_RANKS 64        /* largest R the two-stage (per-rank) calls support */
+#define EP_MOE_MAX_PAIRS 2048  /* largest T*K of the whole-layer calls */
 
 /*
  * ep_layout -- routing layout: per-expert counts, exclusive offsets and stable in-order slots
@@ -507,6 +508,47 @@ int ep_expert_swiglu_fp8_packed(const ep_shape_t *shape, int32_t rows, int32_t I
                                 const int32_t *expert_count, const int32_t *packed_offset,
                                 const uint8_t *w_q, const float *w_scale, uint8_t *h_q,
                                 float *h_scale, hipStream_t stream);
+
+/*
+ * ep_moe_layer / ep_moe_layer_fp8 -- a whole MoE layer for a few tokens (a decode step), from
+ * token rows to combined rows in two launches, with no receive buffer: bound by reading the
+ * chosen experts' weights once.
+ *
+ *   out[t][c] = bf16_rne(acc), acc = +0.0f, then for j = 0 .. K-1 ascending, for each pair with
+ *               0 <= e < E:  acc = fmaf(topk_w[i], y, acc)
+ *   y = sum_k W2[e][c][k] * h[k],  h = g / (1 + exp(-g)) * u,  g = Wg[e] x[t],  u = Wu[e] x[t]
+ * in fp32 (h is held as a pair of bf16 values, hi + lo, 16 significant bits); there is no
+ * capacity, every pair with a valid id counts, and a token with none gives +0. An expert that a
+ * token names twice counts twice. Activations are not quantised: with FP8 weights the layer is
+ * closer to the exact one than the FP8 dispatch and products are.
+ *
+ *   x        [T*H] uint16 (bf16) in, 16-byte aligned; topk_idx [T*K] int32, topk_w [T*K] float
+ *   w13      [E][2I][H], the I gate rows and then the I up rows, 16-byte aligned
+ *   w2       [E][H][I], 16-byte aligned
+ *            bf16 (uint16) in ep_moe_layer; in ep_moe_layer_fp8 E4M3 codes (uint8) with
+ *            w13_scale [E][2I/128][H/128] and w2_scale [E][H/128][I/128] float, one per
+ *            128 x 128 block, 4-byte aligned
+ *   out      [T*H] uint16 (bf16) out, 16-byte aligned; must not overlap x
+ *   workspace  device memory of at least ep_moe_layer_workspace_bytes(shape, I) bytes (else
+ *            EP_ERR_INVALID), 16-byte aligned; overwritten, nothing needs to be in it beforehand.
+ *            Two calls in flight at once need two.
+ *
+ * Requires (else EP_ERR_UNSUPPORTED) T*K <= EP_MOE_MAX_PAIRS, E <= EP_MAX_EXPERTS, H and I
+ * multiples of 64 (bf16) or 128 (FP8), 2*I*H <= 2^29, T*H and T*K*I <= 2^30. C and R are not used. T = 0 does nothing.
+ * Deterministic.
+ *
+ * ep_moe_layer_workspace_bytes: 4 * T*K * I (0 for an invalid shape or I). Host only.
+ */
+size_t ep_moe_layer_workspace_bytes(const ep_shape_t *shape, int32_t I);
+
+int ep_moe_layer(const ep_shape_t *shape, int32_t I, const uint16_t *x, const int32_t *topk_idx,
+                 const float *topk_w, const uint16_t *w13, const uint16_t *w2, uint16_t *out,
+                 void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+int ep_moe_layer_fp8(const ep_shape_t *shape, int32_t I, const uint16_t *x,
+                     const int32_t *topk_idx, const float *topk_w, const uint8_t *w13_q,
+                     const float *w13_scale, const uint8_t *w2_q, const float *w2_scale,
+                     uint16_t *out, void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
  * ep_check_e4m3_conversion -- self-check of the two OCP E4M3 encoders of the FP8 dispatch on

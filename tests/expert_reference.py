@@ -70,3 +70,39 @@ def swiglu64(q, scale, w_q, w_scale):
     h = silu * u
     dh = 1.1 * dg * (u.abs() + du) + (silu.abs() + 1.1 * dg) * du
     return h, dh + h.abs() * U32 * (8 + 3 * g.abs()) + 2.0 ** -120
+
+
+def layer64(x, idx, w, w13, w2):
+    """(out, tolerance) of a whole layer: x [T, H], idx and w [T, K], and per expert the float64
+    weights w13(e) [2I, H] and w2(e) [H, I].
+
+    fp32 sums of exact products: a sum of n terms rounds each at most n times (and the block
+    scales and the wavefronts' meeting add at most 8). h is held as hi + lo, two bf16: |h - hi| <=
+    U16 |h|, and lo is rounded to within U16 of that. The weighted sum rounds K times, out once."""
+    T, H = x.shape
+    out = torch.zeros(T, H, dtype=torch.float64)
+    tol = torch.zeros(T, H, dtype=torch.float64)
+    sums = torch.zeros(T, H, dtype=torch.float64)
+    x = x.double()
+    for e in sorted(set(idx.reshape(-1).tolist())):
+        t, j = torch.nonzero(idx == e, as_tuple=True)
+        a, b = w13(e), w2(e)
+        if a is None:
+            continue
+        I = b.shape[1]
+        v = x[t] @ a.T
+        err = (H + 8) * U32 * (x[t].abs() @ a.abs().T)
+        (g, u), (dg, du) = v.chunk(2, 1), err.chunk(2, 1)
+        silu = g * torch.sigmoid(g)
+        h = silu * u
+        dh = 1.1 * dg * (u.abs() + du) + (silu.abs() + 1.1 * dg) * du
+        dh = dh + h.abs() * U32 * (8 + 3 * g.abs()) + 2.0 ** -120
+        dh = dh + U16 * U16 * (h.abs() + dh)
+        y = h @ b.T
+        dy = dh @ b.abs().T + (2 * I + 8) * U32 * ((h.abs() + dh) @ b.abs().T)
+        wt = w[t, j].double()[:, None]
+        out.index_add_(0, t, wt * y)
+        tol.index_add_(0, t, wt.abs() * dy)
+        sums.index_add_(0, t, wt.abs() * (y.abs() + dy))
+    tol += idx.shape[1] * U32 * sums
+    return out, tol + U16 * (out.abs() + tol) + 2.0 ** -133

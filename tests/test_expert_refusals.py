@@ -111,3 +111,91 @@ def test_host_tensors_are_refused():
     with pytest.raises(ValueError, match="even"):
         B.ep_expert_swiglu_fp8(t["q"], t["s"], t["count"],
                                torch.zeros((4, 255, 256), dtype=torch.uint8), t["ws"], 32)
+
+
+# ------------------------------------------------------------------------------------------
+# the whole layer
+# ------------------------------------------------------------------------------------------
+
+LAYER = dict(T=16, H=256, E=8, K=4, C=1, R=1)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_layer_shapes_refused(lib, fp8):
+    fn, ptrs = (lib.ep_moe_layer_fp8, 8) if fp8 else (lib.ep_moe_layer, 6)
+    go = lambda I=128, **kw: fn(shape(**{**LAYER, **kw}), I, *[A16] * (ptrs + 1), 1 << 40, None)  # noqa: E731
+    assert go(T=-1) == B.EP_ERR_INVALID and go(I=0) == B.EP_ERR_INVALID
+    assert fn(None, 128, *[A16] * (ptrs + 1), 1 << 40, None) == B.EP_ERR_INVALID
+    assert go(T=513) == B.EP_ERR_UNSUPPORTED
+    assert "EP_MOE_MAX_PAIRS" in lib.ep_last_error().decode()
+    assert go(E=1025) == B.EP_ERR_UNSUPPORTED
+    assert go(H=320 if fp8 else 288) == B.EP_ERR_UNSUPPORTED
+    assert go(I=64 if fp8 else 96) == B.EP_ERR_UNSUPPORTED
+    assert go(I=1 << 21) == B.EP_ERR_UNSUPPORTED
+    assert go(H=1 << 20, I=256, T=2048, K=1) == B.EP_ERR_UNSUPPORTED
+    assert go(T=0) == B.EP_OK and lib.ep_last_launches(None, 0) == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_layer_pointers_refused(lib, fp8):
+    fn, ptrs = (lib.ep_moe_layer_fp8, 8) if fp8 else (lib.ep_moe_layer, 6)
+    need = 4 * 64 * 128
+    assert lib.ep_moe_layer_workspace_bytes(shape(**LAYER), 128) == need
+    assert lib.ep_moe_layer_workspace_bytes(None, 128) == 0
+    assert lib.ep_moe_layer_workspace_bytes(shape(**LAYER), 0) == 0
+
+    def go(at=None, value=None, nbytes=need):
+        args = [A16] * (ptrs + 1)
+        if at is not None:
+            args[at] = value
+        return fn(shape(**LAYER), 128, *args, nbytes, None)
+
+    for at in range(ptrs + 1):
+        assert go(at, None) == B.EP_ERR_INVALID, at
+        assert go(at, A16 + 2) == B.EP_ERR_ALIGN, at
+    wide = {0, 3, 5, 7, 8} if fp8 else {0, 3, 4, 5, 6}
+    for at in wide:
+        assert go(at, A16 + 8) == B.EP_ERR_ALIGN, at
+    assert go(nbytes=need - 1) == B.EP_ERR_INVALID
+    assert "below" in lib.ep_last_error().decode()
+
+
+def test_layer_constant_matches_the_header():
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "include", "ep.h")) as f:
+        assert int(re.search(r"#define EP_MOE_MAX_PAIRS\s+(\d+)", f.read())[1]) == B.EP_MOE_MAX_PAIRS
+
+
+@pytest.mark.parametrize("change,error", [
+    (dict(x=torch.zeros((4, 256))), TypeError),
+    (dict(x=torch.zeros((4, 128), dtype=torch.bfloat16)), ValueError),
+    (dict(x=torch.zeros((256, 4), dtype=torch.bfloat16).t()), ValueError),
+    (dict(idx=torch.zeros((4, 2), dtype=torch.int64)), TypeError),
+    (dict(idx=torch.zeros((5, 2), dtype=torch.int32)), ValueError),
+    (dict(w=torch.zeros((4, 2), dtype=torch.bfloat16)), TypeError),
+    (dict(w13=torch.zeros((3, 128, 256), dtype=torch.bfloat16)), ValueError),
+    (dict(w2=torch.zeros((2, 256, 128), dtype=torch.bfloat16)), ValueError),
+    (dict(out=torch.zeros((4, 128), dtype=torch.bfloat16)), ValueError),
+    (dict(out=torch.zeros((4, 256))), TypeError),
+    (dict(workspace=torch.zeros((64, 64)).t()[::2]), ValueError),
+    (dict(), ValueError),                                  # host tensors
+])
+def test_layer_tensors_refused(change, error):
+    t = dict(x=torch.zeros((4, 256), dtype=torch.bfloat16), idx=torch.zeros((4, 2), dtype=torch.int32),
+             w=torch.zeros((4, 2)), w13=torch.zeros((3, 256, 256), dtype=torch.bfloat16),
+             w2=torch.zeros((3, 256, 128), dtype=torch.bfloat16), out=None, workspace=None)
+    t.update(change)
+    with pytest.raises(error):
+        B.ep_moe_layer(t["x"], t["idx"], t["w"], t["w13"], t["w2"], out=t["out"],
+                       workspace=t["workspace"])
+    if not {"w13", "w2"} & set(change):
+        w13, w2 = t["w13"].to(torch.uint8), t["w2"].to(torch.uint8)
+        with pytest.raises(error):
+            B.ep_moe_layer_fp8(t["x"], t["idx"], t["w"], w13, torch.zeros((3, 2, 2)), w2,
+                               torch.zeros((3, 2, 1)), out=t["out"], workspace=t["workspace"])
+    if not change:
+        with pytest.raises(ValueError, match="w13_scale"):
+            B.ep_moe_layer_fp8(t["x"], t["idx"], t["w"], w13, torch.zeros((3, 2, 1)), w2,
+                               torch.zeros((3, 2, 1)))
