@@ -77,6 +77,43 @@ __device__ __forceinline__ int find_expert(const TileTable &t, int E, int m)
     return uniform(lo);
 }
 
+// The tiles of all experts in one row, an expert's tiles in groups of kGroup row tiles: within a
+// group the row tile runs fastest, then the column tile. Neighbours in this order share weights
+// and rows, and each XCD takes one eighth of the order (its workgroups are blockIdx.x mod 8), so
+// that its L2 holds what they share.
+constexpr int kGroup = 8;
+
+struct TileRange {
+    int first, end, step;
+};
+
+__device__ __forceinline__ TileRange my_tiles(int total)
+{
+    const int x = blockIdx.x & 7, i = blockIdx.x >> 3;      // gridDim.x is a multiple of 8
+    const int per = total >> 3, rest = total & 7;
+    const int first = x * per + min(x, rest);
+    return TileRange{first + i, first + per + (x < rest ? 1 : 0), (int)(gridDim.x >> 3)};
+}
+
+struct Tile {
+    int e, row0, n, nblk;      // expert, first row, rows, column tile
+};
+
+__device__ __forceinline__ Tile locate(const TileTable &t, int E, int tile, int n_tiles, int bm)
+{
+    Tile r;
+    r.e = find_expert(t, E, tile / n_tiles);
+    const int n_e = uniform(t.n[r.e]), tiles = (n_e + bm - 1) / bm;
+    int at = tile - (uniform(t.end[r.e]) - tiles) * n_tiles;
+    const int group = at / (kGroup * n_tiles), in_group = min(tiles - group * kGroup, kGroup);
+    at -= group * kGroup * n_tiles;
+    r.nblk = at / in_group;
+    const int m0 = (group * kGroup + at - r.nblk * in_group) * bm;
+    r.row0 = uniform(t.base[r.e]) + m0;
+    r.n = min(n_e - m0, bm);
+    return r;
+}
+
 // h = silu(g) * u.
 __device__ __forceinline__ float swiglu(float g, float u)
 {
@@ -185,13 +222,10 @@ __global__ __launch_bounds__(kThreads) void expert_stream_kernel(ExpertProduct p
     const int n_tiles = SWIGLU ? p.n / kTileN : (p.n + kTileN - 1) / kTileN;
     const int ws_rows = (p.n + 127) >> 7;
     const int total = build_table(table, p, MT * 16) * n_tiles;
-    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
-        const int m = tile / n_tiles, nblk = tile - m * n_tiles;
-        const int e = find_expert(table, p.E, m);
-        const int n_e = uniform(table.n[e]);
-        const int m0 = (m - (uniform(table.end[e]) - (n_e + MT * 16 - 1) / (MT * 16))) * (MT * 16);
-        const int row0 = uniform(table.base[e]) + m0;
-        const int n = min(n_e - m0, MT * 16);        // rows of this tile
+    const TileRange mine = my_tiles(total);
+    for (int tile = mine.first; tile < mine.end; tile += mine.step) {
+        const Tile at = locate(table, p.E, tile, n_tiles, MT * 16);
+        const int e = at.e, row0 = at.row0, n = at.n, nblk = at.nblk;
 
         // lane offsets of the weight rows (clamped) and of the tile's rows (clamped)
         uint32_t woff[4], xoff[MT], soff[MT];
@@ -290,13 +324,194 @@ __global__ __launch_bounds__(kThreads) void expert_stream_kernel(ExpertProduct p
     }
 }
 
+// Many rows per expert: tiles of 128 rows x 256 weight rows, both streams pipelined one block of
+// 128 ahead. The rows' tile (16 KB) goes through LDS, written by direct global-to-LDS loads and read
+// by all four wavefronts; a wavefront's 64 weight rows are its own, so they go straight to
+// registers. The tile's row scales are staged for 16 blocks at a time.
+constexpr int kTileM = 128;
+constexpr int kPanel = 16;         // blocks of 128 whose scales are staged together
+
+typedef __attribute__((address_space(3))) void *LdsPtr;
+
+// A buffer of `bytes` from p: loads take a lane offset and a uniform one, and give 0 past the end.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)bytes, 0x00027000);
+}
+
+__device__ __forceinline__ i32x4 buffer_load16(__amdgpu_buffer_rsrc_t b, int lane_off, int off)
+{
+    return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, lane_off, off, 0));
+}
+
+// v, but what is computed from it is worked out where it is used and not kept in registers.
+__device__ __forceinline__ int fresh(int v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// A barrier that every wavefront reaches with its own global loads done, those into LDS among them
+// (__syncthreads alone does not wait for them).
+__device__ __forceinline__ void sync_loads()
+{
+    __builtin_amdgcn_s_waitcnt(0x0F70);        // vmcnt(0)
+    __syncthreads();
+}
+
+__global__ __launch_bounds__(kThreads, 2) void expert_tile_kernel(ExpertProduct p)
+{
+    constexpr int MT = kTileM / 16;
+    __shared__ TileTable table;
+    __shared__ u32x4 xbuf0[kTileM * 8];
+    __shared__ u32x4 xbuf1[kTileM * 8];
+    __shared__ float xscale[kPanel][kTileM];
+    __shared__ float wscale[kPanel][2];
+    const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
+    const int r16 = lane & 15, g4 = lane >> 4;
+    const int nkb = p.H >> 7;
+    const int n_tiles = (p.n + kTileN - 1) / kTileN;
+    const int ws_rows = (p.n + 127) >> 7;
+    const int total = build_table(table, p, kTileM) * n_tiles;
+    // chunk c of row r is kept at position c ^ (r & 7) of the row's eight 16-byte chunks: the
+    // reads of 8 consecutive lanes (8 rows, one chunk) then touch all banks
+    const int pos0 = g4 ^ (r16 & 7);
+    const TileRange mine = my_tiles(total);
+    for (int tile = mine.first; tile < mine.end; tile += mine.step) {
+        const Tile at = locate(table, p.E, tile, n_tiles, kTileM);
+        const int e = at.e, row0 = at.row0, n = at.n, nblk = at.nblk;
+
+        const int wrow0 = nblk * kTileN + wave * 64;
+        int woff[4], xoff[4];
+        const int l8 = fresh(lane);
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+            woff[nt] = min(wrow0 + nt * 16 + (l8 & 15), p.n - 1) * p.H + (l8 >> 4) * 16;
+        // direct loads: instruction i of a wavefront fills rows wave * 32 + i * 8 + lane / 8
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            xoff[i] = min(wave * 32 + i * 8 + (l8 >> 3), n - 1) * p.H +
+                      ((l8 & 7) ^ (l8 >> 3)) * 16;
+        const __amdgpu_buffer_rsrc_t w = buffer(p.w_q + (size_t)e * p.n * p.H,
+                                                (uint32_t)p.n * p.H);
+        const __amdgpu_buffer_rsrc_t x = buffer(p.q + (size_t)row0 * p.H, (uint32_t)n * p.H);
+        const float *xs = p.scale + (size_t)row0 * nkb;
+        const float *ws = p.w_scale + (size_t)e * ws_rows * nkb;
+
+        i32x8 wf[2][4];
+        f32x4 acc[4][MT];
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) acc[nt][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+        auto load = [&](u32x4 *buf, int d, int kb) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    x, (LdsPtr)(buf + (wave * 32 + i * 8) * 8), 16, xoff[i], kb * 128, 0, 0);
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+                wf[d][nt] = join(buffer_load16(w, woff[nt], kb * 128),
+                                 buffer_load16(w, woff[nt], kb * 128 + 64));
+        };
+        float s[MT];
+        auto scales = [&](int kb) {
+            const float sw = wscale[kb & (kPanel - 1)][wave >> 1];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                s[mt] = xscale[kb & (kPanel - 1)][mt * 16 + r16] * sw;
+        };
+        // the products of one tile of 16 rows are issued between the sums of the previous one
+        auto compute = [&](const u32x4 *buf, int d) {
+            auto frag = [&](int mt) {
+                const i32x4 *row = reinterpret_cast<const i32x4 *>(buf + (mt * 16 + r16) * 8);
+                return join(row[pos0], row[pos0 ^ 4]);
+            };
+            f32x4 v[2][4];
+            i32x8 xf[2];
+            xf[0] = frag(0);
+#pragma unroll
+            for (int mt = 0; mt <= MT; ++mt) {
+                if (mt + 1 < MT) xf[(mt + 1) & 1] = frag(mt + 1);
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) {
+                    if (mt < MT) v[mt & 1][nt] = mfma_e4m3(wf[d][nt], xf[mt & 1]);
+                    if (mt > 0) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            acc[nt][mt - 1][k] = __builtin_fmaf(s[mt - 1], v[(mt - 1) & 1][nt][k],
+                                                                acc[nt][mt - 1][k]);
+                        asm volatile("" : "+v"(acc[nt][mt - 1]));   // summed here, not later
+                    }
+                }
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);          // LDS reads
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // a product
+                    __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);      // four sums
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        auto panel = [&](int kb0) {       // the scales of blocks kb0 .. kb0 + 15
+            const int tid = fresh(wave * kWave + lane);
+            for (int i = tid; i < kTileM * kPanel; i += kThreads) {
+                const int r = i / kPanel, b = i % kPanel;
+                xscale[b][r] = xs[(size_t)min(r, n - 1) * nkb + min(kb0 + b, nkb - 1)];
+            }
+            if (tid < 2 * kPanel) {
+                const int i = tid / kPanel, b = tid % kPanel;
+                wscale[b][i] = ws[(size_t)min(nblk * 2 + i, ws_rows - 1) * nkb +
+                                  min(kb0 + b, nkb - 1)];
+            }
+        };
+        load(xbuf0, 0, 0);
+        for (int kb = 0; kb < nkb; kb += 2) {
+            if ((kb & (kPanel - 1)) == 0) {
+                if (kb > 0) __syncthreads();
+                panel(kb);
+            }
+            sync_loads();
+            scales(kb);
+            if (kb + 1 < nkb) load(xbuf1, 1, kb + 1);
+            compute(xbuf0, 0);
+            sync_loads();
+            if (kb + 1 < nkb) {
+                scales(kb + 1);
+                if (kb + 2 < nkb) load(xbuf0, 0, kb + 2);
+                compute(xbuf1, 1);
+            }
+        }
+        sync_loads();
+        const int ln = fresh(lane);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int r = mt * 16 + (ln & 15);
+            uint16_t *y = p.y + (size_t)(row0 + r) * p.n;
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) {
+                const int c = wrow0 + nt * 16 + (ln >> 4) * 4;
+                if (r < n && c < p.n) {
+                    uint2 o;
+                    o.x = bf16_rne(acc[nt][mt][0]) | (bf16_rne(acc[nt][mt][1]) << 16);
+                    o.y = bf16_rne(acc[nt][mt][2]) | (bf16_rne(acc[nt][mt][3]) << 16);
+                    *reinterpret_cast<uint2 *>(y + c) = o;
+                }
+            }
+        }
+    }
+}
+
 template <bool SWIGLU>
 hipError_t launch_product(const ExpertProduct &p, hipStream_t stream)
 {
     if (p.pairs == 0 || (p.offset && p.rows == 0)) return hipSuccess;
     const int64_t n_tiles = (p.n + kTileN - 1) / kTileN;
     const int64_t tiles = ((int64_t)p.pairs / 64 + p.E) * n_tiles;
-    const int grid = (int)(tiles < 512 ? tiles : 512);
+    const int grid = (int)(tiles < 512 ? (tiles + 7) / 8 * 8 : 512);
+    if (!SWIGLU && p.pairs / p.E >= 32)
+        return launch(expert_tile_kernel, dim3(grid), dim3(kThreads), 0, stream, p);
     return launch(expert_stream_kernel<4, SWIGLU, 1>, dim3(grid), dim3(kThreads), 0, stream, p);
 }
 
