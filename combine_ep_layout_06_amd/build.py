@@ -39,6 +39,9 @@ HIPCC_FLAGS = [
     "-Wall", "-Wextra", "-Werror", "-Wno-unused-command-line-argument",
     # no packed-fp32 instructions (v_pk_*_f32) in the device code
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+    # matrix instructions leave their results in ordinary vector registers, where the scaled sums
+    # read them (in accumulation registers each value would need a move first)
+    "-mllvm", "-amdgpu-mfma-vgpr-form=1",
 ]
 
 # host code under ASan and UBSan, each flag for the host compilation only; device code at -O0

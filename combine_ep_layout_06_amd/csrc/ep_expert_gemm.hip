@@ -65,18 +65,6 @@ __device__ __forceinline__ int build_table(TileTable &t, const ExpertProduct &p,
     return total;
 }
 
-// The expert whose tiles include row tile m (m < total).
-__device__ __forceinline__ int find_expert(const TileTable &t, int E, int m)
-{
-    int lo = 0, hi = E - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (t.end[mid] > m) hi = mid;
-        else lo = mid + 1;
-    }
-    return uniform(lo);
-}
-
 // The tiles of all experts in one row, an expert's tiles in groups of kGroup row tiles: within a
 // group the row tile runs fastest, then the column tile. Neighbours in this order share weights
 // and rows, and each XCD takes one eighth of the order (its workgroups are blockIdx.x mod 8), so
@@ -99,25 +87,39 @@ struct Tile {
     int e, row0, n, nblk;      // expert, first row, rows, column tile
 };
 
+// The tile at place `tile` of the order (below the total); lanes may ask for different ones.
 __device__ __forceinline__ Tile locate(const TileTable &t, int E, int tile, int n_tiles, int bm)
 {
-    Tile r;
-    r.e = find_expert(t, E, tile / n_tiles);
-    const int n_e = uniform(t.n[r.e]), tiles = (n_e + bm - 1) / bm;
-    int at = tile - (uniform(t.end[r.e]) - tiles) * n_tiles;
+    const int m = tile / n_tiles;
+    int lo = 0, hi = E - 1;    // the expert whose row tiles include m
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (t.end[mid] > m) hi = mid;
+        else lo = mid + 1;
+    }
+    const int n_e = t.n[lo], tiles = (n_e + bm - 1) / bm;
+    int at = tile - (t.end[lo] - tiles) * n_tiles;
     const int group = at / (kGroup * n_tiles), in_group = min(tiles - group * kGroup, kGroup);
     at -= group * kGroup * n_tiles;
+    Tile r;
+    r.e = lo;
     r.nblk = at / in_group;
     const int m0 = (group * kGroup + at - r.nblk * in_group) * bm;
-    r.row0 = uniform(t.base[r.e]) + m0;
+    r.row0 = t.base[lo] + m0;
     r.n = min(n_e - m0, bm);
     return r;
 }
 
-// h = silu(g) * u.
+__device__ __forceinline__ Tile uniform(const Tile &t)
+{
+    return Tile{uniform(t.e), uniform(t.row0), uniform(t.n), uniform(t.nblk)};
+}
+
+// h = silu(g) * u; the reciprocal is the hardware's (one step of fp32). g = -inf gives NaN, as
+// -inf / inf does.
 __device__ __forceinline__ float swiglu(float g, float u)
 {
-    return g / (1.0f + __expf(-g)) * u;
+    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 
 // The scale of a block with this amax pattern (integer max of |h|): amax / 448, a NaN amax giving
@@ -224,7 +226,7 @@ __global__ __launch_bounds__(kThreads) void expert_stream_kernel(ExpertProduct p
     const int total = build_table(table, p, MT * 16) * n_tiles;
     const TileRange mine = my_tiles(total);
     for (int tile = mine.first; tile < mine.end; tile += mine.step) {
-        const Tile at = locate(table, p.E, tile, n_tiles, MT * 16);
+        const Tile at = uniform(locate(table, p.E, tile, n_tiles, MT * 16));
         const int e = at.e, row0 = at.row0, n = at.n, nblk = at.nblk;
 
         // lane offsets of the weight rows (clamped) and of the tile's rows (clamped)
@@ -324,183 +326,336 @@ __global__ __launch_bounds__(kThreads) void expert_stream_kernel(ExpertProduct p
     }
 }
 
-// Many rows per expert: tiles of 128 rows x 256 weight rows, both streams pipelined one block of
-// 128 ahead. The rows' tile (16 KB) goes through LDS, written by direct global-to-LDS loads and read
-// by all four wavefronts; a wavefront's 64 weight rows are its own, so they go straight to
-// registers. The tile's row scales are staged for 16 blocks at a time.
+// Many rows per expert: tiles of 128 rows x 256 weight rows (SwiGLU: 128 gate and the same 128 up
+// rows), one workgroup of 4 wavefronts per CU that walks its tiles as one stream of blocks (128
+// channels of a tile each). Loads run three blocks ahead of the products, across tiles, so that
+// neither a block nor a tile waits for memory:
+//   * the rows of a block (16 KB) go to one of four LDS buffers by direct global-to-LDS loads and
+//     are read by all four wavefronts;
+//   * a wavefront's 64 weight rows are its own: straight to registers, four blocks deep;
+//   * the row scales of 16 blocks are staged together, one panel ahead.
+// One barrier per block: when a wavefront passes it, its own direct loads for the next block have
+// landed, and every wavefront is done with the block before, whose buffers the loads then refill.
 constexpr int kTileM = 128;
-constexpr int kPanel = 16;         // blocks of 128 whose scales are staged together
+constexpr int kMT = kTileM / 16;
+constexpr int kPanel = 16;         // blocks whose scales are staged together
+[[maybe_unused]] constexpr int kDepth = 4;          // buffers
+constexpr int kList = 256;         // tiles of a workgroup looked up together
 
-typedef __attribute__((address_space(3))) void *LdsPtr;
+[[maybe_unused]] typedef __attribute__((address_space(3))) void *LdsPtr;
 
 // A buffer of `bytes` from p: loads take a lane offset and a uniform one, and give 0 past the end.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, uint32_t bytes)
+[[maybe_unused]] __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, uint32_t bytes)
 {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)bytes, 0x00027000);
 }
 
-__device__ __forceinline__ i32x4 buffer_load16(__amdgpu_buffer_rsrc_t b, int lane_off, int off)
+[[maybe_unused]] __device__ __forceinline__ i32x4 buffer_load16(__amdgpu_buffer_rsrc_t b, int lane_off, int off)
 {
     return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, lane_off, off, 0));
 }
 
 // v, but what is computed from it is worked out where it is used and not kept in registers.
-__device__ __forceinline__ int fresh(int v)
+[[maybe_unused]] __device__ __forceinline__ int fresh(int v)
 {
     asm volatile("" : "+v"(v));
     return v;
 }
 
-// A barrier that every wavefront reaches with its own global loads done, those into LDS among them
-// (__syncthreads alone does not wait for them).
-__device__ __forceinline__ void sync_loads()
+// Wait until at most N of this wavefront's vector memory operations are left (they finish in
+// order), then meet the other wavefronts; LDS writes before it are seen after it.
+template <int N>
+__device__ __forceinline__ void wait_and_meet()
 {
-    __builtin_amdgcn_s_waitcnt(0x0F70);        // vmcnt(0)
-    __syncthreads();
+    __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));    // vmcnt(N) lgkmcnt(0)
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-__global__ __launch_bounds__(kThreads, 2) void expert_tile_kernel(ExpertProduct p)
+// bf16 pairs of four values, NaN as 0x7FC0.
+[[maybe_unused]] __device__ __forceinline__ uint2 bf16_pairs(f32x4 v)
 {
-    constexpr int MT = kTileM / 16;
+    bf16x2 lo = {(__bf16)v[0], (__bf16)v[1]}, hi = {(__bf16)v[2], (__bf16)v[3]};
+    uint2 o{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+    if (__builtin_isunordered(v[0], v[1]) || __builtin_isunordered(v[2], v[3])) {
+        o.x = bf16_rne(v[0]) | (bf16_rne(v[1]) << 16);
+        o.y = bf16_rne(v[2]) | (bf16_rne(v[3]) << 16);
+    }
+    return o;
+}
+
+template <bool SWIGLU>
+struct TileShared {
+    float xscale[2][kPanel][kTileM + 1];
+    float wscale[2][kPanel][2];
+    int4 list[kList];
+    u32x4 pad[16];             // see the first direct load
+    SwigluShared<SWIGLU ? kMT : 1> h;
+};
+
+template <bool SWIGLU>
+__global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)            // buffer descriptors exist on the device only
     __shared__ TileTable table;
+    // one array per buffer: the compiler then knows that a block's reads do not touch the buffers
+    // that loads in flight are filling, and does not wait for those
     __shared__ u32x4 xbuf0[kTileM * 8];
     __shared__ u32x4 xbuf1[kTileM * 8];
-    __shared__ float xscale[kPanel][kTileM];
-    __shared__ float wscale[kPanel][2];
+    __shared__ u32x4 xbuf2[kTileM * 8];
+    __shared__ u32x4 xbuf3[kTileM * 8];
+    __shared__ TileShared<SWIGLU> sh;
     const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
     const int r16 = lane & 15, g4 = lane >> 4;
     const int nkb = p.H >> 7;
     const int n_tiles = (p.n + kTileN - 1) / kTileN;
     const int ws_rows = (p.n + 127) >> 7;
     const int total = build_table(table, p, kTileM) * n_tiles;
+    const TileRange mine = my_tiles(total);
     // chunk c of row r is kept at position c ^ (r & 7) of the row's eight 16-byte chunks: the
     // reads of 8 consecutive lanes (8 rows, one chunk) then touch all banks
-    const int pos0 = g4 ^ (r16 & 7);
-    const TileRange mine = my_tiles(total);
-    for (int tile = mine.first; tile < mine.end; tile += mine.step) {
-        const Tile at = locate(table, p.E, tile, n_tiles, kTileM);
-        const int e = at.e, row0 = at.row0, n = at.n, nblk = at.nblk;
+    const int pos0 = r16 * 8 + (g4 ^ (r16 & 7));
 
-        const int wrow0 = nblk * kTileN + wave * 64;
+    // the stream of loads: the tile it is in and its next block
+    struct {
+        int tile, kb;
+        __amdgpu_buffer_rsrc_t w, x;
         int woff[4], xoff[4];
-        const int l8 = fresh(lane);
+    } ld;
+    // first weight row of a wavefront's tile nt
+    auto weight_row = [&](int nblk, int nt) {
+        return SWIGLU ? (nt >> 1) * (p.n / 2) + nblk * 128 + wave * 32 + (nt & 1) * 16
+                      : nblk * kTileN + wave * 64 + nt * 16;
+    };
+    auto at = [&](int i) {
+        const int4 v = sh.list[i];
+        return uniform(Tile{v.x, v.y, v.z, v.w});
+    };
+    auto enter = [&](int i) {
+        const Tile t = at(i);
+        ld.tile = i;
+        ld.kb = 0;
+        ld.w = buffer(p.w_q + (size_t)t.e * p.n * p.H, (uint32_t)p.n * p.H);
+        ld.x = buffer(p.q + (size_t)t.row0 * p.H, (uint32_t)t.n * p.H);
+        const int l = fresh(lane);
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt)
-            woff[nt] = min(wrow0 + nt * 16 + (l8 & 15), p.n - 1) * p.H + (l8 >> 4) * 16;
+            ld.woff[nt] = min(weight_row(t.nblk, nt) + (l & 15), p.n - 1) * p.H + (l >> 4) * 16;
         // direct loads: instruction i of a wavefront fills rows wave * 32 + i * 8 + lane / 8
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            xoff[i] = min(wave * 32 + i * 8 + (l8 >> 3), n - 1) * p.H +
-                      ((l8 & 7) ^ (l8 >> 3)) * 16;
-        const __amdgpu_buffer_rsrc_t w = buffer(p.w_q + (size_t)e * p.n * p.H,
-                                                (uint32_t)p.n * p.H);
-        const __amdgpu_buffer_rsrc_t x = buffer(p.q + (size_t)row0 * p.H, (uint32_t)n * p.H);
-        const float *xs = p.scale + (size_t)row0 * nkb;
-        const float *ws = p.w_scale + (size_t)e * ws_rows * nkb;
+        for (int j = 0; j < 4; ++j)
+            ld.xoff[j] = min(wave * 32 + j * 8 + (l >> 3), t.n - 1) * p.H +
+                         ((l & 7) ^ (l >> 3)) * 16;
+    };
 
-        i32x8 wf[2][4];
-        f32x4 acc[4][MT];
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) acc[nt][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    i32x8 wf[kDepth][4];
+    f32x4 acc[4][kMT], v[2][4];
+    constexpr int kAhead = SWIGLU ? 1 : 2;     // row tiles read from LDS ahead of the products
+    constexpr int kRing = 2 * kAhead, kWs = SWIGLU ? 2 : 1;
+    i32x8 xf[kRing];
+    float s[4][kWs];                           // scale of a row tile (gate; up)
+    constexpr int kPer = kTileM * kPanel / kThreads;
+    float ps[kPer], pw = 0.0f;                 // the next panel on its way
+    int par = 0;                               // the panel in use
 
-        auto load = [&](u32x4 *buf, int d, int kb) {
+    auto load_w = [&](int d, int nt) {
+        wf[d][nt] = join(buffer_load16(ld.w, ld.woff[nt], ld.kb * 128),
+                         buffer_load16(ld.w, ld.woff[nt], ld.kb * 128 + 64));
+    };
+    auto load_x = [&](u32x4 *buf, int j) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ld.x, (LdsPtr)(buf + (wave * 32 + j * 8) * 8), 16,
+                                                 ld.xoff[j], ld.kb * 128, 0, 0);
+    };
+    auto advance = [&](int tiles) {            // past the last block: that block again
+        if (++ld.kb == nkb) {
+            if (ld.tile + 1 < tiles) enter(ld.tile + 1);
+            else ld.kb = nkb - 1;
+        }
+    };
+    auto panel_load = [&](int i, int kb0) {
+        const Tile t = at(i);
+        const int l = fresh(wave * kWave + lane);
+        const float *src = p.scale + (size_t)t.row0 * nkb + min(kb0 + (l & 15), nkb - 1);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    x, (LdsPtr)(buf + (wave * 32 + i * 8) * 8), 16, xoff[i], kb * 128, 0, 0);
+        for (int k = 0; k < kPer; ++k) ps[k] = src[(size_t)min(k * 16 + (l >> 4), t.n - 1) * nkb];
+        const int blk = SWIGLU ? ((l >> 4) & 1) * (p.n >> 8) + t.nblk
+                               : min(t.nblk * 2 + ((l >> 4) & 1), ws_rows - 1);
+        pw = p.w_scale[((size_t)t.e * ws_rows + blk) * nkb + min(kb0 + (l & 15), nkb - 1)];
+    };
+    auto panel_store = [&](int to) {
+        const int l = fresh(wave * kWave + lane);
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
-                wf[d][nt] = join(buffer_load16(w, woff[nt], kb * 128),
-                                 buffer_load16(w, woff[nt], kb * 128 + 64));
-        };
-        float s[MT];
-        auto scales = [&](int kb) {
-            const float sw = wscale[kb & (kPanel - 1)][wave >> 1];
+        for (int k = 0; k < kPer; ++k) sh.xscale[to][l & 15][k * 16 + (l >> 4)] = ps[k];
+        if (l < 32) sh.wscale[to][l & 15][l >> 4] = pw;
+    };
+    auto read_row = [&](const u32x4 *buf, int mt) {
+        const i32x4 *row = reinterpret_cast<const i32x4 *>(buf) + mt * 128;
+        return join(row[pos0], row[pos0 ^ 4]);
+    };
+    float ws[kWs];
+    auto read_ws = [&](int b) {
+        ws[0] = sh.wscale[par][b][SWIGLU ? 0 : wave >> 1];
+        if constexpr (SWIGLU) ws[1] = sh.wscale[par][b][1];
+    };
+    auto sum = [&](int mt) {                   // the products of row tile mt, from v[mt & 1]
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-                s[mt] = xscale[kb & (kPanel - 1)][mt * 16 + r16] * sw;
-        };
-        // the products of one tile of 16 rows are issued between the sums of the previous one
-        auto compute = [&](const u32x4 *buf, int d) {
-            auto frag = [&](int mt) {
-                const i32x4 *row = reinterpret_cast<const i32x4 *>(buf + (mt * 16 + r16) * 8);
-                return join(row[pos0], row[pos0 ^ 4]);
-            };
-            f32x4 v[2][4];
-            i32x8 xf[2];
-            xf[0] = frag(0);
+        for (int nt = 0; nt < 4; ++nt) {
 #pragma unroll
-            for (int mt = 0; mt <= MT; ++mt) {
-                if (mt + 1 < MT) xf[(mt + 1) & 1] = frag(mt + 1);
+            for (int k = 0; k < 4; ++k)
+                acc[nt][mt][k] = __builtin_fmaf(s[mt & 3][SWIGLU ? nt >> 1 : 0], v[mt & 1][nt][k],
+                                                acc[nt][mt][k]);
+            asm volatile("" : "+v"(acc[nt][mt]));        // summed here, not later
+        }
+    };
+    auto clear = [&]() {
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt) acc[nt][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            v[(kMT - 1) & 1][nt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};    // no block before the first
+        }
+#pragma unroll
+        for (int i = 0; i < kWs; ++i) s[(kMT - 1) & 3][i] = 0.0f;
+    };
+    // One block: `buf` and d hold it, `next` is the following block's buffer, `fill` and df take the
+    // block three ahead. In each of its 8 regions one row tile is multiplied, the one before summed,
+    // and one read from LDS, kAhead ahead; the fences keep the regions apart.
+    auto step = [&](const u32x4 *buf, int d, const u32x4 *next, u32x4 *fill, int df, int tile,
+                    int kb, int tiles) {
+        if ((kb & (kPanel - 1)) == 0) {
+            if (kb + kPanel < nkb) panel_load(tile, kb + kPanel);
+            else if (tile + 1 < tiles) panel_load(tile + 1, 0);
+        }
+        const int b_next = kb == nkb - 1 ? 0 : (kb + 1) & (kPanel - 1);
+        Bf16Block wb[SWIGLU ? 4 : 1];
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) {
+            const int to = mt + kAhead;
+            if (to == kMT) {
+                if (b_next == 0) {
+                    par ^= 1;
+                    panel_store(par);
+                }
+                // of the operations after the next block's direct loads at least 8 + 4 + 8 remain:
+                // two blocks of weights and one of rows
+                wait_and_meet<20>();
+                read_ws(b_next);
+            }
+            const i32x8 x_in = read_row(to < kMT ? buf : next, to & (kMT - 1));
+            const float s_in =
+                sh.xscale[par][to < kMT ? kb & (kPanel - 1) : b_next][(to & (kMT - 1)) * 16 + r16];
+            if (mt < 4) load_w(df, mt);
+            if (to >= kMT) {
+#pragma unroll
+                for (int j = 0; j < 4 / kAhead; ++j) load_x(fill, (to - kMT) * (4 / kAhead) + j);
+            }
+            if constexpr (SWIGLU) {
+                const Bf16Block xb = bf16_block(xf[mt & (kRing - 1)]);
 #pragma unroll
                 for (int nt = 0; nt < 4; ++nt) {
-                    if (mt < MT) v[mt & 1][nt] = mfma_e4m3(wf[d][nt], xf[mt & 1]);
-                    if (mt > 0) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            acc[nt][mt - 1][k] = __builtin_fmaf(s[mt - 1], v[(mt - 1) & 1][nt][k],
-                                                                acc[nt][mt - 1][k]);
-                        asm volatile("" : "+v"(acc[nt][mt - 1]));   // summed here, not later
-                    }
+                    if (mt == 0) wb[nt] = bf16_block(wf[d][nt]);
+                    v[mt & 1][nt] = mfma_exact(wb[nt], xb);
                 }
-                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);          // LDS reads
+            } else {
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt)
+                    v[mt & 1][nt] = mfma_e4m3(wf[d][nt], xf[mt & (kRing - 1)]);
+            }
+            sum((mt + kMT - 1) & (kMT - 1));
+            xf[to & (kRing - 1)] = x_in;
+#pragma unroll
+            for (int i = 0; i < kWs; ++i) s[to & 3][i] = s_in * ws[i];
+            if constexpr (!SWIGLU) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);          // LDS reads
 #pragma unroll
                 for (int nt = 0; nt < 4; ++nt) {
                     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // a product
                     __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);      // four sums
                 }
-                __builtin_amdgcn_sched_barrier(0);
             }
-        };
-        auto panel = [&](int kb0) {       // the scales of blocks kb0 .. kb0 + 15
-            const int tid = fresh(wave * kWave + lane);
-            for (int i = tid; i < kTileM * kPanel; i += kThreads) {
-                const int r = i / kPanel, b = i % kPanel;
-                xscale[b][r] = xs[(size_t)min(r, n - 1) * nkb + min(kb0 + b, nkb - 1)];
-            }
-            if (tid < 2 * kPanel) {
-                const int i = tid / kPanel, b = tid % kPanel;
-                wscale[b][i] = ws[(size_t)min(nblk * 2 + i, ws_rows - 1) * nkb +
-                                  min(kb0 + b, nkb - 1)];
-            }
-        };
-        load(xbuf0, 0, 0);
-        for (int kb = 0; kb < nkb; kb += 2) {
-            if ((kb & (kPanel - 1)) == 0) {
-                if (kb > 0) __syncthreads();
-                panel(kb);
-            }
-            sync_loads();
-            scales(kb);
-            if (kb + 1 < nkb) load(xbuf1, 1, kb + 1);
-            compute(xbuf0, 0);
-            sync_loads();
-            if (kb + 1 < nkb) {
-                scales(kb + 1);
-                if (kb + 2 < nkb) load(xbuf0, 0, kb + 2);
-                compute(xbuf1, 1);
-            }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        sync_loads();
-        const int ln = fresh(lane);
+        advance(tiles);
+    };
+    auto finish = [&](int tile) {              // the tile's last sums and its output
+        sum(kMT - 1);
+        const Tile t = at(tile);
+        if constexpr (SWIGLU) {
+            store_swiglu<kMT>(sh.h, acc, p, t.row0, t.n, t.nblk);
+        } else {
+            const int l = fresh(lane);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const int r = mt * 16 + (ln & 15);
-            uint16_t *y = p.y + (size_t)(row0 + r) * p.n;
+            for (int mt = 0; mt < kMT; ++mt) {
+                const int r = mt * 16 + (l & 15);
+                uint16_t *y = p.y + (size_t)(t.row0 + r) * p.n;
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                const int c = wrow0 + nt * 16 + (ln >> 4) * 4;
-                if (r < n && c < p.n) {
-                    uint2 o;
-                    o.x = bf16_rne(acc[nt][mt][0]) | (bf16_rne(acc[nt][mt][1]) << 16);
-                    o.y = bf16_rne(acc[nt][mt][2]) | (bf16_rne(acc[nt][mt][3]) << 16);
-                    *reinterpret_cast<uint2 *>(y + c) = o;
+                for (int nt = 0; nt < 4; ++nt) {
+                    const int c = weight_row(t.nblk, nt) + (l >> 4) * 4;
+                    // n % 8 == 0: the four channels together
+                    if (r < t.n && c < p.n) *reinterpret_cast<uint2 *>(y + c) = bf16_pairs(acc[nt][mt]);
                 }
             }
         }
+        clear();
+    };
+
+    // A direct load into `sh`, of zeros: the compiler tells the arrays that direct loads write apart,
+    // but a read of any array that none of them writes would wait for all of them.
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(p.count, 0), (LdsPtr)sh.pad, 4, lane * 4, 0, 0,
+                                             0);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) ps[k] = 0.0f;
+    for (int first = mine.first; first < mine.end; first += kList * mine.step) {
+        const int tiles = min((mine.end - first + mine.step - 1) / mine.step, kList);
+        if ((int)threadIdx.x < tiles) {
+            const Tile t = locate(table, p.E, first + threadIdx.x * mine.step, n_tiles, kTileM);
+            sh.list[threadIdx.x] = int4{t.e, t.row0, t.n, t.nblk};
+        }
+        __syncthreads();
+        enter(0);
+        par = 0;
+        panel_load(0, 0);
+#pragma unroll
+        for (int d = 0; d < kDepth - 1; ++d) {
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) load_w(d, nt);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) load_x(d == 0 ? xbuf0 : d == 1 ? xbuf1 : xbuf2, j);
+            __builtin_amdgcn_sched_barrier(0);
+            advance(tiles);
+        }
+        panel_store(0);
+        wait_and_meet<24>();                   // after the first block's: two blocks of 8 + 4
+        read_ws(0);
+        clear();
+#pragma unroll
+        for (int mt = 0; mt < kAhead; ++mt) {
+            xf[mt] = read_row(xbuf0, mt);
+#pragma unroll
+            for (int i = 0; i < kWs; ++i) s[mt][i] = sh.xscale[0][0][mt * 16 + r16] * ws[i];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        for (int tile = 0, kb = 0;;) {
+#define EP_STEP(BUF, D, NEXT, FILL, DF)                                                         \
+    step(BUF, D, NEXT, FILL, DF, tile, kb, tiles);                                              \
+    if (++kb == nkb) {                                                                          \
+        finish(tile);                                                                           \
+        kb = 0;                                                                                 \
+        if (++tile == tiles) break;                                                             \
     }
+            EP_STEP(xbuf0, 0, xbuf1, xbuf3, 3)
+            EP_STEP(xbuf1, 1, xbuf2, xbuf0, 0)
+            EP_STEP(xbuf2, 2, xbuf3, xbuf1, 1)
+            EP_STEP(xbuf3, 3, xbuf0, xbuf2, 2)
+#undef EP_STEP
+        }
+        wait_and_meet<0>();                    // no direct load is left to write LDS
+    }
+#else
+    (void)p;
+#endif
 }
 
 template <bool SWIGLU>
@@ -510,8 +665,9 @@ hipError_t launch_product(const ExpertProduct &p, hipStream_t stream)
     const int64_t n_tiles = (p.n + kTileN - 1) / kTileN;
     const int64_t tiles = ((int64_t)p.pairs / 64 + p.E) * n_tiles;
     const int grid = (int)(tiles < 512 ? (tiles + 7) / 8 * 8 : 512);
-    if (!SWIGLU && p.pairs / p.E >= 32)
-        return launch(expert_tile_kernel, dim3(grid), dim3(kThreads), 0, stream, p);
+    if (p.pairs / p.E >= 32)
+        return launch(expert_tile_kernel<SWIGLU>, dim3(grid < 256 ? grid : 256), dim3(kThreads), 0,
+                      stream, p);
     return launch(expert_stream_kernel<4, SWIGLU, 1>, dim3(grid), dim3(kThreads), 0, stream, p);
 }
 
