@@ -328,21 +328,19 @@ __global__ __launch_bounds__(kThreads) void expert_stream_kernel(ExpertProduct p
 
 // Many rows per expert: tiles of 128 rows x 256 weight rows (SwiGLU: 128 gate and the same 128 up
 // rows), one workgroup of 4 wavefronts per CU that walks its tiles as one stream of blocks (128
-// channels of a tile each). Loads run three blocks ahead of the products, across tiles, so that
-// neither a block nor a tile waits for memory:
-//   * the rows of a block (16 KB) go to one of four LDS buffers by direct global-to-LDS loads and
-//     are read by all four wavefronts;
-//   * a wavefront's 64 weight rows are its own: straight to registers, four blocks deep;
+// channels of a tile each). Loads run ahead of the products by three blocks (SwiGLU, whose blocks
+// take twice as long: two), across tiles, so that neither a block nor a tile waits for memory:
+//   * a wavefront's 64 weight rows are its own: straight to the registers that multiply them;
+//   * the rows (16 KB a block) come in by registers too, a quarter per wavefront, and go through
+//     one of two LDS buffers one block before their products, for all four wavefronts to read;
 //   * the row scales of 16 blocks are staged together, one panel ahead.
-// One barrier per block: when a wavefront passes it, its own direct loads for the next block have
-// landed, and every wavefront is done with the block before, whose buffers the loads then refill.
+// One barrier per block. (Direct global-to-LDS loads would save the rows' registers, but the
+// compiler then waits for loads in flight before it reads LDS, a stall per block.)
 constexpr int kTileM = 128;
 constexpr int kMT = kTileM / 16;
 constexpr int kPanel = 16;         // blocks whose scales are staged together
 [[maybe_unused]] constexpr int kDepth = 4;          // buffers
 constexpr int kList = 256;         // tiles of a workgroup looked up together
-
-[[maybe_unused]] typedef __attribute__((address_space(3))) void *LdsPtr;
 
 // A buffer of `bytes` from p: loads take a lane offset and a uniform one, and give 0 past the end.
 [[maybe_unused]] __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, uint32_t bytes)
@@ -362,13 +360,11 @@ constexpr int kList = 256;         // tiles of a workgroup looked up together
     return v;
 }
 
-// Wait until at most N of this wavefront's vector memory operations are left (they finish in
-// order), then meet the other wavefronts; LDS writes before it are seen after it.
-template <int N>
-__device__ __forceinline__ void wait_and_meet()
+// Meet the other wavefronts with LDS settled; loads in flight stay in flight.
+[[maybe_unused]] __device__ __forceinline__ void meet()
 {
-    __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));    // vmcnt(N) lgkmcnt(0)
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_waitcnt(0xC07F);        // lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
@@ -387,10 +383,10 @@ __device__ __forceinline__ void wait_and_meet()
 
 template <bool SWIGLU>
 struct TileShared {
+    u32x4 x[2][kTileM * 8];
     float xscale[2][kPanel][kTileM + 1];
     float wscale[2][kPanel][2];
     int4 list[kList];
-    u32x4 pad[16];             // see the first direct load
     SwigluShared<SWIGLU ? kMT : 1> h;
 };
 
@@ -399,12 +395,6 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
 {
 #if defined(__HIP_DEVICE_COMPILE__)            // buffer descriptors exist on the device only
     __shared__ TileTable table;
-    // one array per buffer: the compiler then knows that a block's reads do not touch the buffers
-    // that loads in flight are filling, and does not wait for those
-    __shared__ u32x4 xbuf0[kTileM * 8];
-    __shared__ u32x4 xbuf1[kTileM * 8];
-    __shared__ u32x4 xbuf2[kTileM * 8];
-    __shared__ u32x4 xbuf3[kTileM * 8];
     __shared__ TileShared<SWIGLU> sh;
     const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
     const int r16 = lane & 15, g4 = lane >> 4;
@@ -442,19 +432,20 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt)
             ld.woff[nt] = min(weight_row(t.nblk, nt) + (l & 15), p.n - 1) * p.H + (l >> 4) * 16;
-        // direct loads: instruction i of a wavefront fills rows wave * 32 + i * 8 + lane / 8
+        // load j of a wavefront takes rows wave * 32 + j * 8 + lane / 8, 16 bytes a lane
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            ld.xoff[j] = min(wave * 32 + j * 8 + (l >> 3), t.n - 1) * p.H +
-                         ((l & 7) ^ (l >> 3)) * 16;
+            ld.xoff[j] = min(wave * 32 + j * 8 + (l >> 3), t.n - 1) * p.H + (l & 7) * 16;
     };
 
+    constexpr int kDepth = SWIGLU ? 3 : 4;     // blocks in registers
     i32x8 wf[kDepth][4];
+    i32x4 xr[kDepth][4];
     f32x4 acc[4][kMT], v[2][4];
     constexpr int kAhead = SWIGLU ? 1 : 2;     // row tiles read from LDS ahead of the products
     constexpr int kRing = 2 * kAhead, kWs = SWIGLU ? 2 : 1;
     i32x8 xf[kRing];
-    float s[4][kWs];                           // scale of a row tile (gate; up)
+    float xs[4], s[2][kWs];                    // row scales read; times the weights' (gate; up)
     constexpr int kPer = kTileM * kPanel / kThreads;
     float ps[kPer], pw = 0.0f;                 // the next panel on its way
     int par = 0;                               // the panel in use
@@ -463,9 +454,10 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
         wf[d][nt] = join(buffer_load16(ld.w, ld.woff[nt], ld.kb * 128),
                          buffer_load16(ld.w, ld.woff[nt], ld.kb * 128 + 64));
     };
-    auto load_x = [&](u32x4 *buf, int j) {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ld.x, (LdsPtr)(buf + (wave * 32 + j * 8) * 8), 16,
-                                                 ld.xoff[j], ld.kb * 128, 0, 0);
+    auto load_x = [&](int d, int j) { xr[d][j] = buffer_load16(ld.x, ld.xoff[j], ld.kb * 128); };
+    const int put0 = (wave * 32 + (lane >> 3)) * 8 + ((lane & 7) ^ (lane >> 3));
+    auto put_x = [&](int buf, int d, int j) {
+        sh.x[buf][put0 + j * 64] = __builtin_bit_cast(u32x4, xr[d][j]);
     };
     auto advance = [&](int tiles) {            // past the last block: that block again
         if (++ld.kb == nkb) {
@@ -489,21 +481,21 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
         for (int k = 0; k < kPer; ++k) sh.xscale[to][l & 15][k * 16 + (l >> 4)] = ps[k];
         if (l < 32) sh.wscale[to][l & 15][l >> 4] = pw;
     };
-    auto read_row = [&](const u32x4 *buf, int mt) {
-        const i32x4 *row = reinterpret_cast<const i32x4 *>(buf) + mt * 128;
+    auto read_row = [&](int buf, int mt) {
+        const i32x4 *row = reinterpret_cast<const i32x4 *>(sh.x[buf]) + mt * 128;
         return join(row[pos0], row[pos0 ^ 4]);
     };
     float ws[kWs];
-    auto read_ws = [&](int b) {
-        ws[0] = sh.wscale[par][b][SWIGLU ? 0 : wave >> 1];
-        if constexpr (SWIGLU) ws[1] = sh.wscale[par][b][1];
+    auto read_ws = [&](float (&to)[kWs], int b) {
+        to[0] = sh.wscale[par][b][SWIGLU ? 0 : wave >> 1];
+        if constexpr (SWIGLU) to[1] = sh.wscale[par][b][1];
     };
     auto sum = [&](int mt) {                   // the products of row tile mt, from v[mt & 1]
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                acc[nt][mt][k] = __builtin_fmaf(s[mt & 3][SWIGLU ? nt >> 1 : 0], v[mt & 1][nt][k],
+                acc[nt][mt][k] = __builtin_fmaf(s[mt & 1][SWIGLU ? nt >> 1 : 0], v[mt & 1][nt][k],
                                                 acc[nt][mt][k]);
             asm volatile("" : "+v"(acc[nt][mt]));        // summed here, not later
         }
@@ -516,18 +508,19 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
             v[(kMT - 1) & 1][nt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};    // no block before the first
         }
 #pragma unroll
-        for (int i = 0; i < kWs; ++i) s[(kMT - 1) & 3][i] = 0.0f;
+        for (int i = 0; i < kWs; ++i) s[(kMT - 1) & 1][i] = 0.0f;
     };
-    // One block: `buf` and d hold it, `next` is the following block's buffer, `fill` and df take the
-    // block three ahead. In each of its 8 regions one row tile is multiplied, the one before summed,
-    // and one read from LDS, kAhead ahead; the fences keep the regions apart.
-    auto step = [&](const u32x4 *buf, int d, const u32x4 *next, u32x4 *fill, int df, int tile,
-                    int kb, int tiles) {
+    // One block, whose weights are in slot d and whose rows are in LDS buffer `buf`. In each of its 8
+    // regions one row tile is multiplied, the one before summed, and one read from LDS, kAhead ahead
+    // (the last ones from the next block's buffer); the fences keep the regions apart.
+    auto step = [&](int d, int buf, int tile, int kb, int tiles) {
+        const int df = (d + kDepth - 1) % kDepth, dn = (d + 1) % kDepth;
         if ((kb & (kPanel - 1)) == 0) {
             if (kb + kPanel < nkb) panel_load(tile, kb + kPanel);
             else if (tile + 1 < tiles) panel_load(tile + 1, 0);
         }
         const int b_next = kb == nkb - 1 ? 0 : (kb + 1) & (kPanel - 1);
+        float ws_next[kWs];
         Bf16Block wb[SWIGLU ? 4 : 1];
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt) {
@@ -537,19 +530,19 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
                     par ^= 1;
                     panel_store(par);
                 }
-                // of the operations after the next block's direct loads at least 8 + 4 + 8 remain:
-                // two blocks of weights and one of rows
-                wait_and_meet<20>();
-                read_ws(b_next);
+                meet();
+                read_ws(ws_next, b_next);
             }
-            const i32x8 x_in = read_row(to < kMT ? buf : next, to & (kMT - 1));
+            const i32x8 x_in = read_row(to < kMT ? buf : buf ^ 1, to & (kMT - 1));
             const float s_in =
                 sh.xscale[par][to < kMT ? kb & (kPanel - 1) : b_next][(to & (kMT - 1)) * 16 + r16];
-            if (mt < 4) load_w(df, mt);
-            if (to >= kMT) {
-#pragma unroll
-                for (int j = 0; j < 4 / kAhead; ++j) load_x(fill, (to - kMT) * (4 / kAhead) + j);
+            if (mt < 4) {
+                put_x(buf ^ 1, dn, mt);
+                load_w(df, mt);
+                load_x(df, mt);
             }
+#pragma unroll
+            for (int i = 0; i < kWs; ++i) s[mt & 1][i] = xs[mt & 3] * ws[i];
             if constexpr (SWIGLU) {
                 const Bf16Block xb = bf16_block(xf[mt & (kRing - 1)]);
 #pragma unroll
@@ -564,8 +557,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
             }
             sum((mt + kMT - 1) & (kMT - 1));
             xf[to & (kRing - 1)] = x_in;
-#pragma unroll
-            for (int i = 0; i < kWs; ++i) s[to & 3][i] = s_in * ws[i];
+            xs[to & 3] = s_in;
             if constexpr (!SWIGLU) {
                 __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);          // LDS reads
 #pragma unroll
@@ -576,6 +568,8 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
             }
             __builtin_amdgcn_sched_barrier(0);
         }
+#pragma unroll
+        for (int i = 0; i < kWs; ++i) ws[i] = ws_next[i];
         advance(tiles);
     };
     auto finish = [&](int tile) {              // the tile's last sums and its output
@@ -600,10 +594,6 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
         clear();
     };
 
-    // A direct load into `sh`, of zeros: the compiler tells the arrays that direct loads write apart,
-    // but a read of any array that none of them writes would wait for all of them.
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(p.count, 0), (LdsPtr)sh.pad, 4, lane * 4, 0, 0,
-                                             0);
 #pragma unroll
     for (int k = 0; k < kPer; ++k) ps[k] = 0.0f;
     for (int first = mine.first; first < mine.end; first += kList * mine.step) {
@@ -619,39 +609,36 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
 #pragma unroll
         for (int d = 0; d < kDepth - 1; ++d) {
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) load_w(d, nt);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) load_x(d == 0 ? xbuf0 : d == 1 ? xbuf1 : xbuf2, j);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int j = 0; j < 4; ++j) {
+                load_w(d, j);
+                load_x(d, j);
+            }
             advance(tiles);
         }
         panel_store(0);
-        wait_and_meet<24>();                   // after the first block's: two blocks of 8 + 4
-        read_ws(0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) put_x(0, 0, j);
+        meet();
+        read_ws(ws, 0);
         clear();
 #pragma unroll
         for (int mt = 0; mt < kAhead; ++mt) {
-            xf[mt] = read_row(xbuf0, mt);
-#pragma unroll
-            for (int i = 0; i < kWs; ++i) s[mt][i] = sh.xscale[0][0][mt * 16 + r16] * ws[i];
+            xf[mt] = read_row(0, mt);
+            xs[mt] = sh.xscale[0][0][mt * 16 + r16];
         }
         __builtin_amdgcn_sched_barrier(0);
-        for (int tile = 0, kb = 0;;) {
-#define EP_STEP(BUF, D, NEXT, FILL, DF)                                                         \
-    step(BUF, D, NEXT, FILL, DF, tile, kb, tiles);                                              \
-    if (++kb == nkb) {                                                                          \
-        finish(tile);                                                                           \
-        kb = 0;                                                                                 \
-        if (++tile == tiles) break;                                                             \
-    }
-            EP_STEP(xbuf0, 0, xbuf1, xbuf3, 3)
-            EP_STEP(xbuf1, 1, xbuf2, xbuf0, 0)
-            EP_STEP(xbuf2, 2, xbuf3, xbuf1, 1)
-            EP_STEP(xbuf3, 3, xbuf0, xbuf2, 2)
-#undef EP_STEP
-        }
-        wait_and_meet<0>();                    // no direct load is left to write LDS
+        int tile = 0, kb = 0, buf = 0;
+        auto next = [&](int d) {               // a block; false after the last one
+            step(d, buf, tile, kb, tiles);
+            buf ^= 1;
+            if (++kb < nkb) return true;
+            finish(tile);
+            kb = 0;
+            return ++tile < tiles;
+        };
+        if constexpr (kDepth == 4) while (next(0) && next(1) && next(2) && next(3)) {}
+        else while (next(0) && next(1) && next(2)) {}
+        meet();                                // the list and LDS are free again
     }
 #else
     (void)p;
