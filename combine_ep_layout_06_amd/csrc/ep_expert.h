@@ -50,6 +50,7 @@ hipError_t launch_moe_layer(const MoeLayer &p, bool fp8, hipStream_t stream);
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // D = A * B for a 16 x 128 tile of E4M3 codes A and a 128 x 16 tile B (fp32 result, matrix cores).
 // Lane l holds 32 codes of row (column) l & 15. Which 32 of the 128 products' indices a lane

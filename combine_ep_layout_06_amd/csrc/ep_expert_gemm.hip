@@ -143,63 +143,71 @@ __device__ __forceinline__ uint32_t encode4_any(const float (&h)[4], float scale
     return v;
 }
 
-// SwiGLU: MT tiles of 16 rows, a wavefront's tiles 0, 1 (gate) and 2, 3 (up) of weight rows.
-template <int MT>
+// The SwiGLU epilogue of one tile of ROWS rows x 128 channels of h: the block amax meets in LDS, the
+// codes go out through LDS in whole rows. A wavefront holds 32 of the 128 channels, a lane G groups
+// of 4 consecutive ones (group g at channel wave * 32 + channel(g)) of M rows (row(m)), GROUP lanes
+// apart from the other channels of the row.
+template <int ROWS>
 struct SwigluShared {
-    uint32_t amax[kWaves][MT * 16];
-    float scale[MT * 16];
-    u32x4 code[MT * 16][8];
+    uint32_t amax[kWaves][ROWS];
+    float scale[ROWS];
+    u32x4 code[ROWS][8];
 };
 
-template <int MT>
-__device__ __forceinline__ void store_swiglu(SwigluShared<MT> &sh, f32x4 (&acc)[4][MT],
-                                             const ExpertProduct &p, int row0, int n, int nblk)
+template <int ROWS, int M, int G, int GROUP, typename Row, typename Channel>
+__device__ __forceinline__ void store_swiglu(SwigluShared<ROWS> &sh, float (&h)[M][G][4], Row row,
+                                             Channel channel, const ExpertProduct &p, int row0,
+                                             int n, int nblk)
 {
     const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
-    const int r16 = lane & 15, g4 = lane >> 4;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int m = 0; m < M; ++m) {
         uint32_t amax = 0;
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int g = 0; g < G; ++g)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                acc[nt][mt][k] = swiglu(acc[nt][mt][k], acc[nt + 2][mt][k]);
-                amax = max(amax, __float_as_uint(acc[nt][mt][k]) & 0x7FFFFFFFu);
-            }
-        amax = max(amax, (uint32_t)__shfl_xor((int)amax, 16));
-        amax = max(amax, (uint32_t)__shfl_xor((int)amax, 32));
-        if (g4 == 0) sh.amax[wave][mt * 16 + r16] = amax;
+            for (int k = 0; k < 4; ++k)
+                amax = max(amax, __float_as_uint(h[m][g][k]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int x = GROUP; x < kWave; x *= 2) amax = max(amax, (uint32_t)__shfl_xor((int)amax, x));
+        if (lane < GROUP) sh.amax[wave][row(m)] = amax;
     }
     __syncthreads();
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        const int r = mt * 16 + r16;
+    for (int m = 0; m < M; ++m) {
+        const int r = row(m);
         uint32_t amax = 0;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) amax = max(amax, sh.amax[w][r]);
         const float scale = block_scale(amax);
         // 2^-60 <= amax < inf: the quotients lie where div_by_rcp and the conversion are exact
-        const bool plain = amax < 0x21800000u || amax >= 0x7F800000u;
-        const bool any_plain = __any(plain);
+        const bool plain = __any(amax < 0x21800000u || amax >= 0x7F800000u);
         const float y = 1.0f / scale;
+        uint32_t *code = reinterpret_cast<uint32_t *>(&sh.code[r][0]) + wave * 8;
+        if (plain) {
+#pragma unroll 1
+            for (int g = 0; g < G; ++g) {
+                float v[4];                    // h[m][g] by selects: g is not constant here
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-            const float h[4] = {acc[nt][mt][0], acc[nt][mt][1], acc[nt][mt][2], acc[nt][mt][3]};
-            uint32_t v;
-            if (any_plain)
-                v = encode4_any(h, scale);
-            else
-                v = e4m3_pack4(div_by_rcp(h[0], scale, y), div_by_rcp(h[1], scale, y),
-                               div_by_rcp(h[2], scale, y), div_by_rcp(h[3], scale, y));
-            // channel wave * 32 + nt * 16 + g4 * 4 of the row's block
-            reinterpret_cast<uint32_t *>(&sh.code[r][0])[wave * 8 + nt * 4 + g4] = v;
+                for (int k = 0; k < 4; ++k) {
+                    v[k] = h[m][0][k];
+#pragma unroll
+                    for (int i = 1; i < G; ++i) v[k] = i == g ? h[m][i][k] : v[k];
+                }
+                code[channel(g) >> 2] = encode4_any(v, scale);
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                code[channel(g) >> 2] =
+                    e4m3_pack4(div_by_rcp(h[m][g][0], scale, y), div_by_rcp(h[m][g][1], scale, y),
+                               div_by_rcp(h[m][g][2], scale, y), div_by_rcp(h[m][g][3], scale, y));
         }
-        if (wave == 0 && g4 == 0) sh.scale[r] = scale;
+        if (wave == 0 && lane < GROUP) sh.scale[r] = scale;
     }
     __syncthreads();
     const int I = p.n / 2;
-    for (int i = threadIdx.x; i < MT * 16 * 8; i += kThreads) {
+    for (int i = threadIdx.x; i < ROWS * 8; i += kThreads) {
         const int r = i >> 3;
         if (r < n)
             *reinterpret_cast<u32x4 *>(p.h_q + (size_t)(row0 + r) * I + nblk * 128 + (i & 7) * 16) =
@@ -217,7 +225,7 @@ template <int MT, bool SWIGLU, int D>
 __global__ __launch_bounds__(kThreads) void expert_stream_kernel(ExpertProduct p)
 {
     __shared__ TileTable table;
-    __shared__ SwigluShared<SWIGLU ? MT : 1> sh;
+    __shared__ SwigluShared<SWIGLU ? MT * 16 : 1> sh;
     const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
     const int r16 = lane & 15, g4 = lane >> 4;
     const int nkb = p.H >> 7;
@@ -305,7 +313,17 @@ __global__ __launch_bounds__(kThreads) void expert_stream_kernel(ExpertProduct p
         }
 
         if constexpr (SWIGLU) {
-            store_swiglu<MT>(sh, acc, p, row0, n, nblk);
+            float h[MT][2][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        h[mt][g][k] = swiglu(acc[g][mt][k], acc[g + 2][mt][k]);
+            store_swiglu<MT * 16, MT, 2, 16>(
+                sh, h, [&](int m) { return m * 16 + r16; },
+                [&](int g) { return g * 16 + g4 * 4; }, p, row0, n, nblk);
         } else {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
@@ -328,16 +346,16 @@ __global__ __launch_bounds__(kThreads) void expert_stream_kernel(ExpertProduct p
 
 // Many rows per expert: tiles of 128 rows x 256 weight rows (SwiGLU: 128 gate and the same 128 up
 // rows), one workgroup of 4 wavefronts per CU that walks its tiles as one stream of blocks (128
-// channels of a tile each). Loads run ahead of the products by three blocks (SwiGLU, whose blocks
-// take twice as long: two), across tiles, so that neither a block nor a tile waits for memory:
-//   * a wavefront's 64 weight rows are its own: straight to the registers that multiply them;
-//   * the rows (16 KB a block) come in by registers too, a quarter per wavefront, and go through
-//     one of two LDS buffers one block before their products, for all four wavefronts to read;
-//   * the row scales of 16 blocks are staged together, one panel ahead.
-// One barrier per block. (Direct global-to-LDS loads would save the rows' registers, but the
-// compiler then waits for loads in flight before it reads LDS, a stall per block.)
+// channels of a tile each). Loads run two blocks ahead of LDS and three ahead of the products,
+// across tiles, so that neither a block nor a tile waits for memory. A load instruction covers 8
+// whole 128-byte row segments, 8 lanes a row: the vector cache takes one access per 128 bytes (in
+// the matrix instruction's lane order, 16 rows side by side, it took one per 16 bytes, and that
+// bounded the kernel: 1.35 ms for 65536 rows x 4096 x 4096). From registers a block goes to one of
+// two LDS buffers: the rows a quarter per wavefront, for all four to read; the weights each
+// wavefront's own 64 rows. The row scales of 16 blocks are staged together, one panel ahead.
+// One barrier per block.
 constexpr int kTileM = 128;
-constexpr int kMT = kTileM / 16;
+[[maybe_unused]] constexpr int kMT = kTileM / 32;
 constexpr int kPanel = 16;         // blocks whose scales are staged together
 [[maybe_unused]] constexpr int kDepth = 4;          // buffers
 constexpr int kList = 256;         // tiles of a workgroup looked up together
@@ -370,8 +388,9 @@ constexpr int kList = 256;         // tiles of a workgroup looked up together
 }
 
 // bf16 pairs of four values, NaN as 0x7FC0.
-[[maybe_unused]] __device__ __forceinline__ uint2 bf16_pairs(f32x4 v)
+[[maybe_unused]] __device__ __forceinline__ uint2 bf16_pairs(float a, float b, float c, float d)
 {
+    const float v[4] = {a, b, c, d};
     bf16x2 lo = {(__bf16)v[0], (__bf16)v[1]}, hi = {(__bf16)v[2], (__bf16)v[3]};
     uint2 o{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
     if (__builtin_isunordered(v[0], v[1]) || __builtin_isunordered(v[2], v[3])) {
@@ -384,10 +403,11 @@ constexpr int kList = 256;         // tiles of a workgroup looked up together
 template <bool SWIGLU>
 struct TileShared {
     u32x4 x[2][kTileM * 8];
+    u32x4 w[2][kWaves][64 * 8];
     float xscale[2][kPanel][kTileM + 1];
     float wscale[2][kPanel][2];
     int4 list[kList];
-    SwigluShared<SWIGLU ? kMT : 1> h;
+    SwigluShared<SWIGLU ? kTileM : 1> h;
 };
 
 template <bool SWIGLU>
@@ -397,26 +417,28 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
     __shared__ TileTable table;
     __shared__ TileShared<SWIGLU> sh;
     const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
-    const int r16 = lane & 15, g4 = lane >> 4;
+    const int r32 = lane & 31, half = lane >> 5;
     const int nkb = p.H >> 7;
     const int n_tiles = (p.n + kTileN - 1) / kTileN;
     const int ws_rows = (p.n + 127) >> 7;
     const int total = build_table(table, p, kTileM) * n_tiles;
     const TileRange mine = my_tiles(total);
-    // chunk c of row r is kept at position c ^ (r & 7) of the row's eight 16-byte chunks: the
-    // reads of 8 consecutive lanes (8 rows, one chunk) then touch all banks
-    const int pos0 = r16 * 8 + (g4 ^ (r16 & 7));
+    // Chunk c (16 bytes) of row r is kept at place c ^ swizzle(r) of the row's eight: the lanes that
+    // LDS serves together (8 consecutive rows, and the same 16 further on) then touch all banks.
+    // A lane's j-th chunk of a block is 2 * j + half of row lane & 31.
+    auto swizzle = [](int r) { return (r & 7) ^ ((r >> 4) & 1); };
+    const int row_at = r32 * 8, row_swizzle = swizzle(r32);
 
     // the stream of loads: the tile it is in and its next block
     struct {
         int tile, kb;
         __amdgpu_buffer_rsrc_t w, x;
-        int woff[4], xoff[4];
+        int woff[8], xoff[4];
     } ld;
-    // first weight row of a wavefront's tile nt
+    // first weight row of a wavefront's tile nt (SwiGLU: gate, up)
     auto weight_row = [&](int nblk, int nt) {
-        return SWIGLU ? (nt >> 1) * (p.n / 2) + nblk * 128 + wave * 32 + (nt & 1) * 16
-                      : nblk * kTileN + wave * 64 + nt * 16;
+        return SWIGLU ? nt * (p.n / 2) + nblk * 128 + wave * 32
+                      : nblk * kTileN + wave * 64 + nt * 32;
     };
     auto at = [&](int i) {
         const int4 v = sh.list[i];
@@ -430,34 +452,34 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
         ld.x = buffer(p.q + (size_t)t.row0 * p.H, (uint32_t)t.n * p.H);
         const int l = fresh(lane);
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
-            ld.woff[nt] = min(weight_row(t.nblk, nt) + (l & 15), p.n - 1) * p.H + (l >> 4) * 16;
-        // load j of a wavefront takes rows wave * 32 + j * 8 + lane / 8, 16 bytes a lane
+        for (int j = 0; j < 8; ++j)
+            ld.woff[j] = min(weight_row(t.nblk, j >> 2) + (j & 3) * 8 + (l >> 3), p.n - 1) * p.H +
+                         (l & 7) * 16;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             ld.xoff[j] = min(wave * 32 + j * 8 + (l >> 3), t.n - 1) * p.H + (l & 7) * 16;
     };
 
-    constexpr int kDepth = SWIGLU ? 3 : 4;     // blocks in registers
-    i32x8 wf[kDepth][4];
-    i32x4 xr[kDepth][4];
-    f32x4 acc[4][kMT], v[2][4];
-    constexpr int kAhead = SWIGLU ? 1 : 2;     // row tiles read from LDS ahead of the products
-    constexpr int kRing = 2 * kAhead, kWs = SWIGLU ? 2 : 1;
-    i32x8 xf[kRing];
-    float xs[4], s[2][kWs];                    // row scales read; times the weights' (gate; up)
+    i32x4 wr[2][8], xr[2][4];                  // two blocks on their way to LDS
+    i32x4 wf[SWIGLU ? 1 : 2][2][4];            // the wavefront's weights of a block: [tile][chunk]
+    f32x16 acc[2][kMT], v[2][2];
+    i32x4 xf[2][4];
+    constexpr int kWs = SWIGLU ? 2 : 1;
+    float xs[2], s[2][kWs];                    // row scales read; times the weights' (gate; up)
     constexpr int kPer = kTileM * kPanel / kThreads;
     float ps[kPer], pw = 0.0f;                 // the next panel on its way
     int par = 0;                               // the panel in use
 
-    auto load_w = [&](int d, int nt) {
-        wf[d][nt] = join(buffer_load16(ld.w, ld.woff[nt], ld.kb * 128),
-                         buffer_load16(ld.w, ld.woff[nt], ld.kb * 128 + 64));
-    };
+    auto load_w = [&](int d, int j) { wr[d][j] = buffer_load16(ld.w, ld.woff[j], ld.kb * 128); };
     auto load_x = [&](int d, int j) { xr[d][j] = buffer_load16(ld.x, ld.xoff[j], ld.kb * 128); };
-    const int put0 = (wave * 32 + (lane >> 3)) * 8 + ((lane & 7) ^ (lane >> 3));
-    auto put_x = [&](int buf, int d, int j) {
-        sh.x[buf][put0 + j * 64] = __builtin_bit_cast(u32x4, xr[d][j]);
+    // the lane's place in LDS: its row of each 8, its chunk (rows 16 further on swap neighbours)
+    const int put0 = (lane >> 3) * 8 + ((lane & 7) ^ (lane >> 3));
+    auto put_w = [&](int d, int j) {
+        sh.w[d][wave][j * 64 + (put0 ^ ((j >> 1) & 1))] = __builtin_bit_cast(u32x4, wr[d][j]);
+    };
+    auto put_x = [&](int d, int j) {
+        sh.x[d][wave * 256 + j * 64 + (put0 ^ ((j >> 1) & 1))] =
+            __builtin_bit_cast(u32x4, xr[d][j]);
     };
     auto advance = [&](int tiles) {            // past the last block: that block again
         if (++ld.kb == nkb) {
@@ -481,50 +503,56 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
         for (int k = 0; k < kPer; ++k) sh.xscale[to][l & 15][k * 16 + (l >> 4)] = ps[k];
         if (l < 32) sh.wscale[to][l & 15][l >> 4] = pw;
     };
-    auto read_row = [&](int buf, int mt) {
-        const i32x4 *row = reinterpret_cast<const i32x4 *>(sh.x[buf]) + mt * 128;
-        return join(row[pos0], row[pos0 ^ 4]);
+    auto read_row = [&](int d, int mt) {       // the lane's chunks of row tile mt
+        const i32x4 *x = reinterpret_cast<const i32x4 *>(sh.x[d]) + mt * 256 + row_at;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xf[mt & 1][j] = x[(2 * j + half) ^ row_swizzle];
+    };
+    auto read_w = [&](int d, int nt) {         // and of the wavefront's weight tile nt
+        const i32x4 *w = reinterpret_cast<const i32x4 *>(sh.w[d][wave]) + nt * 256 + row_at;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) wf[SWIGLU ? 0 : d][nt][j] = w[(2 * j + half) ^ row_swizzle];
     };
     float ws[kWs];
     auto read_ws = [&](float (&to)[kWs], int b) {
         to[0] = sh.wscale[par][b][SWIGLU ? 0 : wave >> 1];
         if constexpr (SWIGLU) to[1] = sh.wscale[par][b][1];
     };
-    auto sum = [&](int mt) {                   // the products of row tile mt, from v[mt & 1]
+    auto sum = [&](int mt, int nt, int part) { // a quarter of the products of row tile mt
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                acc[nt][mt][k] = __builtin_fmaf(s[mt & 1][SWIGLU ? nt >> 1 : 0], v[mt & 1][nt][k],
-                                                acc[nt][mt][k]);
-            asm volatile("" : "+v"(acc[nt][mt]));        // summed here, not later
-        }
+        for (int i = part * 4; i < part * 4 + 4; ++i)
+            acc[nt][mt][i] = __builtin_fmaf(s[mt & 1][SWIGLU ? nt : 0], v[mt & 1][nt][i],
+                                            acc[nt][mt][i]);
     };
     auto clear = [&]() {
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
+        for (int nt = 0; nt < 2; ++nt) {
 #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) acc[nt][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            v[(kMT - 1) & 1][nt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};    // no block before the first
+            for (int i = 0; i < 16; ++i) {
+#pragma unroll
+                for (int mt = 0; mt < kMT; ++mt) acc[nt][mt][i] = 0.0f;
+                v[(kMT - 1) & 1][nt][i] = 0.0f;          // no block before the first
+            }
         }
 #pragma unroll
         for (int i = 0; i < kWs; ++i) s[(kMT - 1) & 1][i] = 0.0f;
     };
-    // One block, whose weights are in slot d and whose rows are in LDS buffer `buf`. In each of its 8
-    // regions one row tile is multiplied, the one before summed, and one read from LDS, kAhead ahead
-    // (the last ones from the next block's buffer); the fences keep the regions apart.
-    auto step = [&](int d, int buf, int tile, int kb, int tiles) {
-        const int df = (d + kDepth - 1) % kDepth, dn = (d + 1) % kDepth;
+    // One block, in LDS buffer d. In each of its 4 regions one tile of 32 rows is multiplied, the one
+    // before summed, and the next read from LDS (the last one from the next block's buffer); the
+    // fences keep the regions apart. The next block goes to LDS before the barrier, and the one
+    // three ahead takes its registers.
+    auto step = [&](int d, int tile, int kb, int tiles) {
+        const int dn = d ^ 1, dw = SWIGLU ? 0 : d;
         if ((kb & (kPanel - 1)) == 0) {
             if (kb + kPanel < nkb) panel_load(tile, kb + kPanel);
             else if (tile + 1 < tiles) panel_load(tile + 1, 0);
         }
         const int b_next = kb == nkb - 1 ? 0 : (kb + 1) & (kPanel - 1);
         float ws_next[kWs];
-        Bf16Block wb[SWIGLU ? 4 : 1];
+        bf16x8 wb[SWIGLU ? 2 : 1][8];
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt) {
-            const int to = mt + kAhead;
+            const int to = mt + 1, before = (mt + kMT - 1) & (kMT - 1);
             if (to == kMT) {
                 if (b_next == 0) {
                     par ^= 1;
@@ -533,37 +561,67 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
                 meet();
                 read_ws(ws_next, b_next);
             }
-            const i32x8 x_in = read_row(to < kMT ? buf : buf ^ 1, to & (kMT - 1));
+            read_row(to < kMT ? d : dn, to & (kMT - 1));
             const float s_in =
-                sh.xscale[par][to < kMT ? kb & (kPanel - 1) : b_next][(to & (kMT - 1)) * 16 + r16];
-            if (mt < 4) {
-                put_x(buf ^ 1, dn, mt);
-                load_w(df, mt);
-                load_x(df, mt);
+                sh.xscale[par][to < kMT ? kb & (kPanel - 1) : b_next][(to & (kMT - 1)) * 32 + r32];
+            if (mt < 3) {                      // 4 + 8 pieces over three regions
+#pragma unroll
+                for (int j = mt * 4; j < mt * 4 + 4; ++j) {
+                    if (j < 4) {
+                        put_x(dn, j);
+                        load_x(dn, j);
+                    } else {
+                        put_w(dn, j - 4);
+                        load_w(dn, j - 4);
+                    }
+                }
+            } else if constexpr (!SWIGLU) {
+                read_w(dn, 0);
+                read_w(dn, 1);
             }
 #pragma unroll
-            for (int i = 0; i < kWs; ++i) s[mt & 1][i] = xs[mt & 3] * ws[i];
+            for (int i = 0; i < kWs; ++i) s[mt & 1][i] = xs[mt & 1] * ws[i];
             if constexpr (SWIGLU) {
-                const Bf16Block xb = bf16_block(xf[mt & (kRing - 1)]);
+                if (to == kMT) {               // wb holds this block's
+                    read_w(dn, 0);
+                    read_w(dn, 1);
+                }
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    if (mt == 0) wb[nt] = bf16_block(wf[d][nt]);
-                    v[mt & 1][nt] = mfma_exact(wb[nt], xb);
+                for (int j = 0; j < 8; ++j) {
+                    const bf16x8 xb = bf16_of_e4m3(xf[mt & 1][j >> 1][(j & 1) * 2],
+                                                   xf[mt & 1][j >> 1][(j & 1) * 2 + 1]);
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        if (mt == 0)
+                            wb[nt][j] = bf16_of_e4m3(wf[0][nt][j >> 1][(j & 1) * 2],
+                                                     wf[0][nt][j >> 1][(j & 1) * 2 + 1]);
+                        v[mt & 1][nt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                            wb[nt][j], xb, j == 0 ? f32x16{} : v[mt & 1][nt], 0, 0, 0);
+                    }
+                    sum(before, j >> 2, j & 3);
                 }
             } else {
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
-                    v[mt & 1][nt] = mfma_e4m3(wf[d][nt], xf[mt & (kRing - 1)]);
-            }
-            sum((mt + kMT - 1) & (kMT - 1));
-            xf[to & (kRing - 1)] = x_in;
-            xs[to & 3] = s_in;
-            if constexpr (!SWIGLU) {
-                __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);          // LDS reads
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
+                    for (int nt = 0; nt < 2; ++nt) {
+                        v[mt & 1][nt] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                            join(wf[dw][nt][2 * j], wf[dw][nt][2 * j + 1]),
+                            join(xf[mt & 1][2 * j], xf[mt & 1][2 * j + 1]),
+                            j == 0 ? f32x16{} : v[mt & 1][nt], 0, 0, 0, 0, 0, 0);
+                        sum(before, j, nt * 2);
+                        sum(before, j, nt * 2 + 1);
+                    }
+            }
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) asm volatile("" : "+v"(acc[nt][before]));
+            xs[to & 1] = s_in;
+            if constexpr (!SWIGLU) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 5, 0);          // LDS reads
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
                     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // a product
-                    __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);      // four sums
+                    __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);      // eight sums
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -573,22 +631,36 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
         advance(tiles);
     };
     auto finish = [&](int tile) {              // the tile's last sums and its output
-        sum(kMT - 1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum(kMT - 1, i >> 2, i & 3);
         const Tile t = at(tile);
+        const int l = fresh(lane);
+        // element i of a lane is channel (i >> 2) * 8 + half * 4 + (i & 3) of row lane & 31
         if constexpr (SWIGLU) {
-            store_swiglu<kMT>(sh.h, acc, p, t.row0, t.n, t.nblk);
+            float h[kMT][4][4];
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) h[mt][i >> 2][i & 3] = swiglu(acc[0][mt][i], acc[1][mt][i]);
+            store_swiglu<kTileM, kMT, 4, 32>(
+                sh.h, h, [&](int m) { return m * 32 + (l & 31); },
+                [&](int g) { return g * 8 + (l >> 5) * 4; }, p, t.row0, t.n, t.nblk);
         } else {
-            const int l = fresh(lane);
 #pragma unroll
             for (int mt = 0; mt < kMT; ++mt) {
-                const int r = mt * 16 + (l & 15);
+                const int r = mt * 32 + (l & 31);
                 uint16_t *y = p.y + (size_t)(t.row0 + r) * p.n;
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    const int c = weight_row(t.nblk, nt) + (l >> 4) * 4;
-                    // n % 8 == 0: the four channels together
-                    if (r < t.n && c < p.n) *reinterpret_cast<uint2 *>(y + c) = bf16_pairs(acc[nt][mt]);
-                }
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const int c = weight_row(t.nblk, nt) + g * 8 + (l >> 5) * 4;
+                        // n % 8 == 0: the four channels together
+                        if (r < t.n && c < p.n)
+                            *reinterpret_cast<uint2 *>(y + c) =
+                                bf16_pairs(acc[nt][mt][g * 4], acc[nt][mt][g * 4 + 1],
+                                           acc[nt][mt][g * 4 + 2], acc[nt][mt][g * 4 + 3]);
+                    }
             }
         }
         clear();
@@ -606,38 +678,38 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
         enter(0);
         par = 0;
         panel_load(0, 0);
+        auto load = [&](int d) {
 #pragma unroll
-        for (int d = 0; d < kDepth - 1; ++d) {
+            for (int j = 0; j < 4; ++j) load_x(d, j);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                load_w(d, j);
-                load_x(d, j);
-            }
+            for (int j = 0; j < 8; ++j) load_w(d, j);
             advance(tiles);
-        }
+        };
+        load(0);
+        load(1);
         panel_store(0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) put_x(0, 0, j);
+        for (int j = 0; j < 4; ++j) put_x(0, j);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) put_w(0, j);
+        load(0);
         meet();
         read_ws(ws, 0);
         clear();
-#pragma unroll
-        for (int mt = 0; mt < kAhead; ++mt) {
-            xf[mt] = read_row(0, mt);
-            xs[mt] = sh.xscale[0][0][mt * 16 + r16];
-        }
+        read_w(0, 0);
+        read_w(0, 1);
+        read_row(0, 0);
+        xs[0] = sh.xscale[0][0][r32];
         __builtin_amdgcn_sched_barrier(0);
-        int tile = 0, kb = 0, buf = 0;
+        int tile = 0, kb = 0;
         auto next = [&](int d) {               // a block; false after the last one
-            step(d, buf, tile, kb, tiles);
-            buf ^= 1;
+            step(d, tile, kb, tiles);
             if (++kb < nkb) return true;
             finish(tile);
             kb = 0;
             return ++tile < tiles;
         };
-        if constexpr (kDepth == 4) while (next(0) && next(1) && next(2) && next(3)) {}
-        else while (next(0) && next(1) && next(2)) {}
+        while (next(0) && next(1)) {}
         meet();                                // the list and LDS are free again
     }
 #else
