@@ -16,7 +16,6 @@ namespace ep {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
 constexpr int kTileN = 256;        // weight rows per workgroup: 64 per wavefront
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -25,12 +24,13 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // running number of tiles. Built once per workgroup.
 struct TileTable {
     int32_t end[EP_MAX_EXPERTS], base[EP_MAX_EXPERTS], n[EP_MAX_EXPERTS];
-    int32_t wave_sum[kWaves];
+    int32_t wave_sum[16];
 };
 
+template <int THREADS>
 __device__ __forceinline__ int build_table(TileTable &t, const ExpertProduct &p, int bm)
 {
-    constexpr int kPer = EP_MAX_EXPERTS / kThreads;
+    constexpr int kPer = EP_MAX_EXPERTS / THREADS;
     const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
     const int e0 = threadIdx.x * kPer;
     int tiles[kPer], sum = 0;
@@ -51,7 +51,7 @@ __device__ __forceinline__ int build_table(TileTable &t, const ExpertProduct &p,
     __syncthreads();
     int run = incl - sum, total = 0;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < THREADS / kWave; ++w) {
         const int s = t.wave_sum[w];
         if (w < wave) run += s;
         total += s;
@@ -144,22 +144,22 @@ __device__ __forceinline__ uint32_t encode4_any(const float (&h)[4], float scale
 }
 
 // The SwiGLU epilogue of one tile of ROWS rows x 128 channels of h: the block amax meets in LDS, the
-// codes go out through LDS in whole rows. A wavefront holds 32 of the 128 channels, a lane G groups
-// of 4 consecutive ones (group g at channel wave * 32 + channel(g)) of M rows (row(m)), GROUP lanes
-// apart from the other channels of the row.
+// codes go out through LDS in whole rows. A wavefront holds quarter `part` of the 128 channels, a
+// lane G groups of 4 consecutive ones (group g at channel part * 32 + channel(g)) of M rows
+// (row(m)), GROUP lanes apart from the other channels of the row.
 template <int ROWS>
 struct SwigluShared {
-    uint32_t amax[kWaves][ROWS];
+    uint32_t amax[4][ROWS];
     float scale[ROWS];
     u32x4 code[ROWS][8];
 };
 
-template <int ROWS, int M, int G, int GROUP, typename Row, typename Channel>
-__device__ __forceinline__ void store_swiglu(SwigluShared<ROWS> &sh, float (&h)[M][G][4], Row row,
-                                             Channel channel, const ExpertProduct &p, int row0,
-                                             int n, int nblk)
+template <int THREADS, int ROWS, int M, int G, int GROUP, typename Row, typename Channel>
+__device__ __forceinline__ void store_swiglu(SwigluShared<ROWS> &sh, float (&h)[M][G][4], int part,
+                                             Row row, Channel channel, const ExpertProduct &p,
+                                             int row0, int n, int nblk)
 {
-    const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
+    const int lane = threadIdx.x & (kWave - 1);
 #pragma unroll
     for (int m = 0; m < M; ++m) {
         uint32_t amax = 0;
@@ -170,7 +170,7 @@ __device__ __forceinline__ void store_swiglu(SwigluShared<ROWS> &sh, float (&h)[
                 amax = max(amax, __float_as_uint(h[m][g][k]) & 0x7FFFFFFFu);
 #pragma unroll
         for (int x = GROUP; x < kWave; x *= 2) amax = max(amax, (uint32_t)__shfl_xor((int)amax, x));
-        if (lane < GROUP) sh.amax[wave][row(m)] = amax;
+        if (lane < GROUP) sh.amax[part][row(m)] = amax;
     }
     __syncthreads();
 #pragma unroll
@@ -178,12 +178,12 @@ __device__ __forceinline__ void store_swiglu(SwigluShared<ROWS> &sh, float (&h)[
         const int r = row(m);
         uint32_t amax = 0;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) amax = max(amax, sh.amax[w][r]);
+        for (int w = 0; w < 4; ++w) amax = max(amax, sh.amax[w][r]);
         const float scale = block_scale(amax);
         // 2^-60 <= amax < inf: the quotients lie where div_by_rcp and the conversion are exact
         const bool plain = __any(amax < 0x21800000u || amax >= 0x7F800000u);
         const float y = 1.0f / scale;
-        uint32_t *code = reinterpret_cast<uint32_t *>(&sh.code[r][0]) + wave * 8;
+        uint32_t *code = reinterpret_cast<uint32_t *>(&sh.code[r][0]) + part * 8;
         if (plain) {
 #pragma unroll 1
             for (int g = 0; g < G; ++g) {
@@ -203,17 +203,17 @@ __device__ __forceinline__ void store_swiglu(SwigluShared<ROWS> &sh, float (&h)[
                     e4m3_pack4(div_by_rcp(h[m][g][0], scale, y), div_by_rcp(h[m][g][1], scale, y),
                                div_by_rcp(h[m][g][2], scale, y), div_by_rcp(h[m][g][3], scale, y));
         }
-        if (wave == 0 && lane < GROUP) sh.scale[r] = scale;
+        if (part == 0 && lane < GROUP) sh.scale[r] = scale;
     }
     __syncthreads();
     const int I = p.n / 2;
-    for (int i = threadIdx.x; i < ROWS * 8; i += kThreads) {
+    for (int i = threadIdx.x; i < ROWS * 8; i += THREADS) {
         const int r = i >> 3;
         if (r < n)
             *reinterpret_cast<u32x4 *>(p.h_q + (size_t)(row0 + r) * I + nblk * 128 + (i & 7) * 16) =
                 sh.code[r][i & 7];
     }
-    for (int r = threadIdx.x; r < n; r += kThreads)
+    for (int r = threadIdx.x; r < n; r += THREADS)
         p.h_scale[(size_t)(row0 + r) * (I / 128) + nblk] = sh.scale[r];
     __syncthreads();
 }
@@ -231,7 +231,7 @@ __global__ __launch_bounds__(kThreads) void expert_stream_kernel(ExpertProduct p
     const int nkb = p.H >> 7;
     const int n_tiles = SWIGLU ? p.n / kTileN : (p.n + kTileN - 1) / kTileN;
     const int ws_rows = (p.n + 127) >> 7;
-    const int total = build_table(table, p, MT * 16) * n_tiles;
+    const int total = build_table<kThreads>(table, p, MT * 16) * n_tiles;
     const TileRange mine = my_tiles(total);
     for (int tile = mine.first; tile < mine.end; tile += mine.step) {
         const Tile at = uniform(locate(table, p.E, tile, n_tiles, MT * 16));
@@ -321,8 +321,8 @@ __global__ __launch_bounds__(kThreads) void expert_stream_kernel(ExpertProduct p
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         h[mt][g][k] = swiglu(acc[g][mt][k], acc[g + 2][mt][k]);
-            store_swiglu<MT * 16, MT, 2, 16>(
-                sh, h, [&](int m) { return m * 16 + r16; },
+            store_swiglu<kThreads, MT * 16, MT, 2, 16>(
+                sh, h, wave, [&](int m) { return m * 16 + r16; },
                 [&](int g) { return g * 16 + g4 * 4; }, p, row0, n, nblk);
         } else {
 #pragma unroll
@@ -345,19 +345,19 @@ __global__ __launch_bounds__(kThreads) void expert_stream_kernel(ExpertProduct p
 }
 
 // Many rows per expert: tiles of 128 rows x 256 weight rows (SwiGLU: 128 gate and the same 128 up
-// rows), one workgroup of 4 wavefronts per CU that walks its tiles as one stream of blocks (128
-// channels of a tile each). Loads run two blocks ahead of LDS and three ahead of the products,
+// rows), one workgroup of 8 wavefronts per CU that walks its tiles as one stream of blocks (128
+// channels of a tile each); a wavefront multiplies 64 rows by 64 weight rows. Two wavefronts per
+// SIMD share its issue slots: alone, a wavefront's scaled sums, LDS reads and products queue up. Loads run two blocks ahead of LDS and three ahead of the products,
 // across tiles, so that neither a block nor a tile waits for memory. A load instruction covers 8
 // whole 128-byte row segments, 8 lanes a row: the vector cache takes one access per 128 bytes (in
 // the matrix instruction's lane order, 16 rows side by side, it took one per 16 bytes, and that
 // bounded the kernel: 1.35 ms for 65536 rows x 4096 x 4096). From registers a block goes to one of
-// two LDS buffers: the rows a quarter per wavefront, for all four to read; the weights each
-// wavefront's own 64 rows. The row scales of 16 blocks are staged together, one panel ahead.
-// One barrier per block.
+// two LDS buffers, an eighth per wavefront. The row scales of 16 blocks are staged together, one
+// panel ahead. One barrier per block.
+constexpr int kTileThreads = 512;
 constexpr int kTileM = 128;
-[[maybe_unused]] constexpr int kMT = kTileM / 32;
+[[maybe_unused]] constexpr int kMT = 2;     // tiles of 32 rows of a wavefront
 constexpr int kPanel = 16;         // blocks whose scales are staged together
-[[maybe_unused]] constexpr int kDepth = 4;          // buffers
 constexpr int kList = 256;         // tiles of a workgroup looked up together
 
 // A buffer of `bytes` from p: loads take a lane offset and a uniform one, and give 0 past the end.
@@ -403,7 +403,7 @@ constexpr int kList = 256;         // tiles of a workgroup looked up together
 template <bool SWIGLU>
 struct TileShared {
     u32x4 x[2][kTileM * 8];
-    u32x4 w[2][kWaves][64 * 8];
+    u32x4 w[2][kTileN * 8];
     float xscale[2][kPanel][kTileM + 1];
     float wscale[2][kPanel][2];
     int4 list[kList];
@@ -411,17 +411,18 @@ struct TileShared {
 };
 
 template <bool SWIGLU>
-__global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct p)
+__global__ __launch_bounds__(kTileThreads) void expert_tile_kernel(ExpertProduct p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)            // buffer descriptors exist on the device only
     __shared__ TileTable table;
     __shared__ TileShared<SWIGLU> sh;
     const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
+    const int wm = wave & 1, wn = wave >> 1;   // the wavefront's 64 rows and its weight rows
     const int r32 = lane & 31, half = lane >> 5;
     const int nkb = p.H >> 7;
     const int n_tiles = (p.n + kTileN - 1) / kTileN;
     const int ws_rows = (p.n + 127) >> 7;
-    const int total = build_table(table, p, kTileM) * n_tiles;
+    const int total = build_table<kTileThreads>(table, p, kTileM) * n_tiles;
     const TileRange mine = my_tiles(total);
     // Chunk c (16 bytes) of row r is kept at place c ^ swizzle(r) of the row's eight: the lanes that
     // LDS serves together (8 consecutive rows, and the same 16 further on) then touch all banks.
@@ -433,12 +434,13 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
     struct {
         int tile, kb;
         __amdgpu_buffer_rsrc_t w, x;
-        int woff[8], xoff[4];
+        int woff[4], xoff[2];
     } ld;
-    // first weight row of a wavefront's tile nt (SwiGLU: gate, up)
-    auto weight_row = [&](int nblk, int nt) {
-        return SWIGLU ? nt * (p.n / 2) + nblk * 128 + wave * 32
-                      : nblk * kTileN + wave * 64 + nt * 32;
+    // Weight row i of a tile: SwiGLU keeps 32 gate rows and the same 32 up rows together, so that
+    // every wavefront has a tile of each.
+    auto weight_row = [&](int nblk, int i) {
+        return SWIGLU ? ((i >> 5) & 1) * (p.n / 2) + nblk * 128 + (i >> 6) * 32 + (i & 31)
+                      : nblk * kTileN + i;
     };
     auto at = [&](int i) {
         const int4 v = sh.list[i];
@@ -452,34 +454,35 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
         ld.x = buffer(p.q + (size_t)t.row0 * p.H, (uint32_t)t.n * p.H);
         const int l = fresh(lane);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            ld.woff[j] = min(weight_row(t.nblk, j >> 2) + (j & 3) * 8 + (l >> 3), p.n - 1) * p.H +
+        for (int j = 0; j < 4; ++j)
+            ld.woff[j] = min(weight_row(t.nblk, wave * 32 + j * 8 + (l >> 3)), p.n - 1) * p.H +
                          (l & 7) * 16;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            ld.xoff[j] = min(wave * 32 + j * 8 + (l >> 3), t.n - 1) * p.H + (l & 7) * 16;
+        for (int j = 0; j < 2; ++j)
+            ld.xoff[j] = min(wave * 16 + j * 8 + (l >> 3), t.n - 1) * p.H + (l & 7) * 16;
     };
 
-    i32x4 wr[2][8], xr[2][4];                  // two blocks on their way to LDS
-    i32x4 wf[SWIGLU ? 1 : 2][2][4];            // the wavefront's weights of a block: [tile][chunk]
-    f32x16 acc[2][kMT], v[2][2];
-    i32x4 xf[2][4];
+    constexpr int kStage = SWIGLU ? 1 : 2;     // blocks in registers on their way to LDS
+    i32x4 wr[kStage][4], xr[kStage][2];
+    i32x4 wf[2][4];                            // the wavefront's weights of a block: [tile][chunk]
+    f32x16 acc[2][kMT];
+    constexpr int kXf = SWIGLU ? 1 : 2;
+    i32x4 xf[kXf][4];
     constexpr int kWs = SWIGLU ? 2 : 1;
-    float xs[2], s[2][kWs];                    // row scales read; times the weights' (gate; up)
-    constexpr int kPer = kTileM * kPanel / kThreads;
+    float xs[2];                               // row scales
+    constexpr int kPer = kTileM * kPanel / kTileThreads;
     float ps[kPer], pw = 0.0f;                 // the next panel on its way
     int par = 0;                               // the panel in use
 
-    auto load_w = [&](int d, int j) { wr[d][j] = buffer_load16(ld.w, ld.woff[j], ld.kb * 128); };
-    auto load_x = [&](int d, int j) { xr[d][j] = buffer_load16(ld.x, ld.xoff[j], ld.kb * 128); };
+    auto load_w = [&](int d, int j) { wr[d % kStage][j] = buffer_load16(ld.w, ld.woff[j], ld.kb * 128); };
+    auto load_x = [&](int d, int j) { xr[d % kStage][j] = buffer_load16(ld.x, ld.xoff[j], ld.kb * 128); };
     // the lane's place in LDS: its row of each 8, its chunk (rows 16 further on swap neighbours)
     const int put0 = (lane >> 3) * 8 + ((lane & 7) ^ (lane >> 3));
     auto put_w = [&](int d, int j) {
-        sh.w[d][wave][j * 64 + (put0 ^ ((j >> 1) & 1))] = __builtin_bit_cast(u32x4, wr[d][j]);
+        sh.w[d][wave * 256 + j * 64 + (put0 ^ (j >> 1))] = __builtin_bit_cast(u32x4, wr[d % kStage][j]);
     };
     auto put_x = [&](int d, int j) {
-        sh.x[d][wave * 256 + j * 64 + (put0 ^ ((j >> 1) & 1))] =
-            __builtin_bit_cast(u32x4, xr[d][j]);
+        sh.x[d][wave * 128 + j * 64 + (put0 ^ (wave & 1))] = __builtin_bit_cast(u32x4, xr[d % kStage][j]);
     };
     auto advance = [&](int tiles) {            // past the last block: that block again
         if (++ld.kb == nkb) {
@@ -492,7 +495,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
         const int l = fresh(wave * kWave + lane);
         const float *src = p.scale + (size_t)t.row0 * nkb + min(kb0 + (l & 15), nkb - 1);
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) ps[k] = src[(size_t)min(k * 16 + (l >> 4), t.n - 1) * nkb];
+        for (int k = 0; k < kPer; ++k) ps[k] = src[(size_t)min(k * 32 + (l >> 4), t.n - 1) * nkb];
         const int blk = SWIGLU ? ((l >> 4) & 1) * (p.n >> 8) + t.nblk
                                : min(t.nblk * 2 + ((l >> 4) & 1), ws_rows - 1);
         pw = p.w_scale[((size_t)t.e * ws_rows + blk) * nkb + min(kb0 + (l & 15), nkb - 1)];
@@ -500,49 +503,36 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
     auto panel_store = [&](int to) {
         const int l = fresh(wave * kWave + lane);
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) sh.xscale[to][l & 15][k * 16 + (l >> 4)] = ps[k];
+        for (int k = 0; k < kPer; ++k) sh.xscale[to][l & 15][k * 32 + (l >> 4)] = ps[k];
         if (l < 32) sh.wscale[to][l & 15][l >> 4] = pw;
     };
     auto read_row = [&](int d, int mt) {       // the lane's chunks of row tile mt
-        const i32x4 *x = reinterpret_cast<const i32x4 *>(sh.x[d]) + mt * 256 + row_at;
+        const i32x4 *x = reinterpret_cast<const i32x4 *>(sh.x[d]) + (wm * kMT + mt) * 256 + row_at;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) xf[mt & 1][j] = x[(2 * j + half) ^ row_swizzle];
+        for (int j = 0; j < 4; ++j) xf[mt % kXf][j] = x[(2 * j + half) ^ row_swizzle];
     };
     auto read_w = [&](int d, int nt) {         // and of the wavefront's weight tile nt
-        const i32x4 *w = reinterpret_cast<const i32x4 *>(sh.w[d][wave]) + nt * 256 + row_at;
+        const i32x4 *w = reinterpret_cast<const i32x4 *>(sh.w[d]) + (wn * 2 + nt) * 256 + row_at;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) wf[SWIGLU ? 0 : d][nt][j] = w[(2 * j + half) ^ row_swizzle];
+        for (int j = 0; j < 4; ++j) wf[nt][j] = w[(2 * j + half) ^ row_swizzle];
     };
     float ws[kWs];
     auto read_ws = [&](float (&to)[kWs], int b) {
-        to[0] = sh.wscale[par][b][SWIGLU ? 0 : wave >> 1];
+        to[0] = sh.wscale[par][b][SWIGLU ? 0 : wn >> 1];
         if constexpr (SWIGLU) to[1] = sh.wscale[par][b][1];
-    };
-    auto sum = [&](int mt, int nt, int part) { // a quarter of the products of row tile mt
-#pragma unroll
-        for (int i = part * 4; i < part * 4 + 4; ++i)
-            acc[nt][mt][i] = __builtin_fmaf(s[mt & 1][SWIGLU ? nt : 0], v[mt & 1][nt][i],
-                                            acc[nt][mt][i]);
     };
     auto clear = [&]() {
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
+        for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-                for (int mt = 0; mt < kMT; ++mt) acc[nt][mt][i] = 0.0f;
-                v[(kMT - 1) & 1][nt][i] = 0.0f;          // no block before the first
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kWs; ++i) s[(kMT - 1) & 1][i] = 0.0f;
+                for (int i = 0; i < 16; ++i) acc[nt][mt][i] = 0.0f;
     };
-    // One block, in LDS buffer d. In each of its 4 regions one tile of 32 rows is multiplied, the one
-    // before summed, and the next read from LDS (the last one from the next block's buffer); the
-    // fences keep the regions apart. The next block goes to LDS before the barrier, and the one
-    // three ahead takes its registers.
+    // One block, in LDS buffer d, in 2 regions of one tile of 32 rows each, kept apart by fences. The
+    // next block goes to LDS before the barrier, and the one three ahead takes its registers.
     auto step = [&](int d, int tile, int kb, int tiles) {
-        const int dn = d ^ 1, dw = SWIGLU ? 0 : d;
+        const int dn = d ^ 1;
         if ((kb & (kPanel - 1)) == 0) {
             if (kb + kPanel < nkb) panel_load(tile, kb + kPanel);
             else if (tile + 1 < tiles) panel_load(tile + 1, 0);
@@ -550,10 +540,18 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
         const int b_next = kb == nkb - 1 ? 0 : (kb + 1) & (kPanel - 1);
         float ws_next[kWs];
         bf16x8 wb[SWIGLU ? 2 : 1][8];
+        read_w(d, 0);
+        read_w(d, 1);
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt) {
-            const int to = mt + 1, before = (mt + kMT - 1) & (kMT - 1);
-            if (to == kMT) {
+            // the row tile to read: SwiGLU, short of registers, this one; else the one after, the
+            // last of them the next block's
+            const int to = SWIGLU ? mt : mt + 1;
+            if constexpr (SWIGLU) {
+                read_row(d, mt);
+                xs[mt] = sh.xscale[par][kb & (kPanel - 1)][(wm * kMT + mt) * 32 + r32];
+            }
+            if (mt == kMT - 1) {
                 if (b_next == 0) {
                     par ^= 1;
                     panel_store(par);
@@ -561,68 +559,55 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
                 meet();
                 read_ws(ws_next, b_next);
             }
-            read_row(to < kMT ? d : dn, to & (kMT - 1));
-            const float s_in =
-                sh.xscale[par][to < kMT ? kb & (kPanel - 1) : b_next][(to & (kMT - 1)) * 32 + r32];
-            if (mt < 3) {                      // 4 + 8 pieces over three regions
-#pragma unroll
-                for (int j = mt * 4; j < mt * 4 + 4; ++j) {
-                    if (j < 4) {
-                        put_x(dn, j);
-                        load_x(dn, j);
-                    } else {
-                        put_w(dn, j - 4);
-                        load_w(dn, j - 4);
-                    }
-                }
-            } else if constexpr (!SWIGLU) {
-                read_w(dn, 0);
-                read_w(dn, 1);
+            if constexpr (!SWIGLU) {
+                read_row(to < kMT ? d : dn, to & (kMT - 1));
+                xs[to & 1] = sh.xscale[par][to < kMT ? kb & (kPanel - 1) : b_next]
+                                      [(wm * kMT + (to & (kMT - 1))) * 32 + r32];
             }
+            if (mt < kMT - 1) {
 #pragma unroll
-            for (int i = 0; i < kWs; ++i) s[mt & 1][i] = xs[mt & 1] * ws[i];
-            if constexpr (SWIGLU) {
-                if (to == kMT) {               // wb holds this block's
-                    read_w(dn, 0);
-                    read_w(dn, 1);
+                for (int j = 0; j < 2; ++j) {
+                    put_x(dn, j);
+                    load_x(dn, j);
                 }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    put_w(dn, j);
+                    load_w(dn, j);
+                }
+            }
+            f32x16 v[2] = {};
+            if constexpr (SWIGLU) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const bf16x8 xb = bf16_of_e4m3(xf[mt & 1][j >> 1][(j & 1) * 2],
-                                                   xf[mt & 1][j >> 1][(j & 1) * 2 + 1]);
+                    const bf16x8 xb = bf16_of_e4m3(xf[0][j >> 1][(j & 1) * 2],
+                                                   xf[0][j >> 1][(j & 1) * 2 + 1]);
 #pragma unroll
                     for (int nt = 0; nt < 2; ++nt) {
                         if (mt == 0)
-                            wb[nt][j] = bf16_of_e4m3(wf[0][nt][j >> 1][(j & 1) * 2],
-                                                     wf[0][nt][j >> 1][(j & 1) * 2 + 1]);
-                        v[mt & 1][nt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                            wb[nt][j], xb, j == 0 ? f32x16{} : v[mt & 1][nt], 0, 0, 0);
+                            wb[nt][j] = bf16_of_e4m3(wf[nt][j >> 1][(j & 1) * 2],
+                                                     wf[nt][j >> 1][(j & 1) * 2 + 1]);
+                        v[nt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[nt][j], xb, v[nt], 0, 0,
+                                                                        0);
                     }
-                    sum(before, j >> 2, j & 3);
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        v[mt & 1][nt] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                            join(wf[dw][nt][2 * j], wf[dw][nt][2 * j + 1]),
-                            join(xf[mt & 1][2 * j], xf[mt & 1][2 * j + 1]),
-                            j == 0 ? f32x16{} : v[mt & 1][nt], 0, 0, 0, 0, 0, 0);
-                        sum(before, j, nt * 2);
-                        sum(before, j, nt * 2 + 1);
-                    }
+                    for (int nt = 0; nt < 2; ++nt)
+                        v[nt] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                            join(wf[nt][2 * j], wf[nt][2 * j + 1]),
+                            join(xf[mt % kXf][2 * j], xf[mt % kXf][2 * j + 1]), v[nt], 0, 0, 0, 0, 0,
+                            0);
             }
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) asm volatile("" : "+v"(acc[nt][before]));
-            xs[to & 1] = s_in;
-            if constexpr (!SWIGLU) {
-                __builtin_amdgcn_sched_group_barrier(0x100, 5, 0);          // LDS reads
+            for (int nt = 0; nt < 2; ++nt) {
+                const float s = xs[mt & 1] * ws[SWIGLU ? nt : 0];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // a product
-                    __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);      // eight sums
-                }
+                for (int i = 0; i < 16; ++i)
+                    acc[nt][mt][i] = __builtin_fmaf(s, v[nt][i], acc[nt][mt][i]);
+                asm volatile("" : "+v"(acc[nt][mt]));    // summed here, not later
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -630,9 +615,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
         for (int i = 0; i < kWs; ++i) ws[i] = ws_next[i];
         advance(tiles);
     };
-    auto finish = [&](int tile) {              // the tile's last sums and its output
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum(kMT - 1, i >> 2, i & 3);
+    auto finish = [&](int tile) {              // the tile's output
         const Tile t = at(tile);
         const int l = fresh(lane);
         // element i of a lane is channel (i >> 2) * 8 + half * 4 + (i & 3) of row lane & 31
@@ -642,19 +625,19 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
             for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) h[mt][i >> 2][i & 3] = swiglu(acc[0][mt][i], acc[1][mt][i]);
-            store_swiglu<kTileM, kMT, 4, 32>(
-                sh.h, h, [&](int m) { return m * 32 + (l & 31); },
+            store_swiglu<kTileThreads, kTileM, kMT, 4, 32>(
+                sh.h, h, wn, [&](int m) { return (wm * kMT + m) * 32 + (l & 31); },
                 [&](int g) { return g * 8 + (l >> 5) * 4; }, p, t.row0, t.n, t.nblk);
         } else {
 #pragma unroll
             for (int mt = 0; mt < kMT; ++mt) {
-                const int r = mt * 32 + (l & 31);
+                const int r = (wm * kMT + mt) * 32 + (l & 31);
                 uint16_t *y = p.y + (size_t)(t.row0 + r) * p.n;
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        const int c = weight_row(t.nblk, nt) + g * 8 + (l >> 5) * 4;
+                        const int c = weight_row(t.nblk, wn * 64 + nt * 32) + g * 8 + (l >> 5) * 4;
                         // n % 8 == 0: the four channels together
                         if (r < t.n && c < p.n)
                             *reinterpret_cast<uint2 *>(y + c) =
@@ -671,7 +654,8 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
     for (int first = mine.first; first < mine.end; first += kList * mine.step) {
         const int tiles = min((mine.end - first + mine.step - 1) / mine.step, kList);
         if ((int)threadIdx.x < tiles) {
-            const Tile t = locate(table, p.E, first + threadIdx.x * mine.step, n_tiles, kTileM);
+            const int i = fresh(threadIdx.x);
+            const Tile t = locate(table, p.E, first + i * mine.step, fresh(n_tiles), kTileM);
             sh.list[threadIdx.x] = int4{t.e, t.row0, t.n, t.nblk};
         }
         __syncthreads();
@@ -680,26 +664,24 @@ __global__ __launch_bounds__(kThreads, 1) void expert_tile_kernel(ExpertProduct 
         panel_load(0, 0);
         auto load = [&](int d) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) load_x(d, j);
+            for (int j = 0; j < 2; ++j) load_x(d, j);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) load_w(d, j);
+            for (int j = 0; j < 4; ++j) load_w(d, j);
             advance(tiles);
         };
         load(0);
-        load(1);
+        if constexpr (kStage == 2) load(1);
         panel_store(0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) put_x(0, j);
+        for (int j = 0; j < 2; ++j) put_x(0, j);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) put_w(0, j);
+        for (int j = 0; j < 4; ++j) put_w(0, j);
         load(0);
         meet();
         read_ws(ws, 0);
         clear();
-        read_w(0, 0);
-        read_w(0, 1);
-        read_row(0, 0);
-        xs[0] = sh.xscale[0][0][r32];
+        if constexpr (!SWIGLU) read_row(0, 0);
+        xs[0] = sh.xscale[0][0][wm * kMT * 32 + r32];
         __builtin_amdgcn_sched_barrier(0);
         int tile = 0, kb = 0;
         auto next = [&](int d) {               // a block; false after the last one
@@ -725,7 +707,7 @@ hipError_t launch_product(const ExpertProduct &p, hipStream_t stream)
     const int64_t tiles = ((int64_t)p.pairs / 64 + p.E) * n_tiles;
     const int grid = (int)(tiles < 512 ? (tiles + 7) / 8 * 8 : 512);
     if (p.pairs / p.E >= 32)
-        return launch(expert_tile_kernel<SWIGLU>, dim3(grid < 256 ? grid : 256), dim3(kThreads), 0,
+        return launch(expert_tile_kernel<SWIGLU>, dim3(grid < 256 ? grid : 256), dim3(kTileThreads), 0,
                       stream, p);
     return launch(expert_stream_kernel<4, SWIGLU, 1>, dim3(grid), dim3(kThreads), 0, stream, p);
 }
