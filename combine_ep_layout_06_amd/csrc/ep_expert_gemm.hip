@@ -143,10 +143,24 @@ __device__ __forceinline__ uint32_t encode4_any(const float (&h)[4], float scale
     return v;
 }
 
+// bf16 pairs of four values, NaN as 0x7FC0.
+__device__ __forceinline__ uint2 bf16_pairs(float a, float b, float c, float d)
+{
+    const float v[4] = {a, b, c, d};
+    bf16x2 lo = {(__bf16)v[0], (__bf16)v[1]}, hi = {(__bf16)v[2], (__bf16)v[3]};
+    uint2 o{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+    if (__builtin_isunordered(v[0], v[1]) || __builtin_isunordered(v[2], v[3])) {
+        o.x = bf16_rne(v[0]) | (bf16_rne(v[1]) << 16);
+        o.y = bf16_rne(v[2]) | (bf16_rne(v[3]) << 16);
+    }
+    return o;
+}
+
 // The SwiGLU epilogue of one tile of ROWS rows x 128 channels of h: the block amax meets in LDS, the
 // codes go out through LDS in whole rows. A wavefront holds quarter `part` of the 128 channels, a
 // lane G groups of 4 consecutive ones (group g at channel part * 32 + channel(g)) of M rows
-// (row(m)), GROUP lanes apart from the other channels of the row.
+// (row(m)), GROUP lanes apart from the other channels of the row; one that holds none only helps
+// to store.
 template <int ROWS>
 struct SwigluShared {
     uint32_t amax[4][ROWS];
@@ -155,8 +169,8 @@ struct SwigluShared {
 };
 
 template <int THREADS, int ROWS, int M, int G, int GROUP, typename Row, typename Channel>
-__device__ __forceinline__ void store_swiglu(SwigluShared<ROWS> &sh, float (&h)[M][G][4], int part,
-                                             Row row, Channel channel, const ExpertProduct &p,
+__device__ __forceinline__ void store_swiglu(SwigluShared<ROWS> &sh, float (&h)[M][G][4],
+                                             bool holds, int part, Row row, Channel channel, const ExpertProduct &p,
                                              int row0, int n, int nblk)
 {
     const int lane = threadIdx.x & (kWave - 1);
@@ -170,11 +184,12 @@ __device__ __forceinline__ void store_swiglu(SwigluShared<ROWS> &sh, float (&h)[
                 amax = max(amax, __float_as_uint(h[m][g][k]) & 0x7FFFFFFFu);
 #pragma unroll
         for (int x = GROUP; x < kWave; x *= 2) amax = max(amax, (uint32_t)__shfl_xor((int)amax, x));
-        if (lane < GROUP) sh.amax[part][row(m)] = amax;
+        if (holds && lane < GROUP) sh.amax[part][row(m)] = amax;
     }
     __syncthreads();
 #pragma unroll
     for (int m = 0; m < M; ++m) {
+        if (!holds) break;
         const int r = row(m);
         uint32_t amax = 0;
 #pragma unroll
@@ -218,20 +233,25 @@ __device__ __forceinline__ void store_swiglu(SwigluShared<ROWS> &sh, float (&h)[
     __syncthreads();
 }
 
-// Few rows per expert: every operand straight from global memory to registers, no barrier in the
-// product. MT tiles of 16 rows; a wavefront takes 4 tiles of 16 weight rows (gemm: 64 consecutive
-// rows; SwiGLU: 32 gate rows and the same 32 up rows) and the whole of H, D blocks in flight.
-template <int MT, bool SWIGLU, int D>
-__global__ __launch_bounds__(kThreads) void expert_stream_kernel(ExpertProduct p)
+// Few rows per expert, where reading the weights bounds the product: every operand straight from
+// global memory to registers, no barrier in the product. MT tiles of 16 rows; a wavefront takes 4
+// tiles of 16 weight rows (gemm: 64 consecutive rows; SwiGLU: 32 gate rows and the same 32 up rows),
+// D blocks in flight. KS wavefronts share the same weight rows, each every KS-th block, and their
+// sums meet in LDS in order: with few tiles that keeps more of the chip's memory busy.
+template <int MT, bool SWIGLU, int D, int KS>
+__global__ __launch_bounds__(kThreads *KS) void expert_stream_kernel(ExpertProduct p)
 {
+    constexpr int kStreamThreads = kThreads * KS;
     __shared__ TileTable table;
     __shared__ SwigluShared<SWIGLU ? MT * 16 : 1> sh;
-    const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
+    __shared__ f32x4 parts[KS > 1 ? KS - 1 : 1][KS > 1 ? 4 : 1][KS > 1 ? 4 * MT : 1][kWave];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = uniform(threadIdx.x / kWave) & 3, ks = uniform(threadIdx.x / kThreads);
     const int r16 = lane & 15, g4 = lane >> 4;
     const int nkb = p.H >> 7;
     const int n_tiles = SWIGLU ? p.n / kTileN : (p.n + kTileN - 1) / kTileN;
     const int ws_rows = (p.n + 127) >> 7;
-    const int total = build_table<kThreads>(table, p, MT * 16) * n_tiles;
+    const int total = build_table<kStreamThreads>(table, p, MT * 16) * n_tiles;
     const TileRange mine = my_tiles(total);
     for (int tile = mine.first; tile < mine.end; tile += mine.step) {
         const Tile at = uniform(locate(table, p.E, tile, n_tiles, MT * 16));
@@ -282,34 +302,48 @@ __global__ __launch_bounds__(kThreads) void expert_stream_kernel(ExpertProduct p
         for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) acc[nt][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (ks < nkb) {
 #pragma unroll
-        for (int d = 0; d < D; ++d) load(d, min(d, nkb - 1));
-        for (int kb = 0; kb < nkb; kb += D) {
+            for (int d = 0; d < D; ++d) load(d, min(ks + d * KS, nkb - 1));
+            for (int kb = ks; kb < nkb; kb += D * KS) {
 #pragma unroll
-            for (int d = 0; d < D; ++d) {
-                if (kb + d < nkb) {
-                    Bf16Block xb[SWIGLU ? MT : 1];
-                    if constexpr (SWIGLU)
+                for (int d = 0; d < D; ++d) {
+                    if (kb + d * KS < nkb) {
+                        Bf16Block xb[SWIGLU ? MT : 1];
+                        if constexpr (SWIGLU)
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) xb[mt] = bf16_block(xf[d][mt]);
+                            for (int mt = 0; mt < MT; ++mt) xb[mt] = bf16_block(xf[d][mt]);
 #pragma unroll
-                    for (int nt = 0; nt < 4; ++nt) {
-                        Bf16Block wb;
-                        if constexpr (SWIGLU) wb = bf16_block(wf[d][nt]);
+                        for (int nt = 0; nt < 4; ++nt) {
+                            Bf16Block wb;
+                            if constexpr (SWIGLU) wb = bf16_block(wf[d][nt]);
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            f32x4 v;
-                            if constexpr (SWIGLU) v = mfma_exact(wb, xb[mt]);
-                            else v = mfma_e4m3(wf[d][nt], xf[d][mt]);
-                            const float s = sx[d][mt] * sw[d][nt >> 1];
+                            for (int mt = 0; mt < MT; ++mt) {
+                                f32x4 v;
+                                if constexpr (SWIGLU) v = mfma_exact(wb, xb[mt]);
+                                else v = mfma_e4m3(wf[d][nt], xf[d][mt]);
+                                const float s = sx[d][mt] * sw[d][nt >> 1];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                acc[nt][mt][k] = __builtin_fmaf(s, v[k], acc[nt][mt][k]);
+                                for (int k = 0; k < 4; ++k)
+                                    acc[nt][mt][k] = __builtin_fmaf(s, v[k], acc[nt][mt][k]);
+                            }
                         }
                     }
+                    load(d, min(kb + (d + D) * KS, nkb - 1));
                 }
-                load(d, min(kb + d + D, nkb - 1));
             }
+        }
+        if constexpr (KS > 1) {
+            if (ks > 0)
+#pragma unroll
+                for (int i = 0; i < 4 * MT; ++i) parts[ks - 1][wave][i][lane] = acc[i / MT][i % MT];
+            __syncthreads();
+            if (ks == 0)
+#pragma unroll
+                for (int i = 0; i < 4 * MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < KS - 1; ++j) acc[i / MT][i % MT] += parts[j][wave][i][lane];
+            __syncthreads();
         }
 
         if constexpr (SWIGLU) {
@@ -321,10 +355,10 @@ __global__ __launch_bounds__(kThreads) void expert_stream_kernel(ExpertProduct p
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         h[mt][g][k] = swiglu(acc[g][mt][k], acc[g + 2][mt][k]);
-            store_swiglu<kThreads, MT * 16, MT, 2, 16>(
-                sh, h, wave, [&](int m) { return m * 16 + r16; },
+            store_swiglu<kStreamThreads, MT * 16, MT, 2, 16>(
+                sh, h, ks == 0, wave, [&](int m) { return m * 16 + r16; },
                 [&](int g) { return g * 16 + g4 * 4; }, p, row0, n, nblk);
-        } else {
+        } else if (ks == 0) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 const int r = mt * 16 + r16;
@@ -332,12 +366,10 @@ __global__ __launch_bounds__(kThreads) void expert_stream_kernel(ExpertProduct p
 #pragma unroll
                 for (int nt = 0; nt < 4; ++nt) {
                     const int c = wrow[nt] + g4 * 4;
-                    if (r < n && c < p.n) {          // n % 8 == 0: the four channels together
-                        uint2 o;
-                        o.x = bf16_rne(acc[nt][mt][0]) | (bf16_rne(acc[nt][mt][1]) << 16);
-                        o.y = bf16_rne(acc[nt][mt][2]) | (bf16_rne(acc[nt][mt][3]) << 16);
-                        *reinterpret_cast<uint2 *>(y + c) = o;
-                    }
+                    // n % 8 == 0: the four channels together
+                    if (r < n && c < p.n)
+                        *reinterpret_cast<uint2 *>(y + c) = bf16_pairs(
+                            acc[nt][mt][0], acc[nt][mt][1], acc[nt][mt][2], acc[nt][mt][3]);
                 }
             }
         }
@@ -385,19 +417,6 @@ constexpr int kList = 256;         // tiles of a workgroup looked up together
     __builtin_amdgcn_s_waitcnt(0xC07F);        // lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
-// bf16 pairs of four values, NaN as 0x7FC0.
-[[maybe_unused]] __device__ __forceinline__ uint2 bf16_pairs(float a, float b, float c, float d)
-{
-    const float v[4] = {a, b, c, d};
-    bf16x2 lo = {(__bf16)v[0], (__bf16)v[1]}, hi = {(__bf16)v[2], (__bf16)v[3]};
-    uint2 o{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
-    if (__builtin_isunordered(v[0], v[1]) || __builtin_isunordered(v[2], v[3])) {
-        o.x = bf16_rne(v[0]) | (bf16_rne(v[1]) << 16);
-        o.y = bf16_rne(v[2]) | (bf16_rne(v[3]) << 16);
-    }
-    return o;
 }
 
 template <bool SWIGLU>
@@ -626,7 +645,7 @@ __global__ __launch_bounds__(kTileThreads) void expert_tile_kernel(ExpertProduct
 #pragma unroll
                 for (int i = 0; i < 16; ++i) h[mt][i >> 2][i & 3] = swiglu(acc[0][mt][i], acc[1][mt][i]);
             store_swiglu<kTileThreads, kTileM, kMT, 4, 32>(
-                sh.h, h, wn, [&](int m) { return (wm * kMT + m) * 32 + (l & 31); },
+                sh.h, h, true, wn, [&](int m) { return (wm * kMT + m) * 32 + (l & 31); },
                 [&](int g) { return g * 8 + (l >> 5) * 4; }, p, t.row0, t.n, t.nblk);
         } else {
 #pragma unroll
@@ -699,17 +718,44 @@ __global__ __launch_bounds__(kTileThreads) void expert_tile_kernel(ExpertProduct
 #endif
 }
 
+#ifndef EP_EXPERT_MT1
+#define EP_EXPERT_MT1 12
+#endif
+#ifndef EP_EXPERT_MT2
+#define EP_EXPERT_MT2 24
+#endif
+#ifndef EP_EXPERT_TILE
+#define EP_EXPERT_TILE 40
+#endif
+#ifndef EP_EXPERT_KS
+#define EP_EXPERT_KS 512
+#endif
+#ifndef EP_EXPERT_D1
+#define EP_EXPERT_D1 1
+#endif
 template <bool SWIGLU>
 hipError_t launch_product(const ExpertProduct &p, hipStream_t stream)
 {
     if (p.pairs == 0 || (p.offset && p.rows == 0)) return hipSuccess;
     const int64_t n_tiles = (p.n + kTileN - 1) / kTileN;
-    const int64_t tiles = ((int64_t)p.pairs / 64 + p.E) * n_tiles;
-    const int grid = (int)(tiles < 512 ? (tiles + 7) / 8 * 8 : 512);
-    if (p.pairs / p.E >= 32)
-        return launch(expert_tile_kernel<SWIGLU>, dim3(grid < 256 ? grid : 256), dim3(kTileThreads), 0,
+    const int mean = (int)(((int64_t)p.pairs + p.E - 1) / p.E);
+    // the grid: at most `most` workgroups, no more than there can be tiles of `bm` rows
+    auto grid = [&](int bm, int64_t most) {
+        const int64_t experts = p.pairs < p.E ? p.pairs : p.E;
+        const int64_t tiles = (p.pairs / bm + experts) * n_tiles;
+        return dim3((unsigned)(tiles < most ? (tiles + 7) / 8 * 8 : most));
+    };
+    const dim3 block(kThreads);
+    if (mean >= EP_EXPERT_TILE)
+        return launch(expert_tile_kernel<SWIGLU>, grid(kTileM, 256), dim3(kTileThreads), 0, stream, p);
+    if (mean > EP_EXPERT_MT2)
+        return launch(expert_stream_kernel<4, SWIGLU, 1, 1>, grid(64, 512), block, 0, stream, p);
+    if (mean > EP_EXPERT_MT1)
+        return launch(expert_stream_kernel<2, SWIGLU, 1, 1>, grid(32, 512), block, 0, stream, p);
+    if (grid(16, 1 << 20).x < EP_EXPERT_KS)
+        return launch(expert_stream_kernel<1, SWIGLU, 1, 4>, grid(16, 512), dim3(4 * kThreads), 0,
                       stream, p);
-    return launch(expert_stream_kernel<4, SWIGLU, 1>, dim3(grid), dim3(kThreads), 0, stream, p);
+    return launch(expert_stream_kernel<1, SWIGLU, EP_EXPERT_D1, 1>, grid(16, 1024), block, 0, stream, p);
 }
 
 }  // namespace
