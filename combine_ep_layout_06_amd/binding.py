@@ -977,10 +977,11 @@ def ep_expert_swiglu_fp8_packed(recv_q: torch.Tensor, recv_scale: torch.Tensor,
           packed_offset, w_q, w_scale, h_q, h_scale, stream=stream)
     return h_q, h_scale
 
-def moe_layer_workspace_bytes(T: int, K: int, I: int) -> int:
-    """Bytes of workspace a whole-layer call needs for T tokens, top-K, intermediate size I."""
+def moe_layer_workspace_bytes(T: int, K: int, H: int, I: int) -> int:
+    """Bytes of workspace a whole-layer call needs for T tokens of H channels, top-K,
+    intermediate size I."""
     return int(load_library().ep_moe_layer_workspace_bytes(
-        ctypes.byref(_shape(T, 1, 1, K, 1, 1)), I))
+        ctypes.byref(_shape(T, H, 1, K, 1, 1)), I))
 
 
 def _moe_layer(name, x, topk_idx, topk_w, w13, w2, dtype, out, workspace, stream):
@@ -1001,7 +1002,8 @@ def _moe_layer(name, x, topk_idx, topk_w, w13, w2, dtype, out, workspace, stream
     out = torch.empty((T, H), dtype=_bf16(x), device=dev) if out is None else out
     _need(out, "out", _bf16(out), T * H, dev)
     if workspace is None:
-        workspace = torch.empty(max(4 * T * K * I, 16), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(max(moe_layer_workspace_bytes(T, K, H, I), 16), dtype=torch.uint8,
+                                device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace: must be a contiguous tensor on the tokens' device")
     return (_shape(T, H, E, K, 1, 1), I, out, workspace,
@@ -1010,11 +1012,11 @@ def _moe_layer(name, x, topk_idx, topk_w, w13, w2, dtype, out, workspace, stream
 
 def ep_moe_layer(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
                  w13: torch.Tensor, w2: torch.Tensor, *, out=None, workspace=None, stream=None):
-    """A whole MoE layer for a few tokens (T * K <= EP_MOE_MAX_PAIRS), in two launches:
+    """A whole MoE layer for a few tokens (T * K <= EP_MOE_MAX_PAIRS), in two or three launches:
     ``out[t] = sum_j topk_w[t, j] * W2[e_j] (silu(Wg[e_j] x[t]) * (Wu[e_j] x[t]))`` with bf16
     weights ``w13`` [E, 2I, H] (gate rows, then up rows) and ``w2`` [E, H, I]; ``x`` and ``out``
     [T, H] bf16. Pairs whose id is not a valid expert add nothing. ``workspace``: a device tensor
-    of at least moe_layer_workspace_bytes(T, K, I) bytes (allocated here if not given)."""
+    of at least moe_layer_workspace_bytes(T, K, H, I) bytes (allocated here if not given)."""
     sh, I, out, ws, nbytes = _moe_layer("ep_moe_layer", x, topk_idx, topk_w, w13, w2, _bf16, out,
                                         workspace, stream)
     _call("ep_moe_layer", sh, I, x, topk_idx, topk_w, w13, w2, out, ws, nbytes, stream=stream)

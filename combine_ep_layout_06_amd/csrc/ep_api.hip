@@ -817,8 +817,8 @@ int ep_expert_swiglu_fp8_packed(const ep_shape_t *shape, int32_t rows, int32_t I
 
 size_t ep_moe_layer_workspace_bytes(const ep_shape_t *shape, int32_t I)
 {
-    if (!shape || shape->T < 0 || shape->K < 1 || I < 1) return 0;
-    return (size_t)4 * shape->T * shape->K * I;
+    if (!shape || shape->T < 0 || shape->K < 1 || shape->H < 1 || I < 1) return 0;
+    return ep::moe_workspace_bytes((int64_t)shape->T * shape->K, I, shape->H);
 }
 
 namespace {
@@ -840,8 +840,8 @@ int moe_layer(const ep_shape_t *shape, int32_t I, ep::MoeLayer p, bool fp8, void
     if ((int64_t)2 * I * shape->H > (int64_t)1 << 29)
         return fail(EP_ERR_UNSUPPORTED, f + ": 2*I*H exceeds 2^29");
     if ((int64_t)shape->T * shape->H > (int64_t)1 << 30 ||
-        (int64_t)shape->T * shape->K * I > (int64_t)1 << 30)
-        return fail(EP_ERR_UNSUPPORTED, f + ": T*H or T*K*I exceeds 2^30");
+        (int64_t)shape->T * shape->K * I > (int64_t)1 << 29)
+        return fail(EP_ERR_UNSUPPORTED, f + ": T*H exceeds 2^30 or T*K*I 2^29");
     if (shape->T == 0) return hip_status(hipSuccess, fn);
     if (!p.x || !p.idx || !p.topk_w || !p.w13 || !p.w2 || !p.out ||
         (fp8 && (!p.w13_scale || !p.w2_scale)))
@@ -864,8 +864,13 @@ int moe_layer(const ep_shape_t *shape, int32_t I, ep::MoeLayer p, bool fp8, void
     p.K = shape->K;
     p.H = shape->H;
     p.I = I;
-    p.h_hi = static_cast<uint16_t *>(workspace);
-    p.h_lo = p.h_hi + (size_t)shape->T * shape->K * I;
+    const int pairs = shape->T * shape->K;
+    p.h = static_cast<uint16_t *>(workspace);
+    if (pairs > ep::kMoeSmallPairs) {
+        p.y = reinterpret_cast<float *>(p.h + (size_t)2 * pairs * I);
+        p.named = reinterpret_cast<int32_t *>(p.y + (size_t)pairs * shape->H);
+        p.order = p.named + 4 + (size_t)4 * pairs;
+    }
     return hip_status(ep::launch_moe_layer(p, fp8, stream), fn);
 }
 

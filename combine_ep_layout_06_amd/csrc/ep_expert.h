@@ -36,12 +36,25 @@ struct MoeLayer {
     const float *w13_scale;   // [E][2I/128][H/128]
     const void *w2;           // [E][H][I]
     const float *w2_scale;    // [E][H/128][I/128]
-    uint16_t *h_hi, *h_lo;    // workspace: [T*K][I] each, h = hi + lo
+    uint16_t *h;              // workspace: T*K rows of h, see ep_moe_layer.hip
+    float *y;                 // workspace: [T*K][H], above kMoeSmallPairs pairs
+    int32_t *named;           // workspace: number of named experts, then {expert, first row, rows, 0} each
+    int32_t *order;           // workspace: pair of each row
     uint16_t *out;            // [T][H] bf16
     int T, E, K, H, I;
 };
 
 constexpr int kMoePairs = EP_MOE_MAX_PAIRS;
+
+// Up to here the down kernel keeps every pair's y in LDS and needs no list of the named experts.
+constexpr int kMoeSmallPairs = 64;
+
+// Bytes of the layer's workspace: h in two bf16 parts and, above kMoeSmallPairs, y and the lists (4
+// words per named expert and one per pair; there are at most as many named experts as pairs).
+inline size_t moe_workspace_bytes(int64_t pairs, int64_t I, int64_t H)
+{
+    return (size_t)(pairs * I * 4 + (pairs > kMoeSmallPairs ? pairs * (H + 5) * 4 + 16 : 0));
+}
 
 hipError_t launch_moe_layer(const MoeLayer &p, bool fp8, hipStream_t stream);
 

@@ -1,7 +1,10 @@
-// A whole MoE layer for a few tokens on gfx950, in two launches with no receive buffer:
+// A whole MoE layer for a few tokens on gfx950, in two or three launches with no receive buffer:
 //
 //   moe_up_kernel    h[i] = silu(Wg[e] x[t]) * (Wu[e] x[t]) for each pair i = t*K + j, e = idx[i]
-//   moe_down_kernel  out[t] = bf16( sum_j w[i] * W2[e] h[i] )
+//   moe_small_down_kernel  out[t] = bf16( sum_j w[i] * W2[e] h[i] )
+// or, above kMoeSmallPairs pairs,
+//   moe_down_kernel  y[i] = W2[e] h[i]
+//   moe_sum_kernel   out[t] = bf16( sum_j w[i] * y[i] )
 //
 // With a few rows per expert the layer reads the chosen experts' weights once and does little
 // else, so both kernels stream weight rows from HBM straight into registers as the A operand of
@@ -10,7 +13,10 @@
 //
 // Products are exact and summed in fp32. h goes through the workspace as two bf16 values, hi and
 // lo = h - hi (16 significant bits together): one bf16 alone would add as much error as the final
-// rounding of out does.
+// rounding of out does. It is laid out for the down kernel's loads: an expert's n rows together,
+// [I/8 chunks][hi, lo][n rows][8 channels], so that neighbouring lanes (rows, in the matrix
+// instruction's order) read neighbouring 16 bytes; row-major, every lane's 16 bytes took a cache
+// access of its own, and that bounded the down kernel (128 tokens, FP8: 172 us).
 #include "ep_expert.h"
 
 namespace ep {
@@ -18,7 +24,8 @@ namespace ep {
 namespace {
 
 constexpr int kUpWaves = 4;
-constexpr int kTileC = 16;                    // output columns per workgroup of the down kernel
+constexpr int kSmallWaves = 16;               // at most, in the small down kernel
+static_assert(kMoeSmallPairs <= kWave, "a pair per lane");
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
@@ -69,22 +76,49 @@ __device__ __forceinline__ f32x4 mfma_frag(const Frag<FP8> &a, const Frag<FP8> &
 }
 
 // h = silu(g) * u.
-__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+__device__ __forceinline__ float swiglu(float g, float u)
+{
+    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
+
+// The pairs of one expert: its rows are `first` .. first + n - 1 of h (experts in order of their
+// ids, pairs in order), `mine` lane l's pair: that of row l.
+struct Rows {
+    int first, n;
+};
+
+// At most 64 pairs: lane l holds the id of pair l (-1: none). False if pair i names no expert or one
+// that an earlier pair names; else the expert's rows, and in `pair` the lane's pair: lane r gets the
+// pair of row r (r < n).
+__device__ __forceinline__ bool small_rows(int id, int E, int i, int &e, Rows &r, int &pair)
+{
+    e = __builtin_amdgcn_readlane(id, i);
+    if ((unsigned)e >= (unsigned)E) return false;
+    const uint64_t same = __ballot(id == e);
+    if (same & ((1ull << i) - 1)) return false;
+    r.n = __popcll(same);
+    r.first = __popcll(__ballot(id >= 0 && id < e));
+    const int lane = threadIdx.x & (kWave - 1);
+    const int to = id == e ? count_below(same) : r.n + count_below(~same);
+    pair = __builtin_amdgcn_ds_permute(to * 4, lane);
+    return true;
+}
 
 // NI: tiles of 16 channels of h per workgroup.
-template <bool FP8, int NI>
+template <int NI>
 struct UpShared {
     uint32_t named[EP_MAX_EXPERTS / 32];      // experts that a pair names
-    int n;                                    // pairs of this workgroup's expert
-    uint16_t pair[kMoePairs];
+    int first, n;                             // rows of this workgroup's expert
+    uint16_t pair[kMoePairs];                 // their pairs
     f32x4 part[kUpWaves][2 * NI][kWave];      // the wavefronts' sums of one tile of 16 pairs
 };
 
-// One pass over the expert's weights for MT tiles of 16 pairs. The wavefronts take the steps along
-// H in turn and their sums meet in LDS, in wavefront order.
+// One pass over the expert's weights for MT tiles of 16 pairs, rows row0 .. row0 + n - 1 of its
+// rows.n. The wavefronts take the steps along H in turn and their sums meet in LDS, in wavefront
+// order.
 template <bool FP8, int NI, int MT, int D>
-__device__ __forceinline__ void up_pass(UpShared<FP8, NI> &sh, const MoeLayer &p, int e, int c0,
-                                        int first, int n)
+__device__ __forceinline__ void up_pass(UpShared<NI> &sh, const MoeLayer &p, int e, int c0,
+                                        const Rows &rows, int row0, int n)
 {
     constexpr int kS = Step<FP8>::kElems;
     const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
@@ -99,7 +133,7 @@ __device__ __forceinline__ void up_pass(UpShared<FP8, NI> &sh, const MoeLayer &p
             woff[i][ni] = (uint32_t)(i * p.I + c0 + ni * 16 + r16) * row_bytes + g4 * 16;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        const int t = sh.pair[first + min(mt * 16 + r16, n - 1)] / p.K;
+        const int t = sh.pair[row0 + min(mt * 16 + r16, n - 1)] / p.K;
         xoff[mt] = (uint32_t)t * p.H * 2 + g4 * (FP8 ? 32 : 16);
     }
     const uint8_t *x = reinterpret_cast<const uint8_t *>(p.x);
@@ -166,10 +200,11 @@ __device__ __forceinline__ void up_pass(UpShared<FP8, NI> &sh, const MoeLayer &p
                             }
                         }
                 }
-                load(d, min(s + (d + D) * kUpWaves, nsteps - 1));
+                if (s + (d + D) * kUpWaves < nsteps) load(d, s + (d + D) * kUpWaves);
             }
         }
     }
+    uint16_t *h_e = p.h + (size_t)rows.first * 2 * p.I;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -178,7 +213,8 @@ __device__ __forceinline__ void up_pass(UpShared<FP8, NI> &sh, const MoeLayer &p
             for (int ni = 0; ni < NI; ++ni) sh.part[wave][i * NI + ni][lane] = acc[i][ni][mt];
         __syncthreads();
         for (int f = threadIdx.x; f < NI * 256; f += kUpWaves * kWave) {
-            const int r = f / (NI * 16), c = f % (NI * 16);          // pair, channel
+            // 8 channels of a row next to each other, then the rows
+            const int c = (f & 7) | (f >> 7) << 3, r = (f >> 3) & 15;
             const int ni = c >> 4, l = ((c >> 2) & 3) * 16 + r, k = c & 3;
             float g = 0.0f, u = 0.0f;
 #pragma unroll
@@ -189,224 +225,274 @@ __device__ __forceinline__ void up_pass(UpShared<FP8, NI> &sh, const MoeLayer &p
             if (mt * 16 + r < n) {
                 const float h = swiglu(g, u);
                 const uint32_t hi = bf16_rne(h);
-                const size_t at = (size_t)sh.pair[first + mt * 16 + r] * p.I + c0 + c;
-                p.h_hi[at] = (uint16_t)hi;
                 // an infinite or NaN h is whole in hi
                 const float rest = h - __uint_as_float(hi << 16);
-                p.h_lo[at] = (hi & 0x7F80u) == 0x7F80u ? 0 : (uint16_t)bf16_rne(rest);
+                const int ch = c0 + c;
+                uint16_t *at = h_e + ((size_t)(ch >> 3) * 2 * rows.n + row0 + mt * 16 + r) * 8 + (ch & 7);
+                at[0] = (uint16_t)hi;
+                at[(size_t)rows.n * 8] = (hi & 0x7F80u) == 0x7F80u ? 0 : (uint16_t)bf16_rne(rest);
             }
         }
         __syncthreads();
     }
 }
 
-// blockIdx.x: NI * 16 channels of h; blockIdx.y: the number of an expert among those named.
-template <bool FP8, int NI>
+// blockIdx.x: NI * 16 channels of h; blockIdx.y: the number of an expert among those named (SMALL,
+// at most 64 pairs: a pair, whose expert is taken if no earlier pair names it).
+template <bool FP8, int NI, bool SMALL>
 __global__ __launch_bounds__(kUpWaves *kWave) void moe_up_kernel(MoeLayer p)
 {
-    __shared__ UpShared<FP8, NI> sh;
+    __shared__ UpShared<NI> sh;
     const int lane = threadIdx.x & (kWave - 1);
-    const int pairs = p.T * p.K;
-    if (threadIdx.x < EP_MAX_EXPERTS / 32) sh.named[threadIdx.x] = 0;
-    if (threadIdx.x == 0) sh.n = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < pairs; i += kUpWaves * kWave) {
-        const int e = p.idx[i];
-        if ((unsigned)e < (unsigned)p.E) atomicOr(&sh.named[e >> 5], 1u << (e & 31));
+    const int pairs = p.T * p.K, c0 = blockIdx.x * NI * 16;
+    Rows rows;
+    int e;
+    if constexpr (SMALL) {
+        const int id = lane < pairs ? p.idx[lane] : -1;
+        int pair;
+        if (!small_rows(id, p.E, blockIdx.y, e, rows, pair)) return;
+        if (threadIdx.x < kWave) sh.pair[lane] = (uint16_t)pair;
+        __syncthreads();
+    } else {
+        if (threadIdx.x < EP_MAX_EXPERTS / 32) sh.named[threadIdx.x] = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < pairs; i += kUpWaves * kWave) {
+            const int v = p.idx[i];
+            if ((unsigned)v < (unsigned)p.E) atomicOr(&sh.named[v >> 5], 1u << (v & 31));
+        }
+        __syncthreads();
+        // the blockIdx.y-th set bit
+        const uint32_t word = lane < EP_MAX_EXPERTS / 32 ? sh.named[lane] : 0u;
+        const int bits = __popc(word), incl = wave_inclusive_sum(bits);
+        const int want = blockIdx.y;
+        const uint64_t mine = __ballot(incl - bits <= want && want < incl);
+        if (blockIdx.x == 0 && want == 0 && threadIdx.x == kWave - 1) p.named[0] = incl;
+        if (mine == 0) return;                 // fewer experts are named
+        const int at = __ffsll((unsigned long long)mine) - 1;
+        uint32_t left = (uint32_t)__shfl((int)word, at);
+        for (int skip = want - __shfl(incl - bits, at); skip > 0; --skip) left &= left - 1;
+        e = uniform(at * 32 + __ffs(left) - 1);
+        if (threadIdx.x < kWave) {             // the expert's pairs in order, and the rows before
+            int n = 0, first = 0;
+            for (int i0 = 0; i0 < pairs; i0 += kWave) {
+                const int i = i0 + lane, v = i < pairs ? p.idx[i] : -1;
+                const uint64_t same = __ballot(v == e);
+                if (v == e) sh.pair[n + count_below(same)] = (uint16_t)i;
+                n += __popcll(same);
+                first += __popcll(__ballot(v >= 0 && v < e));
+            }
+            if (lane == 0) {
+                sh.n = n;
+                sh.first = first;
+            }
+        }
+        __syncthreads();
+        rows = Rows{uniform(sh.first), uniform(sh.n)};
+        if (blockIdx.x == 0) {                 // the lists for the down kernel
+            if (threadIdx.x == 0)
+                reinterpret_cast<int4 *>(p.named)[1 + want] = int4{e, rows.first, rows.n, 0};
+            for (int r = threadIdx.x; r < rows.n; r += kUpWaves * kWave)
+                p.order[rows.first + r] = sh.pair[r];
+        }
     }
-    __syncthreads();
-    // the blockIdx.y-th set bit
-    const uint32_t word = lane < EP_MAX_EXPERTS / 32 ? sh.named[lane] : 0u;
-    const int bits = __popc(word), incl = wave_inclusive_sum(bits);
-    const int want = blockIdx.y;
-    const uint64_t mine = __ballot(incl - bits <= want && want < incl);
-    if (mine == 0) return;                     // fewer experts are named
-    const int at = __ffsll((unsigned long long)mine) - 1;
-    uint32_t left = (uint32_t)__shfl((int)word, at);
-    for (int skip = want - __shfl(incl - bits, at); skip > 0; --skip) left &= left - 1;
-    const int e = uniform(at * 32 + __ffs(left) - 1);
-    for (int i = threadIdx.x; i < pairs; i += kUpWaves * kWave)
-        if (p.idx[i] == e) sh.pair[atomicAdd(&sh.n, 1)] = (uint16_t)i;
-    __syncthreads();
-    const int n = uniform(sh.n), c0 = blockIdx.x * NI * 16;
-    int first = 0;
-    while (n - first > 16) {
-        up_pass<FP8, NI, 4, 1>(sh, p, e, c0, first, min(n - first, 64));
-        first += 64;
+    int row0 = 0;
+    while (rows.n - row0 > 16) {
+        up_pass<FP8, NI, 4, 1>(sh, p, e, c0, rows, row0, min(rows.n - row0, 64));
+        row0 += 64;
     }
-    if (first < n) up_pass<FP8, NI, 1, NI == 1 ? 4 : NI == 2 ? 2 : 1>(sh, p, e, c0, first, n - first);
+    if (row0 < rows.n)
+        up_pass<FP8, NI, 1, NI == 1 ? 4 : NI == 2 ? 2 : 1>(sh, p, e, c0, rows, row0, rows.n - row0);
 }
 
-// The down kernel's LDS: y of every pair for the workgroup's 16 columns, and the pairs sorted by
-// expert.
-struct DownShared {
-    int32_t count[EP_MAX_EXPERTS], first[EP_MAX_EXPERTS];
-    uint16_t named[EP_MAX_EXPERTS];
-    uint16_t rank[kMoePairs], pair[kMoePairs];
-    int n_named, next;
-};
-
-template <bool FP8, int MT, int D>
-__device__ __forceinline__ void down_pass(const DownShared &sh, f32x4 *y, const MoeLayer &p, int e,
-                                          int c0, int first, int n)
+// COLS output columns (weight rows) of an expert for MT tiles of 16 of its rows; the sums go to row
+// `pair` of y. The loads of the weights run DW steps ahead.
+template <bool FP8, int COLS, int MT, int DW>
+__device__ __forceinline__ void down_pass(float *y, int stride, const MoeLayer &p, int e, int c0,
+                                          const Rows &rows, int row0, const int (&pair)[MT])
 {
     constexpr int kS = Step<FP8>::kElems;
     const int lane = threadIdx.x & (kWave - 1);
     const int r16 = lane & 15, g4 = lane >> 4;
     const int row_bytes = FP8 ? p.I : 2 * p.I;
     const uint8_t *w = static_cast<const uint8_t *>(p.w2) + (size_t)e * p.H * row_bytes;
-    const uint32_t woff = (uint32_t)(c0 + r16) * row_bytes + g4 * 16;
-    int pair[MT];
+    const uint32_t woff = (uint32_t)(c0 + (r16 & (COLS - 1))) * row_bytes + g4 * 16;
+    const uint8_t *h = reinterpret_cast<const uint8_t *>(p.h + (size_t)rows.first * 2 * p.I);
+    const int n = rows.n, nsteps = p.I / kS;
+    // a lane's place in its chunks of h: chunk c of a step is 2 * n * 16 bytes further per c
     uint32_t hoff[MT];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        pair[mt] = sh.pair[first + min(mt * 16 + r16, n - 1)];
-        hoff[mt] = (uint32_t)pair[mt] * p.I * 2 + g4 * (FP8 ? 32 : 16);
-    }
-    const uint8_t *hi = reinterpret_cast<const uint8_t *>(p.h_hi);
-    const uint8_t *lo = reinterpret_cast<const uint8_t *>(p.h_lo);
-    const int nsteps = p.I / kS;
+    for (int mt = 0; mt < MT; ++mt)
+        hoff[mt] = (uint32_t)((FP8 ? 2 * g4 : g4) * 2 * n + row0 + min(mt * 16 + r16, n - 1 - row0)) * 16;
     const float *ws = nullptr;
     if constexpr (FP8) ws = p.w2_scale + ((size_t)e * (p.H >> 7) + (c0 >> 7)) * (size_t)nsteps;
 
     f32x4 acc[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) acc[mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    i32x4 wf[D][2];
-    Frag<FP8> hf[D][MT][2];
-    float sw[D];
+    i32x4 wf[DW][2];
+    float sw[DW];
     auto load = [&](int d, int s) {
         const uint8_t *wk = w + (size_t)s * 128;
         wf[d][0] = *reinterpret_cast<const i32x4 *>(wk + woff);
         wf[d][1] = *reinterpret_cast<const i32x4 *>(wk + woff + 64);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            hf[d][mt][0] = row_frag<FP8>(hi + (size_t)s * (kS * 2), hoff[mt]);
-            hf[d][mt][1] = row_frag<FP8>(lo + (size_t)s * (kS * 2), hoff[mt]);
-        }
         if constexpr (FP8) sw[d] = ws[s];
     };
 #pragma unroll
-    for (int d = 0; d < D; ++d) load(d, min(d, nsteps - 1));
-    for (int s = 0; s < nsteps; s += D) {
+    for (int d = 0; d < DW; ++d) load(d, min(d, nsteps - 1));
+    for (int s = 0; s < nsteps; s += DW) {
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
+        for (int d = 0; d < DW; ++d) {
             if (s + d < nsteps) {
+                Frag<FP8> hf[MT][2];           // lo, hi
+#pragma unroll
+                for (int i = 0; i < Step<FP8>::kMfma; ++i) {
+                    // the 8 channels that the lane's i-th 8 codes (FP8) or i-th 16 bytes meet
+                    const int c = (s + d) * (kS / 8) + (FP8 ? (i >> 1) * 8 + (i & 1) : i * 4);
+                    const uint8_t *hi = h + (size_t)c * 2 * n * 16, *lo = hi + n * 16;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        hf[mt][1].v[i] = as_bf16(*reinterpret_cast<const i32x4 *>(hi + hoff[mt]));
+                        hf[mt][0].v[i] = as_bf16(*reinterpret_cast<const i32x4 *>(lo + hoff[mt]));
+                    }
+                }
                 const Frag<FP8> a = weight_frag<FP8>(wf[d][0], wf[d][1]);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     if constexpr (FP8) {
                         f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-                        v = mfma_frag<FP8>(a, hf[d][mt][1], v);
-                        v = mfma_frag<FP8>(a, hf[d][mt][0], v);
+                        v = mfma_frag<FP8>(a, hf[mt][0], v);
+                        v = mfma_frag<FP8>(a, hf[mt][1], v);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             acc[mt][k] = __builtin_fmaf(sw[d], v[k], acc[mt][k]);
                     } else {
-                        acc[mt] = mfma_frag<FP8>(a, hf[d][mt][1], acc[mt]);
-                        acc[mt] = mfma_frag<FP8>(a, hf[d][mt][0], acc[mt]);
+                        acc[mt] = mfma_frag<FP8>(a, hf[mt][0], acc[mt]);
+                        acc[mt] = mfma_frag<FP8>(a, hf[mt][1], acc[mt]);
                     }
                 }
             }
-            load(d, min(s + d + D, nsteps - 1));
+            if (s + d + DW < nsteps) load(d, s + d + DW);
         }
     }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
-        if (mt * 16 + r16 < n) y[pair[mt] * (kTileC / 4) + g4] = acc[mt];
+        if (row0 + mt * 16 + r16 < n && g4 * 4 < COLS)
+            *reinterpret_cast<f32x4 *>(y + (size_t)pair[mt] * stride + g4 * 4) = acc[mt];
 }
 
-// A workgroup: 16 columns of out for all tokens. Its wavefronts take the named experts from a
-// counter in LDS; y of every pair meets there, and the weighted sums run over j in order.
-template <bool FP8>
-__global__ __launch_bounds__(1024) void moe_down_kernel(MoeLayer p)
+// At most 64 pairs. A workgroup: COLS columns of out for all tokens. Its wavefronts take the pairs
+// in turn (each named expert once); y of every pair meets in LDS, and the weighted sums run over j
+// in order.
+template <bool FP8, int COLS>
+__global__ __launch_bounds__(kSmallWaves *kWave) void moe_small_down_kernel(MoeLayer p)
 {
-    extern __shared__ f32x4 y[];               // [pairs][16]
-    __shared__ DownShared sh;
-    const int lane = threadIdx.x & (kWave - 1);
-    const int pairs = p.T * p.K, nthreads = blockDim.x;
-    for (int e = threadIdx.x; e < p.E; e += nthreads) sh.count[e] = 0;
-    if (threadIdx.x == 0) sh.next = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < pairs; i += nthreads) {
-        const int e = p.idx[i];
-        if ((unsigned)e < (unsigned)p.E) sh.rank[i] = (uint16_t)atomicAdd(&sh.count[e], 1);
-    }
-    __syncthreads();
-    if (threadIdx.x < kWave) {                 // first pair of each expert, and the named experts
-        int run = 0, named = 0;
-        for (int e0 = 0; e0 < p.E; e0 += kWave) {
-            const int e = e0 + lane, c = e < p.E ? sh.count[e] : 0;
-            const int incl = wave_inclusive_sum(c);
-            const uint64_t some = __ballot(c > 0);
-            if (e < p.E) sh.first[e] = run + incl - c;
-            if (c > 0) sh.named[named + count_below(some)] = (uint16_t)e;
-            run += __shfl(incl, kWave - 1);
-            named += __popcll(some);
+    __shared__ float y[kMoeSmallPairs * COLS];
+    const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
+    const int pairs = p.T * p.K, nthreads = blockDim.x, c0 = blockIdx.x * COLS;
+    const int id = lane < pairs ? p.idx[lane] : -1;
+    for (int i = wave; i < pairs; i += nthreads / kWave) {
+        Rows rows;
+        int e, pair;
+        if (!small_rows(id, p.E, i, e, rows, pair)) continue;
+        for (int row0 = 0; row0 < rows.n; row0 += 16) {
+            const int of[1] = {__shfl(pair, row0 + (lane & 15))};
+            down_pass<FP8, COLS, 1, 4>(y, COLS, p, e, c0, rows, row0, of);
         }
-        if (lane == 0) sh.n_named = named;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < pairs; i += nthreads) {
-        const int e = p.idx[i];
-        if ((unsigned)e < (unsigned)p.E) sh.pair[sh.first[e] + sh.rank[i]] = (uint16_t)i;
-    }
-    __syncthreads();
-
-    const int c0 = blockIdx.x * kTileC, n_named = sh.n_named;
-    while (true) {
-        int a = 0;
-        if (lane == 0) a = atomicAdd(&sh.next, 1);
-        a = uniform(a);
-        if (a >= n_named) break;
-        const int e = uniform(sh.named[a]), n = uniform(sh.count[e]);
-        int first = uniform(sh.first[e]), left = n;
-        while (left > 16) {
-            down_pass<FP8, 4, 1>(sh, y, p, e, c0, first, min(left, 64));
-            first += 64;
-            left -= 64;
-        }
-        if (left > 0) down_pass<FP8, 1, 2>(sh, y, p, e, c0, first, left);
-    }
-    __syncthreads();
-    const float *yf = reinterpret_cast<const float *>(y);
-    for (int f = threadIdx.x; f < p.T * kTileC; f += nthreads) {
-        const int t = f / kTileC, c = f % kTileC;
+    for (int f = threadIdx.x; f < p.T * COLS; f += nthreads) {
+        const int t = f / COLS, c = f % COLS;
         float acc = 0.0f;
         for (int j = 0; j < p.K; ++j) {
             const int i = t * p.K + j;
             if ((unsigned)p.idx[i] < (unsigned)p.E)
-                acc = __builtin_fmaf(p.topk_w[i], yf[i * kTileC + c], acc);
+                acc = __builtin_fmaf(p.topk_w[i], y[i * COLS + c], acc);
         }
         p.out[(size_t)t * p.H + c0 + c] = (uint16_t)bf16_rne(acc);
     }
 }
 
+// blockIdx.x: 64 columns, 16 per wavefront; blockIdx.y: the number of a named expert. y [pair][H].
 template <bool FP8>
-hipError_t launch_fp8(const MoeLayer &p, hipStream_t stream)
+__global__ __launch_bounds__(4 * kWave) void moe_down_kernel(MoeLayer p)
+{
+    const int a = blockIdx.y, r16 = threadIdx.x & 15;
+    if (a >= p.named[0]) return;
+    const int4 v = reinterpret_cast<const int4 *>(p.named)[1 + a];
+    const int e = uniform(v.x), c0 = blockIdx.x * 64 + uniform(threadIdx.x / kWave) * 16;
+    const Rows rows{uniform(v.y), uniform(v.z)};
+    int row0 = 0;
+    while (rows.n - row0 > 16) {
+        int of[2];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+            of[mt] = p.order[rows.first + min(row0 + mt * 16 + r16, rows.n - 1)];
+        down_pass<FP8, 16, 2, 4>(p.y + c0, p.H, p, e, c0, rows, row0, of);
+        row0 += 32;
+    }
+    if (row0 < rows.n) {
+        const int of[1] = {p.order[rows.first + min(row0 + r16, rows.n - 1)]};
+        down_pass<FP8, 16, 1, 6>(p.y + c0, p.H, p, e, c0, rows, row0, of);
+    }
+}
+
+__global__ __launch_bounds__(256) void moe_sum_kernel(MoeLayer p)
+{
+    const int per = p.H / 4, f = blockIdx.x * 256 + threadIdx.x;
+    if (f >= p.T * per) return;
+    const int t = f / per, c = (f - t * per) * 4;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < p.K; ++j) {
+        const int i = t * p.K + j;
+        if ((unsigned)p.idx[i] >= (unsigned)p.E) continue;
+        const float w = p.topk_w[i];
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(p.y + (size_t)i * p.H + c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(w, v[k], acc[k]);
+    }
+    uint2 o;
+    o.x = bf16_rne(acc[0]) | (bf16_rne(acc[1]) << 16);
+    o.y = bf16_rne(acc[2]) | (bf16_rne(acc[3]) << 16);
+    *reinterpret_cast<uint2 *>(p.out + (size_t)t * p.H + c) = o;
+}
+
+template <bool FP8, bool SMALL>
+hipError_t launch_layer(const MoeLayer &p, hipStream_t stream)
 {
     const int pairs = p.T * p.K;
-    const int named = pairs < p.E ? pairs : p.E;       // at most
+    const int named = SMALL ? pairs : pairs < p.E ? pairs : p.E;       // at most
     const dim3 block(kUpWaves * kWave);
     const long tiles = (long)named * (p.I / 16);
     hipError_t e;
     if (tiles >= 4096)
-        e = launch(moe_up_kernel<FP8, 4>, dim3(p.I / 64, named), block, 0, stream, p);
+        e = launch(moe_up_kernel<FP8, 4, SMALL>, dim3(p.I / 64, named), block, 0, stream, p);
     else if (tiles >= 1024)
-        e = launch(moe_up_kernel<FP8, 2>, dim3(p.I / 32, named), block, 0, stream, p);
+        e = launch(moe_up_kernel<FP8, 2, SMALL>, dim3(p.I / 32, named), block, 0, stream, p);
     else
-        e = launch(moe_up_kernel<FP8, 1>, dim3(p.I / 16, named), block, 0, stream, p);
+        e = launch(moe_up_kernel<FP8, 1, SMALL>, dim3(p.I / 16, named), block, 0, stream, p);
     if (e != hipSuccess) return e;
-    const int waves = named < 4 ? 4 : named > 16 ? 16 : named;
-    return launch(moe_down_kernel<FP8>, dim3(p.H / kTileC), dim3(waves * kWave),
-                  (size_t)pairs * kTileC * sizeof(float), stream, p);
+    if constexpr (SMALL) {
+        const int waves = pairs < 4 ? 4 : pairs > kSmallWaves ? kSmallWaves : pairs;
+        // 8 columns per workgroup where 16 would leave half of the 256 CUs without one
+        if (p.H / 16 >= 256)
+            return launch(moe_small_down_kernel<FP8, 16>, dim3(p.H / 16), dim3(waves * kWave), 0,
+                          stream, p);
+        return launch(moe_small_down_kernel<FP8, 8>, dim3(p.H / 8), dim3(waves * kWave), 0, stream, p);
+    } else {
+        e = launch(moe_down_kernel<FP8>, dim3(p.H / 64, named), dim3(4 * kWave), 0, stream, p);
+        if (e != hipSuccess) return e;
+        const int64_t quads = (int64_t)p.T * (p.H / 4);
+        return launch(moe_sum_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, p);
+    }
 }
 
 }  // namespace
 
 hipError_t launch_moe_layer(const MoeLayer &p, bool fp8, hipStream_t stream)
 {
-    return fp8 ? launch_fp8<true>(p, stream) : launch_fp8<false>(p, stream);
+    if (p.T * p.K <= kMoeSmallPairs)
+        return fp8 ? launch_layer<true, true>(p, stream) : launch_layer<false, true>(p, stream);
+    return fp8 ? launch_layer<true, false>(p, stream) : launch_layer<false, false>(p, stream);
 }
 
 }  // namespace ep

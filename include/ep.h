@@ -511,8 +511,8 @@ int ep_expert_swiglu_fp8_packed(const ep_shape_t *shape, int32_t rows, int32_t I
 
 /*
  * ep_moe_layer / ep_moe_layer_fp8 -- a whole MoE layer for a few tokens (a decode step), from
- * token rows to combined rows in two launches, with no receive buffer: bound by reading the
- * chosen experts' weights once.
+ * token rows to combined rows in two launches (three above 64 pairs), with no receive buffer: bound
+ * by reading the chosen experts' weights once.
  *
  *   out[t][c] = bf16_rne(acc), acc = +0.0f, then for j = 0 .. K-1 ascending, for each pair with
  *               0 <= e < E:  acc = fmaf(topk_w[i], y, acc)
@@ -534,10 +534,11 @@ int ep_expert_swiglu_fp8_packed(const ep_shape_t *shape, int32_t rows, int32_t I
  *            Two calls in flight at once need two.
  *
  * Requires (else EP_ERR_UNSUPPORTED) T*K <= EP_MOE_MAX_PAIRS, E <= EP_MAX_EXPERTS, H and I
- * multiples of 64 (bf16) or 128 (FP8), 2*I*H <= 2^29, T*H and T*K*I <= 2^30. C and R are not used. T = 0 does nothing.
+ * multiples of 64 (bf16) or 128 (FP8), 2*I*H and T*K*I <= 2^29, T*H <= 2^30. C and R are not used. T = 0 does nothing.
  * Deterministic.
  *
- * ep_moe_layer_workspace_bytes: 4 * T*K * I (0 for an invalid shape or I). Host only.
+ * ep_moe_layer_workspace_bytes: 4 * T*K * I, and above 64 pairs T*K * (4*H + 20) + 16 more (0 for
+ * T*K = 0 or an invalid shape or I). Host only.
  */
 size_t ep_moe_layer_workspace_bytes(const ep_shape_t *shape, int32_t I);
 

@@ -117,7 +117,7 @@ def test_host_tensors_are_refused():
 # the whole layer
 # ------------------------------------------------------------------------------------------
 
-LAYER = dict(T=16, H=256, E=8, K=4, C=1, R=1)
+LAYER = dict(T=17, H=256, E=8, K=4, C=1, R=1)
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -139,7 +139,8 @@ def test_layer_shapes_refused(lib, fp8):
 @pytest.mark.parametrize("fp8", [False, True])
 def test_layer_pointers_refused(lib, fp8):
     fn, ptrs = (lib.ep_moe_layer_fp8, 8) if fp8 else (lib.ep_moe_layer, 6)
-    need = 4 * 64 * 128
+    need = 68 * 4 * 128 + 68 * (4 * 256 + 20) + 16          # above 64 pairs: y and the lists too
+    assert lib.ep_moe_layer_workspace_bytes(shape(**{**LAYER, "T": 16}), 128) == 64 * 4 * 128
     assert lib.ep_moe_layer_workspace_bytes(shape(**LAYER), 128) == need
     assert lib.ep_moe_layer_workspace_bytes(None, 128) == 0
     assert lib.ep_moe_layer_workspace_bytes(shape(**LAYER), 0) == 0

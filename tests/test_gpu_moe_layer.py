@@ -63,7 +63,7 @@ class Layer:
 
     def check(self, out=None):
         if out is None:
-            ws = torch.full((B.moe_layer_workspace_bytes(self.T, self.K, self.I) // 4,),
+            ws = torch.full((B.moe_layer_workspace_bytes(self.T, self.K, self.H, self.I) // 4,),
                             float("nan"), device=DEV)
             out = torch.full((self.T, self.H), float("nan"), dtype=torch.bfloat16, device=DEV)
             self.run(out=out, workspace=ws)
@@ -158,7 +158,7 @@ def test_same_bits_on_another_stream_and_with_another_workspace(fp8):
     torch.cuda.synchronize()
     other = torch.cuda.Stream()
     other.wait_stream(torch.cuda.current_stream())
-    ws = torch.empty(4 * 24 * 4 * 256 + 512, dtype=torch.uint8, device=DEV)
+    ws = torch.empty(B.moe_layer_workspace_bytes(24, 4, 256, 256) + 512, dtype=torch.uint8, device=DEV)
     out = torch.zeros_like(a)
     with torch.cuda.stream(other):
         x.run(out=out, workspace=ws)
@@ -171,7 +171,7 @@ def test_captured_and_recorded_layers_replay(fp8):
     """A layer captured in a graph and one recorded in a call list, replayed on refilled tokens and
     routes, with eager calls between."""
     x = Layer(9, 12, 3, 256, 128, fp8, seed=7)
-    ws = torch.empty(4 * 27 * 128, dtype=torch.uint8, device=DEV)
+    ws = torch.empty(B.moe_layer_workspace_bytes(9, 3, 256, 128), dtype=torch.uint8, device=DEV)
     out, out2 = torch.zeros_like(x.d["x"]), torch.zeros_like(x.d["x"])
     x.run(out=out, workspace=ws)
     torch.cuda.synchronize()
