@@ -240,7 +240,7 @@ __device__ __forceinline__ void up_pass(UpShared<NI> &sh, const MoeLayer &p, int
 // blockIdx.x: NI * 16 channels of h; blockIdx.y: the number of an expert among those named (SMALL,
 // at most 64 pairs: a pair, whose expert is taken if no earlier pair names it).
 template <bool FP8, int NI, bool SMALL>
-__global__ __launch_bounds__(kUpWaves *kWave) void moe_up_kernel(MoeLayer p)
+__global__ __launch_bounds__(kUpWaves *kWave, 2) void moe_up_kernel(MoeLayer p)
 {
     __shared__ UpShared<NI> sh;
     const int lane = threadIdx.x & (kWave - 1);
@@ -295,18 +295,21 @@ __global__ __launch_bounds__(kUpWaves *kWave) void moe_up_kernel(MoeLayer p)
                 p.order[rows.first + r] = sh.pair[r];
         }
     }
+    // steps in flight: with one tile all that a wavefront has of H = 2048; with two, 2 (FP8) and 3
+    // (bf16) are best (1: 32 tokens bf16 222 us, 3: 207 us; 128 tokens FP8 171 us with 2, 180 with 3)
+    constexpr int kAhead = NI == 1 ? (FP8 ? 4 : 8) : FP8 ? 2 : 3;
     int row0 = 0;
     while (rows.n - row0 > 16) {
-        up_pass<FP8, NI, 4, 1>(sh, p, e, c0, rows, row0, min(rows.n - row0, 64));
-        row0 += 64;
+        up_pass<FP8, NI, 2, 1>(sh, p, e, c0, rows, row0, min(rows.n - row0, 32));
+        row0 += 32;
     }
     if (row0 < rows.n)
-        up_pass<FP8, NI, 1, NI == 1 ? 4 : NI == 2 ? 2 : 1>(sh, p, e, c0, rows, row0, rows.n - row0);
+        up_pass<FP8, NI, 1, kAhead>(sh, p, e, c0, rows, row0, rows.n - row0);
 }
 
 // COLS output columns (weight rows) of an expert for MT tiles of 16 of its rows; the sums go to row
-// `pair` of y. The loads of the weights run DW steps ahead.
-template <bool FP8, int COLS, int MT, int DW>
+// `pair` of y. The loads of the weights run DW steps ahead, those of h DH (DW a multiple of it).
+template <bool FP8, int COLS, int MT, int DW, int DH>
 __device__ __forceinline__ void down_pass(float *y, int stride, const MoeLayer &p, int e, int c0,
                                           const Rows &rows, int row0, const int (&pair)[MT])
 {
@@ -337,40 +340,45 @@ __device__ __forceinline__ void down_pass(float *y, int stride, const MoeLayer &
         wf[d][1] = *reinterpret_cast<const i32x4 *>(wk + woff + 64);
         if constexpr (FP8) sw[d] = ws[s];
     };
+    Frag<FP8> hf[DH][MT][2];                   // lo, hi
+    auto load_h = [&](int d, int s) {
+#pragma unroll
+        for (int i = 0; i < Step<FP8>::kMfma; ++i) {
+            // the 8 channels that the lane's i-th 8 codes (FP8) or i-th 16 bytes meet
+            const int c = s * (kS / 8) + (FP8 ? (i >> 1) * 8 + (i & 1) : i * 4);
+            const uint8_t *hi = h + (size_t)c * 2 * n * 16, *lo = hi + n * 16;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                hf[d][mt][1].v[i] = as_bf16(*reinterpret_cast<const i32x4 *>(hi + hoff[mt]));
+                hf[d][mt][0].v[i] = as_bf16(*reinterpret_cast<const i32x4 *>(lo + hoff[mt]));
+            }
+        }
+    };
 #pragma unroll
     for (int d = 0; d < DW; ++d) load(d, min(d, nsteps - 1));
+#pragma unroll
+    for (int d = 0; d < DH; ++d) load_h(d, min(d, nsteps - 1));
     for (int s = 0; s < nsteps; s += DW) {
 #pragma unroll
         for (int d = 0; d < DW; ++d) {
             if (s + d < nsteps) {
-                Frag<FP8> hf[MT][2];           // lo, hi
-#pragma unroll
-                for (int i = 0; i < Step<FP8>::kMfma; ++i) {
-                    // the 8 channels that the lane's i-th 8 codes (FP8) or i-th 16 bytes meet
-                    const int c = (s + d) * (kS / 8) + (FP8 ? (i >> 1) * 8 + (i & 1) : i * 4);
-                    const uint8_t *hi = h + (size_t)c * 2 * n * 16, *lo = hi + n * 16;
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        hf[mt][1].v[i] = as_bf16(*reinterpret_cast<const i32x4 *>(hi + hoff[mt]));
-                        hf[mt][0].v[i] = as_bf16(*reinterpret_cast<const i32x4 *>(lo + hoff[mt]));
-                    }
-                }
                 const Frag<FP8> a = weight_frag<FP8>(wf[d][0], wf[d][1]);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     if constexpr (FP8) {
                         f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-                        v = mfma_frag<FP8>(a, hf[mt][0], v);
-                        v = mfma_frag<FP8>(a, hf[mt][1], v);
+                        v = mfma_frag<FP8>(a, hf[d % DH][mt][0], v);
+                        v = mfma_frag<FP8>(a, hf[d % DH][mt][1], v);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             acc[mt][k] = __builtin_fmaf(sw[d], v[k], acc[mt][k]);
                     } else {
-                        acc[mt] = mfma_frag<FP8>(a, hf[mt][0], acc[mt]);
-                        acc[mt] = mfma_frag<FP8>(a, hf[mt][1], acc[mt]);
+                        acc[mt] = mfma_frag<FP8>(a, hf[d % DH][mt][0], acc[mt]);
+                        acc[mt] = mfma_frag<FP8>(a, hf[d % DH][mt][1], acc[mt]);
                     }
                 }
             }
+            if (s + d + DH < nsteps) load_h(d % DH, s + d + DH);
             if (s + d + DW < nsteps) load(d, s + d + DW);
         }
     }
@@ -386,17 +394,22 @@ __device__ __forceinline__ void down_pass(float *y, int stride, const MoeLayer &
 template <bool FP8, int COLS>
 __global__ __launch_bounds__(kSmallWaves *kWave) void moe_small_down_kernel(MoeLayer p)
 {
-    __shared__ float y[kMoeSmallPairs * COLS];
+    __shared__ float y[kMoeSmallPairs * COLS], weight[kMoeSmallPairs];
+    __shared__ bool names[kMoeSmallPairs];
     const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
     const int pairs = p.T * p.K, nthreads = blockDim.x, c0 = blockIdx.x * COLS;
     const int id = lane < pairs ? p.idx[lane] : -1;
+    if (wave == 0) {
+        names[lane] = (unsigned)id < (unsigned)p.E;
+        weight[lane] = lane < pairs ? p.topk_w[lane] : 0.0f;
+    }
     for (int i = wave; i < pairs; i += nthreads / kWave) {
         Rows rows;
         int e, pair;
         if (!small_rows(id, p.E, i, e, rows, pair)) continue;
         for (int row0 = 0; row0 < rows.n; row0 += 16) {
             const int of[1] = {__shfl(pair, row0 + (lane & 15))};
-            down_pass<FP8, COLS, 1, 4>(y, COLS, p, e, c0, rows, row0, of);
+            down_pass<FP8, COLS, 1, 4, 1>(y, COLS, p, e, c0, rows, row0, of);
         }
     }
     __syncthreads();
@@ -405,16 +418,18 @@ __global__ __launch_bounds__(kSmallWaves *kWave) void moe_small_down_kernel(MoeL
         float acc = 0.0f;
         for (int j = 0; j < p.K; ++j) {
             const int i = t * p.K + j;
-            if ((unsigned)p.idx[i] < (unsigned)p.E)
-                acc = __builtin_fmaf(p.topk_w[i], y[i * COLS + c], acc);
+            if (names[i]) acc = __builtin_fmaf(weight[i], y[i * COLS + c], acc);
         }
         p.out[(size_t)t * p.H + c0 + c] = (uint16_t)bf16_rne(acc);
     }
 }
 
 // blockIdx.x: 64 columns, 16 per wavefront; blockIdx.y: the number of a named expert. y [pair][H].
+// Four workgroups per CU with 3 steps of weights in flight each, since a workgroup is short and waits
+// for its lists and its first loads (128 tokens FP8: 159 us for the layer; two workgroups with 6
+// steps 171 us).
 template <bool FP8>
-__global__ __launch_bounds__(4 * kWave) void moe_down_kernel(MoeLayer p)
+__global__ __launch_bounds__(4 * kWave, 4) void moe_down_kernel(MoeLayer p)
 {
     const int a = blockIdx.y, r16 = threadIdx.x & 15;
     if (a >= p.named[0]) return;
@@ -427,12 +442,12 @@ __global__ __launch_bounds__(4 * kWave) void moe_down_kernel(MoeLayer p)
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
             of[mt] = p.order[rows.first + min(row0 + mt * 16 + r16, rows.n - 1)];
-        down_pass<FP8, 16, 2, 4>(p.y + c0, p.H, p, e, c0, rows, row0, of);
+        down_pass<FP8, 16, 2, 1, 1>(p.y + c0, p.H, p, e, c0, rows, row0, of);
         row0 += 32;
     }
     if (row0 < rows.n) {
         const int of[1] = {p.order[rows.first + min(row0 + r16, rows.n - 1)]};
-        down_pass<FP8, 16, 1, 6>(p.y + c0, p.H, p, e, c0, rows, row0, of);
+        down_pass<FP8, 16, 1, 3, 1>(p.y + c0, p.H, p, e, c0, rows, row0, of);
     }
 }
 
@@ -442,13 +457,22 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(MoeLayer p)
     if (f >= p.T * per) return;
     const int t = f / per, c = (f - t * per) * 4;
     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int j = 0; j < p.K; ++j) {
-        const int i = t * p.K + j;
-        if ((unsigned)p.idx[i] >= (unsigned)p.E) continue;
-        const float w = p.topk_w[i];
-        const f32x4 v = *reinterpret_cast<const f32x4 *>(p.y + (size_t)i * p.H + c);
+    for (int j0 = 0; j0 < p.K; j0 += 8) {      // 8 pairs in flight; past the last one, it again
+        f32x4 v[8];
+        float w[8];
+        bool names[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(w, v[k], acc[k]);
+        for (int j = 0; j < 8; ++j) {
+            const int i = t * p.K + min(j0 + j, p.K - 1);
+            names[j] = j0 + j < p.K && (unsigned)p.idx[i] < (unsigned)p.E;
+            w[j] = p.topk_w[i];
+            v[j] = *reinterpret_cast<const f32x4 *>(p.y + (size_t)i * p.H + c);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                acc[k] = names[j] ? __builtin_fmaf(w[j], v[j][k], acc[k]) : acc[k];
     }
     uint2 o;
     o.x = bf16_rne(acc[0]) | (bf16_rne(acc[1]) << 16);
@@ -462,11 +486,11 @@ hipError_t launch_layer(const MoeLayer &p, hipStream_t stream)
     const int pairs = p.T * p.K;
     const int named = SMALL ? pairs : pairs < p.E ? pairs : p.E;       // at most
     const dim3 block(kUpWaves * kWave);
+    // 32 channels of h per workgroup, 16 where that would leave CUs without one (64 held more
+    // registers and lost: 32 tokens bf16 227 against 212 us)
     const long tiles = (long)named * (p.I / 16);
     hipError_t e;
-    if (tiles >= 4096)
-        e = launch(moe_up_kernel<FP8, 4, SMALL>, dim3(p.I / 64, named), block, 0, stream, p);
-    else if (tiles >= 1024)
+    if (tiles >= 1024)
         e = launch(moe_up_kernel<FP8, 2, SMALL>, dim3(p.I / 32, named), block, 0, stream, p);
     else
         e = launch(moe_up_kernel<FP8, 1, SMALL>, dim3(p.I / 16, named), block, 0, stream, p);
