@@ -4,19 +4,22 @@
 //
 //   y[r][c] = bf16( sum_b xs[r][b] * ws[e][c / 128][b] * sum_{k in block b} xq[r][k] * wq[e][c][k] )
 //
-// One v_mfma_f32_16x16x128_f8f6f4 covers exactly one scale block of a 16 x 16 tile, so the inner
-// sum is one matrix instruction with a zero start and the outer sum one fmaf per element, in
-// ascending b. The SwiGLU form, whose scales are fp32 outputs, takes the exact product of the same
-// codes (mfma_exact). The weights are the A operand and the rows the B operand: a lane then holds one
-// row (its scale is one value) and four consecutive output channels.
+// The inner sum of a 32 x 32 tile is two matrix instructions of 64 channels with a zero start, the
+// outer sum one fmaf per element, in ascending b. The SwiGLU form, whose scales are fp32 outputs,
+// takes the exact product of the same codes, as bf16 (bf16_of_e4m3). The weights are the A operand
+// and the rows the B operand: a lane then holds one row (its scale is one value) and groups of four
+// consecutive output channels.
 #include "ep_expert.h"
 
 namespace ep {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTileN = 256;        // weight rows per workgroup: 64 per wavefront
+constexpr int kTileThreads = 512;
+constexpr int kTileN = 256;        // weight rows of a tile
+template <int MT> inline constexpr int kTileRows = 64 * MT;     // rows of a tile
+
+#if defined(__HIP_DEVICE_COMPILE__)            // buffer descriptors exist on the device only
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
@@ -24,45 +27,68 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // running number of tiles. Built once per workgroup.
 struct TileTable {
     int32_t end[EP_MAX_EXPERTS], base[EP_MAX_EXPERTS], n[EP_MAX_EXPERTS];
-    int32_t wave_sum[16];
+    int32_t wave_sum[2][kTileThreads / kWave];
 };
 
-template <int THREADS>
-__device__ __forceinline__ int build_table(TileTable &t, const ExpertProduct &p, int bm)
+struct Tiling {
+    int total, mt;                 // row tiles of all experts, of 64 * mt rows
+};
+
+// Builds the table and chooses the height of the tiles from the rows there are. A workgroup takes
+// about 3/2 as long for a tile of 128 rows as for one of 64 (the weights' LDS traffic is the same):
+// 26 us against 17 us where 8 to 32 experts fill the chip 2 to 5 times over (H = 2048), so the
+// taller tiles pay where they leave less than 2/3 as many tiles for the busiest workgroup. Few rows
+// an expert, or few tiles: 64 rows (8 rows for each of 128 experts, gate/up of 2 x 768 x 2048,
+// 82 us against 111); more: 128 rows (341 rows for each of 96 experts, 250 us against 302).
+__device__ __forceinline__ Tiling build_table(TileTable &t, const ExpertProduct &p, int n_tiles)
 {
-    constexpr int kPer = EP_MAX_EXPERTS / THREADS;
+    constexpr int kPer = EP_MAX_EXPERTS / kTileThreads, kWaves = kTileThreads / kWave;
     const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
     const int e0 = threadIdx.x * kPer;
-    int tiles[kPer], sum = 0;
+    int tiles[2][kPer], sum[2] = {0, 0}, incl[2];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        tiles[i] = 0;
+        tiles[0][i] = tiles[1][i] = 0;
         if (e0 + i < p.E) {
             int base, n;
             expert_rows(p.count, p.offset, e0 + i, p.C, p.rows, base, n);
             t.base[e0 + i] = base;
             t.n[e0 + i] = n;
-            tiles[i] = (n + bm - 1) / bm;
+            tiles[0][i] = (n + kTileRows<1> - 1) / kTileRows<1>;
+            tiles[1][i] = (n + kTileRows<2> - 1) / kTileRows<2>;
         }
-        sum += tiles[i];
+        sum[0] += tiles[0][i];
+        sum[1] += tiles[1][i];
     }
-    const int incl = wave_inclusive_sum(sum);
-    if (lane == kWave - 1) t.wave_sum[wave] = incl;
-    __syncthreads();
-    int run = incl - sum, total = 0;
 #pragma unroll
-    for (int w = 0; w < THREADS / kWave; ++w) {
-        const int s = t.wave_sum[w];
-        if (w < wave) run += s;
-        total += s;
+    for (int h = 0; h < 2; ++h) {
+        incl[h] = wave_inclusive_sum(sum[h]);
+        if (lane == kWave - 1) t.wave_sum[h][wave] = incl[h];
     }
+    __syncthreads();
+    int run[2], total[2] = {0, 0};
+    int64_t most[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        run[h] = incl[h] - sum[h];
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const int s = t.wave_sum[h][w];
+            if (w < wave) run[h] += s;
+            total[h] += s;
+        }
+        total[h] = uniform(total[h]);
+        most[h] = ((int64_t)total[h] * n_tiles + gridDim.x - 1) / gridDim.x;
+    }
+    const int h = 3 * most[1] < 2 * most[0] ? 1 : 0;
+    int r = h ? run[1] : run[0];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        run += tiles[i];
-        if (e0 + i < p.E) t.end[e0 + i] = run;
+        r += h ? tiles[1][i] : tiles[0][i];
+        if (e0 + i < p.E) t.end[e0 + i] = r;
     }
     __syncthreads();
-    return total;
+    return Tiling{h ? total[1] : total[0], h + 1};
 }
 
 // The tiles of all experts in one row, an expert's tiles in groups of kGroup row tiles: within a
@@ -159,8 +185,7 @@ __device__ __forceinline__ uint2 bf16_pairs(float a, float b, float c, float d)
 // The SwiGLU epilogue of one tile of ROWS rows x 128 channels of h: the block amax meets in LDS, the
 // codes go out through LDS in whole rows. A wavefront holds quarter `part` of the 128 channels, a
 // lane G groups of 4 consecutive ones (group g at channel part * 32 + channel(g)) of M rows
-// (row(m)), GROUP lanes apart from the other channels of the row; one that holds none only helps
-// to store.
+// (row(m)), GROUP lanes apart from the other channels of the row.
 template <int ROWS>
 struct SwigluShared {
     uint32_t amax[4][ROWS];
@@ -168,12 +193,13 @@ struct SwigluShared {
     u32x4 code[ROWS][8];
 };
 
-template <int THREADS, int ROWS, int M, int G, int GROUP, typename Row, typename Channel>
+template <int ROWS, int M, int G, int GROUP, typename Row, typename Channel>
 __device__ __forceinline__ void store_swiglu(SwigluShared<ROWS> &sh, float (&h)[M][G][4],
-                                             bool holds, int part, Row row, Channel channel, const ExpertProduct &p,
-                                             int row0, int n, int nblk)
+                                             int wave, int lane, int part, Row row,
+                                             Channel channel,
+                                             const ExpertProduct &p, int row0, int n, int nblk)
 {
-    const int lane = threadIdx.x & (kWave - 1);
+    const int thread = wave * kWave + lane;
 #pragma unroll
     for (int m = 0; m < M; ++m) {
         uint32_t amax = 0;
@@ -184,12 +210,11 @@ __device__ __forceinline__ void store_swiglu(SwigluShared<ROWS> &sh, float (&h)[
                 amax = max(amax, __float_as_uint(h[m][g][k]) & 0x7FFFFFFFu);
 #pragma unroll
         for (int x = GROUP; x < kWave; x *= 2) amax = max(amax, (uint32_t)__shfl_xor((int)amax, x));
-        if (holds && lane < GROUP) sh.amax[part][row(m)] = amax;
+        if (lane < GROUP) sh.amax[part][row(m)] = amax;
     }
     __syncthreads();
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-        if (!holds) break;
         const int r = row(m);
         uint32_t amax = 0;
 #pragma unroll
@@ -222,196 +247,54 @@ __device__ __forceinline__ void store_swiglu(SwigluShared<ROWS> &sh, float (&h)[
     }
     __syncthreads();
     const int I = p.n / 2;
-    for (int i = threadIdx.x; i < ROWS * 8; i += THREADS) {
+    for (int i = thread; i < ROWS * 8; i += kTileThreads) {
         const int r = i >> 3;
         if (r < n)
             *reinterpret_cast<u32x4 *>(p.h_q + (size_t)(row0 + r) * I + nblk * 128 + (i & 7) * 16) =
                 sh.code[r][i & 7];
     }
-    for (int r = threadIdx.x; r < n; r += THREADS)
+    for (int r = thread; r < n; r += kTileThreads)
         p.h_scale[(size_t)(row0 + r) * (I / 128) + nblk] = sh.scale[r];
     __syncthreads();
 }
 
-// Few rows per expert, where reading the weights bounds the product: every operand straight from
-// global memory to registers, no barrier in the product. MT tiles of 16 rows; a wavefront takes 4
-// tiles of 16 weight rows (gemm: 64 consecutive rows; SwiGLU: 32 gate rows and the same 32 up rows),
-// D blocks in flight. KS wavefronts share the same weight rows, each every KS-th block, and their
-// sums meet in LDS in order: with few tiles that keeps more of the chip's memory busy.
-template <int MT, bool SWIGLU, int D, int KS>
-__global__ __launch_bounds__(kThreads *KS) void expert_stream_kernel(ExpertProduct p)
-{
-    constexpr int kStreamThreads = kThreads * KS;
-    __shared__ TileTable table;
-    __shared__ SwigluShared<SWIGLU ? MT * 16 : 1> sh;
-    __shared__ f32x4 parts[KS > 1 ? KS - 1 : 1][KS > 1 ? 4 : 1][KS > 1 ? 4 * MT : 1][kWave];
-    const int lane = threadIdx.x & (kWave - 1);
-    const int wave = uniform(threadIdx.x / kWave) & 3, ks = uniform(threadIdx.x / kThreads);
-    const int r16 = lane & 15, g4 = lane >> 4;
-    const int nkb = p.H >> 7;
-    const int n_tiles = SWIGLU ? p.n / kTileN : (p.n + kTileN - 1) / kTileN;
-    const int ws_rows = (p.n + 127) >> 7;
-    const int total = build_table<kStreamThreads>(table, p, MT * 16) * n_tiles;
-    const TileRange mine = my_tiles(total);
-    for (int tile = mine.first; tile < mine.end; tile += mine.step) {
-        const Tile at = uniform(locate(table, p.E, tile, n_tiles, MT * 16));
-        const int e = at.e, row0 = at.row0, n = at.n, nblk = at.nblk;
-
-        // lane offsets of the weight rows (clamped) and of the tile's rows (clamped)
-        uint32_t woff[4], xoff[MT], soff[MT];
-        int wrow[4];
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-            wrow[nt] = SWIGLU ? (nt >> 1) * (p.n / 2) + nblk * 128 + wave * 32 + (nt & 1) * 16
-                              : nblk * kTileN + wave * 64 + nt * 16;
-            woff[nt] = (uint32_t)min(wrow[nt] + r16, p.n - 1) * p.H + g4 * 16;
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const int r = min(mt * 16 + r16, n - 1);
-            xoff[mt] = (uint32_t)r * p.H + g4 * 16;
-            soff[mt] = (uint32_t)r * nkb;
-        }
-        const uint8_t *w = p.w_q + (size_t)e * p.n * p.H;
-        const uint8_t *x = p.q + (size_t)row0 * p.H;
-        const float *xs = p.scale + (size_t)row0 * nkb;
-        const float *ws[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            ws[i] = p.w_scale + ((size_t)e * ws_rows + min(wrow[2 * i] >> 7, ws_rows - 1)) * nkb;
-
-        i32x8 wf[D][4], xf[D][MT];
-        float sx[D][MT], sw[D][2];
-        auto load = [&](int d, int kb) {
-            const uint8_t *wk = w + kb * 128, *xk = x + kb * 128;
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
-                wf[d][nt] = join(*reinterpret_cast<const i32x4 *>(wk + woff[nt]),
-                                 *reinterpret_cast<const i32x4 *>(wk + woff[nt] + 64));
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                xf[d][mt] = join(*reinterpret_cast<const i32x4 *>(xk + xoff[mt]),
-                                 *reinterpret_cast<const i32x4 *>(xk + xoff[mt] + 64));
-                sx[d][mt] = xs[kb + soff[mt]];
-            }
-            sw[d][0] = ws[0][kb];
-            sw[d][1] = ws[1][kb];
-        };
-        f32x4 acc[4][MT];
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) acc[nt][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (ks < nkb) {
-#pragma unroll
-            for (int d = 0; d < D; ++d) load(d, min(ks + d * KS, nkb - 1));
-            for (int kb = ks; kb < nkb; kb += D * KS) {
-#pragma unroll
-                for (int d = 0; d < D; ++d) {
-                    if (kb + d * KS < nkb) {
-                        Bf16Block xb[SWIGLU ? MT : 1];
-                        if constexpr (SWIGLU)
-#pragma unroll
-                            for (int mt = 0; mt < MT; ++mt) xb[mt] = bf16_block(xf[d][mt]);
-#pragma unroll
-                        for (int nt = 0; nt < 4; ++nt) {
-                            Bf16Block wb;
-                            if constexpr (SWIGLU) wb = bf16_block(wf[d][nt]);
-#pragma unroll
-                            for (int mt = 0; mt < MT; ++mt) {
-                                f32x4 v;
-                                if constexpr (SWIGLU) v = mfma_exact(wb, xb[mt]);
-                                else v = mfma_e4m3(wf[d][nt], xf[d][mt]);
-                                const float s = sx[d][mt] * sw[d][nt >> 1];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    acc[nt][mt][k] = __builtin_fmaf(s, v[k], acc[nt][mt][k]);
-                            }
-                        }
-                    }
-                    load(d, min(kb + (d + D) * KS, nkb - 1));
-                }
-            }
-        }
-        if constexpr (KS > 1) {
-            if (ks > 0)
-#pragma unroll
-                for (int i = 0; i < 4 * MT; ++i) parts[ks - 1][wave][i][lane] = acc[i / MT][i % MT];
-            __syncthreads();
-            if (ks == 0)
-#pragma unroll
-                for (int i = 0; i < 4 * MT; ++i)
-#pragma unroll
-                    for (int j = 0; j < KS - 1; ++j) acc[i / MT][i % MT] += parts[j][wave][i][lane];
-            __syncthreads();
-        }
-
-        if constexpr (SWIGLU) {
-            float h[MT][2][4];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int g = 0; g < 2; ++g)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        h[mt][g][k] = swiglu(acc[g][mt][k], acc[g + 2][mt][k]);
-            store_swiglu<kStreamThreads, MT * 16, MT, 2, 16>(
-                sh, h, ks == 0, wave, [&](int m) { return m * 16 + r16; },
-                [&](int g) { return g * 16 + g4 * 4; }, p, row0, n, nblk);
-        } else if (ks == 0) {
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                const int r = mt * 16 + r16;
-                uint16_t *y = p.y + (size_t)(row0 + r) * p.n;
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    const int c = wrow[nt] + g4 * 4;
-                    // n % 8 == 0: the four channels together
-                    if (r < n && c < p.n)
-                        *reinterpret_cast<uint2 *>(y + c) = bf16_pairs(
-                            acc[nt][mt][0], acc[nt][mt][1], acc[nt][mt][2], acc[nt][mt][3]);
-                }
-            }
-        }
-    }
-}
-
-// Many rows per expert: tiles of 128 rows x 256 weight rows (SwiGLU: 128 gate and the same 128 up
-// rows), one workgroup of 8 wavefronts per CU that walks its tiles as one stream of blocks (128
-// channels of a tile each); a wavefront multiplies 64 rows by 64 weight rows. Two wavefronts per
-// SIMD share its issue slots: alone, a wavefront's scaled sums, LDS reads and products queue up. Loads run two blocks ahead of LDS and three ahead of the products,
-// across tiles, so that neither a block nor a tile waits for memory. A load instruction covers 8
-// whole 128-byte row segments, 8 lanes a row: the vector cache takes one access per 128 bytes (in
-// the matrix instruction's lane order, 16 rows side by side, it took one per 16 bytes, and that
-// bounded the kernel: 1.35 ms for 65536 rows x 4096 x 4096). From registers a block goes to one of
-// two LDS buffers, an eighth per wavefront. The row scales of 16 blocks are staged together, one
-// panel ahead. One barrier per block.
-constexpr int kTileThreads = 512;
-constexpr int kTileM = 128;
-[[maybe_unused]] constexpr int kMT = 2;     // tiles of 32 rows of a wavefront
+// Tiles of 64 * MT rows x 256 weight rows (SwiGLU: 128 gate and the same 128 up rows), one workgroup
+// of 8 wavefronts per CU that walks its tiles as one stream of blocks (128 channels of a tile each);
+// a wavefront multiplies 32 * MT rows by 64 weight rows. Two wavefronts per SIMD share its issue
+// slots: alone, a wavefront's scaled sums, LDS reads and products queue up. Loads run ahead of LDS by
+// as many blocks as the registers hold (kStage) and of the products by one more, across tiles, so
+// that neither a block nor a tile waits for memory. A load instruction covers 8 whole 128-byte row
+// segments, 8 lanes a row: the vector cache takes one access per 128 bytes (in the matrix
+// instruction's lane order, 16 rows side by side, it took one per 16 bytes, and that bounded every
+// size: with operands straight from global memory to registers, 65536 rows x 4096 x 4096 took
+// 4.7 ms, and 640 rows over 128 experts, 1536 x 2048, 84 us against 76 us). From registers a block
+// goes to one of two LDS buffers, an eighth per wavefront. The row scales of 16 blocks are staged
+// together, one panel ahead. One barrier per block.
 constexpr int kPanel = 16;         // blocks whose scales are staged together
 constexpr int kList = 256;         // tiles of a workgroup looked up together
 
 // A buffer of `bytes` from p: loads take a lane offset and a uniform one, and give 0 past the end.
-[[maybe_unused]] __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, uint32_t bytes)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, uint32_t bytes)
 {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)bytes, 0x00027000);
 }
 
-[[maybe_unused]] __device__ __forceinline__ i32x4 buffer_load16(__amdgpu_buffer_rsrc_t b, int lane_off, int off)
+__device__ __forceinline__ i32x4 buffer_load16(__amdgpu_buffer_rsrc_t b, int lane_off, int off)
 {
     return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, lane_off, off, 0));
 }
 
-// v, but what is computed from it is worked out where it is used and not kept in registers.
-[[maybe_unused]] __device__ __forceinline__ int fresh(int v)
+// The lane, counted anew: what is computed from it is worked out where it is used, and takes no
+// register through the product (which needs them all).
+__device__ __forceinline__ int lane_now()
 {
-    asm volatile("" : "+v"(v));
-    return v;
+    int l;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(l));
+    return l;
 }
 
 // Meet the other wavefronts with LDS settled; loads in flight stay in flight.
-[[maybe_unused]] __device__ __forceinline__ void meet()
+__device__ __forceinline__ void meet()
 {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
     __builtin_amdgcn_s_waitcnt(0xC07F);        // lgkmcnt(0)
@@ -419,8 +302,9 @@ constexpr int kList = 256;         // tiles of a workgroup looked up together
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-template <bool SWIGLU>
+template <bool SWIGLU, int MT>
 struct TileShared {
+    static constexpr int kTileM = kTileRows<MT>;
     u32x4 x[2][kTileM * 8];
     u32x4 w[2][kTileN * 8];
     float xscale[2][kPanel][kTileM + 1];
@@ -429,20 +313,19 @@ struct TileShared {
     SwigluShared<SWIGLU ? kTileM : 1> h;
 };
 
-template <bool SWIGLU>
-__global__ __launch_bounds__(kTileThreads) void expert_tile_kernel(ExpertProduct p)
+template <bool SWIGLU, int MT>
+__device__ __forceinline__ void run_tiles(const ExpertProduct &p, const TileTable &table,
+                                          TileShared<SWIGLU, MT> &sh, int row_tiles)
 {
-#if defined(__HIP_DEVICE_COMPILE__)            // buffer descriptors exist on the device only
-    __shared__ TileTable table;
-    __shared__ TileShared<SWIGLU> sh;
+    constexpr int kTileM = kTileRows<MT>;
+    constexpr bool kAhead = !SWIGLU && MT > 1; // registers for the rows one tile of 32 ahead
     const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
     const int wm = wave & 1, wn = wave >> 1;   // the wavefront's 64 rows and its weight rows
     const int r32 = lane & 31, half = lane >> 5;
     const int nkb = p.H >> 7;
     const int n_tiles = (p.n + kTileN - 1) / kTileN;
     const int ws_rows = (p.n + 127) >> 7;
-    const int total = build_table<kTileThreads>(table, p, kTileM) * n_tiles;
-    const TileRange mine = my_tiles(total);
+    const TileRange mine = my_tiles(row_tiles * n_tiles);
     // Chunk c (16 bytes) of row r is kept at place c ^ swizzle(r) of the row's eight: the lanes that
     // LDS serves together (8 consecutive rows, and the same 16 further on) then touch all banks.
     // A lane's j-th chunk of a block is 2 * j + half of row lane & 31.
@@ -453,7 +336,7 @@ __global__ __launch_bounds__(kTileThreads) void expert_tile_kernel(ExpertProduct
     struct {
         int tile, kb;
         __amdgpu_buffer_rsrc_t w, x;
-        int woff[4], xoff[2];
+        int woff[4], xoff[MT];
     } ld;
     // Weight row i of a tile: SwiGLU keeps 32 gate rows and the same 32 up rows together, so that
     // every wavefront has a tile of each.
@@ -471,21 +354,21 @@ __global__ __launch_bounds__(kTileThreads) void expert_tile_kernel(ExpertProduct
         ld.kb = 0;
         ld.w = buffer(p.w_q + (size_t)t.e * p.n * p.H, (uint32_t)p.n * p.H);
         ld.x = buffer(p.q + (size_t)t.row0 * p.H, (uint32_t)t.n * p.H);
-        const int l = fresh(lane);
+        const int l = lane_now();
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             ld.woff[j] = min(weight_row(t.nblk, wave * 32 + j * 8 + (l >> 3)), p.n - 1) * p.H +
                          (l & 7) * 16;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            ld.xoff[j] = min(wave * 16 + j * 8 + (l >> 3), t.n - 1) * p.H + (l & 7) * 16;
+        for (int j = 0; j < MT; ++j)
+            ld.xoff[j] = min(wave * (8 * MT) + j * 8 + (l >> 3), t.n - 1) * p.H + (l & 7) * 16;
     };
 
     constexpr int kStage = SWIGLU ? 1 : 2;     // blocks in registers on their way to LDS
-    i32x4 wr[kStage][4], xr[kStage][2];
+    i32x4 wr[kStage][4], xr[kStage][MT];
     i32x4 wf[2][4];                            // the wavefront's weights of a block: [tile][chunk]
-    f32x16 acc[2][kMT];
-    constexpr int kXf = SWIGLU ? 1 : 2;
+    f32x16 acc[2][MT];
+    constexpr int kXf = kAhead ? 2 : 1;
     i32x4 xf[kXf][4];
     constexpr int kWs = SWIGLU ? 2 : 1;
     float xs[2];                               // row scales
@@ -496,12 +379,13 @@ __global__ __launch_bounds__(kTileThreads) void expert_tile_kernel(ExpertProduct
     auto load_w = [&](int d, int j) { wr[d % kStage][j] = buffer_load16(ld.w, ld.woff[j], ld.kb * 128); };
     auto load_x = [&](int d, int j) { xr[d % kStage][j] = buffer_load16(ld.x, ld.xoff[j], ld.kb * 128); };
     // the lane's place in LDS: its row of each 8, its chunk (rows 16 further on swap neighbours)
-    const int put0 = (lane >> 3) * 8 + ((lane & 7) ^ (lane >> 3));
-    auto put_w = [&](int d, int j) {
+    auto place = [](int l) { return (l >> 3) * 8 + ((l & 7) ^ (l >> 3)); };
+    const int put0 = place(lane);
+    auto put_w = [&](int d, int j, int put0) {
         sh.w[d][wave * 256 + j * 64 + (put0 ^ (j >> 1))] = __builtin_bit_cast(u32x4, wr[d % kStage][j]);
     };
-    auto put_x = [&](int d, int j) {
-        sh.x[d][wave * 128 + j * 64 + (put0 ^ (wave & 1))] = __builtin_bit_cast(u32x4, xr[d % kStage][j]);
+    auto put_x = [&](int d, int j, int put0) {
+        sh.x[d][(wave * MT + j) * 64 + (put0 ^ ((wave * MT >> 1) & 1))] = __builtin_bit_cast(u32x4, xr[d % kStage][j]);
     };
     auto advance = [&](int tiles) {            // past the last block: that block again
         if (++ld.kb == nkb) {
@@ -511,7 +395,7 @@ __global__ __launch_bounds__(kTileThreads) void expert_tile_kernel(ExpertProduct
     };
     auto panel_load = [&](int i, int kb0) {
         const Tile t = at(i);
-        const int l = fresh(wave * kWave + lane);
+        const int l = wave * kWave + lane_now();
         const float *src = p.scale + (size_t)t.row0 * nkb + min(kb0 + (l & 15), nkb - 1);
 #pragma unroll
         for (int k = 0; k < kPer; ++k) ps[k] = src[(size_t)min(k * 32 + (l >> 4), t.n - 1) * nkb];
@@ -520,13 +404,13 @@ __global__ __launch_bounds__(kTileThreads) void expert_tile_kernel(ExpertProduct
         pw = p.w_scale[((size_t)t.e * ws_rows + blk) * nkb + min(kb0 + (l & 15), nkb - 1)];
     };
     auto panel_store = [&](int to) {
-        const int l = fresh(wave * kWave + lane);
+        const int l = wave * kWave + lane_now();
 #pragma unroll
         for (int k = 0; k < kPer; ++k) sh.xscale[to][l & 15][k * 32 + (l >> 4)] = ps[k];
         if (l < 32) sh.wscale[to][l & 15][l >> 4] = pw;
     };
     auto read_row = [&](int d, int mt) {       // the lane's chunks of row tile mt
-        const i32x4 *x = reinterpret_cast<const i32x4 *>(sh.x[d]) + (wm * kMT + mt) * 256 + row_at;
+        const i32x4 *x = reinterpret_cast<const i32x4 *>(sh.x[d]) + (wm * MT + mt) * 256 + row_at;
 #pragma unroll
         for (int j = 0; j < 4; ++j) xf[mt % kXf][j] = x[(2 * j + half) ^ row_swizzle];
     };
@@ -544,7 +428,7 @@ __global__ __launch_bounds__(kTileThreads) void expert_tile_kernel(ExpertProduct
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[nt][mt][i] = 0.0f;
     };
@@ -562,15 +446,26 @@ __global__ __launch_bounds__(kTileThreads) void expert_tile_kernel(ExpertProduct
         read_w(d, 0);
         read_w(d, 1);
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
-            // the row tile to read: SwiGLU, short of registers, this one; else the one after, the
-            // last of them the next block's
-            const int to = SWIGLU ? mt : mt + 1;
-            if constexpr (SWIGLU) {
+        for (int mt = 0; mt < MT; ++mt) {
+            // the rows read: this tile of 32, or the one after it, of the last one the next block's
+            const int to = kAhead ? mt + 1 : mt;
+            if constexpr (!kAhead) {
                 read_row(d, mt);
-                xs[mt] = sh.xscale[par][kb & (kPanel - 1)][(wm * kMT + mt) * 32 + r32];
+                xs[mt] = sh.xscale[par][kb & (kPanel - 1)][(wm * MT + mt) * 32 + r32];
             }
-            if (mt == kMT - 1) {
+            if (mt == 0) {
+#pragma unroll
+                for (int j = 0; j < MT; ++j) {
+                    put_x(dn, j, put0);
+                    load_x(dn, j);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    put_w(dn, j, put0);
+                    load_w(dn, j);
+                }
+            }
+            if (mt == MT - 1) {
                 if (b_next == 0) {
                     par ^= 1;
                     panel_store(par);
@@ -578,22 +473,10 @@ __global__ __launch_bounds__(kTileThreads) void expert_tile_kernel(ExpertProduct
                 meet();
                 read_ws(ws_next, b_next);
             }
-            if constexpr (!SWIGLU) {
-                read_row(to < kMT ? d : dn, to & (kMT - 1));
-                xs[to & 1] = sh.xscale[par][to < kMT ? kb & (kPanel - 1) : b_next]
-                                      [(wm * kMT + (to & (kMT - 1))) * 32 + r32];
-            }
-            if (mt < kMT - 1) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    put_x(dn, j);
-                    load_x(dn, j);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    put_w(dn, j);
-                    load_w(dn, j);
-                }
+            if constexpr (kAhead) {
+                read_row(to < MT ? d : dn, to & (MT - 1));
+                xs[to & 1] = sh.xscale[par][to < MT ? kb & (kPanel - 1) : b_next]
+                                      [(wm * MT + (to & (MT - 1))) * 32 + r32];
             }
             f32x16 v[2] = {};
             if constexpr (SWIGLU) {
@@ -636,21 +519,21 @@ __global__ __launch_bounds__(kTileThreads) void expert_tile_kernel(ExpertProduct
     };
     auto finish = [&](int tile) {              // the tile's output
         const Tile t = at(tile);
-        const int l = fresh(lane);
+        const int l = lane_now();
         // element i of a lane is channel (i >> 2) * 8 + half * 4 + (i & 3) of row lane & 31
         if constexpr (SWIGLU) {
-            float h[kMT][4][4];
+            float h[MT][4][4];
 #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) h[mt][i >> 2][i & 3] = swiglu(acc[0][mt][i], acc[1][mt][i]);
-            store_swiglu<kTileThreads, kTileM, kMT, 4, 32>(
-                sh.h, h, true, wn, [&](int m) { return (wm * kMT + m) * 32 + (l & 31); },
+            store_swiglu<kTileM, MT, 4, 32>(
+                sh.h, h, wave, l, wn, [&](int m) { return (wm * MT + m) * 32 + (l & 31); },
                 [&](int g) { return g * 8 + (l >> 5) * 4; }, p, t.row0, t.n, t.nblk);
         } else {
 #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) {
-                const int r = (wm * kMT + mt) * 32 + (l & 31);
+            for (int mt = 0; mt < MT; ++mt) {
+                const int r = (wm * MT + mt) * 32 + (l & 31);
                 uint16_t *y = p.y + (size_t)(t.row0 + r) * p.n;
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt)
@@ -672,10 +555,11 @@ __global__ __launch_bounds__(kTileThreads) void expert_tile_kernel(ExpertProduct
     for (int k = 0; k < kPer; ++k) ps[k] = 0.0f;
     for (int first = mine.first; first < mine.end; first += kList * mine.step) {
         const int tiles = min((mine.end - first + mine.step - 1) / mine.step, kList);
-        if ((int)threadIdx.x < tiles) {
-            const int i = fresh(threadIdx.x);
-            const Tile t = locate(table, p.E, first + i * mine.step, fresh(n_tiles), kTileM);
-            sh.list[threadIdx.x] = int4{t.e, t.row0, t.n, t.nblk};
+        if (const int i = wave * kWave + lane_now(); i < tiles) {
+            int columns = n_tiles;
+            asm volatile("" : "+s"(columns));  // nothing of its divisions stays in registers
+            const Tile t = locate(table, p.E, first + i * mine.step, columns, kTileM);
+            sh.list[i] = int4{t.e, t.row0, t.n, t.nblk};
         }
         __syncthreads();
         enter(0);
@@ -683,7 +567,7 @@ __global__ __launch_bounds__(kTileThreads) void expert_tile_kernel(ExpertProduct
         panel_load(0, 0);
         auto load = [&](int d) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) load_x(d, j);
+            for (int j = 0; j < MT; ++j) load_x(d, j);
 #pragma unroll
             for (int j = 0; j < 4; ++j) load_w(d, j);
             advance(tiles);
@@ -691,16 +575,17 @@ __global__ __launch_bounds__(kTileThreads) void expert_tile_kernel(ExpertProduct
         load(0);
         if constexpr (kStage == 2) load(1);
         panel_store(0);
+        const int put1 = place(lane_now());
 #pragma unroll
-        for (int j = 0; j < 2; ++j) put_x(0, j);
+        for (int j = 0; j < MT; ++j) put_x(0, j, put1);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) put_w(0, j);
+        for (int j = 0; j < 4; ++j) put_w(0, j, put1);
         load(0);
         meet();
         read_ws(ws, 0);
         clear();
-        if constexpr (!SWIGLU) read_row(0, 0);
-        xs[0] = sh.xscale[0][0][wm * kMT * 32 + r32];
+        if constexpr (kAhead) read_row(0, 0);
+        xs[0] = sh.xscale[0][0][wm * MT * 32 + (lane_now() & 31)];
         __builtin_amdgcn_sched_barrier(0);
         int tile = 0, kb = 0;
         auto next = [&](int d) {               // a block; false after the last one
@@ -713,49 +598,35 @@ __global__ __launch_bounds__(kTileThreads) void expert_tile_kernel(ExpertProduct
         while (next(0) && next(1)) {}
         meet();                                // the list and LDS are free again
     }
+}
+#endif
+
+template <bool SWIGLU>
+__global__ __launch_bounds__(kTileThreads) void expert_tile_kernel(ExpertProduct p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    __shared__ TileTable table;
+    __shared__ union {
+        TileShared<SWIGLU, 1> low;
+        TileShared<SWIGLU, 2> high;
+    } sh;
+    const Tiling t = build_table(table, p, (p.n + kTileN - 1) / kTileN);
+    if (t.mt == 1) run_tiles<SWIGLU, 1>(p, table, sh.low, t.total);
+    else run_tiles<SWIGLU, 2>(p, table, sh.high, t.total);
 #else
     (void)p;
 #endif
 }
 
-#ifndef EP_EXPERT_MT1
-#define EP_EXPERT_MT1 12
-#endif
-#ifndef EP_EXPERT_MT2
-#define EP_EXPERT_MT2 24
-#endif
-#ifndef EP_EXPERT_TILE
-#define EP_EXPERT_TILE 40
-#endif
-#ifndef EP_EXPERT_KS
-#define EP_EXPERT_KS 512
-#endif
-#ifndef EP_EXPERT_D1
-#define EP_EXPERT_D1 1
-#endif
+// One workgroup per CU, or as many as there can be tiles of 64 rows.
 template <bool SWIGLU>
 hipError_t launch_product(const ExpertProduct &p, hipStream_t stream)
 {
     if (p.pairs == 0 || (p.offset && p.rows == 0)) return hipSuccess;
-    const int64_t n_tiles = (p.n + kTileN - 1) / kTileN;
-    const int mean = (int)(((int64_t)p.pairs + p.E - 1) / p.E);
-    // the grid: at most `most` workgroups, no more than there can be tiles of `bm` rows
-    auto grid = [&](int bm, int64_t most) {
-        const int64_t experts = p.pairs < p.E ? p.pairs : p.E;
-        const int64_t tiles = (p.pairs / bm + experts) * n_tiles;
-        return dim3((unsigned)(tiles < most ? (tiles + 7) / 8 * 8 : most));
-    };
-    const dim3 block(kThreads);
-    if (mean >= EP_EXPERT_TILE)
-        return launch(expert_tile_kernel<SWIGLU>, grid(kTileM, 256), dim3(kTileThreads), 0, stream, p);
-    if (mean > EP_EXPERT_MT2)
-        return launch(expert_stream_kernel<4, SWIGLU, 1, 1>, grid(64, 512), block, 0, stream, p);
-    if (mean > EP_EXPERT_MT1)
-        return launch(expert_stream_kernel<2, SWIGLU, 1, 1>, grid(32, 512), block, 0, stream, p);
-    if (grid(16, 1 << 20).x < EP_EXPERT_KS)
-        return launch(expert_stream_kernel<1, SWIGLU, 1, 4>, grid(16, 512), dim3(4 * kThreads), 0,
-                      stream, p);
-    return launch(expert_stream_kernel<1, SWIGLU, EP_EXPERT_D1, 1>, grid(16, 1024), block, 0, stream, p);
+    const int64_t experts = p.pairs < p.E ? p.pairs : p.E;
+    const int64_t tiles = (p.pairs / kTileRows<1> + experts) * ((p.n + kTileN - 1) / kTileN);
+    const dim3 grid((unsigned)(tiles < 256 ? (tiles + 7) / 8 * 8 : 256));
+    return launch(expert_tile_kernel<SWIGLU>, grid, dim3(kTileThreads), 0, stream, p);
 }
 
 }  // namespace
