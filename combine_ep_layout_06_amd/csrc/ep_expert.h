@@ -21,7 +21,7 @@ struct ExpertProduct {
     uint8_t *h_q;
     float *h_scale;
     int E, C, rows, H, n;
-    int pairs;                // pairs laid out: chooses the tile size and the grid, nothing else
+    int pairs;                // pairs laid out: chooses the grid, nothing else
 };
 
 hipError_t launch_expert_gemm_fp8(const ExpertProduct &p, hipStream_t stream);
@@ -65,23 +65,11 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// D = A * B for a 16 x 128 tile of E4M3 codes A and a 128 x 16 tile B (fp32 result, matrix cores).
-// Lane l holds 32 codes of row (column) l & 15. Which 32 of the 128 products' indices a lane
-// group l >> 4 holds does not matter as long as A and B agree: here the 16-byte chunks l >> 4
-// and (l >> 4) + 4 of the 128-byte row segment, so that a load instruction covers whole 64-byte
-// pieces of each row. Result: lane l, element r is D[(l >> 4) * 4 + r][l & 15].
-__device__ __forceinline__ f32x4 mfma_e4m3(i32x8 a, i32x8 b)
-{
-    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
-}
-
-// The same product of the same codes, exact: the codes as bf16 (every E4M3 value is one) through
-// the bf16 matrix instructions, whose sums lose nothing above fp32's own rounding. The FP8
-// instruction aligns each group of products to the largest and cuts what lies 14 binary places
-// below it: measured 1.3e-5 (2e-5 with outliers) of the result's norm, against 1e-8 here, at
-// twice this one's rate. Good enough in front of a rounding to bf16 (2e-3), not in front of an
-// fp32 output.
+// Two ways to multiply E4M3 codes. The FP8 matrix instruction aligns each group of products to the
+// largest and cuts what lies 14 binary places below it: measured 1.3e-5 (2e-5 with outliers) of the
+// result's norm, good enough in front of a rounding to bf16 (2e-3), not in front of an fp32 output.
+// The codes as bf16 (every E4M3 value is one) through the bf16 matrix instructions lose nothing above
+// fp32's own rounding (1e-8), at half the rate.
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -93,25 +81,6 @@ __device__ __forceinline__ bf16x8 bf16_of_e4m3(int c0, int c1)
     const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c1, 1.0f, false);
     const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c1, 1.0f, true);
     return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
-struct Bf16Block {
-    bf16x8 v[4];
-};
-
-__device__ __forceinline__ Bf16Block bf16_block(i32x8 c)
-{
-    return Bf16Block{{bf16_of_e4m3(c[0], c[1]), bf16_of_e4m3(c[2], c[3]),
-                      bf16_of_e4m3(c[4], c[5]), bf16_of_e4m3(c[6], c[7])}};
-}
-
-__device__ __forceinline__ f32x4 mfma_exact(const Bf16Block &a, const Bf16Block &b)
-{
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], v, 0, 0, 0);
-    return v;
 }
 
 __device__ __forceinline__ i32x8 join(i32x4 lo, i32x4 hi)

@@ -320,7 +320,7 @@ __device__ __forceinline__ void run_tiles(const ExpertProduct &p, const TileTabl
     constexpr int kTileM = kTileRows<MT>;
     constexpr bool kAhead = !SWIGLU && MT > 1; // registers for the rows one tile of 32 ahead
     const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
-    const int wm = wave & 1, wn = wave >> 1;   // the wavefront's 64 rows and its weight rows
+    const int wm = wave & 1, wn = wave >> 1;   // the wavefront's rows and weight rows
     const int r32 = lane & 31, half = lane >> 5;
     const int nkb = p.H >> 7;
     const int n_tiles = (p.n + kTileN - 1) / kTileN;
@@ -364,7 +364,9 @@ __device__ __forceinline__ void run_tiles(const ExpertProduct &p, const TileTabl
             ld.xoff[j] = min(wave * (8 * MT) + j * 8 + (l >> 3), t.n - 1) * p.H + (l & 7) * 16;
     };
 
-    constexpr int kStage = SWIGLU ? 1 : 2;     // blocks in registers on their way to LDS
+    // blocks in registers on their way to LDS: as many as there is room for, two at most (four
+    // changed nothing: one tile of 64 rows is bound by LDS, 1100 cycles a block of 136 KB)
+    constexpr int kStage = SWIGLU && MT == 2 ? 1 : 2;
     i32x4 wr[kStage][4], xr[kStage][MT];
     i32x4 wf[2][4];                            // the wavefront's weights of a block: [tile][chunk]
     f32x16 acc[2][MT];
