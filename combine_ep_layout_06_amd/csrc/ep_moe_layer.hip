@@ -24,8 +24,7 @@ namespace ep {
 namespace {
 
 constexpr int kUpWaves = 4;
-constexpr int kSmallWaves = 16;               // at most, in the small down kernel
-static_assert(kMoeSmallPairs <= kWave, "a pair per lane");
+static_assert(kMoeSmallPairs <= 16, "a wavefront per pair, one tile of rows per expert");
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
@@ -87,7 +86,7 @@ struct Rows {
     int first, n;
 };
 
-// At most 64 pairs: lane l holds the id of pair l (-1: none). False if pair i names no expert or one
+// At most kMoeSmallPairs pairs: lane l holds the id of pair l (-1: none). False if pair i names no expert or one
 // that an earlier pair names; else the expert's rows, and in `pair` the lane's pair: lane r gets the
 // pair of row r (r < n).
 __device__ __forceinline__ bool small_rows(int id, int E, int i, int &e, Rows &r, int &pair)
@@ -238,7 +237,7 @@ __device__ __forceinline__ void up_pass(UpShared<NI> &sh, const MoeLayer &p, int
 }
 
 // blockIdx.x: NI * 16 channels of h; blockIdx.y: the number of an expert among those named (SMALL,
-// at most 64 pairs: a pair, whose expert is taken if no earlier pair names it).
+// at most kMoeSmallPairs pairs: a pair, whose expert is taken if no earlier pair names it).
 template <bool FP8, int NI, bool SMALL>
 __global__ __launch_bounds__(kUpWaves *kWave, 2) void moe_up_kernel(MoeLayer p)
 {
@@ -299,17 +298,18 @@ __global__ __launch_bounds__(kUpWaves *kWave, 2) void moe_up_kernel(MoeLayer p)
     // (bf16) are best (1: 32 tokens bf16 222 us, 3: 207 us; 128 tokens FP8 171 us with 2, 180 with 3)
     constexpr int kAhead = NI == 1 ? (FP8 ? 4 : 8) : FP8 ? 2 : 3;
     int row0 = 0;
-    while (rows.n - row0 > 16) {
-        up_pass<FP8, NI, 2, 1>(sh, p, e, c0, rows, row0, min(rows.n - row0, 32));
-        row0 += 32;
-    }
+    if constexpr (!SMALL)
+        while (rows.n - row0 > 16) {
+            up_pass<FP8, NI, 2, 1>(sh, p, e, c0, rows, row0, min(rows.n - row0, 32));
+            row0 += 32;
+        }
     if (row0 < rows.n)
         up_pass<FP8, NI, 1, kAhead>(sh, p, e, c0, rows, row0, rows.n - row0);
 }
 
-// COLS output columns (weight rows) of an expert for MT tiles of 16 of its rows; the sums go to row
+// 16 output columns (weight rows) of an expert for MT tiles of 16 of its rows; the sums go to row
 // `pair` of y. The loads of the weights run DW steps ahead, those of h DH (DW a multiple of it).
-template <bool FP8, int COLS, int MT, int DW, int DH>
+template <bool FP8, int MT, int DW, int DH>
 __device__ __forceinline__ void down_pass(float *y, int stride, const MoeLayer &p, int e, int c0,
                                           const Rows &rows, int row0, const int (&pair)[MT])
 {
@@ -318,7 +318,7 @@ __device__ __forceinline__ void down_pass(float *y, int stride, const MoeLayer &
     const int r16 = lane & 15, g4 = lane >> 4;
     const int row_bytes = FP8 ? p.I : 2 * p.I;
     const uint8_t *w = static_cast<const uint8_t *>(p.w2) + (size_t)e * p.H * row_bytes;
-    const uint32_t woff = (uint32_t)(c0 + (r16 & (COLS - 1))) * row_bytes + g4 * 16;
+    const uint32_t woff = (uint32_t)(c0 + r16) * row_bytes + g4 * 16;
     const uint8_t *h = reinterpret_cast<const uint8_t *>(p.h + (size_t)rows.first * 2 * p.I);
     const int n = rows.n, nsteps = p.I / kS;
     // a lane's place in its chunks of h: chunk c of a step is 2 * n * 16 bytes further per c
@@ -384,41 +384,41 @@ __device__ __forceinline__ void down_pass(float *y, int stride, const MoeLayer &
     }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
-        if (row0 + mt * 16 + r16 < n && g4 * 4 < COLS)
+        if (row0 + mt * 16 + r16 < n)
             *reinterpret_cast<f32x4 *>(y + (size_t)pair[mt] * stride + g4 * 4) = acc[mt];
 }
 
-// At most 64 pairs. A workgroup: COLS columns of out for all tokens. Its wavefronts take the pairs
-// in turn (each named expert once); y of every pair meets in LDS, and the weighted sums run over j
-// in order.
-template <bool FP8, int COLS>
-__global__ __launch_bounds__(kSmallWaves *kWave) void moe_small_down_kernel(MoeLayer p)
+// At most kMoeSmallPairs pairs. A workgroup: 16 columns of out for all tokens (8, for twice the
+// workgroups, won nowhere: one token, H = 4096, FP8 22.3 against 19.4 us; H = 1024 13.9 against 13.6).
+// A wavefront takes a pair's expert if no earlier pair names it; y of every pair meets in LDS, and
+// the weighted sums run over j in order.
+constexpr int kCols = 16;
+
+template <bool FP8>
+__global__ __launch_bounds__(kMoeSmallPairs *kWave) void moe_small_down_kernel(MoeLayer p)
 {
-    __shared__ float y[kMoeSmallPairs * COLS], weight[kMoeSmallPairs];
+    __shared__ float y[kMoeSmallPairs * kCols], weight[kMoeSmallPairs];
     __shared__ bool names[kMoeSmallPairs];
     const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
-    const int pairs = p.T * p.K, nthreads = blockDim.x, c0 = blockIdx.x * COLS;
+    const int pairs = p.T * p.K, nthreads = blockDim.x, c0 = blockIdx.x * kCols;
     const int id = lane < pairs ? p.idx[lane] : -1;
-    if (wave == 0) {
+    if (threadIdx.x < kMoeSmallPairs) {
         names[lane] = (unsigned)id < (unsigned)p.E;
         weight[lane] = lane < pairs ? p.topk_w[lane] : 0.0f;
     }
-    for (int i = wave; i < pairs; i += nthreads / kWave) {
-        Rows rows;
-        int e, pair;
-        if (!small_rows(id, p.E, i, e, rows, pair)) continue;
-        for (int row0 = 0; row0 < rows.n; row0 += 16) {
-            const int of[1] = {__shfl(pair, row0 + (lane & 15))};
-            down_pass<FP8, COLS, 1, 4, 1>(y, COLS, p, e, c0, rows, row0, of);
-        }
+    Rows rows;
+    int e, pair;
+    if (wave < pairs && small_rows(id, p.E, wave, e, rows, pair)) {
+        const int of[1] = {__shfl(pair, lane & 15)};
+        down_pass<FP8, 1, 4, 1>(y, kCols, p, e, c0, rows, 0, of);
     }
     __syncthreads();
-    for (int f = threadIdx.x; f < p.T * COLS; f += nthreads) {
-        const int t = f / COLS, c = f % COLS;
+    for (int f = threadIdx.x; f < p.T * kCols; f += nthreads) {
+        const int t = f / kCols, c = f % kCols;
         float acc = 0.0f;
         for (int j = 0; j < p.K; ++j) {
             const int i = t * p.K + j;
-            if (names[i]) acc = __builtin_fmaf(weight[i], y[i * COLS + c], acc);
+            if (names[i]) acc = __builtin_fmaf(weight[i], y[i * kCols + c], acc);
         }
         p.out[(size_t)t * p.H + c0 + c] = (uint16_t)bf16_rne(acc);
     }
@@ -442,12 +442,12 @@ __global__ __launch_bounds__(4 * kWave, 4) void moe_down_kernel(MoeLayer p)
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
             of[mt] = p.order[rows.first + min(row0 + mt * 16 + r16, rows.n - 1)];
-        down_pass<FP8, 16, 2, 1, 1>(p.y + c0, p.H, p, e, c0, rows, row0, of);
+        down_pass<FP8, 2, 1, 1>(p.y + c0, p.H, p, e, c0, rows, row0, of);
         row0 += 32;
     }
     if (row0 < rows.n) {
         const int of[1] = {p.order[rows.first + min(row0 + r16, rows.n - 1)]};
-        down_pass<FP8, 16, 1, 3, 1>(p.y + c0, p.H, p, e, c0, rows, row0, of);
+        down_pass<FP8, 1, 3, 1>(p.y + c0, p.H, p, e, c0, rows, row0, of);
     }
 }
 
@@ -486,7 +486,8 @@ hipError_t launch_layer(const MoeLayer &p, hipStream_t stream)
     const int pairs = p.T * p.K;
     const int named = SMALL ? pairs : pairs < p.E ? pairs : p.E;       // at most
     const dim3 block(kUpWaves * kWave);
-    // 32 channels of h per workgroup, 16 where that would leave CUs without one (64 held more
+    // 32 channels of h per workgroup, 16 where that would leave the chip half empty (2 tokens of 8
+    // experts, I = 768, FP8: 27.2 us with 16, 28.6 with 32; 16 tokens: 109 and 90; 64 held more
     // registers and lost: 32 tokens bf16 227 against 212 us)
     const long tiles = (long)named * (p.I / 16);
     hipError_t e;
@@ -496,12 +497,8 @@ hipError_t launch_layer(const MoeLayer &p, hipStream_t stream)
         e = launch(moe_up_kernel<FP8, 1, SMALL>, dim3(p.I / 16, named), block, 0, stream, p);
     if (e != hipSuccess) return e;
     if constexpr (SMALL) {
-        const int waves = pairs < 4 ? 4 : pairs > kSmallWaves ? kSmallWaves : pairs;
-        // 8 columns per workgroup where 16 would leave half of the 256 CUs without one
-        if (p.H / 16 >= 256)
-            return launch(moe_small_down_kernel<FP8, 16>, dim3(p.H / 16), dim3(waves * kWave), 0,
-                          stream, p);
-        return launch(moe_small_down_kernel<FP8, 8>, dim3(p.H / 8), dim3(waves * kWave), 0, stream, p);
+        const int waves = pairs < 4 ? 4 : pairs;
+        return launch(moe_small_down_kernel<FP8>, dim3(p.H / kCols), dim3(waves * kWave), 0, stream, p);
     } else {
         e = launch(moe_down_kernel<FP8>, dim3(p.H / 64, named), dim3(4 * kWave), 0, stream, p);
         if (e != hipSuccess) return e;

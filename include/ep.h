@@ -450,7 +450,7 @@ int ep_combine_reduce(const ep_shape_t *shape, const uint16_t *part, const int32
  * min(max(n, 0), C)), or from row packed_offset[e] of a packed buffer of `rows` rows (rows outside
  * the buffer are left out; C is not used). Only these rows are read and written; other rows of the
  * outputs keep what they hold. shape->T * shape->K is the number of pairs laid out; it chooses
- * the tile size and the grid, never the result, except that T = 0 means no rows: the call does
+ * the grid, never the result, except that T = 0 means no rows: the call does
  * nothing. R is not used. H is the width of the INPUT rows.
  *
  * Weights are row-major per expert, one row of H codes per output channel, with one fp32 scale
@@ -469,8 +469,8 @@ int ep_combine_reduce(const ep_shape_t *shape, const uint16_t *part, const int32
  *             dot_b = sum over k in block b of recv_q[r][k] * w_q[e][c][k] in fp32
  *   recv_q [E*C*H] (packed: [rows*H]) uint8, 16-byte aligned; recv_scale [.../128] float
  *   y      [E*C*N] (packed: [rows*N]) uint16 (bf16) out, 16-byte aligned
- * dot_b is one FP8 matrix instruction: it aligns each group of (at most 16 consecutive) products
- * to the largest exponent among them and cuts what lies 14 or more binary places below it, which
+ * dot_b is two FP8 matrix instructions, which align each group of (at most 16 consecutive) products
+ * to the largest exponent among them and cut what lies 14 or more binary places below it, which
  * is about 2e-5 of the result's norm on real data, a hundredth of y's own rounding.
  * Deterministic: the same inputs give the same bits.
  * NaN codes and non-finite scales propagate to the elements they enter. N % 8 == 0.
@@ -511,13 +511,14 @@ int ep_expert_swiglu_fp8_packed(const ep_shape_t *shape, int32_t rows, int32_t I
 
 /*
  * ep_moe_layer / ep_moe_layer_fp8 -- a whole MoE layer for a few tokens (a decode step), from
- * token rows to combined rows in two launches (three above 64 pairs), with no receive buffer: bound
+ * token rows to combined rows in two launches (three above 16 pairs), with no receive buffer: bound
  * by reading the chosen experts' weights once.
  *
  *   out[t][c] = bf16_rne(acc), acc = +0.0f, then for j = 0 .. K-1 ascending, for each pair with
  *               0 <= e < E:  acc = fmaf(topk_w[i], y, acc)
  *   y = sum_k W2[e][c][k] * h[k],  h = g / (1 + exp(-g)) * u,  g = Wg[e] x[t],  u = Wu[e] x[t]
- * in fp32 (h is held as a pair of bf16 values, hi + lo, 16 significant bits); there is no
+ * in fp32 (h is held as a pair of bf16 values, hi + lo, 16 significant bits, so an infinite
+ * weight in W2 may give NaN where the sum would be infinite); there is no
  * capacity, every pair with a valid id counts, and a token with none gives +0. An expert that a
  * token names twice counts twice. Activations are not quantised: with FP8 weights the layer is
  * closer to the exact one than the FP8 dispatch and products are.
@@ -534,10 +535,10 @@ int ep_expert_swiglu_fp8_packed(const ep_shape_t *shape, int32_t rows, int32_t I
  *            Two calls in flight at once need two.
  *
  * Requires (else EP_ERR_UNSUPPORTED) T*K <= EP_MOE_MAX_PAIRS, E <= EP_MAX_EXPERTS, H and I
- * multiples of 64 (bf16) or 128 (FP8), 2*I*H and T*K*I <= 2^29, T*H <= 2^30. C and R are not used. T = 0 does nothing.
- * Deterministic.
+ * multiples of 64 (bf16) or 128 (FP8), 2*I*H and T*K*I <= 2^29, T*H <= 2^30. C and R are not
+ * used. T = 0 does nothing. Deterministic.
  *
- * ep_moe_layer_workspace_bytes: 4 * T*K * I, and above 64 pairs T*K * (4*H + 20) + 16 more (0 for
+ * ep_moe_layer_workspace_bytes: 4 * T*K * I, and above 16 pairs T*K * (4*H + 20) + 16 more (0 for
  * T*K = 0 or an invalid shape or I). Host only.
  */
 size_t ep_moe_layer_workspace_bytes(const ep_shape_t *shape, int32_t I);

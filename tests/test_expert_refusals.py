@@ -139,8 +139,8 @@ def test_layer_shapes_refused(lib, fp8):
 @pytest.mark.parametrize("fp8", [False, True])
 def test_layer_pointers_refused(lib, fp8):
     fn, ptrs = (lib.ep_moe_layer_fp8, 8) if fp8 else (lib.ep_moe_layer, 6)
-    need = 68 * 4 * 128 + 68 * (4 * 256 + 20) + 16          # above 64 pairs: y and the lists too
-    assert lib.ep_moe_layer_workspace_bytes(shape(**{**LAYER, "T": 16}), 128) == 64 * 4 * 128
+    need = 68 * 4 * 128 + 68 * (4 * 256 + 20) + 16          # above 16 pairs: y and the lists too
+    assert lib.ep_moe_layer_workspace_bytes(shape(**{**LAYER, "T": 4}), 128) == 16 * 4 * 128
     assert lib.ep_moe_layer_workspace_bytes(shape(**LAYER), 128) == need
     assert lib.ep_moe_layer_workspace_bytes(None, 128) == 0
     assert lib.ep_moe_layer_workspace_bytes(shape(**LAYER), 0) == 0

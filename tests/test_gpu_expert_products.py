@@ -112,8 +112,10 @@ def check_gemm(x, pairs=None):
     return y
 
 
-def check_swiglu(x):
+def check_swiglu(x, pairs=None):
     print(f"[swiglu] counts={x.counts} H={x.H} I={x.N // 2} C={x.C} packed={x.packed}", flush=True)
+    if pairs is not None:
+        x.pairs = pairs
     I = x.N // 2
     h_q = torch.full((*x.lead(), I), 0xA5, dtype=torch.uint8, device=DEV)
     h_s = torch.full((*x.lead(), I // 128), -7.25, device=DEV)
@@ -183,6 +185,45 @@ def test_many_experts():
 def test_the_number_of_pairs_only_chooses_the_launch(pairs):
     """Any count of pairs computes every row (it sets the tile size and the grid)."""
     check_gemm(Experts([150, 3, 0, 77], 256, 264, C=150, seed=9), pairs=pairs)
+
+
+@pytest.mark.parametrize("A", [0, 8])
+@pytest.mark.parametrize("counts,H", [([256, 128, 1], 128), ([130, 300, 0, 63], 256),
+                                      ([256, 129], 2432), ([384], 2048)])
+def test_both_tile_heights_give_the_same_bits(counts, H, A):
+    """Tiles of 64 and of 128 rows (one workgroup for each tile there is, or 8 workgroups for all,
+    which halves the tiles of the busiest): the same sums in the same order."""
+    x = Experts(counts, H, 520, C=max(counts), A=A, seed=H)
+    a = check_gemm(x)
+    assert torch.equal(check_gemm(x, pairs=1), a)
+    x = Experts(counts, H, 768, C=max(counts), A=A, seed=H + 1)
+    a = check_swiglu(x)
+    b = check_swiglu(x, pairs=1)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1].view(torch.int32), b[1].view(torch.int32))
+
+
+@pytest.mark.parametrize("rows", [1, 70])
+def test_a_workgroup_walks_hundreds_of_tiles(rows):
+    """8 workgroups for 700 experts of 4 column tiles: more tiles each than it looks up at once."""
+    counts = [rows if e % 97 == 0 else e % 2 for e in range(700)]
+    counts[3] = 1
+    check_gemm(Experts(counts, 128, 776, C=rows, seed=37), pairs=1)
+    check_swiglu(Experts(counts, 128, 1024, A=1, seed=38), pairs=1)
+
+
+def test_two_products_at_once():
+    """Calls on two streams with nothing between them share no state."""
+    a, b = (Experts([90, 40], 1024, 512, C=90, seed=s) for s in (41, 42))
+    ya, yb = (torch.zeros((2, 90, 512), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    held = a.rows_d(), b.rows_d(), a.w_q.to(DEV), b.w_q.to(DEV), a.w_s.to(DEV), b.w_s.to(DEV)
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    for _ in range(8):
+        B.ep_expert_gemm_fp8(*held[0], a.count, held[2], held[4], a.pairs, y=ya)
+        B.ep_expert_gemm_fp8(*held[1], b.count, held[3], held[5], b.pairs, y=yb, stream=other)
+    torch.cuda.synchronize()
+    for x, y in ((a, ya), (b, yb)):
+        assert torch.equal(y.cpu().view(torch.int16).reshape(180, 512)[x.held], check_gemm(x)[x.held])
 
 
 def test_no_pairs_writes_nothing():

@@ -78,6 +78,9 @@ SHAPES = [  # T, E, K, H, I
     (1, 1, 1, 128, 128), (1, 8, 2, 256, 128), (1, 128, 8, 512, 256), (3, 5, 5, 384, 128),
     (16, 8, 1, 128, 384), (17, 2, 1, 256, 128), (33, 16, 4, 640, 256), (128, 128, 8, 256, 512),
     (130, 3, 2, 128, 128), (7, 1000, 8, 128, 128), (40, 96, 6, 896, 384),
+    # 16 pairs and 17; 16 pairs of one expert; 32 channels of h a workgroup; long rows
+    (2, 12, 8, 256, 128), (17, 12, 1, 256, 128), (16, 1, 1, 128, 128), (4, 6, 4, 128, 1024),
+    (1, 3, 2, 4096, 256), (2, 2, 2, 128, 2048), (5, 4, 4, 2048, 1152),
 ]
 
 
@@ -164,6 +167,25 @@ def test_same_bits_on_another_stream_and_with_another_workspace(fp8):
         x.run(out=out, workspace=ws)
     other.synchronize()
     assert torch.equal(a, out)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_two_layers_at_once(fp8):
+    """Layers on two streams, a workspace each, with nothing between them share no state."""
+    xs = [Layer(T, 8, 4, 512, 256, fp8, seed=T) for T in (3, 25)]
+    want = [x.run() for x in xs]
+    torch.cuda.synchronize()
+    ws = [torch.empty(B.moe_layer_workspace_bytes(x.T, 4, 512, 256), dtype=torch.uint8, device=DEV)
+          for x in xs]
+    out = [torch.zeros_like(w) for w in want]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(8):
+        for x, o, w, s in zip(xs, out, ws, streams):
+            x.run(out=o, workspace=w, stream=s)
+    torch.cuda.synchronize()
+    for o, w in zip(out, want):
+        assert torch.equal(o, w)
 
 
 @pytest.mark.parametrize("fp8", [False, True])
