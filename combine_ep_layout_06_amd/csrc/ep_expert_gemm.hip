@@ -364,8 +364,8 @@ __device__ __forceinline__ void run_tiles(const ExpertProduct &p, const TileTabl
             ld.xoff[j] = min(wave * (8 * MT) + j * 8 + (l >> 3), t.n - 1) * p.H + (l & 7) * 16;
     };
 
-    // blocks in registers on their way to LDS: as many as there is room for, two at most (four
-    // changed nothing: one tile of 64 rows is bound by LDS, 1100 cycles a block of 136 KB)
+    // blocks in registers on their way to LDS: as many as there is room for, two at most (four won
+    // nothing: 4 experts of 64 rows, 2048 x 2048, 17.2 us with two, 18.1 with four)
     constexpr int kStage = SWIGLU && MT == 2 ? 1 : 2;
     i32x4 wr[kStage][4], xr[kStage][MT];
     i32x4 wf[2][4];                            // the wavefront's weights of a block: [tile][chunk]
@@ -558,8 +558,8 @@ __device__ __forceinline__ void run_tiles(const ExpertProduct &p, const TileTabl
     for (int first = mine.first; first < mine.end; first += kList * mine.step) {
         const int tiles = min((mine.end - first + mine.step - 1) / mine.step, kList);
         if (const int i = wave * kWave + lane_now(); i < tiles) {
-            int columns = n_tiles;
-            asm volatile("" : "+s"(columns));  // nothing of its divisions stays in registers
+            int columns;                       // nothing of its divisions stays in registers
+            asm volatile("" : "=s"(columns) : "0"(uniform(n_tiles)));
             const Tile t = locate(table, p.E, first + i * mine.step, columns, kTileM);
             sh.list[i] = int4{t.e, t.row0, t.n, t.nblk};
         }
