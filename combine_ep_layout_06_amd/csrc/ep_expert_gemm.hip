@@ -11,6 +11,8 @@
 // consecutive output channels.
 #include "ep_expert.h"
 
+#include <type_traits>
+
 namespace ep {
 
 namespace {
@@ -22,6 +24,15 @@ template <int MT> inline constexpr int kTileRows = 64 * MT;     // rows of a til
 #if defined(__HIP_DEVICE_COMPILE__)            // buffer descriptors exist on the device only
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The lane, counted anew: what is computed from it is worked out where it is used, and takes no
+// register through the product (which needs them all).
+__device__ __forceinline__ int lane_now()
+{
+    int l;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(l));
+    return l;
+}
 
 // The experts' rows cut into tiles of `bm` rows: rows and first row of each expert, and the
 // running number of tiles. Built once per workgroup.
@@ -43,8 +54,8 @@ struct Tiling {
 __device__ __forceinline__ Tiling build_table(TileTable &t, const ExpertProduct &p, int n_tiles)
 {
     constexpr int kPer = EP_MAX_EXPERTS / kTileThreads, kWaves = kTileThreads / kWave;
-    const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
-    const int e0 = threadIdx.x * kPer;
+    const int lane = lane_now(), wave = uniform(threadIdx.x / kWave);
+    const int e0 = (wave * kWave + lane) * kPer;
     int tiles[2][kPer], sum[2] = {0, 0}, incl[2];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -94,8 +105,9 @@ __device__ __forceinline__ Tiling build_table(TileTable &t, const ExpertProduct 
 // The tiles of all experts in one row, an expert's tiles in groups of kGroup row tiles: within a
 // group the row tile runs fastest, then the column tile. Neighbours in this order share weights
 // and rows, and each XCD takes one eighth of the order (its workgroups are blockIdx.x mod 8), so
-// that its L2 holds what they share.
-constexpr int kGroup = 8;
+// that its L2 holds what they share. Groups of 4: 65536 rows x 4096 x 4096 1.17 ms; of 8 1.21 ms, of
+// 16 1.25 ms (SwiGLU of the same rows: within 1%).
+constexpr int kGroup = 4;
 
 struct TileRange {
     int first, end, step;
@@ -258,18 +270,27 @@ __device__ __forceinline__ void store_swiglu(SwigluShared<ROWS> &sh, float (&h)[
     __syncthreads();
 }
 
-// Tiles of 64 * MT rows x 256 weight rows (SwiGLU: 128 gate and the same 128 up rows), one workgroup
-// of 8 wavefronts per CU that walks its tiles as one stream of blocks (128 channels of a tile each);
-// a wavefront multiplies 32 * MT rows by 64 weight rows. Two wavefronts per SIMD share its issue
-// slots: alone, a wavefront's scaled sums, LDS reads and products queue up. Loads run ahead of LDS by
-// as many blocks as the registers hold (kStage) and of the products by one more, across tiles, so
+// Both kernels: tiles of 64 * MT rows x 256 weight rows (SwiGLU: 128 gate and the same 128 up rows),
+// one workgroup of 8 wavefronts per CU that walks its tiles as one stream of blocks (128 channels of
+// a tile each); a wavefront multiplies 32 * MT rows by 64 weight rows. Two wavefronts per SIMD share
+// its issue slots: one alone issues an instruction in about 5 cycles, and its scaled sums and LDS
+// reads then take longer than the products they should hide behind. Loads run ahead across tiles, so
 // that neither a block nor a tile waits for memory. A load instruction covers 8 whole 128-byte row
 // segments, 8 lanes a row: the vector cache takes one access per 128 bytes (in the matrix
 // instruction's lane order, 16 rows side by side, it took one per 16 bytes, and that bounded every
 // size: with operands straight from global memory to registers, 65536 rows x 4096 x 4096 took
-// 4.7 ms, and 640 rows over 128 experts, 1536 x 2048, 84 us against 76 us). From registers a block
-// goes to one of two LDS buffers, an eighth per wavefront. The row scales of 16 blocks are staged
-// together, one panel ahead. One barrier per block.
+// 4.7 ms, and 640 rows over 128 experts, 1536 x 2048, 84 us against 76 us). The row scales of some
+// blocks are staged together, one panel ahead. One barrier per block.
+//
+// In LDS, chunk c (16 bytes) of row r is kept at place c ^ swizzle(r) of the row's eight: the lanes
+// that LDS serves together (8 consecutive rows, and the same 16 further on) then touch all banks. A
+// lane's j-th chunk of a block is 2 * j + half of row lane & 31.
+__device__ __forceinline__ int swizzle(int r) { return (r & 7) ^ ((r >> 4) & 1); }
+
+// The SwiGLU form. Its products, in bf16, keep the matrix units busier than the loads (65536 rows x
+// 2 x 2048 x 4096: 2.03 ms, 84% of the rate of a large bf16 product on the same card), and the codes'
+// conversion takes registers: loads go to registers, up to two blocks ahead, and from there to one of
+// two LDS buffers, an eighth per wavefront.
 constexpr int kPanel = 16;         // blocks whose scales are staged together
 constexpr int kList = 256;         // tiles of a workgroup looked up together
 
@@ -284,15 +305,6 @@ __device__ __forceinline__ i32x4 buffer_load16(__amdgpu_buffer_rsrc_t b, int lan
     return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(b, lane_off, off, 0));
 }
 
-// The lane, counted anew: what is computed from it is worked out where it is used, and takes no
-// register through the product (which needs them all).
-__device__ __forceinline__ int lane_now()
-{
-    int l;
-    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(l));
-    return l;
-}
-
 // Meet the other wavefronts with LDS settled; loads in flight stay in flight.
 __device__ __forceinline__ void meet()
 {
@@ -302,34 +314,39 @@ __device__ __forceinline__ void meet()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-template <bool SWIGLU, int MT>
-struct TileShared {
+// The same with at most N of this wavefront's vector memory operations left (they finish in order).
+template <int N>
+__device__ __forceinline__ void meet_loaded()
+{
+    static_assert(N < 64, "the counter's range");
+    __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));    // vmcnt(N) lgkmcnt(0)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <int MT>
+struct SwigluTiles {
     static constexpr int kTileM = kTileRows<MT>;
     u32x4 x[2][kTileM * 8];
     u32x4 w[2][kTileN * 8];
     float xscale[2][kPanel][kTileM + 1];
     float wscale[2][kPanel][2];
     int4 list[kList];
-    SwigluShared<SWIGLU ? kTileM : 1> h;
+    SwigluShared<kTileM> h;
 };
 
-template <bool SWIGLU, int MT>
-__device__ __forceinline__ void run_tiles(const ExpertProduct &p, const TileTable &table,
-                                          TileShared<SWIGLU, MT> &sh, int row_tiles)
+template <int MT>
+__device__ __forceinline__ void run_swiglu(const ExpertProduct &p, const TileTable &table,
+                                           SwigluTiles<MT> &sh, int row_tiles)
 {
     constexpr int kTileM = kTileRows<MT>;
-    constexpr bool kAhead = !SWIGLU && MT > 1; // registers for the rows one tile of 32 ahead
     const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
     const int wm = wave & 1, wn = wave >> 1;   // the wavefront's rows and weight rows
     const int r32 = lane & 31, half = lane >> 5;
     const int nkb = p.H >> 7;
-    const int n_tiles = (p.n + kTileN - 1) / kTileN;
-    const int ws_rows = (p.n + 127) >> 7;
+    const int n_tiles = p.n / kTileN, ws_rows = p.n >> 7;
     const TileRange mine = my_tiles(row_tiles * n_tiles);
-    // Chunk c (16 bytes) of row r is kept at place c ^ swizzle(r) of the row's eight: the lanes that
-    // LDS serves together (8 consecutive rows, and the same 16 further on) then touch all banks.
-    // A lane's j-th chunk of a block is 2 * j + half of row lane & 31.
-    auto swizzle = [](int r) { return (r & 7) ^ ((r >> 4) & 1); };
     const int row_at = r32 * 8, row_swizzle = swizzle(r32);
 
     // the stream of loads: the tile it is in and its next block
@@ -338,11 +355,10 @@ __device__ __forceinline__ void run_tiles(const ExpertProduct &p, const TileTabl
         __amdgpu_buffer_rsrc_t w, x;
         int woff[4], xoff[MT];
     } ld;
-    // Weight row i of a tile: SwiGLU keeps 32 gate rows and the same 32 up rows together, so that
-    // every wavefront has a tile of each.
+    // Weight row i of a tile: 32 gate rows and the same 32 up rows together, so that every wavefront
+    // has a tile of each.
     auto weight_row = [&](int nblk, int i) {
-        return SWIGLU ? ((i >> 5) & 1) * (p.n / 2) + nblk * 128 + (i >> 6) * 32 + (i & 31)
-                      : nblk * kTileN + i;
+        return ((i >> 5) & 1) * (p.n / 2) + nblk * 128 + (i >> 6) * 32 + (i & 31);
     };
     auto at = [&](int i) {
         const int4 v = sh.list[i];
@@ -357,22 +373,19 @@ __device__ __forceinline__ void run_tiles(const ExpertProduct &p, const TileTabl
         const int l = lane_now();
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            ld.woff[j] = min(weight_row(t.nblk, wave * 32 + j * 8 + (l >> 3)), p.n - 1) * p.H +
-                         (l & 7) * 16;
+            ld.woff[j] = weight_row(t.nblk, wave * 32 + j * 8 + (l >> 3)) * p.H + (l & 7) * 16;
 #pragma unroll
         for (int j = 0; j < MT; ++j)
             ld.xoff[j] = min(wave * (8 * MT) + j * 8 + (l >> 3), t.n - 1) * p.H + (l & 7) * 16;
     };
 
-    // blocks in registers on their way to LDS: as many as there is room for, two at most (four won
-    // nothing: 4 experts of 64 rows, 2048 x 2048, 17.2 us with two, 18.1 with four)
-    constexpr int kStage = SWIGLU && MT == 2 ? 1 : 2;
+    // blocks in registers on their way to LDS, as many as there is room for (with one, 128 tokens over
+    // 128 experts 82 us, with two 79)
+    constexpr int kStage = MT == 2 ? 1 : 2;
     i32x4 wr[kStage][4], xr[kStage][MT];
     i32x4 wf[2][4];                            // the wavefront's weights of a block: [tile][chunk]
     f32x16 acc[2][MT];
-    constexpr int kXf = kAhead ? 2 : 1;
-    i32x4 xf[kXf][4];
-    constexpr int kWs = SWIGLU ? 2 : 1;
+    i32x4 xf[4];
     float xs[2];                               // row scales
     constexpr int kPer = kTileM * kPanel / kTileThreads;
     float ps[kPer], pw = 0.0f;                 // the next panel on its way
@@ -383,11 +396,12 @@ __device__ __forceinline__ void run_tiles(const ExpertProduct &p, const TileTabl
     // the lane's place in LDS: its row of each 8, its chunk (rows 16 further on swap neighbours)
     auto place = [](int l) { return (l >> 3) * 8 + ((l & 7) ^ (l >> 3)); };
     const int put0 = place(lane);
-    auto put_w = [&](int d, int j, int put0) {
-        sh.w[d][wave * 256 + j * 64 + (put0 ^ (j >> 1))] = __builtin_bit_cast(u32x4, wr[d % kStage][j]);
+    auto put_w = [&](int d, int j, int at) {
+        sh.w[d][wave * 256 + j * 64 + (at ^ (j >> 1))] = __builtin_bit_cast(u32x4, wr[d % kStage][j]);
     };
-    auto put_x = [&](int d, int j, int put0) {
-        sh.x[d][(wave * MT + j) * 64 + (put0 ^ ((wave * MT >> 1) & 1))] = __builtin_bit_cast(u32x4, xr[d % kStage][j]);
+    auto put_x = [&](int d, int j, int at) {
+        sh.x[d][(wave * MT + j) * 64 + (at ^ ((wave * MT >> 1) & 1))] =
+            __builtin_bit_cast(u32x4, xr[d % kStage][j]);
     };
     auto advance = [&](int tiles) {            // past the last block: that block again
         if (++ld.kb == nkb) {
@@ -401,8 +415,7 @@ __device__ __forceinline__ void run_tiles(const ExpertProduct &p, const TileTabl
         const float *src = p.scale + (size_t)t.row0 * nkb + min(kb0 + (l & 15), nkb - 1);
 #pragma unroll
         for (int k = 0; k < kPer; ++k) ps[k] = src[(size_t)min(k * 32 + (l >> 4), t.n - 1) * nkb];
-        const int blk = SWIGLU ? ((l >> 4) & 1) * (p.n >> 8) + t.nblk
-                               : min(t.nblk * 2 + ((l >> 4) & 1), ws_rows - 1);
+        const int blk = ((l >> 4) & 1) * (p.n >> 8) + t.nblk;
         pw = p.w_scale[((size_t)t.e * ws_rows + blk) * nkb + min(kb0 + (l & 15), nkb - 1)];
     };
     auto panel_store = [&](int to) {
@@ -414,17 +427,17 @@ __device__ __forceinline__ void run_tiles(const ExpertProduct &p, const TileTabl
     auto read_row = [&](int d, int mt) {       // the lane's chunks of row tile mt
         const i32x4 *x = reinterpret_cast<const i32x4 *>(sh.x[d]) + (wm * MT + mt) * 256 + row_at;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) xf[mt % kXf][j] = x[(2 * j + half) ^ row_swizzle];
+        for (int j = 0; j < 4; ++j) xf[j] = x[(2 * j + half) ^ row_swizzle];
     };
     auto read_w = [&](int d, int nt) {         // and of the wavefront's weight tile nt
         const i32x4 *w = reinterpret_cast<const i32x4 *>(sh.w[d]) + (wn * 2 + nt) * 256 + row_at;
 #pragma unroll
         for (int j = 0; j < 4; ++j) wf[nt][j] = w[(2 * j + half) ^ row_swizzle];
     };
-    float ws[kWs];
-    auto read_ws = [&](float (&to)[kWs], int b) {
-        to[0] = sh.wscale[par][b][SWIGLU ? 0 : wn >> 1];
-        if constexpr (SWIGLU) to[1] = sh.wscale[par][b][1];
+    float ws[2];                               // weight scales, gate and up
+    auto read_ws = [&](float (&to)[2], int b) {
+        to[0] = sh.wscale[par][b][0];
+        to[1] = sh.wscale[par][b][1];
     };
     auto clear = [&]() {
 #pragma unroll
@@ -434,8 +447,8 @@ __device__ __forceinline__ void run_tiles(const ExpertProduct &p, const TileTabl
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[nt][mt][i] = 0.0f;
     };
-    // One block, in LDS buffer d, in 2 regions of one tile of 32 rows each, kept apart by fences. The
-    // next block goes to LDS before the barrier, and the one three ahead takes its registers.
+    // One block, in LDS buffer d, in MT regions of one tile of 32 rows each, kept apart by fences. The
+    // next block goes to LDS before the barrier, and the one kStage further takes its registers.
     auto step = [&](int d, int tile, int kb, int tiles) {
         const int dn = d ^ 1;
         if ((kb & (kPanel - 1)) == 0) {
@@ -443,18 +456,14 @@ __device__ __forceinline__ void run_tiles(const ExpertProduct &p, const TileTabl
             else if (tile + 1 < tiles) panel_load(tile + 1, 0);
         }
         const int b_next = kb == nkb - 1 ? 0 : (kb + 1) & (kPanel - 1);
-        float ws_next[kWs];
-        bf16x8 wb[SWIGLU ? 2 : 1][8];
+        float ws_next[2];
+        bf16x8 wb[2][8];
         read_w(d, 0);
         read_w(d, 1);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            // the rows read: this tile of 32, or the one after it, of the last one the next block's
-            const int to = kAhead ? mt + 1 : mt;
-            if constexpr (!kAhead) {
-                read_row(d, mt);
-                xs[mt] = sh.xscale[par][kb & (kPanel - 1)][(wm * MT + mt) * 32 + r32];
-            }
+            read_row(d, mt);
+            xs[mt] = sh.xscale[par][kb & (kPanel - 1)][(wm * MT + mt) * 32 + r32];
             if (mt == 0) {
 #pragma unroll
                 for (int j = 0; j < MT; ++j) {
@@ -475,39 +484,21 @@ __device__ __forceinline__ void run_tiles(const ExpertProduct &p, const TileTabl
                 meet();
                 read_ws(ws_next, b_next);
             }
-            if constexpr (kAhead) {
-                read_row(to < MT ? d : dn, to & (MT - 1));
-                xs[to & 1] = sh.xscale[par][to < MT ? kb & (kPanel - 1) : b_next]
-                                      [(wm * MT + (to & (MT - 1))) * 32 + r32];
-            }
             f32x16 v[2] = {};
-            if constexpr (SWIGLU) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const bf16x8 xb = bf16_of_e4m3(xf[0][j >> 1][(j & 1) * 2],
-                                                   xf[0][j >> 1][(j & 1) * 2 + 1]);
+            for (int j = 0; j < 8; ++j) {
+                const bf16x8 xb = bf16_of_e4m3(xf[j >> 1][(j & 1) * 2], xf[j >> 1][(j & 1) * 2 + 1]);
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        if (mt == 0)
-                            wb[nt][j] = bf16_of_e4m3(wf[nt][j >> 1][(j & 1) * 2],
-                                                     wf[nt][j >> 1][(j & 1) * 2 + 1]);
-                        v[nt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[nt][j], xb, v[nt], 0, 0,
-                                                                        0);
-                    }
+                for (int nt = 0; nt < 2; ++nt) {
+                    if (mt == 0)
+                        wb[nt][j] = bf16_of_e4m3(wf[nt][j >> 1][(j & 1) * 2],
+                                                 wf[nt][j >> 1][(j & 1) * 2 + 1]);
+                    v[nt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[nt][j], xb, v[nt], 0, 0, 0);
                 }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
-                        v[nt] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                            join(wf[nt][2 * j], wf[nt][2 * j + 1]),
-                            join(xf[mt % kXf][2 * j], xf[mt % kXf][2 * j + 1]), v[nt], 0, 0, 0, 0, 0,
-                            0);
             }
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
-                const float s = xs[mt & 1] * ws[SWIGLU ? nt : 0];
+                const float s = xs[mt] * ws[nt];
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     acc[nt][mt][i] = __builtin_fmaf(s, v[nt][i], acc[nt][mt][i]);
@@ -516,40 +507,21 @@ __device__ __forceinline__ void run_tiles(const ExpertProduct &p, const TileTabl
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
-        for (int i = 0; i < kWs; ++i) ws[i] = ws_next[i];
+        for (int i = 0; i < 2; ++i) ws[i] = ws_next[i];
         advance(tiles);
     };
     auto finish = [&](int tile) {              // the tile's output
         const Tile t = at(tile);
         const int l = lane_now();
         // element i of a lane is channel (i >> 2) * 8 + half * 4 + (i & 3) of row lane & 31
-        if constexpr (SWIGLU) {
-            float h[MT][4][4];
+        float h[MT][4][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) h[mt][i >> 2][i & 3] = swiglu(acc[0][mt][i], acc[1][mt][i]);
-            store_swiglu<kTileM, MT, 4, 32>(
-                sh.h, h, wave, l, wn, [&](int m) { return (wm * MT + m) * 32 + (l & 31); },
-                [&](int g) { return g * 8 + (l >> 5) * 4; }, p, t.row0, t.n, t.nblk);
-        } else {
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                const int r = (wm * MT + mt) * 32 + (l & 31);
-                uint16_t *y = p.y + (size_t)(t.row0 + r) * p.n;
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const int c = weight_row(t.nblk, wn * 64 + nt * 32) + g * 8 + (l >> 5) * 4;
-                        // n % 8 == 0: the four channels together
-                        if (r < t.n && c < p.n)
-                            *reinterpret_cast<uint2 *>(y + c) =
-                                bf16_pairs(acc[nt][mt][g * 4], acc[nt][mt][g * 4 + 1],
-                                           acc[nt][mt][g * 4 + 2], acc[nt][mt][g * 4 + 3]);
-                    }
-            }
-        }
+            for (int i = 0; i < 16; ++i) h[mt][i >> 2][i & 3] = swiglu(acc[0][mt][i], acc[1][mt][i]);
+        store_swiglu<kTileM, MT, 4, 32>(
+            sh.h, h, wave, l, wn, [&](int m) { return (wm * MT + m) * 32 + (l & 31); },
+            [&](int g) { return g * 8 + (l >> 5) * 4; }, p, t.row0, t.n, t.nblk);
         clear();
     };
 
@@ -586,8 +558,6 @@ __device__ __forceinline__ void run_tiles(const ExpertProduct &p, const TileTabl
         meet();
         read_ws(ws, 0);
         clear();
-        if constexpr (kAhead) read_row(0, 0);
-        xs[0] = sh.xscale[0][0][wm * MT * 32 + (lane_now() & 31)];
         __builtin_amdgcn_sched_barrier(0);
         int tile = 0, kb = 0;
         auto next = [&](int d) {               // a block; false after the last one
@@ -601,46 +571,344 @@ __device__ __forceinline__ void run_tiles(const ExpertProduct &p, const TileTabl
         meet();                                // the list and LDS are free again
     }
 }
+
+// The bf16 product. A block's rows and weights go from global memory to LDS directly, into one of three
+// stages, and take no registers on the way: they hold instead three products on their way to the
+// sums, so that the sums of a product run beside the two after it, and the next block's weights and
+// rows, read behind the products that used this block's. The three stages are variables of their own:
+// by that the compiler can tell a stage's reads from the loads in flight into another, and does not
+// wait for those. The loads of the block three ahead start at the barrier behind which no wavefront
+// reads the stage any more, a few at a time: all at once they held up the issue of everything else
+// (65536 rows x 4096 x 4096: 1.34 ms; spread over a block's products 1.26 ms; with 8 wavefronts rather
+// than 4 of 64 * MT rows x 128 weight rows 1.23 ms, 58% of the rate of a large FP8 product. There the
+// loads still cost 0.24 ms, mostly of waiting for what misses L2, and the reads of LDS 0.1 ms).
+constexpr int kGemmPanel = 8;      // blocks whose scales are staged together
+
+typedef __attribute__((address_space(3))) uint8_t *LdsBytes;
+
+struct GemmShared {
+    float xscale[2][kGemmPanel][kTileRows<2> + 1];
+    float wscale[2][kGemmPanel][2];
+    int4 list[kList];
+};
+
+template <int MT, typename Stage>
+__device__ __forceinline__ void run_gemm(const ExpertProduct &p, const Stage &stage, GemmShared &sh,
+                                         int tiles)
+{
+    constexpr int kRows = kTileRows<MT>;
+    constexpr int kW = kRows * 128;            // a stage: rows, then weights
+    const int wave = uniform(threadIdx.x / kWave), lane = lane_now();
+    const int wm = wave & 1, wn = wave >> 1;
+    const int r32 = lane & 31, half = lane >> 5;
+    const int nkb = p.H >> 7;
+    const int ws_rows = (p.n + 127) >> 7;
+    const int row_at = r32 * 8, row_swizzle = swizzle(r32);
+
+    struct {
+        int tile, kb;
+        __amdgpu_buffer_rsrc_t w, x;
+        int woff[4], xoff[MT];
+    } ld;
+    auto at = [&](int i) {
+        const int4 v = sh.list[i];
+        return uniform(Tile{v.x, v.y, v.z, v.w});
+    };
+    auto enter = [&](int i) {
+        const Tile t = at(i);
+        ld.tile = i;
+        ld.kb = 0;
+        ld.w = buffer(p.w_q + (size_t)t.e * p.n * p.H, (uint32_t)p.n * p.H);
+        ld.x = buffer(p.q + (size_t)t.row0 * p.H, (uint32_t)t.n * p.H);
+        // a direct load fills 8 rows, lane l place l & 7 of row l >> 3: it loads the chunk kept there
+        const int l = lane_now();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            ld.woff[j] = min(t.nblk * kTileN + wave * 32 + j * 8 + (l >> 3), p.n - 1) * p.H +
+                         ((l & 7) ^ (l >> 3) ^ (j >> 1)) * 16;
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+            ld.xoff[j] = min(wave * 8 * MT + j * 8 + (l >> 3), t.n - 1) * p.H +
+                         ((l & 7) ^ (l >> 3) ^ (((wave * MT + j) >> 1) & 1)) * 16;
+    };
+    constexpr int kLoads = 4 + MT;             // direct loads of a wavefront per block
+    auto load_some = [&](uint8_t *to, int i0, int i1) {
+#pragma unroll
+        for (int i = i0; i < i1; ++i) {
+            if (i < 4)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    ld.w, (LdsBytes)(to + kW + (wave * 4 + i) * 1024), 16, ld.woff[i], ld.kb * 128, 0, 0);
+            else
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    ld.x, (LdsBytes)(to + (wave * MT + i - 4) * 1024), 16, ld.xoff[i - 4],
+                    ld.kb * 128, 0, 0);
+        }
+    };
+    auto advance = [&]() {                     // past the last block: that block again
+        if (++ld.kb == nkb) {
+            if (ld.tile + 1 < tiles) enter(ld.tile + 1);
+            else ld.kb = nkb - 1;
+        }
+    };
+
+    constexpr int kNT = 2, kQ = kNT * MT;      // tiles of 32 weight rows, products of a block
+    f32x16 acc[kNT][MT];
+    f32x16 v[3];                               // products on their way to acc
+    i32x4 wf[kNT][4], xf[2][4];
+    float sw[2], ws, xs[2];
+    constexpr int kPer = kRows * kGemmPanel / kTileThreads;
+    float ps[kPer], pw = 0.0f;                 // the next panel on its way
+    int par = 0;                               // the panel in use
+    auto panel_load = [&](int i, int kb0) {
+        const Tile t = at(i);
+        const int l = wave * kWave + lane_now();
+        const float *src = p.scale + (size_t)t.row0 * nkb + min(kb0 + (l & 7), nkb - 1);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) ps[k] = src[(size_t)min(k * 64 + (l >> 3), t.n - 1) * nkb];
+        const int blk = min(t.nblk * 2 + ((l >> 3) & 1), ws_rows - 1);
+        pw = p.w_scale[((size_t)t.e * ws_rows + blk) * nkb + min(kb0 + (l & 7), nkb - 1)];
+    };
+    auto panel_store = [&](int to) {
+        const int l = wave * kWave + lane_now();
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) sh.xscale[to][l & 7][k * 64 + (l >> 3)] = ps[k];
+        if (l < 16) sh.wscale[to][l & 7][l >> 3] = pw;
+    };
+    auto read_row = [&](i32x4 (&to)[4], const uint8_t *from, int mt) {
+        const i32x4 *x = reinterpret_cast<const i32x4 *>(from) + (wm * MT + mt) * 256 + row_at;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) to[j] = x[(2 * j + half) ^ row_swizzle];
+    };
+    auto read_w = [&](i32x4 (&to)[4], const uint8_t *from, int nt) {
+        const i32x4 *w = reinterpret_cast<const i32x4 *>(from + kW) + (wn * kNT + nt) * 256 + row_at;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) to[j] = w[(2 * j + half) ^ row_swizzle];
+    };
+    auto read_xs = [&](int b, int mt) { return sh.xscale[par][b][(wm * MT + mt) * 32 + r32]; };
+    auto clear = [&]() {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) acc[nt][mt][i] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) v[k][i] = 0.0f;
+        }
+        sw[0] = sw[1] = 0.0f;
+    };
+    // sums half of product number q of a block (those before 0: the last ones of the block before)
+    auto sum = [&](auto at_q, int ring, int parity, int h) {
+        constexpr int q = (decltype(at_q)::value + 2 * kQ) % kQ;
+        constexpr int nt = q % kNT, mt = q / kNT;
+        const float f = sw[MT == 1 ? parity : mt];
+#pragma unroll
+        for (int i = h * 8; i < h * 8 + 8; ++i)
+            acc[nt][mt][i] = __builtin_fmaf(f, v[ring][i], acc[nt][mt][i]);
+        asm volatile("" : "+v"(acc[nt][mt]));            // summed here, not later
+    };
+    auto step = [&](auto at_s, auto at_p, int tile, int kb) {
+        constexpr int S = decltype(at_s)::value, P = decltype(at_p)::value;
+        constexpr int R = S * kQ % 3;         // ring place of the block's first product
+        uint8_t *cur = stage(std::integral_constant<int, S>{});
+        uint8_t *prev = stage(std::integral_constant<int, (S + 2) % 3>{});
+        const uint8_t *nxt = stage(std::integral_constant<int, (S + 1) % 3>{});
+        if ((kb & (kGemmPanel - 1)) == 0) {
+            if (kb + kGemmPanel < nkb) panel_load(tile, kb + kGemmPanel);
+            else if (tile + 1 < tiles) panel_load(tile + 1, 0);
+        }
+        const int b = kb & (kGemmPanel - 1), b_next = kb == nkb - 1 ? 0 : (kb + 1) & (kGemmPanel - 1);
+        auto part = [&](auto at_q) {
+            constexpr int q = decltype(at_q)::value, nt = q % kNT, mt = q / kNT;
+            constexpr int X = MT == 1 ? P : mt;
+            constexpr bool last = mt == MT - 1;
+            if constexpr (last && nt == 0) {
+                if (b_next == 0) {
+                    par ^= 1;
+                    panel_store(par);
+                }
+                // the next block's loads are done; those of the one after may be in flight
+                meet_loaded<kLoads>();
+            }
+            f32x16 &to = v[(R + q) % 3];
+            const f32x16 zero = {};
+            const i32x8 x0 = join(xf[X][0], xf[X][1]), x1 = join(xf[X][2], xf[X][3]);
+            to = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join(wf[nt][0], wf[nt][1]), x0, zero, 0,
+                                                                 0, 0, 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            sum(std::integral_constant<int, q - 2>{}, (R + q + 1) % 3, q < 2 ? P ^ 1 : P, 0);
+            if constexpr (nt == 0 && !last) {
+                read_row(xf[(mt + 1) & 1], cur, mt + 1);
+                xs[(mt + 1) & 1] = read_xs(b, mt + 1);
+            }
+            // the loads of the block three ahead, from the barrier on for as many products as a
+            // block has: MT = 2 ends them in the next block
+            constexpr int since = (q + kNT) % kQ;               // products since the barrier
+            constexpr int i0 = since * kLoads / kQ, i1 = (since + 1) * kLoads / kQ;
+            load_some(last ? cur : prev, i0, i1);
+            if constexpr (i1 == kLoads) advance();
+            __builtin_amdgcn_sched_barrier(0);
+            to = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join(wf[nt][2], wf[nt][3]), x1, to, 0,
+                                                                 0, 0, 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            sum(std::integral_constant<int, q - 2>{}, (R + q + 1) % 3, q < 2 ? P ^ 1 : P, 1);
+            if constexpr (nt == 1) sw[X] = xs[X] * ws;     // the sums before it are done
+            if constexpr (last) {
+                if constexpr (nt == 0) {
+                    read_row(xf[MT == 1 ? P ^ 1 : 0], nxt, 0);
+                    xs[MT == 1 ? P ^ 1 : 0] = read_xs(b_next, 0);
+                }
+                read_w(wf[nt], nxt, nt);
+                if constexpr (nt == kNT - 1) ws = sh.wscale[par][b_next][wn >> 1];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        part(std::integral_constant<int, 0>{});
+        part(std::integral_constant<int, 1>{});
+        if constexpr (MT == 2) {
+            part(std::integral_constant<int, 2>{});
+            part(std::integral_constant<int, 3>{});
+        }
+    };
+    auto finish = [&](auto at_s, auto at_p, int tile) {
+        constexpr int R = decltype(at_s)::value * kQ % 3, P = decltype(at_p)::value;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            sum(std::integral_constant<int, -2>{}, (R + kQ - 2) % 3, P, h);
+            sum(std::integral_constant<int, -1>{}, (R + kQ - 1) % 3, P, h);
+        }
+        const Tile t = at(tile);
+        const int l = lane_now();
+        // element i of a lane is channel (i >> 2) * 8 + half * 4 + (i & 3) of row lane & 31
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int r = (wm * MT + mt) * 32 + (l & 31);
+            uint16_t *y = p.y + (size_t)(t.row0 + r) * p.n;
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int c = t.nblk * kTileN + wn * 64 + nt * 32 + g * 8 + (l >> 5) * 4;
+                    // n % 8 == 0: the four channels together
+                    if (r < t.n && c < p.n)
+                        *reinterpret_cast<uint2 *>(y + c) =
+                            bf16_pairs(acc[nt][mt][g * 4], acc[nt][mt][g * 4 + 1],
+                                       acc[nt][mt][g * 4 + 2], acc[nt][mt][g * 4 + 3]);
+                }
+        }
+        clear();
+    };
+
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) ps[k] = 0.0f;
+    enter(0);
+    panel_load(0, 0);
+    panel_store(0);
+    load_some(stage(std::integral_constant<int, 0>{}), 0, kLoads);
+    advance();
+    load_some(stage(std::integral_constant<int, 1>{}), 0, kLoads);
+    advance();
+    load_some(stage(std::integral_constant<int, 2>{}), 0, kLoads / MT);
+    if constexpr (MT == 1) advance();
+    constexpr int kAfter = kLoads + kLoads / MT;         // than the first block's
+    meet_loaded<kAfter>();
+    const uint8_t *first = stage(std::integral_constant<int, 0>{});
+    read_row(xf[0], first, 0);
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) read_w(wf[nt], first, nt);
+    xs[0] = read_xs(0, 0);
+    ws = sh.wscale[0][0][wn >> 1];
+    clear();
+    int tile = 0, kb = 0;
+    auto next = [&](auto at_s, auto at_p) {    // a block; false after the last one
+        step(at_s, at_p, tile, kb);
+        if (++kb < nkb) return true;
+        finish(at_s, at_p, tile);
+        kb = 0;
+        return ++tile < tiles;
+    };
+    std::integral_constant<int, 0> c0;
+    std::integral_constant<int, 1> c1;
+    std::integral_constant<int, 2> c2;
+    while (next(c0, c0) && next(c1, c1) && next(c2, c0) && next(c0, c1) && next(c1, c0) && next(c2, c1)) {}
+    meet_loaded<0>();                          // no direct load is left to write LDS
+}
 #endif
 
-template <bool SWIGLU>
-__global__ __launch_bounds__(kTileThreads) void expert_tile_kernel(ExpertProduct p)
+__global__ __launch_bounds__(kTileThreads) void expert_gemm_kernel(ExpertProduct p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    __shared__ __attribute__((aligned(16))) uint8_t s0[(kTileRows<2> + kTileN) * 128];
+    __shared__ __attribute__((aligned(16))) uint8_t s1[(kTileRows<2> + kTileN) * 128];
+    __shared__ __attribute__((aligned(16))) uint8_t s2[(kTileRows<2> + kTileN) * 128];
+    __shared__ GemmShared sh;
+    static_assert(sizeof(TileTable) <= sizeof(s0), "the table is done with before the first block");
+    auto stage = [&](auto s) -> uint8_t * {
+        if constexpr (decltype(s)::value == 0) return s0;
+        else if constexpr (decltype(s)::value == 1) return s1;
+        else return s2;
+    };
+    TileTable &table = *reinterpret_cast<TileTable *>(s0);
+    const int wave = uniform(threadIdx.x / kWave);
+    const int n_tiles = (p.n + kTileN - 1) / kTileN;
+    for (int done = 0;;) {                     // kList tiles at a time
+        const Tiling t = build_table(table, p, n_tiles);
+        const TileRange mine = my_tiles(t.total * n_tiles);
+        const int first = mine.first + done * mine.step;
+        if (first >= mine.end) break;
+        const int tiles = min((mine.end - first + mine.step - 1) / mine.step, kList);
+        if (const int i = wave * kWave + lane_now(); i < tiles) {
+            int columns;                       // nothing of its divisions stays in registers
+            asm volatile("" : "=s"(columns) : "0"(uniform(n_tiles)));
+            const Tile l = locate(table, p.E, first + i * mine.step, columns, t.mt * 64);
+            sh.list[i] = int4{l.e, l.row0, l.n, l.nblk};
+        }
+        __syncthreads();                       // the table is done with
+        if (t.mt == 1) run_gemm<1>(p, stage, sh, tiles);
+        else run_gemm<2>(p, stage, sh, tiles);
+        done += tiles;
+    }
+#else
+    (void)p;
+#endif
+}
+
+__global__ __launch_bounds__(kTileThreads) void expert_swiglu_kernel(ExpertProduct p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
     __shared__ TileTable table;
     __shared__ union {
-        TileShared<SWIGLU, 1> low;
-        TileShared<SWIGLU, 2> high;
+        SwigluTiles<1> low;
+        SwigluTiles<2> high;
     } sh;
-    const Tiling t = build_table(table, p, (p.n + kTileN - 1) / kTileN);
-    if (t.mt == 1) run_tiles<SWIGLU, 1>(p, table, sh.low, t.total);
-    else run_tiles<SWIGLU, 2>(p, table, sh.high, t.total);
+    const Tiling t = build_table(table, p, p.n / kTileN);
+    if (t.mt == 1) run_swiglu<1>(p, table, sh.low, t.total);
+    else run_swiglu<2>(p, table, sh.high, t.total);
 #else
     (void)p;
 #endif
 }
 
 // One workgroup per CU, or as many as there can be tiles of 64 rows.
-template <bool SWIGLU>
-hipError_t launch_product(const ExpertProduct &p, hipStream_t stream)
+hipError_t launch_product(void (*kernel)(ExpertProduct), const ExpertProduct &p, hipStream_t stream)
 {
     if (p.pairs == 0 || (p.offset && p.rows == 0)) return hipSuccess;
     const int64_t experts = p.pairs < p.E ? p.pairs : p.E;
     const int64_t tiles = (p.pairs / kTileRows<1> + experts) * ((p.n + kTileN - 1) / kTileN);
     const dim3 grid((unsigned)(tiles < 256 ? (tiles + 7) / 8 * 8 : 256));
-    return launch(expert_tile_kernel<SWIGLU>, grid, dim3(kTileThreads), 0, stream, p);
+    return launch(kernel, grid, dim3(kTileThreads), 0, stream, p);
 }
 
 }  // namespace
 
 hipError_t launch_expert_gemm_fp8(const ExpertProduct &p, hipStream_t stream)
 {
-    return launch_product<false>(p, stream);
+    return launch_product(expert_gemm_kernel, p, stream);
 }
 
 hipError_t launch_expert_swiglu_fp8(const ExpertProduct &p, hipStream_t stream)
 {
-    return launch_product<true>(p, stream);
+    return launch_product(expert_swiglu_kernel, p, stream);
 }
 
 }  // namespace ep
