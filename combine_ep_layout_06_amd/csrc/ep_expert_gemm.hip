@@ -45,12 +45,13 @@ struct Tiling {
     int total, mt;                 // row tiles of all experts, of 64 * mt rows
 };
 
-// Builds the table and chooses the height of the tiles from the rows there are. A workgroup takes
-// about 3/2 as long for a tile of 128 rows as for one of 64 (the weights' LDS traffic is the same):
-// 26 us against 17 us where 8 to 32 experts fill the chip 2 to 5 times over (H = 2048), so the
-// taller tiles pay where they leave less than 2/3 as many tiles for the busiest workgroup. Few rows
-// an expert, or few tiles: 64 rows (8 rows for each of 128 experts, gate/up of 2 x 768 x 2048,
-// 82 us against 111); more: 128 rows (341 rows for each of 96 experts, 250 us against 302).
+// Builds the table and chooses the height of the tiles from the rows there are. A workgroup takes 1.35
+// to 1.5 times as long for a tile of 128 rows as for one of 64 (the weights' share of the loads and
+// LDS reads is the same): 19.4 against 14.6 us with one tile each of 4 experts' rows, 39.5 for two
+// against 41.1 for three, H = 2048; SwiGLU 30.3 against 21.7 us, and 64.5 against 63.6. So the taller
+// tiles pay where they leave less than 5/7 as many tiles for the busiest workgroup. Few rows an
+// expert, or few tiles: 64 rows (8 rows for each of 128 experts, gate/up of 2 x 768 x 2048, 79 us
+// against 111); more: 128 rows (341 rows for each of 96 experts, 250 us against 302).
 __device__ __forceinline__ Tiling build_table(TileTable &t, const ExpertProduct &p, int n_tiles)
 {
     constexpr int kPer = EP_MAX_EXPERTS / kTileThreads, kWaves = kTileThreads / kWave;
@@ -78,7 +79,7 @@ __device__ __forceinline__ Tiling build_table(TileTable &t, const ExpertProduct 
     }
     __syncthreads();
     int run[2], total[2] = {0, 0};
-    int64_t most[2];
+    uint32_t most[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         run[h] = incl[h] - sum[h];
@@ -89,9 +90,9 @@ __device__ __forceinline__ Tiling build_table(TileTable &t, const ExpertProduct 
             total[h] += s;
         }
         total[h] = uniform(total[h]);
-        most[h] = ((int64_t)total[h] * n_tiles + gridDim.x - 1) / gridDim.x;
+        most[h] = ((uint32_t)total[h] * n_tiles + gridDim.x - 1) / gridDim.x;
     }
-    const int h = 3 * most[1] < 2 * most[0] ? 1 : 0;
+    const int h = 7 * most[1] < 5 * most[0] ? 1 : 0;
     int r = h ? run[1] : run[0];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
