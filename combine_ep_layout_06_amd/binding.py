@@ -38,7 +38,8 @@ EXPORTED = ("ep_layout", "ep_dispatch", "ep_dispatch_fp8", "ep_layout_dispatch",
             "ep_layout_workspace_bytes", "ep_layout_dispatch_ws", "ep_layout_dispatch_fp8_ws",
             "ep_layout_dispatch_noalloc", "ep_expert_gemm_fp8", "ep_expert_gemm_fp8_packed",
             "ep_expert_swiglu_fp8", "ep_expert_swiglu_fp8_packed", "ep_moe_layer",
-            "ep_moe_layer_fp8", "ep_moe_layer_workspace_bytes", "ep_error_string", "ep_last_error", "ep_version")
+            "ep_moe_layer_fp8", "ep_moe_layer_workspace_bytes", "ep_error_string", "ep_last_error",
+            "ep_version")
 
 
 class EpShape(ctypes.Structure):
@@ -906,7 +907,8 @@ def ep_expert_gemm_fp8(recv_q: torch.Tensor, recv_scale: torch.Tensor,
     ``recv_scale`` [E, C, H/128] float32 (as ep_dispatch_fp8 writes them), the first
     ``expert_count[e]`` rows of each expert; weights ``w_q`` [E, N, H] codes and ``w_scale``
     [E, ceil(N/128), H/128] -> ``y`` [E, C, N] bf16. Rows that hold no pair are neither read nor
-    written. ``pairs``: T * K, the pairs the layout placed (chooses the tile size)."""
+    written. ``pairs``: T * K, the pairs the layout placed (chooses the grid, never the result;
+    0: nothing is computed)."""
     E, N, H = _product_args(recv_q, recv_scale, expert_count, w_q, w_scale, 2)
     C, dev = recv_q.shape[1], recv_q.device
     y = torch.empty((E, C, N), dtype=torch.bfloat16, device=dev) if y is None else y
@@ -1004,6 +1006,8 @@ def _moe_layer(name, x, topk_idx, topk_w, w13, w2, dtype, out, workspace, stream
     if workspace is None:
         workspace = torch.empty(max(moe_layer_workspace_bytes(T, K, H, I), 16), dtype=torch.uint8,
                                 device=dev)
+        if stream is not None and workspace.is_cuda:
+            workspace.record_stream(stream)     # not handed out again before the stream is done
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace: must be a contiguous tensor on the tokens' device")
     return (_shape(T, H, E, K, 1, 1), I, out, workspace,

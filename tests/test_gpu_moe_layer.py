@@ -170,6 +170,24 @@ def test_same_bits_on_another_stream_and_with_another_workspace(fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+def test_own_workspace_outlives_a_call_on_another_stream(fp8):
+    """A workspace allocated by the call is not handed out again while the call's stream is behind."""
+    x = Layer(3, 8, 4, 512, 256, fp8, seed=9)
+    want = x.run()
+    torch.cuda.synchronize()
+    other, out = torch.cuda.Stream(), torch.zeros_like(want)
+    n = B.moe_layer_workspace_bytes(3, 4, 512, 256)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(other):
+        torch.cuda._sleep(20_000_000)            # about 10 ms
+    x.run(out=out, stream=other)
+    mine = [torch.zeros(n, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert all((m == 0).all() for m in mine), "the layer wrote into memory that was handed out"
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_two_layers_at_once(fp8):
     """Layers on two streams, a workspace each, with nothing between them share no state."""
     xs = [Layer(T, 8, 4, 512, 256, fp8, seed=T) for T in (3, 25)]
