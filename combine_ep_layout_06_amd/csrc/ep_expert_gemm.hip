@@ -182,17 +182,20 @@ __device__ __forceinline__ uint32_t encode4_any(const float (&h)[4], float scale
     return v;
 }
 
-// bf16 pairs of four values, NaN as 0x7FC0.
-__device__ __forceinline__ uint2 bf16_pairs(float a, float b, float c, float d)
+// Sixteen values as bf16 pairs, NaN as 0x7FC0 (the conversion instruction would keep its payload).
+__device__ __forceinline__ void bf16_pairs(const f32x16 &v, uint32_t (&d)[8])
 {
-    const float v[4] = {a, b, c, d};
-    bf16x2 lo = {(__bf16)v[0], (__bf16)v[1]}, hi = {(__bf16)v[2], (__bf16)v[3]};
-    uint2 o{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
-    if (__builtin_isunordered(v[0], v[1]) || __builtin_isunordered(v[2], v[3])) {
-        o.x = bf16_rne(v[0]) | (bf16_rne(v[1]) << 16);
-        o.y = bf16_rne(v[2]) | (bf16_rne(v[3]) << 16);
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) nan |= __builtin_isunordered(v[2 * i], v[2 * i + 1]);
+    if (__any(nan)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = bf16_rne(v[2 * i]) | (bf16_rne(v[2 * i + 1]) << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            d[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[2 * i], (__bf16)v[2 * i + 1]});
     }
-    return o;
 }
 
 // The SwiGLU epilogue of one tile of ROWS rows x 128 channels of h: the block amax meets in LDS, the
@@ -780,22 +783,26 @@ __device__ __forceinline__ void run_gemm(const ExpertProduct &p, const Stage &st
         }
         const Tile t = at(tile);
         const int l = lane_now();
-        // element i of a lane is channel (i >> 2) * 8 + half * 4 + (i & 3) of row lane & 31
+        // element i of a lane is channel (i >> 2) * 8 + half * 4 + (i & 3) of row lane & 31; the lanes'
+        // halves trade, so that one stores the eight channels of an even i >> 2 and one those of the
+        // odd one behind it (n % 8 == 0: all or none are there): 16 bytes a store instead of 8, 97 us
+        // against 112 with 32768 rows x 768 x 2048, where an output comes every six blocks
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            const int r = (wm * MT + mt) * 32 + (l & 31);
-            uint16_t *y = p.y + (size_t)(t.row0 + r) * p.n;
+            const int r = (wm * MT + mt) * 32 + (l & 31), c0 = t.nblk * kTileN + wn * 64 + (l >> 5) * 8;
+            uint16_t *y = p.y + (size_t)(t.row0 + r) * p.n + c0;
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
+            for (int nt = 0; nt < kNT; ++nt) {
+                uint32_t d[8];
+                bf16_pairs(acc[nt][mt], d);
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int c = t.nblk * kTileN + wn * 64 + nt * 32 + g * 8 + (l >> 5) * 4;
-                    // n % 8 == 0: the four channels together
-                    if (r < t.n && c < p.n)
-                        *reinterpret_cast<uint2 *>(y + c) =
-                            bf16_pairs(acc[nt][mt][g * 4], acc[nt][mt][g * 4 + 1],
-                                       acc[nt][mt][g * 4 + 2], acc[nt][mt][g * 4 + 3]);
+                for (int g = 0; g < 4; g += 2) {
+                    const auto a = __builtin_amdgcn_permlane32_swap(d[2 * g], d[2 * g + 2], false, false);
+                    const auto b = __builtin_amdgcn_permlane32_swap(d[2 * g + 1], d[2 * g + 3], false, false);
+                    if (r < t.n && c0 + nt * 32 + g * 8 < p.n)
+                        *reinterpret_cast<u32x4 *>(y + nt * 32 + g * 8) = u32x4{a[0], b[0], a[1], b[1]};
                 }
+            }
         }
         clear();
     };
