@@ -239,7 +239,11 @@ __device__ __forceinline__ void store_swiglu(SwigluShared<ROWS> &sh, float (&h)[
         // 2^-60 <= amax < inf: the quotients lie where div_by_rcp and the conversion are exact
         const bool plain = __any(amax < 0x21800000u || amax >= 0x7F800000u);
         const float y = 1.0f / scale;
-        uint32_t *code = reinterpret_cast<uint32_t *>(&sh.code[r][0]) + part * 8;
+        // chunk c of row r at place c ^ (r & 7): the lanes of a store are rows, 128 bytes apart
+        auto put = [&](int g, uint32_t code) {
+            const int w = part * 8 + (channel(g) >> 2);
+            reinterpret_cast<uint32_t *>(&sh.code[r][(w >> 2) ^ (r & 7)])[w & 3] = code;
+        };
         if (plain) {
 #pragma unroll 1
             for (int g = 0; g < G; ++g) {
@@ -250,14 +254,13 @@ __device__ __forceinline__ void store_swiglu(SwigluShared<ROWS> &sh, float (&h)[
 #pragma unroll
                     for (int i = 1; i < G; ++i) v[k] = i == g ? h[m][i][k] : v[k];
                 }
-                code[channel(g) >> 2] = encode4_any(v, scale);
+                put(g, encode4_any(v, scale));
             }
         } else {
 #pragma unroll
             for (int g = 0; g < G; ++g)
-                code[channel(g) >> 2] =
-                    e4m3_pack4(div_by_rcp(h[m][g][0], scale, y), div_by_rcp(h[m][g][1], scale, y),
-                               div_by_rcp(h[m][g][2], scale, y), div_by_rcp(h[m][g][3], scale, y));
+                put(g, e4m3_pack4(div_by_rcp(h[m][g][0], scale, y), div_by_rcp(h[m][g][1], scale, y),
+                                  div_by_rcp(h[m][g][2], scale, y), div_by_rcp(h[m][g][3], scale, y)));
         }
         if (part == 0 && lane < GROUP) sh.scale[r] = scale;
     }
@@ -267,7 +270,7 @@ __device__ __forceinline__ void store_swiglu(SwigluShared<ROWS> &sh, float (&h)[
         const int r = i >> 3;
         if (r < n)
             *reinterpret_cast<u32x4 *>(p.h_q + (size_t)(row0 + r) * I + nblk * 128 + (i & 7) * 16) =
-                sh.code[r][i & 7];
+                sh.code[r][(i & 7) ^ (r & 7)];
     }
     for (int r = thread; r < n; r += kTileThreads)
         p.h_scale[(size_t)(row0 + r) * (I / 128) + nblk] = sh.scale[r];
@@ -345,7 +348,7 @@ __device__ __forceinline__ void run_swiglu(const ExpertProduct &p, const TileTab
                                            SwigluTiles<MT> &sh, int row_tiles)
 {
     constexpr int kTileM = kTileRows<MT>;
-    const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
+    const int wave = uniform(threadIdx.x / kWave), lane = lane_now();
     const int wm = wave & 1, wn = wave >> 1;   // the wavefront's rows and weight rows
     const int r32 = lane & 31, half = lane >> 5;
     const int nkb = p.H >> 7;
@@ -420,7 +423,7 @@ __device__ __forceinline__ void run_swiglu(const ExpertProduct &p, const TileTab
 #pragma unroll
         for (int k = 0; k < kPer; ++k) ps[k] = src[(size_t)min(k * 32 + (l >> 4), t.n - 1) * nkb];
         const int blk = ((l >> 4) & 1) * (p.n >> 8) + t.nblk;
-        pw = p.w_scale[((size_t)t.e * ws_rows + blk) * nkb + min(kb0 + (l & 15), nkb - 1)];
+        pw = (p.w_scale + (size_t)t.e * ws_rows * nkb)[blk * nkb + min(kb0 + (l & 15), nkb - 1)];
     };
     auto panel_store = [&](int to) {
         const int l = wave * kWave + lane_now();
@@ -670,7 +673,7 @@ __device__ __forceinline__ void run_gemm(const ExpertProduct &p, const Stage &st
 #pragma unroll
         for (int k = 0; k < kPer; ++k) ps[k] = src[(size_t)min(k * 64 + (l >> 3), t.n - 1) * nkb];
         const int blk = min(t.nblk * 2 + ((l >> 3) & 1), ws_rows - 1);
-        pw = p.w_scale[((size_t)t.e * ws_rows + blk) * nkb + min(kb0 + (l & 7), nkb - 1)];
+        pw = (p.w_scale + (size_t)t.e * ws_rows * nkb)[blk * nkb + min(kb0 + (l & 7), nkb - 1)];
     };
     auto panel_store = [&](int to) {
         const int l = wave * kWave + lane_now();
