@@ -295,7 +295,7 @@ __device__ __forceinline__ void store_swiglu(SwigluShared<ROWS> &sh, float (&h)[
 __device__ __forceinline__ int swizzle(int r) { return (r & 7) ^ ((r >> 4) & 1); }
 
 // The SwiGLU form. Its products, in bf16, keep the matrix units busier than the loads (65536 rows x
-// 2 x 2048 x 4096: 2.03 ms, 84% of the rate of a large bf16 product on the same card), and the codes'
+// 2 x 2048 x 4096: 2.05 ms, 83% of the rate of a large bf16 product on the same card), and the codes'
 // conversion takes registers: loads go to registers, up to two blocks ahead, and from there to one of
 // two LDS buffers, an eighth per wavefront.
 constexpr int kPanel = 16;         // blocks whose scales are staged together
@@ -587,8 +587,9 @@ __device__ __forceinline__ void run_swiglu(const ExpertProduct &p, const TileTab
 // wait for those. The loads of the block three ahead start at the barrier behind which no wavefront
 // reads the stage any more, a few at a time: all at once they held up the issue of everything else
 // (65536 rows x 4096 x 4096: 1.34 ms; spread over a block's products 1.26 ms; with 8 wavefronts rather
-// than 4 of 64 * MT rows x 128 weight rows 1.23 ms, 58% of the rate of a large FP8 product. There the
-// loads still cost 0.24 ms, mostly of waiting for what misses L2, and the reads of LDS 0.1 ms).
+// than 4 of 64 * MT rows x 128 weight rows 1.23 ms; with what tiles' order and stores gain 1.15 ms,
+// 62% of the rate of a large FP8 product. At 1.23 ms the loads cost 0.24 ms, mostly of waiting for what
+// misses L2, and the reads of LDS 0.1 ms).
 constexpr int kGemmPanel = 8;      // blocks whose scales are staged together
 
 typedef __attribute__((address_space(3))) uint8_t *LdsBytes;
