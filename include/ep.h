@@ -458,7 +458,7 @@ int ep_combine_reduce(const ep_shape_t *shape, const uint16_t *part, const int32
  * [E][ceil(N/128)][H/128] float, the last row of blocks covering the N % 128 rows that are left.
  *
  * Common requirements (else EP_ERR_UNSUPPORTED): E <= EP_MAX_EXPERTS, H % 128 == 0, H and the
- * weights of one expert within 2^30 elements (H <= 2^23).
+ * weights of one expert below 2^30 elements (H < 2^23).
  * Outputs must not overlap inputs, and no two experts' rows may overlap.
  */
 

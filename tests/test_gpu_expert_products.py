@@ -211,6 +211,50 @@ def test_a_workgroup_walks_hundreds_of_tiles(rows):
     check_swiglu(Experts(counts, 128, 1024, A=1, seed=38), pairs=1)
 
 
+def test_rows_beyond_4_gib():
+    """The last rows of a packed buffer of 4.5 GB (codes and y): the bits of the same rows in front."""
+    x = Experts([3, 5], 2048, 1024, A=1, seed=43)
+    rows, n = 2_200_000, 8
+    want = torch.zeros((x.rows, 1024), dtype=torch.bfloat16, device=DEV)
+    x.gemm(want)
+    h_want = [torch.zeros((x.rows, 512), dtype=torch.uint8, device=DEV),
+              torch.zeros((x.rows, 4), device=DEV)]
+    x.swiglu(*h_want)
+    small = x.rows_d()
+    q = torch.empty((rows, 2048), dtype=small[0].dtype, device=DEV)
+    s = torch.empty((rows, 16), device=DEV)
+    q.view(torch.uint8)[-n:], s[-n:] = small[0].view(torch.uint8)[:n], small[1][:n]
+    offset = torch.tensor([rows - 8, rows - 5, rows], dtype=torch.int32, device=DEV)
+    w_q, w_s = x.w_q.to(DEV), x.w_s.to(DEV)
+    y = B.ep_expert_gemm_fp8_packed(q, s, x.count, offset, w_q, w_s, n)
+    h_q, h_s = B.ep_expert_swiglu_fp8_packed(q, s, x.count, offset, w_q, w_s, n)
+    torch.cuda.synchronize()
+    assert torch.equal(y[-n:].view(torch.int16), want[:n].view(torch.int16))
+    assert torch.equal(h_q[-n:].view(torch.uint8), h_want[0][:n])
+    assert torch.equal(h_s[-n:], h_want[1][:n])
+
+
+def test_weights_beyond_2_gib():
+    """The third expert of three with 2^30 codes each (the most an expert may have)."""
+    H, N = 4096, 262144
+    gen = torch.Generator(device=DEV).manual_seed(47)
+    w = torch.randint(0, 120, (3, N, H), dtype=torch.uint8, device=DEV, generator=gen)
+    w_s = torch.rand((3, N // 128, H // 128), device=DEV, generator=gen)
+    q = torch.randint(0, 120, (3, 2, H), dtype=torch.uint8, device=DEV, generator=gen)
+    s = torch.rand((3, 2, H // 128), device=DEV, generator=gen)
+    n = lambda *c: torch.tensor(c, dtype=torch.int32, device=DEV)  # noqa: E731
+    with pytest.raises(RuntimeError, match="2\\^30"):
+        B.ep_expert_gemm_fp8(q, s, n(0, 0, 2), w, w_s, 2)
+    N -= 128                                      # just below
+    w, w_s = w.view(-1)[:3 * N * H].view(3, N, H), w_s.view(-1)[:3 * N * H >> 14].view(3, N // 128, -1)
+    y = B.ep_expert_gemm_fp8(q, s, n(0, 0, 2), w, w_s, 2)
+    alone = B.ep_expert_gemm_fp8(q[2:], s[2:], n(2), w[2:], w_s[2:], 2)
+    part = B.ep_expert_gemm_fp8(q[2:], s[2:], n(2), w[2:, -512:], w_s[2:, -4:], 2)
+    torch.cuda.synchronize()
+    assert torch.equal(y[2].view(torch.int16), alone[0].view(torch.int16))
+    assert torch.equal(y[2, :, -512:].view(torch.int16), part[0].view(torch.int16))
+
+
 def test_two_products_at_once():
     """Calls on two streams with nothing between them share no state."""
     a, b = (Experts([90, 40], 1024, 512, C=90, seed=s) for s in (41, 42))
