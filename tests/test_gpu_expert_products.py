@@ -444,3 +444,32 @@ def test_fp8_chain_from_dispatch_to_combine():
         tol = tol + R.U16 * (want.abs() + tol) + 2.0 ** -133
         assert ((out[t] - want).abs() <= tol).all(), t
     assert (out[5] == 0).all()
+
+
+def tiles(counts, columns, pairs):
+    """(rows of a tile, tiles of the busiest workgroup) by the products' launch and tile rules:
+    one workgroup for each tile of 64 rows there can be, up to 256; tiles of 128 rows where they
+    leave the busiest less than 5/7 as many; an eighth of the tiles for each eighth of the grid."""
+    most_tiles = (pairs // 64 + min(pairs, len(counts))) * columns
+    grid = -(-most_tiles // 8) * 8 if most_tiles < 256 else 256
+    total = lambda rows: sum(-(-c // rows) for c in counts) * columns  # noqa: E731
+    busiest = lambda rows: -(-total(rows) // grid)  # noqa: E731
+    rows = 128 if 7 * busiest(128) < 5 * busiest(64) else 64
+    return rows, -(-(-(-total(rows) // 8)) // (grid // 8))
+
+
+@pytest.mark.parametrize("experts,rows,H,height,most", [
+    (700, 3, 128, 64, 350),           # a second list of 94 tiles
+    (512, 2, 256, 64, 256),           # one full list
+    (513, 1, 128, 64, 257),           # a second list of one tile (and, for some workgroups, none)
+    (1024, 2, 128, 64, 512),          # two full lists
+    (600, 72, 256, 128, 300),         # tall tiles
+])
+def test_a_workgroup_walks_more_tiles_than_one_list(experts, rows, H, height, most):
+    """8 workgroups for every expert's 4 column tiles: the tiles of one are looked up 256 at a time."""
+    counts = [max(1, rows - e % 3) for e in range(experts)]
+    if rows > 64:
+        counts = [rows - e % 5 for e in range(experts)]          # all above one low tile
+    assert tiles(counts, 4, 1) == (height, most)
+    check_gemm(Experts(counts, H, 776, C=rows, seed=experts), pairs=1)
+    check_swiglu(Experts(counts, H, 1024, A=1, seed=experts + 1), pairs=1)
