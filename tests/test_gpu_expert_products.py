@@ -473,3 +473,17 @@ def test_a_workgroup_walks_more_tiles_than_one_list(experts, rows, H, height, mo
     assert tiles(counts, 4, 1) == (height, most)
     check_gemm(Experts(counts, H, 776, C=rows, seed=experts), pairs=1)
     check_swiglu(Experts(counts, H, 1024, A=1, seed=experts + 1), pairs=1)
+
+
+@pytest.mark.parametrize("A", [0, 8])
+@pytest.mark.parametrize("counts,columns", [([130, 300, 0, 63], 8), ([0, 129, 0, 0, 255, 1, 192], 4),
+                                            ([97, 0, 97], 4)])
+def test_both_heights_with_uneven_rests_and_empty_experts(counts, columns, A):
+    """The same rows in tiles of 64 rows and of 128, which this asks for: the same bits."""
+    pairs = sum(counts)
+    assert tiles(counts, columns, pairs)[0] == 64 and tiles(counts, columns, 1)[0] == 128
+    x = Experts(counts, 256, 256 * columns - 24, C=max(counts), A=A, seed=columns)
+    assert torch.equal(check_gemm(x), check_gemm(x, pairs=1))
+    x = Experts(counts, 256, 256 * columns, C=max(counts), A=A, seed=columns + 1)
+    a, b = check_swiglu(x), check_swiglu(x, pairs=1)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1].view(torch.int32), b[1].view(torch.int32))
