@@ -91,6 +91,21 @@ __device__ __forceinline__ i32x8 join(i32x4 lo, i32x4 hi)
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// h = g / (1 + exp(-g)) * u. The reciprocal is the hardware's, within one step of fp32, for a
+// division's tenth of the instructions. Its result must not be subnormal, for it would be 0: for
+// g below -87.3 the sum passes 2^126, and with a large u h is of an ordinary size there. So it is
+// taken of a sixteenth of the sum (exact), and its sixteenth by a product, which keeps subnormals.
+// The exponential is the hardware's 2^x: rounding its argument gives h a relative error of
+// 1.5 |g| + 8 half steps of fp32 at most, which shows where g is far below 0 and h small. Below
+// -88.7 exp(-g) is infinite in fp32 and h a zero; g = -inf gives NaN, as -inf / inf does.
+__device__ __forceinline__ float swiglu(float g, float u)
+{
+    const float sum16 = __builtin_fmaf(__expf(-g), 0x1p-4f, 0x1p-4f);
+    return g * (__builtin_amdgcn_rcpf(sum16) * 0x1p-4f) * u;
+}
+
 // Rows of expert e: first row and number (0 if the counts or offsets leave none in the buffer).
 __device__ __forceinline__ void expert_rows(const int32_t *count, const int32_t *offset, int e,
                                             int C, int rows, int &base, int &n)

@@ -23,7 +23,7 @@ template <int MT> inline constexpr int kTileRows = 64 * MT;     // rows of a til
 
 #if defined(__HIP_DEVICE_COMPILE__)            // buffer descriptors exist on the device only
 
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+using ep::uniform;                  // the form for a Tile, below, would hide it
 
 // The lane, counted anew: what is computed from it is worked out where it is used, and takes no
 // register through the product (which needs them all).
@@ -152,13 +152,6 @@ __device__ __forceinline__ Tile locate(const TileTable &t, int E, int tile, int 
 __device__ __forceinline__ Tile uniform(const Tile &t)
 {
     return Tile{uniform(t.e), uniform(t.row0), uniform(t.n), uniform(t.nblk)};
-}
-
-// h = silu(g) * u; the reciprocal is the hardware's (one step of fp32). g = -inf gives NaN, as
-// -inf / inf does.
-__device__ __forceinline__ float swiglu(float g, float u)
-{
-    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 
 // The scale of a block with this amax pattern (integer max of |h|): amax / 448, a NaN amax giving

@@ -26,8 +26,6 @@ namespace {
 constexpr int kUpWaves = 4;
 static_assert(kMoeSmallPairs <= 16, "a wavefront per pair, one tile of rows per expert");
 
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
 // A step along a weight row: 128 bytes, 32 of them per lane (chunks g4 and g4 + 4 of 16 bytes),
 // and the same elements of a bf16 row.
 template <bool FP8>
@@ -72,12 +70,6 @@ __device__ __forceinline__ f32x4 mfma_frag(const Frag<FP8> &a, const Frag<FP8> &
     for (int i = 0; i < Step<FP8>::kMfma; ++i)
         c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], c, 0, 0, 0);
     return c;
-}
-
-// h = silu(g) * u.
-__device__ __forceinline__ float swiglu(float g, float u)
-{
-    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 
 // The pairs of one expert: its rows are `first` .. first + n - 1 of h (experts in order of their

@@ -491,7 +491,8 @@ int ep_expert_gemm_fp8_packed(const ep_shape_t *shape, int32_t rows, int32_t N,
  * FP8 cast in one launch. The weights hold the I gate rows, then the I up rows: w_q [E][2I][H],
  * w_scale [E][2I/128][H/128]. With g and u the same products (not rounded; here each dot_b is
  * exact up to fp32's rounding, since h_scale is an fp32 output):
- *   h = g / (1 + exp(-g)) * u   (fp32)
+ *   h = g / (1 + exp(-g)) * u   (fp32, within (1.5 |g| + 8) * 2^-24 of its value for g above -88.7;
+ *                                below, where exp(-g) is infinite in fp32, a zero of h's sign)
  * and per row and block of 128 channels of h, the cast of ep_dispatch_fp8:
  *   h_scale = amax|h| / 448, h_q = e4m3(h / h_scale); the same rules for zeros and non-finite
  *   values (a NaN h makes its block's scale the quiet NaN).

@@ -487,3 +487,26 @@ def test_both_heights_with_uneven_rests_and_empty_experts(counts, columns, A):
     x = Experts(counts, 256, 256 * columns, C=max(counts), A=A, seed=columns + 1)
     a, b = check_swiglu(x), check_swiglu(x, pairs=1)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1].view(torch.int32), b[1].view(torch.int32))
+
+
+@pytest.mark.parametrize("A", [0, 1])
+def test_swiglu_gate_of_minus_88_is_not_lost(A):
+    """1 + exp(88) is above 2^126, its reciprocal subnormal, h of an ordinary size where up is large."""
+    x = Experts([3], 128, 256, C=3, A=A, seed=53)
+    up = torch.arange(1, 128, dtype=torch.uint8)                 # every positive code but NaN
+    code = torch.zeros(256, 128, dtype=torch.uint8)
+    code[:128, 0] = torch.tensor(-88.0).to(torch.float8_e4m3fn).view(torch.uint8)
+    code[128:254, 0] = up[:126]
+    code[254:, 0] = up[125]
+    x.w_q = code.view(torch.float8_e4m3fn)[None]
+    x.w_s = torch.tensor([1.0, 2.0 ** 60]).view(1, 2, 1)
+    q = torch.zeros(x.q.shape)
+    q[:3, 0] = 1
+    x.q, x.s = q.to(torch.float8_e4m3fn), torch.ones(x.s.shape)
+    h_q = torch.zeros((*x.lead(), 128), dtype=torch.uint8, device=DEV)
+    h_s = torch.zeros((*x.lead(), 1), device=DEV)
+    x.swiglu(h_q, h_s)
+    h_q, h_s = h_q.cpu().view(x.rows, 128)[:3], h_s.cpu().view(-1)[:3].double()
+    want = 88 / (1 + np.exp(88.0)) * 2.0 ** 60                   # times up's code; amax has 448
+    assert ((h_s - want).abs() <= (3 * 88 + 8) * R.U32 * want).all(), (h_s, want)
+    assert torch.equal(h_q, (code[128:, 0] | 0x80).expand(3, 128))

@@ -246,3 +246,42 @@ def test_layer_agrees_with_the_bf16_calls_around_an_expert():
     # the same value but for two different orders of fp32 sums: one step of bf16 apart at most
     step = R.U16 * 2 * comb.float().abs() + 1e-4
     assert ((comb.float() - out.float()).abs() <= step).all()
+
+
+def diagonal_layer(T, fp8, gate, up, down):
+    """A layer of one expert, H = I = 128, whose tokens are ones in the first len(up) channels: gate
+    channel c is `gate`, up channel c (-1)^c times the sum of `up`, and W2 `down` on its diagonal.
+    Values are (code, power of two), so that FP8 weights hold them exactly too."""
+    x = Layer(T, 1, 1, 128, 128, fp8, idx=np.zeros((T, 1)), seed=T)
+    x.x.zero_()
+    x.x[:, :len(up)] = 1
+    x.w.fill_(1.0)
+    code = torch.zeros(256, 128, dtype=torch.float64)
+    code[:128, 0] = gate[0]
+    sign = 1 - 2 * (torch.arange(128) % 2)
+    for k, c in enumerate(up):
+        code[128:, k] = c[0] * sign
+    scale = torch.tensor([gate[1], up[0][1]], dtype=torch.float64)
+    code2 = torch.eye(128, dtype=torch.float64) * down[0]
+    if fp8:
+        f8 = torch.float8_e4m3fn
+        x.w13, x.s13 = code.to(f8)[None], scale.float().view(1, 2, 1)
+        x.w2, x.s2 = code2.to(f8)[None], torch.full((1, 1, 1), down[1])
+    else:
+        x.w13 = (code * scale.repeat_interleave(128)[:, None]).to(torch.bfloat16)[None]
+        x.w2 = (code2 * down[1]).to(torch.bfloat16)[None]
+    for k in x.d:
+        x.d[k] = getattr(x, k).to(DEV)
+    return x, sign
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T", [1, 20])
+def test_gate_of_minus_88_is_not_lost(T, fp8):
+    """1 + exp(88) is above 2^126, its reciprocal subnormal, h of an ordinary size with up = 2^70."""
+    x, sign = diagonal_layer(T, fp8, (-88.0, 1.0), [(64.0, 2.0 ** 64)], (1.0, 1.0))
+    out = x.run().cpu().double()
+    want = -88 / (1 + np.exp(88.0)) * 2.0 ** 70 * sign.double()
+    # the exponential's argument (3 |g| + 8 half steps of fp32 for h), h's two parts, out's rounding
+    tol = (R.U16 + (3 * 88 + 8) * R.U32 + R.U16 ** 2) * (1 + 2.0 ** -7) * want.abs()
+    assert ((out - want).abs() <= tol).all(), (out[0, :2], want[:2])
