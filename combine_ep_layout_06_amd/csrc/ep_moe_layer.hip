@@ -215,8 +215,10 @@ __device__ __forceinline__ void up_pass(UpShared<NI> &sh, const MoeLayer &p, int
             }
             if (mt * 16 + r < n) {
                 const float h = swiglu(g, u);
-                const uint32_t hi = bf16_rne(h);
-                // an infinite or NaN h is whole in hi
+                uint32_t hi = bf16_rne(h);
+                // a finite h that rounds to infinity keeps the largest finite value in hi and the
+                // rest in lo; an infinite or NaN h is whole in hi
+                if ((hi & 0x7FFFu) == 0x7F80u && __builtin_isfinite(h)) --hi;
                 const float rest = h - __uint_as_float(hi << 16);
                 const int ch = c0 + c;
                 uint16_t *at = h_e + ((size_t)(ch >> 3) * 2 * rows.n + row0 + mt * 16 + r) * 8 + (ch & 7);

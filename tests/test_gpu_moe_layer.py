@@ -285,3 +285,14 @@ def test_gate_of_minus_88_is_not_lost(T, fp8):
     # the exponential's argument (3 |g| + 8 half steps of fp32 for h), h's two parts, out's rounding
     tol = (R.U16 + (3 * 88 + 8) * R.U32 + R.U16 ** 2) * (1 + 2.0 ** -7) * want.abs()
     assert ((out - want).abs() <= tol).all(), (out[0, :2], want[:2])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T", [1, 20])
+def test_largest_finite_h_stays_finite(T, fp8):
+    """h = +-511 * 2^119, finite in fp32 and a tie between the largest bf16 value and infinity: its
+    two parts hold it exactly, and out is its product with 2^-100 rounded once (to 2^28)."""
+    x, sign = diagonal_layer(T, fp8, (64.0, 2.0 ** 58), [(448.0, 2.0 ** 55), (60.0, 2.0 ** 55),
+                                                         (3.0, 2.0 ** 55)], (1.0, 2.0 ** -100))
+    out = x.run().cpu().double()
+    assert torch.equal(out, (2.0 ** 28 * sign.double()).expand(T, 128)), out[0, :2]
