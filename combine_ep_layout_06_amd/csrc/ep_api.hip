@@ -683,10 +683,10 @@ int ep_combine_packed(const ep_shape_t *shape, int32_t rows, const uint16_t *y,
 
 namespace {
 
-// Checks shared by the experts' FP8 products: `n` weight rows per expert (a multiple of
-// `n_multiple`), rows of H channels.
+// Checks shared by the experts' FP8 products: `n` output channels (a multiple of `n_multiple`), for
+// each of which an expert has `weight_rows` rows of H channels.
 int check_product(const ep_shape_t *shape, int32_t n, int n_multiple, const char *n_name,
-                  const uint8_t *q, const float *scale, const int32_t *expert_count,
+                  int weight_rows, const uint8_t *q, const float *scale, const int32_t *expert_count,
                   const uint8_t *w_q, const float *w_scale, const void *out, const char *fn)
 {
     const std::string f(fn);
@@ -699,7 +699,7 @@ int check_product(const ep_shape_t *shape, int32_t n, int n_multiple, const char
         return fail(EP_ERR_UNSUPPORTED, f + ": " + n_name + " must be a multiple of " +
                                             std::to_string(n_multiple));
     // lane offsets inside one expert's weights and inside one tile of rows are 32 bits wide
-    if ((int64_t)n * 2 * shape->H > INT32_MAX || (int64_t)shape->H * 256 > INT32_MAX)
+    if ((int64_t)n * weight_rows * shape->H >= int64_t(1) << 30 || shape->H >= 1 << 23)
         return fail(EP_ERR_UNSUPPORTED, f + ": an expert's weights exceed 2^30 elements");
     const bool empty = (int64_t)shape->T * shape->K == 0;
     if (!empty && (!q || !scale || !expert_count || !w_q || !w_scale || !out))
@@ -747,7 +747,7 @@ int ep_expert_gemm_fp8(const ep_shape_t *shape, int32_t N, const uint8_t *recv_q
                        const float *w_scale, uint16_t *y, hipStream_t stream)
 {
     const char *fn = "ep_expert_gemm_fp8";
-    if (int rc = check_product(shape, N, 8, "N", recv_q, recv_scale, expert_count, w_q, w_scale, y,
+    if (int rc = check_product(shape, N, 8, "N", 1, recv_q, recv_scale, expert_count, w_q, w_scale, y,
                                fn))
         return rc;
     ep::ExpertProduct p = product(shape, N, recv_q, recv_scale, expert_count, w_q, w_scale);
@@ -762,7 +762,7 @@ int ep_expert_gemm_fp8_packed(const ep_shape_t *shape, int32_t rows, int32_t N,
                               hipStream_t stream)
 {
     const char *fn = "ep_expert_gemm_fp8_packed";
-    if (int rc = check_product(shape, N, 8, "N", recv_q, recv_scale, expert_count, w_q, w_scale, y,
+    if (int rc = check_product(shape, N, 8, "N", 1, recv_q, recv_scale, expert_count, w_q, w_scale, y,
                                fn))
         return rc;
     if (int rc = check_packed_rows(shape, rows, packed_offset, fn)) return rc;
@@ -779,7 +779,7 @@ int ep_expert_swiglu_fp8(const ep_shape_t *shape, int32_t I, const uint8_t *recv
                          hipStream_t stream)
 {
     const char *fn = "ep_expert_swiglu_fp8";
-    if (int rc = check_product(shape, I, EP_FP8_BLOCK, "I", recv_q, recv_scale, expert_count, w_q,
+    if (int rc = check_product(shape, I, EP_FP8_BLOCK, "I", 2, recv_q, recv_scale, expert_count, w_q,
                                w_scale, h_q, fn))
         return rc;
     if ((int64_t)shape->T * shape->K > 0 && !h_scale)
@@ -799,7 +799,7 @@ int ep_expert_swiglu_fp8_packed(const ep_shape_t *shape, int32_t rows, int32_t I
                                 float *h_scale, hipStream_t stream)
 {
     const char *fn = "ep_expert_swiglu_fp8_packed";
-    if (int rc = check_product(shape, I, EP_FP8_BLOCK, "I", recv_q, recv_scale, expert_count, w_q,
+    if (int rc = check_product(shape, I, EP_FP8_BLOCK, "I", 2, recv_q, recv_scale, expert_count, w_q,
                                w_scale, h_q, fn))
         return rc;
     if (int rc = check_packed_rows(shape, rows, packed_offset, fn)) return rc;

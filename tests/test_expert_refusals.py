@@ -200,3 +200,16 @@ def test_layer_tensors_refused(change, error):
         with pytest.raises(ValueError, match="w13_scale"):
             B.ep_moe_layer_fp8(t["x"], t["idx"], t["w"], w13, torch.zeros((3, 2, 1)), w2,
                                torch.zeros((3, 2, 1)))
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("op,rows", [(GEMM, 1), (SWIGLU, 2)], ids=["gemm", "swiglu"])
+def test_weights_of_2_to_30_codes_are_refused(lib, op, rows, packed):
+    """The limit counts an expert's weight rows: N of the product, 2I of the gate and up product.
+    With no tokens, a call that passes the checks launches nothing."""
+    H = 4096
+    at = (1 << 30) // H // rows
+    go = lambda n: call(lib, op, shape(T=0, H=H, E=1), n=n, packed=packed)  # noqa: E731
+    assert go(at) == B.EP_ERR_UNSUPPORTED and "2^30" in lib.ep_last_error().decode()
+    assert go(2 * at - 128) == B.EP_ERR_UNSUPPORTED
+    assert go(at - 128) == B.EP_OK and lib.ep_last_launches(None, 0) == 0

@@ -510,3 +510,24 @@ def test_swiglu_gate_of_minus_88_is_not_lost(A):
     want = 88 / (1 + np.exp(88.0)) * 2.0 ** 60                   # times up's code; amax has 448
     assert ((h_s - want).abs() <= (3 * 88 + 8) * R.U32 * want).all(), (h_s, want)
     assert torch.equal(h_q, (code[128:, 0] | 0x80).expand(3, 128))
+
+
+def test_swiglu_weights_beyond_2_gib():
+    """The third expert of three, each with the most codes a gate and up product takes."""
+    H, I = 4096, (1 << 17) - 128
+    gen = torch.Generator(device=DEV).manual_seed(59)
+    w = torch.randint(0, 120, (3, 2 * I, H), dtype=torch.uint8, device=DEV, generator=gen)
+    w_s = torch.rand((3, 2 * I // 128, H // 128), device=DEV, generator=gen)
+    q = torch.randint(0, 120, (3, 2, H), dtype=torch.uint8, device=DEV, generator=gen)
+    s = torch.rand((3, 2, H // 128), device=DEV, generator=gen)
+    n = lambda *c: torch.tensor(c, dtype=torch.int32, device=DEV)  # noqa: E731
+    h_q, h_s = B.ep_expert_swiglu_fp8(q, s, n(0, 0, 2), w, w_s, 2)
+    alone = B.ep_expert_swiglu_fp8(q[2:], s[2:], n(2), w[2:], w_s[2:], 2)
+    # the last 256 channels: the last gate rows and the last up rows
+    part_w = torch.cat([w[2:, I - 256:I], w[2:, -256:]], 1)
+    part_s = torch.cat([w_s[2:, I // 128 - 2:I // 128], w_s[2:, -2:]], 1)
+    part = B.ep_expert_swiglu_fp8(q[2:], s[2:], n(2), part_w, part_s, 2)
+    torch.cuda.synchronize()
+    assert torch.equal(h_q[2], alone[0][0]) and torch.equal(h_s[2], alone[1][0])
+    assert torch.equal(h_q[2, :, -256:], part[0][0]) and torch.equal(h_s[2, :, -2:], part[1][0])
+    assert torch.isfinite(h_s[2]).all() and (h_s[2] > 0).all()
