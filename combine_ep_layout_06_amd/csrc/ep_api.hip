@@ -817,8 +817,11 @@ int ep_expert_swiglu_fp8_packed(const ep_shape_t *shape, int32_t rows, int32_t I
 
 size_t ep_moe_layer_workspace_bytes(const ep_shape_t *shape, int32_t I)
 {
-    if (!shape || shape->T < 0 || shape->K < 1 || shape->H < 1 || I < 1) return 0;
-    return ep::moe_workspace_bytes((int64_t)shape->T * shape->K, I, shape->H);
+    if (!shape || shape->T < 0 || shape->E < 1 || shape->K < 1 || shape->H < 1 || I < 1 ||
+        (int64_t)shape->T * shape->K > INT32_MAX)
+        return 0;
+    if (shape->H > 1 << 29 || I > 1 << 29) return 0;     // no call takes them; the sum stays below 2^64
+    return ep::moe_workspace_bytes((size_t)shape->T * shape->K, I, shape->H);
 }
 
 namespace {

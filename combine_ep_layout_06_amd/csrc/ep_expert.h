@@ -54,9 +54,9 @@ constexpr int kMoeSmallPairs = 16;
 
 // Bytes of the layer's workspace: h in two bf16 parts and, above kMoeSmallPairs, y and the lists (4
 // words per named expert and one per pair; there are at most as many named experts as pairs).
-inline size_t moe_workspace_bytes(int64_t pairs, int64_t I, int64_t H)
+inline size_t moe_workspace_bytes(size_t pairs, size_t I, size_t H)
 {
-    return (size_t)(pairs * I * 4 + (pairs > kMoeSmallPairs ? pairs * (H + 5) * 4 + 16 : 0));
+    return pairs * I * 4 + (pairs > kMoeSmallPairs ? pairs * (H + 5) * 4 + 16 : 0);
 }
 
 hipError_t launch_moe_layer(const MoeLayer &p, bool fp8, hipStream_t stream);

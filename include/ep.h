@@ -541,7 +541,7 @@ int ep_expert_swiglu_fp8_packed(const ep_shape_t *shape, int32_t rows, int32_t I
  * used. T = 0 does nothing. Deterministic.
  *
  * ep_moe_layer_workspace_bytes: 4 * T*K * I, and above 16 pairs T*K * (4*H + 20) + 16 more (0 for
- * T*K = 0 or an invalid shape or I). Host only.
+ * T*K = 0, an invalid shape or I, or H or I above 2^29; C and R are not looked at). Host only.
  */
 size_t ep_moe_layer_workspace_bytes(const ep_shape_t *shape, int32_t I);
 

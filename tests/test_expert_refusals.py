@@ -213,3 +213,13 @@ def test_weights_of_2_to_30_codes_are_refused(lib, op, rows, packed):
     assert go(at) == B.EP_ERR_UNSUPPORTED and "2^30" in lib.ep_last_error().decode()
     assert go(2 * at - 128) == B.EP_ERR_UNSUPPORTED
     assert go(at - 128) == B.EP_OK and lib.ep_last_launches(None, 0) == 0
+
+
+def test_layer_workspace_of_shapes_no_call_takes(lib):
+    """0 for an invalid shape or size, and no wrapped products of large ones."""
+    bytes_of = lambda I=128, **kw: lib.ep_moe_layer_workspace_bytes(shape(**{**LAYER, **kw}), I)  # noqa: E731
+    assert bytes_of(T=1 << 30, K=4) == 0                 # T*K above INT32_MAX
+    assert bytes_of(E=0) == 0 and bytes_of(T=-1) == 0 and bytes_of(H=0) == 0 and bytes_of(K=0) == 0
+    assert bytes_of(I=(1 << 31) - 1, T=(1 << 31) - 1, K=1, H=(1 << 31) - 128) == 0
+    assert bytes_of(I=1 << 29, T=(1 << 31) - 1, K=1, H=1 << 29) == ((1 << 31) - 1) * ((8 << 29) + 20) + 16
+    assert bytes_of(T=1 << 20, K=1, H=1 << 20, I=1 << 20) == (8 << 40) + (20 << 20) + 16
