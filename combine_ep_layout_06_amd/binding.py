@@ -1004,8 +1004,9 @@ def _moe_layer(name, x, topk_idx, topk_w, w13, w2, dtype, out, workspace, stream
     out = torch.empty((T, H), dtype=_bf16(x), device=dev) if out is None else out
     _need(out, "out", _bf16(out), T * H, dev)
     if workspace is None:
-        workspace = torch.empty(max(moe_layer_workspace_bytes(T, K, H, I), 16), dtype=torch.uint8,
-                                device=dev)
+        # more pairs are refused below, whatever the workspace
+        need = moe_layer_workspace_bytes(T, K, H, I) if T * K <= EP_MOE_MAX_PAIRS else 0
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
         if stream is not None and workspace.is_cuda:
             workspace.record_stream(stream)     # not handed out again before the stream is done
     elif workspace.device != dev or not workspace.is_contiguous():

@@ -223,3 +223,16 @@ def test_layer_workspace_of_shapes_no_call_takes(lib):
     assert bytes_of(I=(1 << 31) - 1, T=(1 << 31) - 1, K=1, H=(1 << 31) - 128) == 0
     assert bytes_of(I=1 << 29, T=(1 << 31) - 1, K=1, H=1 << 29) == ((1 << 31) - 1) * ((8 << 29) + 20) + 16
     assert bytes_of(T=1 << 20, K=1, H=1 << 20, I=1 << 20) == (8 << 40) + (20 << 20) + 16
+
+
+def test_layer_of_too_many_pairs_allocates_no_workspace(monkeypatch):
+    """Such a batch is refused; a workspace for it could be gigabytes."""
+    T, K = 4096, 8
+    sizes = []
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: sizes.append(a) or empty(*a, **kw))
+    bf16 = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    with pytest.raises((ValueError, RuntimeError)):
+        B.ep_moe_layer(bf16(T, 128), torch.zeros((T, K), dtype=torch.int32), torch.zeros((T, K)),
+                       bf16(2, 256, 128), bf16(2, 128, 128), out=bf16(T, 128))
+    assert all(a[0] <= 4096 for a in sizes), sizes
