@@ -157,7 +157,10 @@ def _shape(T, H, E, K, C, R) -> EpShape:
     if sh is None:
         if len(_shapes) >= 4096:
             _shapes.clear()
-        sh = _shapes[key] = EpShape(*(int(v) for v in key))
+        values = [int(v) for v in key]
+        if any(v != ctypes.c_int32(v).value for v in values):      # a field would keep its low half
+            raise ValueError(f"a shape's T, H, E, K, C, R must fit 32 bits: {values}")
+        sh = _shapes[key] = EpShape(*values)
     return sh
 
 

@@ -236,3 +236,11 @@ def test_layer_of_too_many_pairs_allocates_no_workspace(monkeypatch):
         B.ep_moe_layer(bf16(T, 128), torch.zeros((T, K), dtype=torch.int32), torch.zeros((T, K)),
                        bf16(2, 256, 128), bf16(2, 128, 128), out=bf16(T, 128))
     assert all(a[0] <= 4096 for a in sizes), sizes
+
+
+@pytest.mark.parametrize("pairs", [1 << 32, (1 << 32) + 32, 1 << 31, -(1 << 31) - 1])
+def test_pairs_beyond_32_bits_are_refused(pairs):
+    """2^32 pairs are not 0 pairs (for which the product would do nothing)."""
+    t = tensors()
+    with B.record(), pytest.raises(ValueError, match="32 bits"):
+        B.ep_expert_gemm_fp8(t["q"], t["s"], t["count"], t["w"], t["ws"], pairs)
