@@ -996,7 +996,7 @@ def _moe_layer(name, x, topk_idx, topk_w, w13, w2, dtype, out, workspace, stream
                          f"w2 [E, H, I]")
     dev = x.device
     (T, H), K, (E, n, _), I = x.shape, topk_idx.shape[1], w13.shape, w2.shape[2]
-    if n != 2 * I or topk_idx.shape[0] != T:
+    if n != 2 * I or topk_idx.shape[0] != T or w13.shape[2] != H or w2.shape[:2] != (E, H):
         raise ValueError(f"{name}: x {tuple(x.shape)}, topk_idx {tuple(topk_idx.shape)}, w13 "
                          f"{tuple(w13.shape)} and w2 {tuple(w2.shape)} do not fit together")
     _need(x, "x", _bf16(x), T * H, dev)

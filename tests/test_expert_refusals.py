@@ -244,3 +244,18 @@ def test_pairs_beyond_32_bits_are_refused(pairs):
     t = tensors()
     with B.record(), pytest.raises(ValueError, match="32 bits"):
         B.ep_expert_gemm_fp8(t["q"], t["s"], t["count"], t["w"], t["ws"], pairs)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("w2", [(256, 3, 128), (1, 768, 128), (6, 128, 128)])
+def test_layer_weights_of_another_order_are_refused(w2, fp8):
+    """w2 with as many elements as [E, H, I] and the same I is not [E, H, I]."""
+    dtype = torch.uint8 if fp8 else torch.bfloat16
+    w13, w2 = torch.zeros((3, 256, 256), dtype=dtype), torch.zeros(w2, dtype=dtype)
+    x, idx = torch.zeros((4, 256), dtype=torch.bfloat16), torch.zeros((4, 2), dtype=torch.int32)
+    with B.record(), pytest.raises(ValueError, match="do not fit"):
+        if fp8:
+            B.ep_moe_layer_fp8(x, idx, torch.zeros((4, 2)), w13, torch.zeros((3, 2, 2)), w2,
+                               torch.zeros((3, 2, 1)))
+        else:
+            B.ep_moe_layer(x, idx, torch.zeros((4, 2)), w13, w2)
