@@ -346,10 +346,19 @@ def layout_workspace_bytes(T: int, K: int, E: int) -> int:
     return int(load_library().ep_layout_workspace_bytes(ctypes.byref(_shape(T, 1, E, K, 1, 1))))
 
 
-def _workspace(workspace, T, K, E, dev):
+def _own_workspace(nbytes: int, dev, stream):
+    """A workspace that lives for one call, as memory of the stream the call runs on: the allocator
+    then hands it out and takes it back in that stream's order. (A block of another stream may have
+    work of its last owner pending there, which the call would not wait for.)"""
+    on = contextlib.nullcontext() if stream is None or dev.type != "cuda" else torch.cuda.stream(stream)
+    with on:
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+
+
+def _workspace(workspace, T, K, E, dev, stream):
     need = layout_workspace_bytes(T, K, E)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        workspace = _own_workspace(need, dev, stream)
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace: must be a contiguous tensor on the batch's device")
     return workspace, workspace.numel() * workspace.element_size()
@@ -370,7 +379,7 @@ def ep_layout_dispatch_ws(x: torch.Tensor, topk_idx: torch.Tensor, recv: torch.T
     _need(x, "x", _bf16(x), T * H, dev)
     _need(topk_idx, "topk_idx", torch.int32, T * K, dev)
     _need(recv, "recv", _bf16(recv), E * C * H, dev)
-    ws, nbytes = _workspace(workspace, T, K, E, dev)
+    ws, nbytes = _workspace(workspace, T, K, E, dev, stream)
     sh = _shape(T, H, E, K, C, R)
     _call("ep_layout_dispatch_ws", sh, x, topk_idx, *_layout_ts(lay), recv, ws, nbytes,
           stream=stream)
@@ -412,7 +421,7 @@ def ep_layout_dispatch_fp8_ws(x: torch.Tensor, topk_idx: torch.Tensor, recv_q: t
     _need(recv_q, "recv_q", recv_q.dtype if recv_q.dtype in (torch.uint8, torch.float8_e4m3fn)
           else torch.uint8, E * C * H, dev)
     _need(recv_scale, "recv_scale", torch.float32, E * C * (H // EP_FP8_BLOCK), dev)
-    ws, nbytes = _workspace(workspace, T, K, E, dev)
+    ws, nbytes = _workspace(workspace, T, K, E, dev, stream)
     sh = _shape(T, H, E, K, C, R)
     _call("ep_layout_dispatch_fp8_ws", sh, x, topk_idx, *_layout_ts(lay), recv_q, recv_scale,
           ws, nbytes, stream=stream)
@@ -1009,9 +1018,7 @@ def _moe_layer(name, x, topk_idx, topk_w, w13, w2, dtype, out, workspace, stream
     if workspace is None:
         # more pairs are refused below, whatever the workspace
         need = moe_layer_workspace_bytes(T, K, H, I) if T * K <= EP_MOE_MAX_PAIRS else 0
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        if stream is not None and workspace.is_cuda:
-            workspace.record_stream(stream)     # not handed out again before the stream is done
+        workspace = _own_workspace(need, dev, stream)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace: must be a contiguous tensor on the tokens' device")
     return (_shape(T, H, E, K, 1, 1), I, out, workspace,

@@ -296,3 +296,36 @@ def test_largest_finite_h_stays_finite(T, fp8):
                                                          (3.0, 2.0 ** 55)], (1.0, 2.0 ** -100))
     out = x.run().cpu().double()
     assert torch.equal(out, (2.0 ** 28 * sign.double()).expand(T, 128)), out[0, :2]
+
+
+@pytest.mark.parametrize("call", ["layer", "layer_fp8", "layout_ws", "layout_fp8_ws"])
+def test_own_workspace_is_memory_of_the_calls_stream(call, monkeypatch):
+    """On another stream than torch's current one, a workspace that the call allocates belongs to that
+    stream: a block of the current one may have a kernel of its last owner still to come, which the
+    call's stream does not wait for. Nothing is launched here."""
+    used = []
+    empty = torch.empty
+
+    def note(*a, **kw):
+        if kw.get("dtype") == torch.uint8:
+            used.append(torch.cuda.current_stream())
+        return empty(*a, **kw)
+
+    other = torch.cuda.Stream()
+    fp8 = call.endswith("fp8") or "fp8" in call
+    if call.startswith("layer"):
+        x = Layer(3, 8, 4, 512, 256, fp8, seed=9)
+        go = lambda out: x.run(out=out, stream=other)  # noqa: E731
+        out = torch.zeros_like(x.d["x"])
+    else:
+        tokens = torch.zeros((8, 128), dtype=torch.bfloat16, device=DEV)
+        idx = torch.zeros((8, 2), dtype=torch.int32, device=DEV)
+        q, s = torch.zeros((4, 8, 128), dtype=torch.uint8, device=DEV), torch.zeros((4, 8, 1), device=DEV)
+        out = torch.zeros((4, 8, 128), dtype=torch.bfloat16, device=DEV)
+        go = lambda out: (B.ep_layout_dispatch_fp8_ws(tokens, idx, q, s, 4, 8, 1, stream=other)  # noqa: E731
+                          if fp8 else B.ep_layout_dispatch_ws(tokens, idx, out, 4, 8, 1, stream=other))
+    monkeypatch.setattr(B, "_call", lambda *a, **kw: None)
+    monkeypatch.setattr(torch, "empty", note)
+    go(out)
+    assert used == [other], used
+    assert torch.cuda.current_stream() != other
