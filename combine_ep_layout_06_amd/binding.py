@@ -274,6 +274,18 @@ def _bf16(t: torch.Tensor) -> torch.dtype:
     return t.dtype if t.dtype in (torch.bfloat16, torch.int16, torch.uint16) else torch.bfloat16
 
 
+def _new(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """An output that the caller did not pass in. For a call on another stream it is memory of that
+    stream (a block of the current one may have work of its last owner pending, which the call would
+    not wait for), not reused before the current stream's work at its release is done either."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def ep_layout(topk_idx: torch.Tensor, E: int, C: int, R: int, *, slot=None, expert_count=None,
               expert_offset=None, rank_count=None, rank_offset=None, stats=None, stream=None):
     """Routing layout. ``topk_idx`` int32 [T, K] on the GPU. Returns a dict of the outputs
@@ -282,7 +294,7 @@ def ep_layout(topk_idx: torch.Tensor, E: int, C: int, R: int, *, slot=None, expe
     passed in preallocated."""
     dev = topk_idx.device
     T, K = topk_idx.shape
-    mk = lambda n: torch.empty(n, dtype=torch.int32, device=dev)
+    mk = lambda n: _new(n, torch.int32, dev, stream)
     slot = mk((T, K)) if slot is None else slot
     expert_count = mk(E) if expert_count is None else expert_count
     expert_offset = mk(E) if expert_offset is None else expert_offset
@@ -302,9 +314,9 @@ def ep_layout(topk_idx: torch.Tensor, E: int, C: int, R: int, *, slot=None, expe
                 rank_count=rank_count, rank_offset=rank_offset, stats=stats)
 
 
-def _layout_outputs(dev, T, K, E, R, slot, expert_count, expert_offset, rank_count,
+def _layout_outputs(dev, stream, T, K, E, R, slot, expert_count, expert_offset, rank_count,
                     rank_offset, stats):
-    mk = lambda n: torch.empty(n, dtype=torch.int32, device=dev)
+    mk = lambda n: _new(n, torch.int32, dev, stream)
     out = dict(slot=mk((T, K)) if slot is None else slot,
                expert_count=mk(E) if expert_count is None else expert_count,
                expert_offset=mk(E) if expert_offset is None else expert_offset,
@@ -331,7 +343,7 @@ def ep_layout_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, recv: torch.Tens
     dev = x.device
     T, H = x.shape
     K = topk_idx.shape[1]
-    lay = _layout_outputs(dev, T, K, E, R, slot, expert_count, expert_offset, rank_count,
+    lay = _layout_outputs(dev, stream, T, K, E, R, slot, expert_count, expert_offset, rank_count,
                           rank_offset, stats)
     _need(x, "x", _bf16(x), T * H, dev)
     _need(topk_idx, "topk_idx", torch.int32, T * K, dev)
@@ -374,7 +386,7 @@ def ep_layout_dispatch_ws(x: torch.Tensor, topk_idx: torch.Tensor, recv: torch.T
     dev = x.device
     T, H = x.shape
     K = topk_idx.shape[1]
-    lay = _layout_outputs(dev, T, K, E, R, slot, expert_count, expert_offset, rank_count,
+    lay = _layout_outputs(dev, stream, T, K, E, R, slot, expert_count, expert_offset, rank_count,
                           rank_offset, stats)
     _need(x, "x", _bf16(x), T * H, dev)
     _need(topk_idx, "topk_idx", torch.int32, T * K, dev)
@@ -396,7 +408,7 @@ def ep_layout_dispatch_noalloc(x: torch.Tensor, topk_idx: torch.Tensor, recv: to
     dev = x.device
     T, H = x.shape
     K = topk_idx.shape[1]
-    lay = _layout_outputs(dev, T, K, E, R, slot, expert_count, expert_offset, rank_count,
+    lay = _layout_outputs(dev, stream, T, K, E, R, slot, expert_count, expert_offset, rank_count,
                           rank_offset, stats)
     _need(x, "x", _bf16(x), T * H, dev)
     _need(topk_idx, "topk_idx", torch.int32, T * K, dev)
@@ -414,7 +426,7 @@ def ep_layout_dispatch_fp8_ws(x: torch.Tensor, topk_idx: torch.Tensor, recv_q: t
     dev = x.device
     T, H = x.shape
     K = topk_idx.shape[1]
-    lay = _layout_outputs(dev, T, K, E, R, slot, expert_count, expert_offset, rank_count,
+    lay = _layout_outputs(dev, stream, T, K, E, R, slot, expert_count, expert_offset, rank_count,
                           rank_offset, stats)
     _need(x, "x", _bf16(x), T * H, dev)
     _need(topk_idx, "topk_idx", torch.int32, T * K, dev)
@@ -437,7 +449,7 @@ def ep_layout_dispatch_fp8(x: torch.Tensor, topk_idx: torch.Tensor, recv_q: torc
     dev = x.device
     T, H = x.shape
     K = topk_idx.shape[1]
-    lay = _layout_outputs(dev, T, K, E, R, slot, expert_count, expert_offset, rank_count,
+    lay = _layout_outputs(dev, stream, T, K, E, R, slot, expert_count, expert_offset, rank_count,
                           rank_offset, stats)
     _need(x, "x", _bf16(x), T * H, dev)
     _need(topk_idx, "topk_idx", torch.int32, T * K, dev)
@@ -492,7 +504,7 @@ def ep_combine(y: torch.Tensor, topk_idx: torch.Tensor, slot: torch.Tensor,
     T, K = topk_idx.shape
     H = y.shape[-1]
     E = y.numel() // (C * H)
-    out = torch.empty((T, H), dtype=_bf16(y), device=dev) if out is None else out
+    out = _new((T, H), _bf16(y), dev, stream) if out is None else out
     _need(y, "y", _bf16(y), E * C * H, dev)
     _need(topk_idx, "topk_idx", torch.int32, T * K, dev)
     _need(slot, "slot", torch.int32, T * K, dev)
@@ -513,8 +525,8 @@ def ep_rank_layout(topk_idx: torch.Tensor, E: int, R: int, *, rank_slot=None, ra
     rank's tokens, -1 if not sent) and ``rank_tokens`` int32 [R]."""
     dev = topk_idx.device
     T, K = topk_idx.shape
-    rank_slot = torch.empty((T, R), dtype=torch.int32, device=dev) if rank_slot is None else rank_slot
-    rank_tokens = (torch.empty(R, dtype=torch.int32, device=dev) if rank_tokens is None
+    rank_slot = _new((T, R), torch.int32, dev, stream) if rank_slot is None else rank_slot
+    rank_tokens = (_new(R, torch.int32, dev, stream) if rank_tokens is None
                    else rank_tokens)
     _need(topk_idx, "topk_idx", torch.int32, T * K, dev)
     _need(rank_slot, "rank_slot", torch.int32, T * R, dev)
@@ -561,9 +573,9 @@ def ep_rank_layout_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, E: int, R: 
     dev = x.device
     T, H = x.shape
     K = topk_idx.shape[1]
-    stage = torch.empty((R, T, H), dtype=_bf16(x), device=dev) if stage is None else stage
-    rank_slot = torch.empty((T, R), dtype=torch.int32, device=dev) if rank_slot is None else rank_slot
-    rank_tokens = (torch.empty(R, dtype=torch.int32, device=dev) if rank_tokens is None
+    stage = _new((R, T, H), _bf16(x), dev, stream) if stage is None else stage
+    rank_slot = _new((T, R), torch.int32, dev, stream) if rank_slot is None else rank_slot
+    rank_tokens = (_new(R, torch.int32, dev, stream) if rank_tokens is None
                    else rank_tokens)
     _need(x, "x", _bf16(x), T * H, dev)
     _need(topk_idx, "topk_idx", torch.int32, T * K, dev)
@@ -584,11 +596,11 @@ def ep_rank_layout_dispatch_fp8(x: torch.Tensor, topk_idx: torch.Tensor, E: int,
     T, H = x.shape
     K = topk_idx.shape[1]
     NB = H // EP_FP8_BLOCK
-    stage_q = torch.empty((R, T, H), dtype=torch.uint8, device=dev) if stage_q is None else stage_q
-    stage_scale = (torch.empty((R, T, NB), dtype=torch.float32, device=dev)
+    stage_q = _new((R, T, H), torch.uint8, dev, stream) if stage_q is None else stage_q
+    stage_scale = (_new((R, T, NB), torch.float32, dev, stream)
                    if stage_scale is None else stage_scale)
-    rank_slot = torch.empty((T, R), dtype=torch.int32, device=dev) if rank_slot is None else rank_slot
-    rank_tokens = (torch.empty(R, dtype=torch.int32, device=dev) if rank_tokens is None
+    rank_slot = _new((T, R), torch.int32, dev, stream) if rank_slot is None else rank_slot
+    rank_tokens = (_new(R, torch.int32, dev, stream) if rank_tokens is None
                    else rank_tokens)
     _need(x, "x", _bf16(x), T * H, dev)
     _need(topk_idx, "topk_idx", torch.int32, T * K, dev)
@@ -629,7 +641,7 @@ def ep_layout_dispatch_expand(stage: torch.Tensor, topk_idx: torch.Tensor,
     dev = stage.device
     R, T, H = stage.shape
     K = topk_idx.shape[1]
-    lay = _layout_outputs(dev, T, K, E, R, slot, expert_count, expert_offset, rank_count,
+    lay = _layout_outputs(dev, stream, T, K, E, R, slot, expert_count, expert_offset, rank_count,
                           rank_offset, stats)
     _need(stage, "stage", _bf16(stage), R * T * H, dev)
     _need(topk_idx, "topk_idx", torch.int32, T * K, dev)
@@ -651,7 +663,7 @@ def ep_layout_dispatch_expand_fp8(stage_q: torch.Tensor, stage_scale: torch.Tens
     dev = stage_q.device
     R, T, H = stage_q.shape
     K = topk_idx.shape[1]
-    lay = _layout_outputs(dev, T, K, E, R, slot, expert_count, expert_offset, rank_count,
+    lay = _layout_outputs(dev, stream, T, K, E, R, slot, expert_count, expert_offset, rank_count,
                           rank_offset, stats)
     _need(stage_q, "stage_q", stage_q.dtype if stage_q.dtype in (torch.uint8, torch.float8_e4m3fn)
           else torch.uint8, R * T * H, dev)
@@ -700,7 +712,7 @@ def ep_combine_ranks(y: torch.Tensor, topk_idx: torch.Tensor, slot: torch.Tensor
     R = rank_slot.shape[1]
     H = y.shape[-1]
     E = y.numel() // (C * H)
-    part = torch.empty((R, T, H), dtype=_bf16(y), device=dev) if part is None else part
+    part = _new((R, T, H), _bf16(y), dev, stream) if part is None else part
     _need(y, "y", _bf16(y), E * C * H, dev)
     _need(topk_idx, "topk_idx", torch.int32, T * K, dev)
     _need(slot, "slot", torch.int32, T * K, dev)
@@ -718,7 +730,7 @@ def ep_combine_reduce(part: torch.Tensor, rank_slot: torch.Tensor, K: int, *, ou
     routing) bounds the ranks a token reaches."""
     dev = part.device
     R, T, H = part.shape
-    out = torch.empty((T, H), dtype=_bf16(part), device=dev) if out is None else out
+    out = _new((T, H), _bf16(part), dev, stream) if out is None else out
     _need(part, "part", _bf16(part), R * T * H, dev)
     _need(rank_slot, "rank_slot", torch.int32, T * R, dev)
     _need(out, "out", _bf16(out), T * H, dev)
@@ -744,7 +756,7 @@ def ep_layout_packed(topk_idx: torch.Tensor, E: int, C: int, R: int, alignment: 
     ``rank_offset`` (padded rows per rank) and ``stats``."""
     dev = topk_idx.device
     T, K = topk_idx.shape
-    mk = lambda n: torch.empty(n, dtype=torch.int32, device=dev)
+    mk = lambda n: _new(n, torch.int32, dev, stream)
     slot = mk((T, K)) if slot is None else slot
     expert_count = mk(E) if expert_count is None else expert_count
     packed_offset = mk(E + 1) if packed_offset is None else packed_offset
@@ -803,9 +815,9 @@ def ep_dispatch_packed_fp8(x: torch.Tensor, topk_idx: torch.Tensor, slot: torch.
     return recv_q, recv_scale
 
 
-def _packed_layout_outputs(dev, T, K, E, R, slot, expert_count, packed_offset, rank_count,
+def _packed_layout_outputs(dev, stream, T, K, E, R, slot, expert_count, packed_offset, rank_count,
                            rank_offset, stats):
-    mk = lambda n: torch.empty(n, dtype=torch.int32, device=dev)
+    mk = lambda n: _new(n, torch.int32, dev, stream)
     out = dict(slot=mk((T, K)) if slot is None else slot,
                expert_count=mk(E) if expert_count is None else expert_count,
                packed_offset=mk(E + 1) if packed_offset is None else packed_offset,
@@ -829,7 +841,7 @@ def ep_layout_dispatch_packed(x: torch.Tensor, topk_idx: torch.Tensor, recv: tor
     T, H = x.shape
     K = topk_idx.shape[1]
     rows = recv.shape[0]
-    o = _packed_layout_outputs(dev, T, K, E, R, slot, expert_count, packed_offset, rank_count,
+    o = _packed_layout_outputs(dev, stream, T, K, E, R, slot, expert_count, packed_offset, rank_count,
                                rank_offset, stats)
     _need(x, "x", _bf16(x), T * H, dev)
     _need(topk_idx, "topk_idx", torch.int32, T * K, dev)
@@ -852,7 +864,7 @@ def ep_layout_dispatch_packed_fp8(x: torch.Tensor, topk_idx: torch.Tensor, recv_
     T, H = x.shape
     K = topk_idx.shape[1]
     rows = recv_q.shape[0]
-    o = _packed_layout_outputs(dev, T, K, E, R, slot, expert_count, packed_offset, rank_count,
+    o = _packed_layout_outputs(dev, stream, T, K, E, R, slot, expert_count, packed_offset, rank_count,
                                rank_offset, stats)
     _need(x, "x", _bf16(x), T * H, dev)
     _need(topk_idx, "topk_idx", torch.int32, T * K, dev)
@@ -872,7 +884,7 @@ def ep_combine_packed(y: torch.Tensor, topk_idx: torch.Tensor, slot: torch.Tenso
     dev = y.device
     T, K = topk_idx.shape
     rows, H = y.shape
-    out = torch.empty((T, H), dtype=_bf16(y), device=dev) if out is None else out
+    out = _new((T, H), _bf16(y), dev, stream) if out is None else out
     _need(y, "y", _bf16(y), rows * H, dev)
     _need(topk_idx, "topk_idx", torch.int32, T * K, dev)
     _need(slot, "slot", torch.int32, T * K, dev)
@@ -923,7 +935,7 @@ def ep_expert_gemm_fp8(recv_q: torch.Tensor, recv_scale: torch.Tensor,
     0: nothing is computed)."""
     E, N, H = _product_args(recv_q, recv_scale, expert_count, w_q, w_scale, 2)
     C, dev = recv_q.shape[1], recv_q.device
-    y = torch.empty((E, C, N), dtype=torch.bfloat16, device=dev) if y is None else y
+    y = _new((E, C, N), torch.bfloat16, dev, stream) if y is None else y
     _need(y, "y", _bf16(y), E * C * N, dev)
     sh = _shape(pairs, H, E, 1, C, 1)
     _call("ep_expert_gemm_fp8", sh, N, recv_q, recv_scale, expert_count, w_q, w_scale, y,
@@ -940,7 +952,7 @@ def ep_expert_gemm_fp8_packed(recv_q: torch.Tensor, recv_scale: torch.Tensor,
     E, N, H = _product_args(recv_q, recv_scale, expert_count, w_q, w_scale, 1)
     rows, dev = recv_q.shape[0], recv_q.device
     _need(packed_offset, "packed_offset", torch.int32, E + 1, dev)
-    y = torch.empty((rows, N), dtype=torch.bfloat16, device=dev) if y is None else y
+    y = _new((rows, N), torch.bfloat16, dev, stream) if y is None else y
     _need(y, "y", _bf16(y), rows * N, dev)
     sh = _shape(pairs, H, E, 1, 1, 1)
     _call("ep_expert_gemm_fp8_packed", sh, rows, N, recv_q, recv_scale, expert_count,
@@ -959,8 +971,8 @@ def ep_expert_swiglu_fp8(recv_q: torch.Tensor, recv_scale: torch.Tensor,
     if n % 2:
         raise ValueError(f"w_q: expected an even number of rows (gate, then up), got {n}")
     C, I, dev = recv_q.shape[1], n // 2, recv_q.device
-    h_q = torch.empty((E, C, I), dtype=recv_q.dtype, device=dev) if h_q is None else h_q
-    h_scale = (torch.empty((E, C, I // EP_FP8_BLOCK), dtype=torch.float32, device=dev)
+    h_q = _new((E, C, I), recv_q.dtype, dev, stream) if h_q is None else h_q
+    h_scale = (_new((E, C, I // EP_FP8_BLOCK), torch.float32, dev, stream)
                if h_scale is None else h_scale)
     _need(h_q, "h_q", _e4m3(h_q), E * C * I, dev)
     _need(h_scale, "h_scale", torch.float32, E * C * (I // EP_FP8_BLOCK), dev)
@@ -981,8 +993,8 @@ def ep_expert_swiglu_fp8_packed(recv_q: torch.Tensor, recv_scale: torch.Tensor,
         raise ValueError(f"w_q: expected an even number of rows (gate, then up), got {n}")
     rows, I, dev = recv_q.shape[0], n // 2, recv_q.device
     _need(packed_offset, "packed_offset", torch.int32, E + 1, dev)
-    h_q = torch.empty((rows, I), dtype=recv_q.dtype, device=dev) if h_q is None else h_q
-    h_scale = (torch.empty((rows, I // EP_FP8_BLOCK), dtype=torch.float32, device=dev)
+    h_q = _new((rows, I), recv_q.dtype, dev, stream) if h_q is None else h_q
+    h_scale = (_new((rows, I // EP_FP8_BLOCK), torch.float32, dev, stream)
                if h_scale is None else h_scale)
     _need(h_q, "h_q", _e4m3(h_q), rows * I, dev)
     _need(h_scale, "h_scale", torch.float32, rows * (I // EP_FP8_BLOCK), dev)
@@ -1013,7 +1025,7 @@ def _moe_layer(name, x, topk_idx, topk_w, w13, w2, dtype, out, workspace, stream
     _need(topk_w, "topk_w", torch.float32, T * K, dev)
     _need(w13, "w13", dtype(w13), E * n * H, dev)
     _need(w2, "w2", dtype(w2), E * H * I, dev)
-    out = torch.empty((T, H), dtype=_bf16(x), device=dev) if out is None else out
+    out = _new((T, H), _bf16(x), dev, stream) if out is None else out
     _need(out, "out", _bf16(out), T * H, dev)
     if workspace is None:
         # more pairs are refused below, whatever the workspace
@@ -1060,7 +1072,7 @@ def ep_check_e4m3_conversion(first_pattern: int, count: int, *, device=None, str
     one) on the fp32 bit patterns [first_pattern, first_pattern + count) on the current
     device. Returns (mismatches, smallest mismatching pattern or None) after synchronising."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
-    res = torch.empty(2, dtype=torch.int32, device=dev)
+    res = _new(2, torch.int32, dev, stream)
     _require_current("ep_check_e4m3_conversion", dev)
     L = load_library()
     rc = L.ep_check_e4m3_conversion(first_pattern, count, res.data_ptr(), res.data_ptr() + 4,
