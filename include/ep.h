@@ -467,12 +467,14 @@ int ep_combine_reduce(const ep_shape_t *shape, const uint16_t *part, const int32
  *
  *   y[r][c] = bf16_rne(acc), acc = +0.0f, then for b = 0 .. H/128-1 ascending
  *             acc = fmaf(recv_scale[r][b] * w_scale[e][c/128][b], dot_b, acc),
- *             dot_b = sum over k in block b of recv_q[r][k] * w_q[e][c][k] in fp32
+ *             dot_b = sum over k in block b of recv_q[r][k] * w_q[e][c][k]
  *   recv_q [E*C*H] (packed: [rows*H]) uint8, 16-byte aligned; recv_scale [.../128] float
  *   y      [E*C*N] (packed: [rows*N]) uint16 (bf16) out, 16-byte aligned
- * dot_b is two FP8 matrix instructions, which align each group of (at most 16 consecutive) products
- * to the largest exponent among them and cut what lies 14 or more binary places below it, which
- * is about 2e-5 of the result's norm on real data, a hundredth of y's own rounding.
+ * dot_b is two FP8 matrix instructions with an fp32 result, which inside align each group of (at
+ * most 16 consecutive) products to the largest exponent among them and cut what lies 14 or more
+ * binary places below it: about 2e-5 of the result's norm on real data, a hundredth of y's own
+ * rounding, but an element that cancels to far below the norm can be off by more than its own
+ * rounding to bf16.
  * Deterministic: the same inputs give the same bits.
  * NaN codes and non-finite scales propagate to the elements they enter. N % 8 == 0.
  */
