@@ -3,7 +3,8 @@
 Argument marshalling only: each function checks dtypes, devices, sizes and contiguity, then
 passes ``data_ptr()`` values and torch's current HIP stream to the C entry point of the same
 name. Under ``record()`` the C calls are captured into a CallList instead, whose ``replay()``
-re-issues them without the Python-side checks (for loops that refill the same buffers). Every
+re-issues them without the Python-side checks (for loops that refill the same buffers). What a
+call with ``stream=`` allocates (outputs not passed in, a workspace) is memory of that stream. Every
 step of the computation runs in the library's gfx950 kernels; there is no other code path. If
 the library is missing the functions raise instead of computing anything.
 """

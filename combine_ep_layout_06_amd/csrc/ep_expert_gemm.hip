@@ -894,13 +894,15 @@ __global__ __launch_bounds__(kTileThreads) void expert_swiglu_kernel(ExpertProdu
 #endif
 }
 
+constexpr int kCus = 256;
+
 // One workgroup per CU, or as many as there can be tiles of 64 rows.
 hipError_t launch_product(void (*kernel)(ExpertProduct), const ExpertProduct &p, hipStream_t stream)
 {
     if (p.pairs == 0 || (p.offset && p.rows == 0)) return hipSuccess;
     const int64_t experts = p.pairs < p.E ? p.pairs : p.E;
     const int64_t tiles = (p.pairs / kTileRows<1> + experts) * ((p.n + kTileN - 1) / kTileN);
-    const dim3 grid((unsigned)(tiles < 256 ? (tiles + 7) / 8 * 8 : 256));
+    const dim3 grid((unsigned)(tiles < kCus ? (tiles + 7) / 8 * 8 : kCus));
     return launch(kernel, grid, dim3(kTileThreads), 0, stream, p);
 }
 
