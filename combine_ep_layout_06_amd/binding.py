@@ -39,8 +39,16 @@ EXPORTED = ("ep_layout", "ep_dispatch", "ep_dispatch_fp8", "ep_layout_dispatch",
             "ep_layout_workspace_bytes", "ep_layout_dispatch_ws", "ep_layout_dispatch_fp8_ws",
             "ep_layout_dispatch_noalloc", "ep_expert_gemm_fp8", "ep_expert_gemm_fp8_packed",
             "ep_expert_swiglu_fp8", "ep_expert_swiglu_fp8_packed", "ep_moe_layer",
-            "ep_moe_layer_fp8", "ep_moe_layer_workspace_bytes", "ep_error_string", "ep_last_error",
-            "ep_version")
+            "ep_moe_layer_fp8", "ep_moe_layer_workspace_bytes", "ep_expert_gemm",
+            "ep_expert_gemm_packed", "ep_expert_swiglu", "ep_expert_swiglu_packed",
+            "ep_expert_gemm_dgrad", "ep_expert_gemm_dgrad_packed", "ep_expert_swiglu_dgrad",
+            "ep_expert_swiglu_dgrad_packed", "ep_expert_gemm_wgrad", "ep_expert_gemm_wgrad_packed",
+            "ep_expert_gemm_wgrad_f32", "ep_expert_gemm_wgrad_f32_packed", "ep_combine_grad",
+            "ep_combine_grad_packed", "ep_linear", "ep_linear_grad",
+            "ep_linear_grad_workspace_bytes", "ep_error_string", "ep_last_error", "ep_version")
+
+#: activations of ep_linear by name (EP_ACT_* of the header)
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
 
 class EpShape(ctypes.Structure):
@@ -118,13 +126,32 @@ def load_library():
         L.ep_moe_layer_fp8.argtypes = [sp, i32] + [vp] * 9 + [ctypes.c_size_t, vp]
         L.ep_moe_layer_workspace_bytes.argtypes = [sp, i32]
         L.ep_moe_layer_workspace_bytes.restype = ctypes.c_size_t
+        L.ep_expert_gemm.argtypes = [sp, i32] + [vp] * 5
+        L.ep_expert_gemm_packed.argtypes = [sp, i32, i32] + [vp] * 6
+        L.ep_expert_swiglu.argtypes = [sp, i32] + [vp] * 6
+        L.ep_expert_swiglu_packed.argtypes = [sp, i32, i32] + [vp] * 7
+        L.ep_expert_gemm_dgrad.argtypes = [sp, i32] + [vp] * 5
+        L.ep_expert_gemm_dgrad_packed.argtypes = [sp, i32, i32] + [vp] * 6
+        L.ep_expert_swiglu_dgrad.argtypes = [sp, i32] + [vp] * 6
+        L.ep_expert_swiglu_dgrad_packed.argtypes = [sp, i32, i32] + [vp] * 7
+        L.ep_expert_gemm_wgrad.argtypes = [sp, i32] + [vp] * 5
+        L.ep_expert_gemm_wgrad_packed.argtypes = [sp, i32, i32] + [vp] * 6
+        L.ep_expert_gemm_wgrad_f32.argtypes = [sp, i32, i32] + [vp] * 5
+        L.ep_expert_gemm_wgrad_f32_packed.argtypes = [sp, i32, i32, i32] + [vp] * 6
+        L.ep_combine_grad.argtypes = [sp] + [vp] * 8
+        L.ep_combine_grad_packed.argtypes = [sp, i32] + [vp] * 9
+        L.ep_linear.argtypes = [sp, i32, i32] + [vp] * 7
+        L.ep_linear_grad.argtypes = [sp, i32, i32] + [vp] * 8 + [ctypes.c_size_t, vp]
+        L.ep_linear_grad_workspace_bytes.argtypes = [sp, i32, i32]
         for fn in EXPORTED:
             if fn.startswith("ep_") and fn not in ("ep_error_string", "ep_last_error",
                                                    "ep_version", "ep_layout_workspace_bytes",
-                                                   "ep_moe_layer_workspace_bytes"):
+                                                   "ep_moe_layer_workspace_bytes",
+                                                   "ep_linear_grad_workspace_bytes"):
                 getattr(L, fn).restype = ctypes.c_int
         L.ep_layout_workspace_bytes.argtypes = [sp]
         L.ep_layout_workspace_bytes.restype = ctypes.c_size_t
+        L.ep_linear_grad_workspace_bytes.restype = ctypes.c_size_t
         L.ep_error_string.argtypes = [ctypes.c_int]
         L.ep_error_string.restype = ctypes.c_char_p
         L.ep_last_error.argtypes = []
@@ -1066,6 +1093,319 @@ def ep_moe_layer_fp8(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tens
     _call("ep_moe_layer_fp8", sh, I, x, topk_idx, topk_w, w13_q, w13_scale, w2_q, w2_scale, out,
           ws, nbytes, stream=stream)
     return out
+
+
+# ------------------------------------------------------------------------------------------
+# the experts in bf16, forward and backward
+# ------------------------------------------------------------------------------------------
+
+def _rows(t: torch.Tensor, name: str, width: int, lead: tuple, device):
+    """Checks that `t` is a bf16 row buffer of `width` channels with the leading sizes `lead`."""
+    if tuple(t.shape) != (*lead, width):
+        raise ValueError(f"{name}: expected {(*lead, width)}, got {tuple(t.shape)}")
+    _need(t, name, _bf16(t), t.numel(), device)
+
+
+def _weights3(w: torch.Tensor, name: str):
+    if w.dim() != 3:
+        raise ValueError(f"{name}: expected three dimensions, [E, rows, columns], got {tuple(w.shape)}")
+    return w.shape
+
+
+def _expert_rows(x: torch.Tensor, name: str, E: int, expert_count: torch.Tensor, packed_offset,
+                 pairs: int):
+    """The leading sizes of a receive buffer and the shape's T (pairs) and C, with the counts and
+    offsets checked: [E, C, width], or [rows, width] with `packed_offset`."""
+    if x.dim() != (3 if packed_offset is None else 2):
+        raise ValueError(f"{name}: expected {'[E, C, width]' if packed_offset is None else '[rows, width]'}"
+                         f", got {tuple(x.shape)}")
+    if packed_offset is None and x.shape[0] != E:
+        raise ValueError(f"{name}: {x.shape[0]} experts' rows for {E} experts")
+    _need(expert_count, "expert_count", torch.int32, E, x.device)
+    if packed_offset is not None:
+        _need(packed_offset, "packed_offset", torch.int32, E + 1, x.device)
+    return tuple(x.shape[:-1])
+
+
+def _expert_call(fn: str, E, H, n, lead, packed_offset, pairs, head, count, tail, stream):
+    """One call of an experts' bf16 product: `head` are the arguments in front of expert_count."""
+    if packed_offset is None:
+        _call(fn, _shape(pairs, H, E, 1, lead[1], 1), n, *head, count, *tail, stream=stream)
+    else:
+        _call(fn + "_packed", _shape(pairs, H, E, 1, 1, 1), lead[0], n, *head, count, packed_offset,
+              *tail, stream=stream)
+
+
+def _expert_gemm(x, count, offset, w, pairs, y, stream):
+    E, N, H = _weights3(w, "w")
+    lead = _expert_rows(x, "recv", E, count, offset, pairs)
+    dev = x.device
+    _rows(x, "recv", H, lead, dev)
+    _need(w, "w", _bf16(w), E * N * H, dev)
+    y = _new((*lead, N), _bf16(x), dev, stream) if y is None else y
+    _rows(y, "y", N, lead, dev)
+    _expert_call("ep_expert_gemm", E, H, N, lead, offset, pairs, (x,), count, (w, y), stream)
+    return y
+
+
+def ep_expert_gemm(recv: torch.Tensor, expert_count: torch.Tensor, w: torch.Tensor, pairs: int, *,
+                   y=None, stream=None):
+    """The experts' product on a padded bf16 receive buffer ``recv`` [E, C, H] (as ep_dispatch
+    writes it), the first ``expert_count[e]`` rows of each expert: weights ``w`` [E, N, H] ->
+    ``y`` [E, C, N] bf16. Rows that hold no pair are neither read nor written. ``pairs``: T * K, the
+    pairs the layout placed (chooses the grid, never the result; 0: no rows)."""
+    return _expert_gemm(recv, expert_count, None, w, pairs, y, stream)
+
+
+def ep_expert_gemm_packed(recv: torch.Tensor, expert_count: torch.Tensor,
+                          packed_offset: torch.Tensor, w: torch.Tensor, pairs: int, *, y=None,
+                          stream=None):
+    """ep_expert_gemm on a packed buffer: ``recv`` [rows, H], expert e's rows from
+    ``packed_offset[e]`` on -> ``y`` [rows, N] bf16."""
+    return _expert_gemm(recv, expert_count, packed_offset, w, pairs, y, stream)
+
+
+def _expert_swiglu(x, count, offset, w13, pairs, h, gu, stream):
+    E, n, H = _weights3(w13, "w13")
+    if n % 2:
+        raise ValueError(f"w13: expected an even number of rows (gate, then up), got {n}")
+    lead = _expert_rows(x, "recv", E, count, offset, pairs)
+    dev = x.device
+    _rows(x, "recv", H, lead, dev)
+    _need(w13, "w13", _bf16(w13), E * n * H, dev)
+    h = _new((*lead, n // 2), _bf16(x), dev, stream) if h is None else h
+    _rows(h, "h", n // 2, lead, dev)
+    if gu is not None:
+        _rows(gu, "gu", n, lead, dev)
+    _expert_call("ep_expert_swiglu", E, H, n // 2, lead, offset, pairs, (x,), count, (w13, gu, h),
+                 stream)
+    return h
+
+
+def ep_expert_swiglu(recv: torch.Tensor, expert_count: torch.Tensor, w13: torch.Tensor, pairs: int,
+                     *, h=None, gu=None, stream=None):
+    """The gate and up products and SwiGLU on a padded bf16 receive buffer: ``recv`` [E, C, H],
+    ``w13`` [E, 2I, H] (the I gate rows, then the I up rows) -> ``h`` [E, C, I] bf16, which
+    ep_expert_gemm takes as its rows. ``gu`` [E, C, 2I] bf16, if given, receives the two products,
+    which ep_expert_swiglu_dgrad needs."""
+    return _expert_swiglu(recv, expert_count, None, w13, pairs, h, gu, stream)
+
+
+def ep_expert_swiglu_packed(recv: torch.Tensor, expert_count: torch.Tensor,
+                            packed_offset: torch.Tensor, w13: torch.Tensor, pairs: int, *, h=None,
+                            gu=None, stream=None):
+    """ep_expert_swiglu on a packed buffer: ``recv`` [rows, H] -> ``h`` [rows, I], ``gu``
+    [rows, 2I]."""
+    return _expert_swiglu(recv, expert_count, packed_offset, w13, pairs, h, gu, stream)
+
+
+def _expert_dgrad(dy, count, offset, w, pairs, dx, stream):
+    E, N, H = _weights3(w, "w")
+    lead = _expert_rows(dy, "dy", E, count, offset, pairs)
+    dev = dy.device
+    _rows(dy, "dy", N, lead, dev)
+    _need(w, "w", _bf16(w), E * N * H, dev)
+    dx = _new((*lead, H), _bf16(dy), dev, stream) if dx is None else dx
+    _rows(dx, "dx", H, lead, dev)
+    _expert_call("ep_expert_gemm_dgrad", E, H, N, lead, offset, pairs, (dy,), count, (w, dx), stream)
+    return dx
+
+
+def ep_expert_gemm_dgrad(dy: torch.Tensor, expert_count: torch.Tensor, w: torch.Tensor, pairs: int,
+                         *, dx=None, stream=None):
+    """The gradient of ep_expert_gemm's rows: ``dy`` [E, C, N], the forward call's ``w`` [E, N, H] ->
+    ``dx`` [E, C, H] bf16. ep_combine of ``dx`` with weights 1 is the gradient of the token rows."""
+    return _expert_dgrad(dy, expert_count, None, w, pairs, dx, stream)
+
+
+def ep_expert_gemm_dgrad_packed(dy: torch.Tensor, expert_count: torch.Tensor,
+                                packed_offset: torch.Tensor, w: torch.Tensor, pairs: int, *,
+                                dx=None, stream=None):
+    """ep_expert_gemm_dgrad on a packed buffer: ``dy`` [rows, N] -> ``dx`` [rows, H]."""
+    return _expert_dgrad(dy, expert_count, packed_offset, w, pairs, dx, stream)
+
+
+def _expert_swiglu_dgrad(dy, count, offset, w2, gu, pairs, dgu, stream):
+    E, H, I = _weights3(w2, "w2")
+    lead = _expert_rows(dy, "dy", E, count, offset, pairs)
+    dev = dy.device
+    _rows(dy, "dy", H, lead, dev)
+    _need(w2, "w2", _bf16(w2), E * H * I, dev)
+    _rows(gu, "gu", 2 * I, lead, dev)
+    dgu = _new((*lead, 2 * I), _bf16(dy), dev, stream) if dgu is None else dgu
+    _rows(dgu, "dgu", 2 * I, lead, dev)
+    _expert_call("ep_expert_swiglu_dgrad", E, H, I, lead, offset, pairs, (dy,), count, (w2, gu, dgu),
+                 stream)
+    return dgu
+
+
+def ep_expert_swiglu_dgrad(dy: torch.Tensor, expert_count: torch.Tensor, w2: torch.Tensor,
+                           gu: torch.Tensor, pairs: int, *, dgu=None, stream=None):
+    """Back through the down projection and SwiGLU: ``dy`` [E, C, H], the gradient of the
+    projection's output, its weights ``w2`` [E, H, I] and ``gu`` [E, C, 2I] as ep_expert_swiglu kept
+    it -> ``dgu`` [E, C, 2I] bf16 (may be ``gu`` itself), whose ep_expert_gemm_dgrad and
+    ep_expert_gemm_wgrad are the gradients of the gate and up products."""
+    return _expert_swiglu_dgrad(dy, expert_count, None, w2, gu, pairs, dgu, stream)
+
+
+def ep_expert_swiglu_dgrad_packed(dy: torch.Tensor, expert_count: torch.Tensor,
+                                  packed_offset: torch.Tensor, w2: torch.Tensor, gu: torch.Tensor,
+                                  pairs: int, *, dgu=None, stream=None):
+    """ep_expert_swiglu_dgrad on a packed buffer: ``dy`` [rows, H], ``gu`` and ``dgu`` [rows, 2I]."""
+    return _expert_swiglu_dgrad(dy, expert_count, packed_offset, w2, gu, pairs, dgu, stream)
+
+
+def _expert_wgrad(dy, x, count, offset, pairs, dw, accumulate, stream):
+    E = _experts(count)
+    lead = _expert_rows(dy, "dy", E, count, offset, pairs)
+    dev = dy.device
+    N, H = dy.shape[-1], x.shape[-1]
+    _rows(dy, "dy", N, lead, dev)
+    _rows(x, "recv", H, lead, dev)
+    if dw is None:
+        if accumulate:
+            raise ValueError("dw: accumulate adds to a float32 dw that the caller passes in")
+        dw = _new((E, N, H), _bf16(dy), dev, stream)
+    if tuple(dw.shape) != (E, N, H):
+        raise ValueError(f"dw: expected {(E, N, H)}, got {tuple(dw.shape)}")
+    f32 = dw.dtype == torch.float32
+    if accumulate and not f32:
+        raise TypeError(f"dw: accumulate needs torch.float32, got {dw.dtype}")
+    _need(dw, "dw", torch.float32 if f32 else _bf16(dw), E * N * H, dev)
+    fn = "ep_expert_gemm_wgrad_f32" if f32 else "ep_expert_gemm_wgrad"
+    head = (int(bool(accumulate)), dy, x) if f32 else (dy, x)
+    _expert_call(fn, E, H, N, lead, offset, pairs, head, count, (dw,), stream)
+    return dw
+
+
+def _experts(expert_count: torch.Tensor) -> int:
+    if expert_count.dim() != 1:
+        raise ValueError(f"expert_count: expected [E], got {tuple(expert_count.shape)}")
+    return expert_count.shape[0]
+
+
+def ep_expert_gemm_wgrad(dy: torch.Tensor, recv: torch.Tensor, expert_count: torch.Tensor,
+                         pairs: int, *, dw=None, accumulate=False, stream=None):
+    """The gradient of an experts' product's weights: ``dy`` [E, C, N] and the product's rows ``recv``
+    [E, C, H] -> ``dw`` [E, N, H], all of it (zeros for an expert without rows). bf16, or float32 if
+    such a ``dw`` is passed in; then ``accumulate`` adds to what it holds."""
+    return _expert_wgrad(dy, recv, expert_count, None, pairs, dw, accumulate, stream)
+
+
+def ep_expert_gemm_wgrad_packed(dy: torch.Tensor, recv: torch.Tensor, expert_count: torch.Tensor,
+                                packed_offset: torch.Tensor, pairs: int, *, dw=None,
+                                accumulate=False, stream=None):
+    """ep_expert_gemm_wgrad on packed buffers: ``dy`` [rows, N], ``recv`` [rows, H]."""
+    return _expert_wgrad(dy, recv, expert_count, packed_offset, pairs, dw, accumulate, stream)
+
+
+def _combine_grad(dout, y, idx, slot, topk_w, dy, dtopk_w, stream):
+    dev = dout.device
+    (T, H), K = dout.shape, idx.shape[1]
+    lead = tuple(y.shape[:-1])
+    dy = _new(y.shape, _bf16(y), dev, stream) if dy is None else dy
+    dtopk_w = _new((T, K), torch.float32, dev, stream) if dtopk_w is None else dtopk_w
+    _rows(dout, "dout", H, (T,), dev)
+    _rows(y, "y", H, lead, dev)
+    _rows(dy, "dy", H, lead, dev)
+    for name, t, dtype in (("topk_idx", idx, torch.int32), ("slot", slot, torch.int32),
+                           ("topk_w", topk_w, torch.float32), ("dtopk_w", dtopk_w, torch.float32)):
+        _need(t, name, dtype, T * K, dev)
+    return T, H, K, dy, dtopk_w
+
+
+def ep_combine_grad(dout: torch.Tensor, y: torch.Tensor, topk_idx: torch.Tensor, slot: torch.Tensor,
+                    topk_w: torch.Tensor, C: int, *, dy=None, dtopk_w=None, stream=None):
+    """The gradient of ep_combine: ``dout`` [T, H] bf16 and the forward call's ``y`` [E, C, H],
+    ``topk_idx``, ``slot`` and ``topk_w`` [T, K] -> ``dy`` [E, C, H] bf16, the rows that hold a pair
+    (others keep what they hold), and ``dtopk_w`` [T, K] float32 (0 for a pair that is not kept)."""
+    if dout.dim() != 2 or topk_idx.dim() != 2 or y.dim() != 3 or y.shape[1] != C:
+        raise ValueError(f"expected dout [T, H], topk_idx [T, K] and y [E, {C}, H], got "
+                         f"{tuple(dout.shape)}, {tuple(topk_idx.shape)} and {tuple(y.shape)}")
+    T, H, K, dy, dtopk_w = _combine_grad(dout, y, topk_idx, slot, topk_w, dy, dtopk_w, stream)
+    _call("ep_combine_grad", _shape(T, H, y.shape[0], K, C, 1), dout, y, topk_idx, slot, topk_w, dy,
+          dtopk_w, stream=stream)
+    return dy, dtopk_w
+
+
+def ep_combine_grad_packed(dout: torch.Tensor, y: torch.Tensor, topk_idx: torch.Tensor,
+                           slot: torch.Tensor, packed_offset: torch.Tensor, topk_w: torch.Tensor,
+                           E: int, C: int, *, dy=None, dtopk_w=None, stream=None):
+    """ep_combine_grad on packed buffers: ``y`` and ``dy`` [rows, H]."""
+    if dout.dim() != 2 or topk_idx.dim() != 2 or y.dim() != 2:
+        raise ValueError(f"expected dout [T, H], topk_idx [T, K] and y [rows, H], got "
+                         f"{tuple(dout.shape)}, {tuple(topk_idx.shape)} and {tuple(y.shape)}")
+    T, H, K, dy, dtopk_w = _combine_grad(dout, y, topk_idx, slot, topk_w, dy, dtopk_w, stream)
+    _need(packed_offset, "packed_offset", torch.int32, E + 1, dout.device)
+    _call("ep_combine_grad_packed", _shape(T, H, E, K, C, 1), y.shape[0], dout, y, topk_idx, slot,
+          packed_offset, topk_w, dy, dtopk_w, stream=stream)
+    return dy, dtopk_w
+
+
+# ------------------------------------------------------------------------------------------
+# the dense product beside the experts
+# ------------------------------------------------------------------------------------------
+
+def _linear_args(x, w, act):
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+        raise ValueError(f"expected x [T, H] and w [N, H], got {tuple(x.shape)} and {tuple(w.shape)}")
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act: expected one of {sorted(ACTIVATIONS)}, got {act!r}")
+    _need(x, "x", _bf16(x), x.numel(), x.device)
+    _need(w, "w", _bf16(w), w.numel(), x.device)
+    return x.shape[0], x.shape[1], w.shape[0], ACTIVATIONS[act]
+
+
+def ep_linear(x: torch.Tensor, w: torch.Tensor, *, bias=None, act="none", residual=None, pre=None,
+              out=None, stream=None):
+    """``out = act(x @ w.T + bias) + residual``, one rounding: ``x`` [T, H], ``w`` [N, H], ``bias`` [N]
+    and ``residual`` [T, N] (or None) bf16 -> ``out`` [T, N] bf16 (may be ``residual`` itself). ``act``:
+    "none", "relu", "silu" or "gelu" (with the normal distribution). ``pre`` [T, N] bf16, if given,
+    receives ``x @ w.T + bias``, which ep_linear_grad needs for an activation."""
+    T, H, N, a = _linear_args(x, w, act)
+    dev = x.device
+    out = _new((T, N), _bf16(x), dev, stream) if out is None else out
+    if bias is not None:
+        _need(bias, "bias", _bf16(bias), N, dev)
+    for name, t in (("residual", residual), ("pre", pre), ("out", out)):
+        if t is not None:
+            _rows(t, name, N, (T,), dev)
+    _call("ep_linear", _shape(T, H, 1, 1, 1, 1), N, a, x, w, bias, residual, pre, out, stream=stream)
+    return out
+
+
+def linear_grad_workspace_bytes(T: int, N: int, act: str) -> int:
+    """Bytes of workspace ep_linear_grad needs for T rows, N outputs and an activation."""
+    return int(load_library().ep_linear_grad_workspace_bytes(
+        ctypes.byref(_shape(T, 8, 1, 1, 1, 1)), N, ACTIVATIONS[act]))
+
+
+def ep_linear_grad(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *, act="none", pre=None,
+                   dx=None, dw=None, dbias=None, workspace=None, stream=None):
+    """The gradients of ep_linear: ``dout`` [T, N] bf16 and the forward call's ``x``, ``w``, ``act`` and
+    (with an activation) ``pre`` -> ``dx`` [T, H] bf16, ``dw`` [N, H] bf16, ``dbias`` [N] float32. The
+    residual's gradient is ``dout``. ``workspace``: a device tensor of at least
+    linear_grad_workspace_bytes(T, N, act) bytes (allocated here if not given)."""
+    T, H, N, a = _linear_args(x, w, act)
+    dev = x.device
+    _rows(dout, "dout", N, (T,), dev)
+    if (pre is None) != (act == "none"):
+        raise ValueError("pre: given exactly for an activation")
+    if pre is not None:
+        _rows(pre, "pre", N, (T,), dev)
+    dx = _new((T, H), _bf16(x), dev, stream) if dx is None else dx
+    dw = _new((N, H), _bf16(x), dev, stream) if dw is None else dw
+    dbias = _new((N,), torch.float32, dev, stream) if dbias is None else dbias
+    _rows(dx, "dx", H, (T,), dev)
+    _rows(dw, "dw", H, (N,), dev)
+    _need(dbias, "dbias", torch.float32, N, dev)
+    if workspace is None:
+        workspace = _own_workspace(linear_grad_workspace_bytes(T, N, act), dev, stream)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: must be a contiguous tensor on the rows' device")
+    _call("ep_linear_grad", _shape(T, H, 1, 1, 1, 1), N, a, dout, pre, x, w, dx, dw, dbias, workspace,
+          workspace.numel() * workspace.element_size(), stream=stream)
+    return dx, dw, dbias
 
 
 def ep_check_e4m3_conversion(first_pattern: int, count: int, *, device=None, stream=None):

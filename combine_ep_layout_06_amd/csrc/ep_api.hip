@@ -9,6 +9,7 @@
 #include "ep.h"
 #include "ep_expert.h"
 #include "ep_internal.h"
+#include "ep_product.h"
 
 #ifndef EP_VERSION_STRING
 #define EP_VERSION_STRING "0.1.0"
@@ -908,6 +909,334 @@ int ep_moe_layer_fp8(const ep_shape_t *shape, int32_t I, const uint16_t *x,
     p.w2_scale = w2_scale;
     p.out = out;
     return moe_layer(shape, I, p, true, workspace, workspace_bytes, stream, "ep_moe_layer_fp8");
+}
+
+namespace {
+
+// Widths and weights of the bf16 products: rows in 16-byte chunks; lane offsets inside one matrix and
+// inside one tile of rows are 32 bits wide.
+int check_widths(int64_t H, int64_t N, const char *n_name, int64_t weights, const char *fn)
+{
+    const std::string f(fn);
+    if (N < 1) return fail(EP_ERR_INVALID, f + ": need " + n_name + " >= 1");
+    if (H % 8 != 0 || N % 8 != 0)
+        return fail(EP_ERR_UNSUPPORTED, f + ": H and " + n_name + " must be multiples of 8");
+    if (H >= 1 << 22 || N >= 1 << 22 || weights >= int64_t(1) << 30)
+        return fail(EP_ERR_UNSUPPORTED, f + ": a width reaches 2^22, or a weight matrix 2^30 elements");
+    return EP_OK;
+}
+
+// Checks shared by the experts' bf16 products: `n` channels beside H, n * halves rows or columns of an
+// expert's weights; `extra` is a third row buffer.
+int check_bf16_product(const ep_shape_t *shape, int32_t n, int halves, const char *n_name,
+                       const void *x, const void *w, const int32_t *expert_count, const void *extra,
+                       const void *out, const char *fn)
+{
+    const std::string f(fn);
+    if (int rc = check_shape(shape, fn)) return rc;
+    if (shape->E > EP_MAX_EXPERTS) return fail(EP_ERR_UNSUPPORTED, f + ": E exceeds EP_MAX_EXPERTS");
+    if (int rc = check_widths(shape->H, (int64_t)n * halves, n_name, (int64_t)n * halves * shape->H, fn))
+        return rc;
+    if (n % 8 != 0)
+        return fail(EP_ERR_UNSUPPORTED, f + ": H and " + n_name + " must be multiples of 8");
+    if (shape->T > 0 && (!x || !w || !expert_count || !out))
+        return fail(EP_ERR_INVALID, f + ": NULL required pointer");
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(extra, 16) || !aligned(out, 16))
+        return fail(EP_ERR_ALIGN, f + ": row buffers, weights and outputs must be 16-byte aligned");
+    if (!aligned(expert_count, 4))
+        return fail(EP_ERR_ALIGN, f + ": expert_count must be 4-byte aligned");
+    return EP_OK;
+}
+
+ep::Product bf16_product(const ep_shape_t *s, const uint16_t *x, const uint16_t *w,
+                         const int32_t *count, int k, int n, void *out)
+{
+    ep::Product p{};
+    p.x = x;
+    p.w = w;
+    p.count = count;
+    p.E = s->E;
+    p.C = s->C;
+    p.k = k;
+    p.n = n;
+    p.pairs = s->T * s->K;
+    p.out = out;
+    return p;
+}
+
+// The packed form of a product.
+void pack(ep::Product &p, const int32_t *packed_offset, int32_t rows)
+{
+    p.offset = packed_offset;
+    p.rows = p.C = rows;
+}
+
+int expert_wgrad(const ep_shape_t *shape, int32_t N, const uint16_t *dy, const uint16_t *recv,
+                 const int32_t *expert_count, const int32_t *packed_offset, bool packed, int32_t rows,
+                 bool f32, int32_t accumulate, void *dw, hipStream_t stream, const char *fn)
+{
+    if (int rc = check_bf16_product(shape, N, 1, "N", dy, recv, expert_count, nullptr, dw, fn)) return rc;
+    if (packed)
+        if (int rc = check_packed_rows(shape, rows, packed_offset, fn)) return rc;
+    if (!dw) return fail(EP_ERR_INVALID, std::string(fn) + ": NULL required pointer");
+    ep::Product p = bf16_product(shape, dy, recv, expert_count, 0, shape->H, dw);
+    p.m = N;
+    p.accumulate = accumulate != 0;
+    if (packed) pack(p, packed_offset, rows);
+    return hip_status(ep::launch_expert_wgrad(p, f32, stream), fn);
+}
+
+}  // namespace
+
+int ep_expert_gemm(const ep_shape_t *shape, int32_t N, const uint16_t *recv,
+                   const int32_t *expert_count, const uint16_t *w, uint16_t *y, hipStream_t stream)
+{
+    const char *fn = "ep_expert_gemm";
+    if (int rc = check_bf16_product(shape, N, 1, "N", recv, w, expert_count, nullptr, y, fn)) return rc;
+    return hip_status(
+        ep::launch_expert_gemm(bf16_product(shape, recv, w, expert_count, shape->H, N, y), stream), fn);
+}
+
+int ep_expert_gemm_packed(const ep_shape_t *shape, int32_t rows, int32_t N, const uint16_t *recv,
+                          const int32_t *expert_count, const int32_t *packed_offset,
+                          const uint16_t *w, uint16_t *y, hipStream_t stream)
+{
+    const char *fn = "ep_expert_gemm_packed";
+    if (int rc = check_bf16_product(shape, N, 1, "N", recv, w, expert_count, nullptr, y, fn)) return rc;
+    if (int rc = check_packed_rows(shape, rows, packed_offset, fn)) return rc;
+    ep::Product p = bf16_product(shape, recv, w, expert_count, shape->H, N, y);
+    pack(p, packed_offset, rows);
+    return hip_status(ep::launch_expert_gemm(p, stream), fn);
+}
+
+int ep_expert_swiglu(const ep_shape_t *shape, int32_t I, const uint16_t *recv,
+                     const int32_t *expert_count, const uint16_t *w13, uint16_t *gu, uint16_t *h,
+                     hipStream_t stream)
+{
+    const char *fn = "ep_expert_swiglu";
+    if (int rc = check_bf16_product(shape, I, 2, "I", recv, w13, expert_count, gu, h, fn)) return rc;
+    ep::Product p = bf16_product(shape, recv, w13, expert_count, shape->H, 2 * I, h);
+    p.out2 = gu;
+    return hip_status(ep::launch_expert_swiglu(p, stream), fn);
+}
+
+int ep_expert_swiglu_packed(const ep_shape_t *shape, int32_t rows, int32_t I, const uint16_t *recv,
+                            const int32_t *expert_count, const int32_t *packed_offset,
+                            const uint16_t *w13, uint16_t *gu, uint16_t *h, hipStream_t stream)
+{
+    const char *fn = "ep_expert_swiglu_packed";
+    if (int rc = check_bf16_product(shape, I, 2, "I", recv, w13, expert_count, gu, h, fn)) return rc;
+    if (int rc = check_packed_rows(shape, rows, packed_offset, fn)) return rc;
+    ep::Product p = bf16_product(shape, recv, w13, expert_count, shape->H, 2 * I, h);
+    p.out2 = gu;
+    pack(p, packed_offset, rows);
+    return hip_status(ep::launch_expert_swiglu(p, stream), fn);
+}
+
+int ep_expert_gemm_dgrad(const ep_shape_t *shape, int32_t N, const uint16_t *dy,
+                         const int32_t *expert_count, const uint16_t *w, uint16_t *dx,
+                         hipStream_t stream)
+{
+    const char *fn = "ep_expert_gemm_dgrad";
+    if (int rc = check_bf16_product(shape, N, 1, "N", dy, w, expert_count, nullptr, dx, fn)) return rc;
+    return hip_status(
+        ep::launch_expert_dgrad(bf16_product(shape, dy, w, expert_count, N, shape->H, dx), stream), fn);
+}
+
+int ep_expert_gemm_dgrad_packed(const ep_shape_t *shape, int32_t rows, int32_t N, const uint16_t *dy,
+                                const int32_t *expert_count, const int32_t *packed_offset,
+                                const uint16_t *w, uint16_t *dx, hipStream_t stream)
+{
+    const char *fn = "ep_expert_gemm_dgrad_packed";
+    if (int rc = check_bf16_product(shape, N, 1, "N", dy, w, expert_count, nullptr, dx, fn)) return rc;
+    if (int rc = check_packed_rows(shape, rows, packed_offset, fn)) return rc;
+    ep::Product p = bf16_product(shape, dy, w, expert_count, N, shape->H, dx);
+    pack(p, packed_offset, rows);
+    return hip_status(ep::launch_expert_dgrad(p, stream), fn);
+}
+
+int ep_expert_swiglu_dgrad(const ep_shape_t *shape, int32_t I, const uint16_t *dy,
+                           const int32_t *expert_count, const uint16_t *w2, const uint16_t *gu,
+                           uint16_t *dgu, hipStream_t stream)
+{
+    const char *fn = "ep_expert_swiglu_dgrad";
+    if (int rc = check_bf16_product(shape, I, 1, "I", dy, w2, expert_count, gu, dgu, fn)) return rc;
+    if (shape->T > 0 && !gu) return fail(EP_ERR_INVALID, std::string(fn) + ": NULL required pointer");
+    ep::Product p = bf16_product(shape, dy, w2, expert_count, shape->H, I, dgu);
+    p.in = gu;
+    return hip_status(ep::launch_expert_swiglu_dgrad(p, stream), fn);
+}
+
+int ep_expert_swiglu_dgrad_packed(const ep_shape_t *shape, int32_t rows, int32_t I,
+                                  const uint16_t *dy, const int32_t *expert_count,
+                                  const int32_t *packed_offset, const uint16_t *w2,
+                                  const uint16_t *gu, uint16_t *dgu, hipStream_t stream)
+{
+    const char *fn = "ep_expert_swiglu_dgrad_packed";
+    if (int rc = check_bf16_product(shape, I, 1, "I", dy, w2, expert_count, gu, dgu, fn)) return rc;
+    if (shape->T > 0 && !gu) return fail(EP_ERR_INVALID, std::string(fn) + ": NULL required pointer");
+    if (int rc = check_packed_rows(shape, rows, packed_offset, fn)) return rc;
+    ep::Product p = bf16_product(shape, dy, w2, expert_count, shape->H, I, dgu);
+    p.in = gu;
+    pack(p, packed_offset, rows);
+    return hip_status(ep::launch_expert_swiglu_dgrad(p, stream), fn);
+}
+
+int ep_expert_gemm_wgrad(const ep_shape_t *shape, int32_t N, const uint16_t *dy, const uint16_t *recv,
+                         const int32_t *expert_count, uint16_t *dw, hipStream_t stream)
+{
+    return expert_wgrad(shape, N, dy, recv, expert_count, nullptr, false, 0, false, 0, dw, stream,
+                        "ep_expert_gemm_wgrad");
+}
+
+int ep_expert_gemm_wgrad_packed(const ep_shape_t *shape, int32_t rows, int32_t N, const uint16_t *dy,
+                                const uint16_t *recv, const int32_t *expert_count,
+                                const int32_t *packed_offset, uint16_t *dw, hipStream_t stream)
+{
+    return expert_wgrad(shape, N, dy, recv, expert_count, packed_offset, true, rows, false, 0, dw, stream,
+                        "ep_expert_gemm_wgrad_packed");
+}
+
+int ep_expert_gemm_wgrad_f32(const ep_shape_t *shape, int32_t N, int32_t accumulate,
+                             const uint16_t *dy, const uint16_t *recv, const int32_t *expert_count,
+                             float *dw, hipStream_t stream)
+{
+    return expert_wgrad(shape, N, dy, recv, expert_count, nullptr, false, 0, true, accumulate, dw, stream,
+                        "ep_expert_gemm_wgrad_f32");
+}
+
+int ep_expert_gemm_wgrad_f32_packed(const ep_shape_t *shape, int32_t rows, int32_t N,
+                                    int32_t accumulate, const uint16_t *dy, const uint16_t *recv,
+                                    const int32_t *expert_count, const int32_t *packed_offset,
+                                    float *dw, hipStream_t stream)
+{
+    return expert_wgrad(shape, N, dy, recv, expert_count, packed_offset, true, rows, true, accumulate, dw,
+                        stream, "ep_expert_gemm_wgrad_f32_packed");
+}
+
+namespace {
+
+int combine_grad(const ep_shape_t *shape, const uint16_t *dout, const uint16_t *y,
+                 const int32_t *topk_idx, const int32_t *slot, const float *topk_w, uint16_t *dy,
+                 float *dtopk_w, ep::RowMap map, hipStream_t stream, const char *fn)
+{
+    const std::string f(fn);
+    if (shape->T > 0 && (!dout || !y || !topk_idx || !slot || !topk_w || !dy || !dtopk_w))
+        return fail(EP_ERR_INVALID, f + ": NULL required pointer");
+    if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(dy, 16))
+        return fail(EP_ERR_ALIGN, f + ": dout, y and dy must be 16-byte aligned");
+    if (!aligned(topk_idx, 4) || !aligned(slot, 4) || !aligned(topk_w, 4) || !aligned(dtopk_w, 4))
+        return fail(EP_ERR_ALIGN, f + ": ids, slots and weights must be 4-byte aligned");
+    return hip_status(ep::launch_combine_grad(*shape, dout, y, topk_idx, slot, topk_w, dy, dtopk_w,
+                                              stream, map),
+                      fn);
+}
+
+}  // namespace
+
+int ep_combine_grad(const ep_shape_t *shape, const uint16_t *dout, const uint16_t *y,
+                    const int32_t *topk_idx, const int32_t *slot, const float *topk_w, uint16_t *dy,
+                    float *dtopk_w, hipStream_t stream)
+{
+    const char *fn = "ep_combine_grad";
+    if (int rc = check_shape(shape, fn)) return rc;
+    if (int rc = check_rows(shape, fn, 8)) return rc;
+    return combine_grad(shape, dout, y, topk_idx, slot, topk_w, dy, dtopk_w, ep::RowMap(), stream, fn);
+}
+
+int ep_combine_grad_packed(const ep_shape_t *shape, int32_t rows, const uint16_t *dout,
+                           const uint16_t *y, const int32_t *topk_idx, const int32_t *slot,
+                           const int32_t *packed_offset, const float *topk_w, uint16_t *dy,
+                           float *dtopk_w, hipStream_t stream)
+{
+    const char *fn = "ep_combine_grad_packed";
+    if (int rc = check_packed(shape, rows, packed_offset, fn, 8)) return rc;
+    return combine_grad(shape, dout, y, topk_idx, slot, topk_w, dy, dtopk_w,
+                        ep::RowMap{packed_offset, rows}, stream, fn);
+}
+
+namespace {
+
+int check_linear(const ep_shape_t *shape, int32_t N, int32_t act, const char *fn)
+{
+    if (int rc = check_shape(shape, fn)) return rc;
+    if (int rc = check_widths(shape->H, N, "N", (int64_t)N * shape->H, fn)) return rc;
+    if (act < EP_ACT_NONE || act > EP_ACT_GELU)
+        return fail(EP_ERR_INVALID, std::string(fn) + ": act is no EP_ACT_ value");
+    return EP_OK;
+}
+
+// A product over the T rows of dense matrices.
+ep::Product dense(const ep_shape_t *s, const uint16_t *x, const uint16_t *w, int k, int n, void *out)
+{
+    ep::Product p = bf16_product(s, x, w, nullptr, k, n, out);
+    p.E = 1;
+    p.C = p.pairs = s->T;
+    return p;
+}
+
+}  // namespace
+
+int ep_linear(const ep_shape_t *shape, int32_t N, int32_t act, const uint16_t *x, const uint16_t *w,
+              const uint16_t *bias, const uint16_t *residual, uint16_t *pre, uint16_t *out,
+              hipStream_t stream)
+{
+    const char *fn = "ep_linear";
+    if (int rc = check_linear(shape, N, act, fn)) return rc;
+    if (shape->T > 0 && (!x || !w || !out))
+        return fail(EP_ERR_INVALID, std::string(fn) + ": NULL required pointer");
+    for (const void *q : {(const void *)x, (const void *)w, (const void *)bias, (const void *)residual,
+                          (const void *)pre, (const void *)out})
+        if (!aligned(q, 16)) return fail(EP_ERR_ALIGN, std::string(fn) + ": arrays must be 16-byte aligned");
+    ep::Product p = dense(shape, x, w, shape->H, N, out);
+    p.out2 = pre;
+    p.in = residual;
+    p.bias = bias;
+    p.act = act;
+    return hip_status(ep::launch_linear(p, stream), fn);
+}
+
+size_t ep_linear_grad_workspace_bytes(const ep_shape_t *shape, int32_t N, int32_t act)
+{
+    if (!shape || shape->T < 0 || N < 1 || act < EP_ACT_NONE || act > EP_ACT_GELU) return 0;
+    const size_t T = shape->T, chunks = (T + ep::kLinearGradRows - 1) / ep::kLinearGradRows;
+    return (size_t)N * (4 * chunks + (act == EP_ACT_NONE ? 0 : 2 * T));
+}
+
+int ep_linear_grad(const ep_shape_t *shape, int32_t N, int32_t act, const uint16_t *dout,
+                   const uint16_t *pre, const uint16_t *x, const uint16_t *w, uint16_t *dx,
+                   uint16_t *dw, float *dbias, void *workspace, size_t workspace_bytes,
+                   hipStream_t stream)
+{
+    const char *fn = "ep_linear_grad";
+    const std::string f(fn);
+    if (int rc = check_linear(shape, N, act, fn)) return rc;
+    if (shape->T > 1 << 21) return fail(EP_ERR_UNSUPPORTED, f + ": T exceeds 2^21");
+    const bool some = shape->T > 0;
+    if ((some && (!dout || !x || !w || !dx || (act != EP_ACT_NONE && !pre))) || !dw || !dbias)
+        return fail(EP_ERR_INVALID, f + ": NULL required pointer");
+    for (const void *q : {(const void *)dout, (const void *)pre, (const void *)x, (const void *)w,
+                          (const void *)dx, (const void *)dw, (const void *)workspace})
+        if (!aligned(q, 16)) return fail(EP_ERR_ALIGN, f + ": arrays must be 16-byte aligned");
+    if (!aligned(dbias, 4)) return fail(EP_ERR_ALIGN, f + ": dbias must be 4-byte aligned");
+    const size_t need = ep_linear_grad_workspace_bytes(shape, N, act);
+    if (need && !workspace) return fail(EP_ERR_INVALID, f + ": workspace is NULL");
+    if (workspace_bytes < need)
+        return fail(EP_ERR_INVALID, f + ": workspace_bytes " + std::to_string(workspace_bytes) +
+                                        " below the " + std::to_string(need) + " this shape needs");
+    // dz first: its T*N values are a multiple of 16 bytes
+    uint16_t *dz = act == EP_ACT_NONE ? nullptr : static_cast<uint16_t *>(workspace);
+    float *part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
+                                            (dz ? (size_t)2 * shape->T * N : 0));
+    hipError_t e = ep::launch_act_grad(dout, pre, dz, part, dbias, shape->T, N, act, stream);
+    const uint16_t *g = dz ? dz : dout;
+    if (e == hipSuccess) e = ep::launch_expert_dgrad(dense(shape, g, w, N, shape->H, dx), stream);
+    if (e == hipSuccess) {
+        ep::Product p = dense(shape, g, x, 0, shape->H, dw);
+        p.m = N;
+        e = ep::launch_expert_wgrad(p, false, stream);
+    }
+    return hip_status(e, fn);
 }
 
 int ep_check_e4m3_conversion(uint32_t first_pattern, uint32_t count, uint32_t *mismatches,

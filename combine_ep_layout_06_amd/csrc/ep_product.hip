@@ -1,0 +1,623 @@
+// The bf16 products on gfx950: the experts' product and its two gradients, the same with SwiGLU or its
+// gradient in the epilogue, and the dense product with bias, activation and residual.
+//
+//   forward   out[r][c]    = sum_k x[r][k] w[e][c][k]
+//   dgrad     out[r][c]    = sum_k x[r][k] w[e][k][c]
+//   wgrad     out[e][r][c] = sum_i x[i][r] w[i][c]       i over the rows of expert e
+//
+// One kernel for the three. A tile is 256 rows x 256 columns of the output, in blocks of 64 of the sum:
+// a workgroup of 8 wavefronts per CU walks its tiles as one stream of blocks, loads running ahead
+// across tiles, each wavefront with 128 x 64 of the tile in 128 registers (32 x 32 x 16 matrix
+// instructions; w is the A operand, so that a lane holds one row and groups of four columns). Of a
+// tile with fewer rows the wavefronts multiply only the parts of 64 that hold some.
+//
+// Operands go from global memory to LDS directly, in two stages of a block each. An operand whose sum
+// index runs along its rows in memory is kept row by row, 128 bytes of a row, and read 16 bytes a
+// lane. One whose sum index is the row number is kept as it lies, 64 rows of 256 values, and read
+// with the transposing LDS read, which gives a lane four consecutive sum indexes of one column.
+#include "ep_product.h"
+
+#include <type_traits>
+
+namespace ep {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kTile = 256;         // rows and columns of a tile
+constexpr int kCus = 256;
+
+enum class Form { kForward, kDgrad, kWgrad };
+enum class Out { kBf16, kSwiglu, kSwigluGrad, kF32, kLinear };
+
+#if defined(__HIP_DEVICE_COMPILE__)            // buffer descriptors exist on the device only
+
+constexpr int kWaves = kThreads / kWave;
+constexpr int kPart = 64;          // rows of a part
+constexpr int kBlock = 64;         // sum indexes of a block
+constexpr int kOperand = kTile * kBlock * 2;    // bytes of one operand of a block
+constexpr int kList = 256;         // tiles of a workgroup looked up together
+
+typedef __attribute__((address_space(3))) uint8_t *LdsBytes;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 *LdsTr;
+
+using ep::uniform;
+
+// The experts' rows cut into row tiles: rows and first row of each expert, the running number of row
+// tiles, and the rows of a tile. An expert's tiles are of one height, a multiple of kPart.
+struct TileTable {
+    int32_t end[EP_MAX_EXPERTS], base[EP_MAX_EXPERTS], n[EP_MAX_EXPERTS];
+    int32_t wave_sum[kWaves];
+};
+
+__device__ __forceinline__ void rows_of(const Product &p, int e, int &base, int &n)
+{
+    if (!p.count || p.pairs == 0) {            // dense, or no rows: the arrays need not be there
+        base = 0;
+        n = p.pairs == 0 ? 0 : p.C;
+    } else {
+        expert_rows(p.count, p.offset, e, p.C, p.rows, base, n);
+    }
+}
+
+__device__ __forceinline__ int tiles_of(int n) { return (n + kTile - 1) / kTile; }
+
+// Rows of a tile of an expert with n rows: its rows spread evenly over its tiles.
+__device__ __forceinline__ int height_of(int n)
+{
+    const int tiles = max(tiles_of(n), 1);
+    return ((n + tiles - 1) / tiles + kPart - 1) / kPart * kPart;
+}
+
+__device__ __forceinline__ int build_table(TileTable &t, const Product &p)
+{
+    constexpr int kPer = EP_MAX_EXPERTS / kThreads;
+    const int lane = threadIdx.x & (kWave - 1), wave = uniform(threadIdx.x / kWave);
+    const int e0 = threadIdx.x * kPer;
+    int tiles[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        tiles[i] = 0;
+        if (e0 + i < p.E) {
+            int base, n;
+            rows_of(p, e0 + i, base, n);
+            t.base[e0 + i] = base;
+            t.n[e0 + i] = n;
+            tiles[i] = tiles_of(n);
+        }
+        sum += tiles[i];
+    }
+    const int incl = wave_inclusive_sum(sum);
+    if (lane == kWave - 1) t.wave_sum[wave] = incl;
+    __syncthreads();
+    int run = incl - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        const int s = t.wave_sum[w];
+        if (w < wave) run += s;
+        total += s;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        run += tiles[i];
+        if (e0 + i < p.E) t.end[e0 + i] = run;
+    }
+    __syncthreads();
+    return uniform(total);
+}
+
+// A tile. Forward and dgrad: rows row0 .. row0 + n of expert e. Wgrad: the sum is over these rows, and
+// `mblk` is the row tile of the output. nblk: column tile.
+struct Tile {
+    int e, row0, n, nblk, mblk;
+};
+
+constexpr int kGroup = 8;
+
+// The tile at place `at` of the order: an expert's tiles in groups of kGroup row tiles, within a group
+// the row tile runs fastest, then the column tile.
+__device__ __forceinline__ Tile locate(const TileTable &t, const Product &p, int at, int n_tiles)
+{
+    const int m = at / n_tiles;
+    int lo = 0, hi = p.E - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (t.end[mid] > m) hi = mid;
+        else lo = mid + 1;
+    }
+    const int n_e = t.n[lo], tiles = tiles_of(n_e), h = height_of(n_e);
+    at -= (t.end[lo] - tiles) * n_tiles;
+    const int group = at / (kGroup * n_tiles), in_group = min(tiles - group * kGroup, kGroup);
+    at -= group * kGroup * n_tiles;
+    Tile r;
+    r.e = lo;
+    r.nblk = at / in_group;
+    const int m0 = (group * kGroup + at - r.nblk * in_group) * h;
+    r.row0 = t.base[lo] + m0;
+    r.n = min(max(n_e - m0, 0), h);
+    r.mblk = 0;
+    return r;
+}
+
+__device__ __forceinline__ Tile locate_wgrad(const Product &p, int at, int m_tiles, int n_tiles)
+{
+    Tile r;
+    r.e = at / (m_tiles * n_tiles);
+    at -= r.e * m_tiles * n_tiles;
+    r.nblk = at / m_tiles;
+    r.mblk = at - r.nblk * m_tiles;
+    rows_of(p, r.e, r.row0, r.n);
+    return r;
+}
+
+// A buffer's descriptor, of `bytes` from p: loads past them give 0.
+__device__ __forceinline__ i32x4 buffer(const void *p, int64_t bytes)
+{
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    const int n = bytes <= 0 ? 0 : bytes > 0x7FFFFFFF ? 0x7FFFFFFF : (int)bytes;
+    return i32x4{(int)(uint32_t)a, (int)(uint32_t)(a >> 32), n, 0x00027000};
+}
+
+// 16 bytes a lane from buffer `b` to 1 KiB of LDS from `to` on, lane after lane. Written out, because
+// the compiler cannot tell which of the stages a load of the builtin's form fills once paths meet, and
+// then waits for all of them before the next LDS read. It has no register output: the waits for it are
+// those of meet_loaded, and the compiler's own waits for later loads are only stricter by it. Nothing
+// else in these kernels uses m0.
+__device__ __forceinline__ void load_lds(i32x4 b, uint8_t *to, uint32_t off, uint32_t soff)
+{
+    const uint32_t at = (uint32_t)(uintptr_t)(LdsBytes)to;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(uniform(at)), "v"(off),
+                    "s"(i32x4{uniform(b[0]), uniform(b[1]), uniform(b[2]), uniform(b[3])}),
+                    "s"(uniform(soff)) : "memory");
+}
+
+// Meet the other wavefronts with this one's loads and LDS reads done.
+__device__ __forceinline__ void meet_loaded()
+{
+    __builtin_amdgcn_s_waitcnt(0x0070);        // vmcnt(0) lgkmcnt(0)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Two values as bf16, NaN as 0x7FC0.
+__device__ __forceinline__ uint32_t pair(float a, float b)
+{
+    const uint32_t v = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+    const uint32_t lo = a != a ? 0x7FC0u : v & 0xFFFFu, hi = b != b ? 0x7FC00000u : v & 0xFFFF0000u;
+    return lo | hi;
+}
+
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8])
+{
+    return u32x4{pair(v[0], v[1]), pair(v[2], v[3]), pair(v[4], v[5]), pair(v[6], v[7])};
+}
+
+__device__ __forceinline__ void unpack8(u32x4 d, float (&v)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(d[i]);
+        v[2 * i + 1] = bf16_hi(d[i]);
+    }
+}
+
+// 1 / (1 + exp(-g)), the reciprocal as in swiglu().
+__device__ __forceinline__ float sigmoid(float g)
+{
+    return __builtin_amdgcn_rcpf(__builtin_fmaf(__expf(-g), 0x1p-4f, 0x1p-4f)) * 0x1p-4f;
+}
+
+__device__ __forceinline__ float activate(int act, float z)
+{
+    if (act == EP_ACT_RELU) return z > 0.0f || z != z ? z : 0.0f;
+    if (act == EP_ACT_SILU) return z * sigmoid(z);
+    if (act == EP_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+    return z;
+}
+
+// swizzle of row r of an operand kept row by row: chunk c (16 bytes) of the row's eight is at place
+// c ^ swizzle(r)
+__device__ __forceinline__ int swizzle(int r) { return (r & 7) ^ ((r >> 4) & 1); }
+
+// and of one kept as it lies: the 64-byte unit u of row k is at place u ^ tr_swizzle(k): the eight rows
+// that one transposing read touches (four, and the same eight further on) then lie in different units
+__device__ __forceinline__ int tr_swizzle(int k) { return (k & 3) | ((k >> 1) & 4); }
+
+template <Form F, Out O, typename Stage>
+__device__ __forceinline__ void run(const Product &p, const Stage &stage, const Tile *list, int tiles)
+{
+    constexpr bool kXTr = F == Form::kWgrad, kWTr = F != Form::kForward;
+    const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
+    const int wm = wave & 1, wn = wave >> 1;
+    const int half = lane >> 5;
+    const int ldx = F == Form::kWgrad ? p.m : p.k;       // values of a row in memory
+    const int ldw = F == Form::kForward ? p.k : p.n;
+
+    auto at = [&](int i) {
+        const Tile t = list[i];
+        return Tile{uniform(t.e), uniform(t.row0), uniform(t.n), uniform(t.nblk), uniform(t.mblk)};
+    };
+    auto blocks_of = [&](const Tile &t) {
+        return F == Form::kWgrad ? max((t.n + kBlock - 1) / kBlock, 1) : (p.k + kBlock - 1) / kBlock;
+    };
+
+    // the stream of loads: the tile it is in and its next block
+    struct {
+        int tile, kb, nkb;
+        const uint8_t *x, *w;
+        int64_t xleft, wleft;              // bytes from x and w to the operands' ends
+        i32x4 xb, wb;
+        uint32_t xoff[2], woff[2];
+    } ld;
+    // A load of an operand kept row by row fills 8 rows of 8 chunks, one of an operand kept as it lies 2
+    // rows of 32; load j of a wavefront begins j times as many rows further on, and its lanes' chunks are
+    // one of two choices (`v`).
+    auto chunk = [&](int v) { return (lane & 7) ^ (lane >> 3) ^ v; };
+    auto tr_byte = [&](int v) {
+        return ((((lane & 31) >> 2) ^ tr_swizzle(wave * 8 + half) ^ (v * 2)) << 6) + (lane & 3) * 16;
+    };
+    auto weight_row = [&](int nblk, int i) {
+        if constexpr (O == Out::kSwiglu)       // 32 gate rows and the same 32 up rows together
+            return ((i >> 5) & 1) * (p.n / 2) + nblk * 128 + (i >> 6) * 32 + (i & 31);
+        else
+            return nblk * kTile + i;
+    };
+    auto enter = [&](int i) {
+        const Tile t = at(i);
+        ld.tile = i;
+        ld.kb = 0;
+        ld.nkb = blocks_of(t);
+        if constexpr (F == Form::kForward) {
+            ld.w = reinterpret_cast<const uint8_t *>(p.w + (size_t)t.e * p.n * p.k);
+            ld.wleft = (int64_t)p.n * p.k * 2;
+        } else if constexpr (F == Form::kDgrad) {
+            ld.w = reinterpret_cast<const uint8_t *>(p.w + (size_t)t.e * p.n * p.k + t.nblk * kTile);
+            ld.wleft = ((int64_t)p.n * p.k - t.nblk * kTile) * 2;
+        } else {
+            ld.w = reinterpret_cast<const uint8_t *>(p.w + (size_t)t.row0 * p.n + t.nblk * kTile);
+            ld.wleft = ((int64_t)t.n * p.n - t.nblk * kTile) * 2;
+        }
+        ld.x = reinterpret_cast<const uint8_t *>(p.x + (size_t)t.row0 * ldx + t.mblk * kTile);
+        ld.xleft = ((int64_t)t.n * ldx - t.mblk * kTile) * 2;
+        ld.xb = buffer(ld.x, ld.xleft);
+        ld.wb = buffer(ld.w, ld.wleft);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            const int r = wave * 32 + (lane >> 3), k = wave * 8 + half;
+            if constexpr (kXTr) ld.xoff[v] = (uint32_t)k * ldx * 2 + tr_byte(v);
+            else ld.xoff[v] = (uint32_t)r * ldx * 2 + chunk(v) * 16;
+            if constexpr (kWTr) ld.woff[v] = (uint32_t)k * ldw * 2 + tr_byte(v);
+            else ld.woff[v] = (uint32_t)weight_row(t.nblk, r) * ldw * 2 + chunk(v) * 16;
+        }
+    };
+    const int tail = (p.k & (kBlock - 1)) ? (p.k & (kBlock - 1)) / 8 : 8;    // chunks of the last block
+    // the loads of one block: past an operand's end they give 0
+    auto load_some = [&](uint8_t *to, int i0, int i1) {
+        const bool last = ld.kb == ld.nkb - 1;
+#pragma unroll
+        for (int i = i0; i < i1; ++i) {
+            const int j = i & 3;
+            const bool w = i >= 4;
+            const bool tr = w ? kWTr : kXTr;
+            const int v = tr ? j & 1 : j >> 1, rows = j * (w ? ldw : ldx) * (tr ? 4 : 16);
+            uint32_t off = w ? ld.woff[v] : ld.xoff[v];
+            if (!tr && last && chunk(v) >= tail) off = 0x80000000u;
+            const uint32_t soff = rows + (tr ? 0 : ld.kb * (kBlock * 2));
+            load_lds(w ? ld.wb : ld.xb, to + (w ? kOperand : 0) + (wave * 4 + j) * 1024, off, soff);
+        }
+    };
+    auto advance = [&]() {                     // past the last block: that block again
+        if (ld.kb + 1 < ld.nkb) {
+            ++ld.kb;
+            if constexpr (kXTr) {
+                ld.x += (size_t)kBlock * ldx * 2;
+                ld.xleft -= (int64_t)kBlock * ldx * 2;
+                ld.xb = buffer(ld.x, ld.xleft);
+            }
+            if constexpr (kWTr) {
+                ld.w += (size_t)kBlock * ldw * 2;
+                ld.wleft -= (int64_t)kBlock * ldw * 2;
+                ld.wb = buffer(ld.w, ld.wleft);
+            }
+        } else if (ld.tile + 1 < tiles) {
+            enter(ld.tile + 1);
+        }
+    };
+
+    f32x16 acc[2][4];
+    bf16x8 wf[2][2], xf[2][4];                 // the operands of 16 sum indexes, and the next ones
+    auto clear = [&]() {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[nt][mt][i] = 0.0f;
+    };
+    // Where a lane reads sum indexes 0 .. of its wavefront's first 32 rows (columns) in an operand. Row
+    // by row: chunk 2 * j + half of row lane & 31 for those from 16 * j on. As it lies: rows half * 8 +
+    // 0 .. 3 (and, 4 rows further, the rest), its 16 lanes' half of a unit.
+    const int r32 = lane & 31, i16 = lane & 15;
+    const int row_at = r32 * 128 + ((half ^ swizzle(r32)) << 4);
+    const int tr_sw = (i16 >> 2) | (half << 2);
+    const int tr_at = (half * 8 + (i16 >> 2)) * 512 + ((lane >> 4) & 1) * 32 + (i16 & 3) * 8;
+    const int x_at = kXTr ? tr_at + ((wm ^ tr_sw) << 6) : row_at + wm * 4096;
+    const int w_at = kOperand + (kWTr ? tr_at + (((wn * 2) ^ tr_sw) << 6) : row_at + wn * 8192);
+    // worked out where it is used: kept for every j and unit it would take more registers than there are
+    auto flip = [](int a, int bits) {
+        if (bits) asm volatile("v_xor_b32 %0, %1, %2" : "=v"(a) : "s"(uniform(bits)), "0"(a));
+        return a;
+    };
+    // `unit`: how many 32 rows (columns) further on
+    auto read = [&](auto tr, const uint8_t *from, int lane_at, int unit, int j) -> bf16x8 {
+        if constexpr (decltype(tr)::value) {
+            const uint8_t *a = from + flip(lane_at, unit << 6) + j * 8192;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)a);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(a + 2048));
+            return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            return *reinterpret_cast<const bf16x8 *>(from + flip(lane_at, j << 5) + unit * 4096);
+        }
+    };
+    auto read_x = [&](bf16x8 &to, const uint8_t *from, int mt, int j) {
+        to = read(std::bool_constant<kXTr>{}, from, x_at, mt * 2, j);
+    };
+    auto read_w = [&](bf16x8 &to, const uint8_t *from, int nt, int j) {
+        to = read(std::bool_constant<kWTr>{}, from, w_at, nt, j);
+    };
+
+    // One block, in stage S, of a tile whose wavefronts have `parts` parts. The operands of the next 16
+    // sum indexes are read behind the products of these.
+    auto step = [&](auto at_s, int parts) {
+        constexpr int S = decltype(at_s)::value;
+        uint8_t *cur = stage(std::integral_constant<int, S>{});
+        const uint8_t *nxt = stage(std::integral_constant<int, S ^ 1>{});
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int b = j & 1;
+            if (j == 3) meet_loaded();         // this block is read, the next one is there
+            const uint8_t *from = j == 3 ? nxt : cur;
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+                if (mt == 0) {
+                    read_w(wf[b ^ 1][0], from, 0, (j + 1) & 3);
+                    read_w(wf[b ^ 1][1], from, 1, (j + 1) & 3);
+                }
+                if (j == 3) {                  // the next tile may have more parts
+                    read_x(xf[b ^ 1][mt], from, mt, 0);
+                    load_some(cur, 2 * mt, 2 * mt + 2);
+                }
+                if (mt == 0 || parts > mt) {
+                    if (j < 3) read_x(xf[b ^ 1][mt], from, mt, j + 1);
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt)
+                        acc[nt][mt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf[b][nt], xf[b][mt],
+                                                                              acc[nt][mt], 0, 0, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        advance();
+    };
+
+    // Eight consecutive columns of a row: the lanes' halves trade, so that a lane of half h has those of
+    // columns nt * 32 + (2 * g + h) * 8 of its wavefront's 64.
+    auto eight = [&](const f32x16 &v, int g, float (&to)[8]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[g * 8 + i]),
+                                                            __float_as_uint(v[g * 8 + 4 + i]), false, false);
+            to[i] = __uint_as_float(s[0]);
+            to[4 + i] = __uint_as_float(s[1]);
+        }
+    };
+    auto finish = [&](int tile) {              // the tile's output
+        const Tile t = at(tile);
+        const int m0 = F == Form::kWgrad ? t.mblk * kTile : 0;
+        const int rows = F == Form::kWgrad ? min(p.m - m0, kTile) : t.n;
+        const size_t first = F == Form::kWgrad ? (size_t)t.e * p.m + m0 : (size_t)t.row0;
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+            const int r = (mt * 2 + wm) * 32 + r32;
+            const size_t row = first + r;
+            if constexpr (O == Out::kSwiglu) {
+                const int I = p.n / 2;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const int c = t.nblk * 128 + wn * 32 + (2 * g + half) * 8;
+                    float gate[8], up[8], h[8];
+                    eight(acc[0][mt], g, gate);
+                    eight(acc[1][mt], g, up);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) h[i] = swiglu(gate[i], up[i]);
+                    if (r < rows && c < I) {
+                        *reinterpret_cast<u32x4 *>((uint16_t *)p.out + row * I + c) = pack8(h);
+                        if (p.out2) {
+                            *reinterpret_cast<u32x4 *>(p.out2 + row * p.n + c) = pack8(gate);
+                            *reinterpret_cast<u32x4 *>(p.out2 + row * p.n + I + c) = pack8(up);
+                        }
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const int c = t.nblk * kTile + wn * 64 + nt * 32 + (2 * g + half) * 8;
+                        float v[8];
+                        eight(acc[nt][mt], g, v);
+                        if (r >= rows || c >= p.n) continue;
+                        if constexpr (O == Out::kBf16) {
+                            *reinterpret_cast<u32x4 *>((uint16_t *)p.out + row * p.n + c) = pack8(v);
+                        } else if constexpr (O == Out::kF32) {
+                            f32x4 *o = reinterpret_cast<f32x4 *>((float *)p.out + row * p.n + c);
+                            f32x4 a{v[0], v[1], v[2], v[3]}, b{v[4], v[5], v[6], v[7]};
+                            if (p.accumulate) {
+                                a += o[0];
+                                b += o[1];
+                            }
+                            o[0] = a;
+                            o[1] = b;
+                        } else if constexpr (O == Out::kSwigluGrad) {
+                            const uint16_t *gu = p.in + row * p.n * 2 + c;
+                            float gate[8], up[8], dg[8], du[8];
+                            unpack8(*reinterpret_cast<const u32x4 *>(gu), gate);
+                            unpack8(*reinterpret_cast<const u32x4 *>(gu + p.n), up);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float s = sigmoid(gate[i]);
+                                du[i] = v[i] * (gate[i] * s);
+                                dg[i] = v[i] * up[i] * (s * __builtin_fmaf(gate[i], 1.0f - s, 1.0f));
+                            }
+                            uint16_t *o = (uint16_t *)p.out + row * p.n * 2 + c;
+                            *reinterpret_cast<u32x4 *>(o) = pack8(dg);
+                            *reinterpret_cast<u32x4 *>(o + p.n) = pack8(du);
+                        } else {
+                            float b[8];
+                            if (p.bias) {
+                                unpack8(*reinterpret_cast<const u32x4 *>(p.bias + c), b);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) v[i] += b[i];
+                            }
+                            if (p.out2) *reinterpret_cast<u32x4 *>(p.out2 + row * p.n + c) = pack8(v);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) v[i] = activate(p.act, v[i]);
+                            if (p.in) {
+                                unpack8(*reinterpret_cast<const u32x4 *>(p.in + row * p.n + c), b);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) v[i] += b[i];
+                            }
+                            *reinterpret_cast<u32x4 *>((uint16_t *)p.out + row * p.n + c) = pack8(v);
+                        }
+                    }
+            }
+        }
+        clear();
+    };
+
+    enter(0);
+    load_some(stage(std::integral_constant<int, 0>{}), 0, 8);
+    advance();
+    meet_loaded();
+    const uint8_t *first = stage(std::integral_constant<int, 0>{});
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) read_w(wf[0][nt], first, nt, 0);
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) read_x(xf[0][mt], first, mt, 0);
+    load_some(stage(std::integral_constant<int, 1>{}), 0, 8);
+    advance();
+    clear();
+    int tile = 0, kb = 0, nkb, parts;
+    auto open = [&]() {
+        const Tile t = at(tile);
+        const int rows = F == Form::kWgrad ? min(p.m - t.mblk * kTile, kTile) : t.n;
+        parts = (rows + kPart - 1) / kPart;
+        nkb = blocks_of(t);
+        kb = 0;
+    };
+    auto next = [&](auto at_s) {               // a block; false after the last one
+        step(at_s, parts);
+        if (++kb < nkb) return true;
+        finish(tile);
+        if (++tile == tiles) return false;
+        open();
+        return true;
+    };
+    open();
+    while (next(std::integral_constant<int, 0>{}) && next(std::integral_constant<int, 1>{})) {}
+    meet_loaded();                             // no direct load is left to write LDS
+}
+#endif
+
+template <Form F, Out O>
+__global__ __launch_bounds__(kThreads) void product_kernel(Product p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    __shared__ __attribute__((aligned(16))) uint8_t s0[2 * kOperand];
+    __shared__ __attribute__((aligned(16))) uint8_t s1[2 * kOperand];
+    __shared__ Tile list[kList];
+    static_assert(sizeof(TileTable) <= sizeof(s0), "the table is done with before the first block");
+    auto stage = [&](auto s) -> uint8_t * {
+        if constexpr (decltype(s)::value == 0) return s0;
+        else return s1;
+    };
+    TileTable &table = *reinterpret_cast<TileTable *>(s0);
+    const int n_tiles = (p.n + kTile - 1) / kTile, m_tiles = (p.m + kTile - 1) / kTile;
+    // Neighbours in the tiles' order share operands: of each gridDim.x tiles in a row an XCD takes one
+    // eighth (its workgroups are blockIdx.x mod 8, gridDim.x is a multiple of 8)
+    const int place = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+    for (int first = place;;) {                // kList tiles at a time
+        int total;
+        if constexpr (F == Form::kWgrad) total = p.E * m_tiles * n_tiles;
+        else total = build_table(table, p) * n_tiles;
+        if (first >= total) break;
+        const int tiles = min((total - first + (int)gridDim.x - 1) / (int)gridDim.x, kList);
+        if ((int)threadIdx.x < tiles) {
+            const int at = first + threadIdx.x * gridDim.x;
+            int columns;                       // nothing of its divisions stays in registers
+            asm volatile("" : "=s"(columns) : "0"(uniform(n_tiles)));
+            if constexpr (F == Form::kWgrad) list[threadIdx.x] = locate_wgrad(p, at, m_tiles, columns);
+            else list[threadIdx.x] = locate(table, p, at, columns);
+        }
+        __syncthreads();                       // the table is done with
+        run<F, O>(p, stage, list, tiles);
+        first += tiles * gridDim.x;
+    }
+#else
+    (void)p;
+#endif
+}
+
+// One workgroup per CU, or as many as there can be tiles.
+template <Form F, Out O>
+hipError_t launch_product(const Product &p, hipStream_t stream)
+{
+    int64_t tiles = (p.n + kTile - 1) / kTile;
+    if (F == Form::kWgrad) {
+        tiles *= (int64_t)p.E * ((p.m + kTile - 1) / kTile);
+    } else {
+        if (p.pairs == 0 || (p.offset && p.rows == 0)) return hipSuccess;
+        const int64_t experts = p.pairs < p.E ? p.pairs : p.E;
+        tiles *= p.pairs / kTile + experts;
+    }
+    const dim3 grid((unsigned)(tiles < kCus ? (tiles + 7) / 8 * 8 : kCus));
+    return launch(product_kernel<F, O>, grid, dim3(kThreads), 0, stream, p);
+}
+
+}  // namespace
+
+hipError_t launch_expert_gemm(const Product &p, hipStream_t stream)
+{
+    return launch_product<Form::kForward, Out::kBf16>(p, stream);
+}
+
+hipError_t launch_expert_swiglu(const Product &p, hipStream_t stream)
+{
+    return launch_product<Form::kForward, Out::kSwiglu>(p, stream);
+}
+
+hipError_t launch_expert_dgrad(const Product &p, hipStream_t stream)
+{
+    return launch_product<Form::kDgrad, Out::kBf16>(p, stream);
+}
+
+hipError_t launch_expert_swiglu_dgrad(const Product &p, hipStream_t stream)
+{
+    return launch_product<Form::kDgrad, Out::kSwigluGrad>(p, stream);
+}
+
+hipError_t launch_expert_wgrad(const Product &p, bool f32, hipStream_t stream)
+{
+    return f32 ? launch_product<Form::kWgrad, Out::kF32>(p, stream)
+               : launch_product<Form::kWgrad, Out::kBf16>(p, stream);
+}
+
+hipError_t launch_linear(const Product &p, hipStream_t stream)
+{
+    return launch_product<Form::kForward, Out::kLinear>(p, stream);
+}
+
+}  // namespace ep

@@ -557,6 +557,171 @@ int ep_moe_layer_fp8(const ep_shape_t *shape, int32_t I, const uint16_t *x,
                      uint16_t *out, void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * The experts in bf16, forward and backward: products over the rows of the bf16 receive buffer (what
+ * ep_dispatch and its kin write and ep_combine reads).
+ *
+ * Rows are as in the FP8 products: each expert e holds n = expert_count[e] rows from row e*C of a padded
+ * buffer [E][C] (n taken as min(max(n, 0), C)), or from row packed_offset[e] of a packed buffer of
+ * `rows` rows (rows outside the buffer are left out; C is not used). Only these rows are read and
+ * written; other rows of the outputs keep what they hold. shape->T * shape->K is the number of pairs
+ * laid out; it chooses the grid, never the result, except that T = 0 means no rows. R is not used. H is
+ * the width of the rows that the forward product takes, in its gradients too.
+ *
+ * Sums are fp32 (of exact products of bf16 values), rounded once to the output's type. NaN and
+ * infinite values propagate to the elements they enter. Deterministic: the same inputs give the same
+ * bits.
+ *
+ * Common requirements: all widths multiples of 8 and below 2^22, an expert's weights below 2^30
+ * elements, E <= EP_MAX_EXPERTS (else EP_ERR_UNSUPPORTED); row buffers, weights and outputs 16-byte
+ * aligned, counts and offsets 4-byte aligned (else EP_ERR_ALIGN). Outputs must not overlap inputs, and
+ * no two experts' rows may overlap.
+ */
+
+/*
+ * ep_expert_gemm / ep_expert_gemm_packed -- y[r][c] = bf16(sum_k recv[r][k] * w[e][c][k]).
+ *   recv [E*C*H] (packed: [rows*H]) uint16 (bf16);  w [E][N][H] uint16 (bf16)
+ *   y    [E*C*N] (packed: [rows*N]) uint16 (bf16) out
+ */
+int ep_expert_gemm(const ep_shape_t *shape, int32_t N, const uint16_t *recv,
+                   const int32_t *expert_count, const uint16_t *w, uint16_t *y, hipStream_t stream);
+
+int ep_expert_gemm_packed(const ep_shape_t *shape, int32_t rows, int32_t N, const uint16_t *recv,
+                          const int32_t *expert_count, const int32_t *packed_offset,
+                          const uint16_t *w, uint16_t *y, hipStream_t stream);
+
+/*
+ * ep_expert_swiglu / ep_expert_swiglu_packed -- the gate and up products and SwiGLU in one launch. With
+ * g and u the products (fp32, not rounded), h = g / (1 + exp(-g)) * u, within (1.5 |g| + 8) * 2^-24 of
+ * its value before its rounding to bf16 for g above -88.7 (a zero of h's sign below).
+ *   w13  [E][2I][H] uint16 (bf16), the I gate rows and then the I up rows
+ *   gu   [E*C*2I] (packed: [rows*2I]) uint16 (bf16) out: per row the I values bf16(g), then the I values
+ *        bf16(u), which ep_expert_swiglu_dgrad takes; NULL: not kept
+ *   h    [E*C*I] (packed: [rows*I]) uint16 (bf16) out
+ */
+int ep_expert_swiglu(const ep_shape_t *shape, int32_t I, const uint16_t *recv,
+                     const int32_t *expert_count, const uint16_t *w13, uint16_t *gu, uint16_t *h,
+                     hipStream_t stream);
+
+int ep_expert_swiglu_packed(const ep_shape_t *shape, int32_t rows, int32_t I, const uint16_t *recv,
+                            const int32_t *expert_count, const int32_t *packed_offset,
+                            const uint16_t *w13, uint16_t *gu, uint16_t *h, hipStream_t stream);
+
+/*
+ * ep_expert_gemm_dgrad / ep_expert_gemm_dgrad_packed -- the gradient of ep_expert_gemm's rows,
+ *   dx[r][k] = bf16(sum_c dy[r][c] * w[e][c][k])
+ *   dy [E*C*N] (packed: [rows*N]) uint16 (bf16);  w [E][N][H], as in the forward product
+ *   dx [E*C*H] (packed: [rows*H]) uint16 (bf16) out
+ * The gradient of the token rows that ep_dispatch placed is ep_combine of dx with weights 1.
+ */
+int ep_expert_gemm_dgrad(const ep_shape_t *shape, int32_t N, const uint16_t *dy,
+                         const int32_t *expert_count, const uint16_t *w, uint16_t *dx,
+                         hipStream_t stream);
+
+int ep_expert_gemm_dgrad_packed(const ep_shape_t *shape, int32_t rows, int32_t N, const uint16_t *dy,
+                                const int32_t *expert_count, const int32_t *packed_offset,
+                                const uint16_t *w, uint16_t *dx, hipStream_t stream);
+
+/*
+ * ep_expert_swiglu_dgrad / ep_expert_swiglu_dgrad_packed -- back through the down projection and SwiGLU:
+ *   dh[r][i] = sum_c dy[r][c] * w2[e][c][i]   (fp32, not rounded),  s = 1 / (1 + exp(-g)),
+ *   dgu[r] = bf16(dh * u * s * (1 + g * (1 - s))), then bf16(dh * g * s)
+ *   dy [E*C*H] (packed: [rows*H]) uint16 (bf16), the gradient of the down projection's output
+ *   w2 [E][H][I] uint16 (bf16);  gu as ep_expert_swiglu keeps it
+ *   dgu [E*C*2I] (packed: [rows*2I]) uint16 (bf16) out; may be gu itself
+ * ep_expert_gemm_dgrad and ep_expert_gemm_wgrad of dgu with N = 2I go on from there.
+ */
+int ep_expert_swiglu_dgrad(const ep_shape_t *shape, int32_t I, const uint16_t *dy,
+                           const int32_t *expert_count, const uint16_t *w2, const uint16_t *gu,
+                           uint16_t *dgu, hipStream_t stream);
+
+int ep_expert_swiglu_dgrad_packed(const ep_shape_t *shape, int32_t rows, int32_t I,
+                                  const uint16_t *dy, const int32_t *expert_count,
+                                  const int32_t *packed_offset, const uint16_t *w2,
+                                  const uint16_t *gu, uint16_t *dgu, hipStream_t stream);
+
+/*
+ * ep_expert_gemm_wgrad / ep_expert_gemm_wgrad_packed and their _f32 forms -- the gradient of the weights,
+ *   dw[e][c][k] = sum over the rows r of expert e of dy[r][c] * recv[r][k]
+ *   dy [E*C*N], recv [E*C*H] (packed: [rows*N], [rows*H]) uint16 (bf16)
+ *   dw [E][N][H] out, all of it: an expert without rows gets zeros (T = 0: all of them).
+ *      uint16 (bf16), or float in the _f32 forms; with accumulate != 0 these add the sum to what dw
+ *      holds (one rounding more).
+ */
+int ep_expert_gemm_wgrad(const ep_shape_t *shape, int32_t N, const uint16_t *dy, const uint16_t *recv,
+                         const int32_t *expert_count, uint16_t *dw, hipStream_t stream);
+
+int ep_expert_gemm_wgrad_packed(const ep_shape_t *shape, int32_t rows, int32_t N, const uint16_t *dy,
+                                const uint16_t *recv, const int32_t *expert_count,
+                                const int32_t *packed_offset, uint16_t *dw, hipStream_t stream);
+
+int ep_expert_gemm_wgrad_f32(const ep_shape_t *shape, int32_t N, int32_t accumulate,
+                             const uint16_t *dy, const uint16_t *recv, const int32_t *expert_count,
+                             float *dw, hipStream_t stream);
+
+int ep_expert_gemm_wgrad_f32_packed(const ep_shape_t *shape, int32_t rows, int32_t N,
+                                    int32_t accumulate, const uint16_t *dy, const uint16_t *recv,
+                                    const int32_t *expert_count, const int32_t *packed_offset,
+                                    float *dw, hipStream_t stream);
+
+/*
+ * ep_combine_grad / ep_combine_grad_packed -- the gradient of ep_combine (ep_combine_packed): for each
+ * kept pair i = t*K + j, with its row r as in the forward call,
+ *   dy[r][h] = bf16(topk_w[i] * dout[t][h]),  dtopk_w[i] = sum_h dout[t][h] * y[r][h]  (fp32)
+ * A pair that is not kept gets dtopk_w = 0; rows of dy that hold no pair keep what they hold.
+ *   dout [T*H] uint16 (bf16), y and dy [E*C*H] (packed: [rows*H]) uint16 (bf16), 16-byte aligned;
+ *   topk_idx, slot [T*K] int32, topk_w and dtopk_w [T*K] float, 4-byte aligned. dy may be y itself.
+ * K <= EP_MAX_TOPK, H % 8 == 0 (else EP_ERR_UNSUPPORTED).
+ */
+int ep_combine_grad(const ep_shape_t *shape, const uint16_t *dout, const uint16_t *y,
+                    const int32_t *topk_idx, const int32_t *slot, const float *topk_w, uint16_t *dy,
+                    float *dtopk_w, hipStream_t stream);
+
+int ep_combine_grad_packed(const ep_shape_t *shape, int32_t rows, const uint16_t *dout,
+                           const uint16_t *y, const int32_t *topk_idx, const int32_t *slot,
+                           const int32_t *packed_offset, const float *topk_w, uint16_t *dy,
+                           float *dtopk_w, hipStream_t stream);
+
+/*
+ * ep_linear -- a dense product with its epilogue, for what runs beside the routed experts (a shared
+ * expert, a projection; with the combined rows as the residual it adds itself to them):
+ *   z[t][c] = sum_k x[t][k] * w[c][k] + bias[c],  out[t][c] = bf16(act(z[t][c]) + residual[t][c])
+ * in fp32, one rounding. act: EP_ACT_NONE z, EP_ACT_RELU max(z, 0), EP_ACT_SILU z / (1 + exp(-z)),
+ * EP_ACT_GELU z * Phi(z) with the normal distribution Phi.
+ *   x [T*H], w [N*H], bias [N] or NULL, residual [T*N] or NULL: uint16 (bf16)
+ *   pre [T*N] uint16 (bf16) out: bf16(z), which ep_linear_grad takes; NULL: not kept
+ *   out [T*N] uint16 (bf16) out; may be residual itself
+ * All 16-byte aligned. H and N multiples of 8 below 2^22, N*H < 2^30 (else EP_ERR_UNSUPPORTED). E, K, C
+ * and R are not used. T = 0 does nothing. Deterministic.
+ */
+enum { EP_ACT_NONE = 0, EP_ACT_RELU = 1, EP_ACT_SILU = 2, EP_ACT_GELU = 3 };
+
+int ep_linear(const ep_shape_t *shape, int32_t N, int32_t act, const uint16_t *x, const uint16_t *w,
+              const uint16_t *bias, const uint16_t *residual, uint16_t *pre, uint16_t *out,
+              hipStream_t stream);
+
+/*
+ * ep_linear_grad -- the gradients of ep_linear from dout [T*N] uint16 (bf16), the gradient of its output
+ * (the residual's gradient is dout itself). With dz = dout * act'(pre) in fp32:
+ *   dbias[c] = sum_t dz[t][c]                       [N] float out
+ *   dx[t][k] = bf16(sum_c dzr[t][c] * w[c][k])      [T*H] uint16 (bf16) out
+ *   dw[c][k] = bf16(sum_t dzr[t][c] * x[t][k])      [N*H] uint16 (bf16) out
+ * where dzr is dz rounded to bf16, the matrix instruction's operand. With EP_ACT_NONE dzr = dz = dout and
+ * pre is not read (NULL). relu' is 0 at z <= 0. T = 0 writes dw and dbias as zeros.
+ *   workspace  device memory of at least ep_linear_grad_workspace_bytes(shape, N, act) bytes (else
+ *            EP_ERR_INVALID), 16-byte aligned; overwritten. Two calls in flight at once need two.
+ * The requirements of ep_linear; T <= 2^21.
+ *
+ * ep_linear_grad_workspace_bytes: 4*N * ceil(T / 64), and with an activation 2*T*N more (0 for an
+ * invalid shape, N or act). Host only.
+ */
+size_t ep_linear_grad_workspace_bytes(const ep_shape_t *shape, int32_t N, int32_t act);
+
+int ep_linear_grad(const ep_shape_t *shape, int32_t N, int32_t act, const uint16_t *dout,
+                   const uint16_t *pre, const uint16_t *x, const uint16_t *w, uint16_t *dx,
+                   uint16_t *dw, float *dbias, void *workspace, size_t workspace_bytes,
+                   hipStream_t stream);
+
+/*
  * ep_check_e4m3_conversion -- self-check of the two OCP E4M3 encoders of the FP8 dispatch on
  * the current device.
  *
