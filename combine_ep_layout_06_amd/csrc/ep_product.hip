@@ -11,10 +11,15 @@
 // instructions; w is the A operand, so that a lane holds one row and groups of four columns). Of a
 // tile with fewer rows the wavefronts multiply only the parts of 64 that hold some.
 //
-// Operands go from global memory to LDS directly, in two stages of a block each. An operand whose sum
-// index runs along its rows in memory is kept row by row, 128 bytes of a row, and read 16 bytes a
-// lane. One whose sum index is the row number is kept as it lies, 64 rows of 256 values, and read
-// with the transposing LDS read, which gives a lane four consecutive sum indexes of one column.
+// Operands go from global memory to LDS directly, in two stages of a block each, and a block in halves
+// of 128 rows or columns. An operand whose sum index runs along its rows in memory is kept row by row,
+// 128 bytes of a row, and read 16 bytes a lane. One whose sum index is the row number is kept as it
+// lies, 64 rows of 128 values, and read with the transposing LDS read, which gives a lane four
+// consecutive sum indexes of one column.
+//
+// A block is four phases of a quarter of its products. In each a wavefront reads from LDS what the next
+// phase needs and starts loading one of the four halves of the block after the next into the place of
+// one that all have read: so the loads are spread evenly, and every one has six phases to arrive.
 #include "ep_product.h"
 
 #include <type_traits>
@@ -27,16 +32,16 @@ constexpr int kThreads = 512;
 constexpr int kTile = 256;         // rows and columns of a tile
 constexpr int kCus = 256;
 
-enum class Form { kForward, kDgrad, kWgrad };
-enum class Out { kBf16, kSwiglu, kSwigluGrad, kF32, kLinear };
+namespace form { constexpr int kForward = 0, kDgrad = 1, kWgrad = 2; }
+namespace to { constexpr int kBf16 = 0, kSwiglu = 1, kSwigluGrad = 2, kF32 = 3, kLinear = 4; }
 
 #if defined(__HIP_DEVICE_COMPILE__)            // buffer descriptors exist on the device only
 
 constexpr int kWaves = kThreads / kWave;
 constexpr int kPart = 64;          // rows of a part
 constexpr int kBlock = 64;         // sum indexes of a block
-constexpr int kOperand = kTile * kBlock * 2;    // bytes of one operand of a block
-constexpr int kList = 256;         // tiles of a workgroup looked up together
+constexpr int kHalf = kTile / 2 * kBlock * 2;    // bytes of half an operand of a block
+constexpr int kList = kWave;       // tiles of a workgroup looked up together
 
 typedef __attribute__((address_space(3))) uint8_t *LdsBytes;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -173,13 +178,24 @@ __device__ __forceinline__ void load_lds(i32x4 b, uint8_t *to, uint32_t off, uin
                     "s"(uniform(soff)) : "memory");
 }
 
-// Meet the other wavefronts with this one's loads and LDS reads done.
+// Meet the other wavefronts with this one's LDS reads done, and all but its last N loads.
+template <int N>
 __device__ __forceinline__ void meet_loaded()
 {
-    __builtin_amdgcn_s_waitcnt(0x0070);        // vmcnt(0) lgkmcnt(0)
+    static_assert(N < 64, "the counter's range");
+    __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));    // vmcnt(N) lgkmcnt(0)
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+}
+
+// The lane, counted anew: what is computed from it is worked out where it is used, and takes no
+// register through the products (which need them all).
+__device__ __forceinline__ int lane_now()
+{
+    int l;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(l));
+    return l;
 }
 
 // Two values as bf16, NaN as 0x7FC0.
@@ -218,30 +234,30 @@ __device__ __forceinline__ float activate(int act, float z)
     return z;
 }
 
-// swizzle of row r of an operand kept row by row: chunk c (16 bytes) of the row's eight is at place
-// c ^ swizzle(r)
+// Swizzle of row r of an operand kept row by row: chunk c (16 bytes) of the row's eight is at place
+// c ^ swizzle(r). LDS serves 16 lanes together, 8 consecutive rows and those 16 further on: they then
+// touch all banks once.
 __device__ __forceinline__ int swizzle(int r) { return (r & 7) ^ ((r >> 4) & 1); }
 
-// and of one kept as it lies: the 64-byte unit u of row k is at place u ^ tr_swizzle(k): the eight rows
-// that one transposing read touches (four, and the same eight further on) then lie in different units
-__device__ __forceinline__ int tr_swizzle(int k) { return (k & 3) | ((k >> 1) & 4); }
+// In one kept as it lies the 64-byte unit u of row k's four is at place u ^ (k & 3): the four rows whose
+// units a transposing read of 32 lanes takes then lie in different banks.
 
-template <Form F, Out O, typename Stage>
+// The tiles of `list`, which all have A parts.
+template <int F, int O, int A, typename Stage>
 __device__ __forceinline__ void run(const Product &p, const Stage &stage, const Tile *list, int tiles)
 {
-    constexpr bool kXTr = F == Form::kWgrad, kWTr = F != Form::kForward;
-    const int wave = uniform(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
+    constexpr bool kXTr = F == form::kWgrad, kWTr = F != form::kForward;
+    const int wave = uniform(threadIdx.x / kWave);
     const int wm = wave & 1, wn = wave >> 1;
-    const int half = lane >> 5;
-    const int ldx = F == Form::kWgrad ? p.m : p.k;       // values of a row in memory
-    const int ldw = F == Form::kForward ? p.k : p.n;
+    const int ldx = F == form::kWgrad ? p.m : p.k;       // values of a row in memory
+    const int ldw = F == form::kForward ? p.k : p.n;
 
     auto at = [&](int i) {
         const Tile t = list[i];
         return Tile{uniform(t.e), uniform(t.row0), uniform(t.n), uniform(t.nblk), uniform(t.mblk)};
     };
     auto blocks_of = [&](const Tile &t) {
-        return F == Form::kWgrad ? max((t.n + kBlock - 1) / kBlock, 1) : (p.k + kBlock - 1) / kBlock;
+        return F == form::kWgrad ? max((t.n + kBlock - 1) / kBlock, 1) : (p.k + kBlock - 1) / kBlock;
     };
 
     // the stream of loads: the tile it is in and its next block
@@ -250,30 +266,20 @@ __device__ __forceinline__ void run(const Product &p, const Stage &stage, const 
         const uint8_t *x, *w;
         int64_t xleft, wleft;              // bytes from x and w to the operands' ends
         i32x4 xb, wb;
-        uint32_t xoff[2], woff[2];
+        uint32_t xoff, woff;
     } ld;
-    // A load of an operand kept row by row fills 8 rows of 8 chunks, one of an operand kept as it lies 2
-    // rows of 32; load j of a wavefront begins j times as many rows further on, and its lanes' chunks are
-    // one of two choices (`v`).
-    auto chunk = [&](int v) { return (lane & 7) ^ (lane >> 3) ^ v; };
-    auto tr_byte = [&](int v) {
-        return ((((lane & 31) >> 2) ^ tr_swizzle(wave * 8 + half) ^ (v * 2)) << 6) + (lane & 3) * 16;
-    };
-    auto weight_row = [&](int nblk, int i) {
-        if constexpr (O == Out::kSwiglu)       // 32 gate rows and the same 32 up rows together
-            return ((i >> 5) & 1) * (p.n / 2) + nblk * 128 + (i >> 6) * 32 + (i & 31);
-        else
-            return nblk * kTile + i;
-    };
+    // A load of an operand kept row by row fills 8 rows of 8 chunks, one of an operand kept as it lies 4
+    // rows of 16; a wavefront makes two of each half.
+    auto chunk_of = [&](int l) { return (l & 7) ^ (l >> 3) ^ (wave & 1); };
     auto enter = [&](int i) {
         const Tile t = at(i);
         ld.tile = i;
         ld.kb = 0;
         ld.nkb = blocks_of(t);
-        if constexpr (F == Form::kForward) {
+        if constexpr (F == form::kForward) {
             ld.w = reinterpret_cast<const uint8_t *>(p.w + (size_t)t.e * p.n * p.k);
             ld.wleft = (int64_t)p.n * p.k * 2;
-        } else if constexpr (F == Form::kDgrad) {
+        } else if constexpr (F == form::kDgrad) {
             ld.w = reinterpret_cast<const uint8_t *>(p.w + (size_t)t.e * p.n * p.k + t.nblk * kTile);
             ld.wleft = ((int64_t)p.n * p.k - t.nblk * kTile) * 2;
         } else {
@@ -284,30 +290,28 @@ __device__ __forceinline__ void run(const Product &p, const Stage &stage, const 
         ld.xleft = ((int64_t)t.n * ldx - t.mblk * kTile) * 2;
         ld.xb = buffer(ld.x, ld.xleft);
         ld.wb = buffer(ld.w, ld.wleft);
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            const int r = wave * 32 + (lane >> 3), k = wave * 8 + half;
-            if constexpr (kXTr) ld.xoff[v] = (uint32_t)k * ldx * 2 + tr_byte(v);
-            else ld.xoff[v] = (uint32_t)r * ldx * 2 + chunk(v) * 16;
-            if constexpr (kWTr) ld.woff[v] = (uint32_t)k * ldw * 2 + tr_byte(v);
-            else ld.woff[v] = (uint32_t)weight_row(t.nblk, r) * ldw * 2 + chunk(v) * 16;
-        }
+        const int l = lane_now(), chunk = chunk_of(l);
+        const int row8 = wave * 16 + (l >> 3), row4 = wave * 8 + (l >> 4);
+        const int tr_byte = ((((l >> 2) ^ (l >> 4)) & 3) << 6) + (l & 3) * 16;
+        const int wrow = t.nblk * (O == to::kSwiglu ? kTile / 2 : kTile) + row8;
+        if constexpr (kXTr) ld.xoff = (uint32_t)row4 * ldx * 2 + tr_byte;
+        else ld.xoff = (uint32_t)row8 * ldx * 2 + chunk * 16;
+        if constexpr (kWTr) ld.woff = (uint32_t)row4 * ldw * 2 + tr_byte;
+        else ld.woff = (uint32_t)wrow * ldw * 2 + chunk * 16;
     };
     const int tail = (p.k & (kBlock - 1)) ? (p.k & (kBlock - 1)) / 8 : 8;    // chunks of the last block
-    // the loads of one block: past an operand's end they give 0
-    auto load_some = [&](uint8_t *to, int i0, int i1) {
-        const bool last = ld.kb == ld.nkb - 1;
-#pragma unroll
-        for (int i = i0; i < i1; ++i) {
-            const int j = i & 3;
-            const bool w = i >= 4;
-            const bool tr = w ? kWTr : kXTr;
-            const int v = tr ? j & 1 : j >> 1, rows = j * (w ? ldw : ldx) * (tr ? 4 : 16);
-            uint32_t off = w ? ld.woff[v] : ld.xoff[v];
-            if (!tr && last && chunk(v) >= tail) off = 0x80000000u;
-            const uint32_t soff = rows + (tr ? 0 : ld.kb * (kBlock * 2));
-            load_lds(w ? ld.wb : ld.xb, to + (w ? kOperand : 0) + (wave * 4 + j) * 1024, off, soff);
-        }
+    // One half of an operand of the block: past an operand's end the loads give 0.
+    auto load = [&](uint8_t *to, auto is_w, int half_no) {
+        constexpr bool W = decltype(is_w)::value, TR = W ? kWTr : kXTr;
+        uint8_t *at = to + (2 * W + half_no) * kHalf + wave * 2048;
+        const int ldm = W ? ldw : ldx;
+        uint32_t off = W ? ld.woff : ld.xoff;
+        if (!TR && tail < 8 && ld.kb == ld.nkb - 1 && chunk_of(lane_now()) >= tail) off = 0x80000000u;
+        uint32_t soff = TR ? half_no * 256 : ld.kb * (kBlock * 2);
+        if (!TR && half_no)                    // SwiGLU: the second half are the up rows
+            soff += (W && O == to::kSwiglu ? (uint32_t)(p.n / 2) : 128u) * ldm * 2;
+        load_lds(W ? ld.wb : ld.xb, at, off, soff);
+        load_lds(W ? ld.wb : ld.xb, at + 1024, off, soff + (TR ? 8 : 16) * ldm);
     };
     auto advance = [&]() {                     // past the last block: that block again
         if (ld.kb + 1 < ld.nkb) {
@@ -327,25 +331,24 @@ __device__ __forceinline__ void run(const Product &p, const Stage &stage, const 
         }
     };
 
-    f32x16 acc[2][4];
-    bf16x8 wf[2][2], xf[2][4];                 // the operands of 16 sum indexes, and the next ones
+    f32x16 acc[2][A];
+    bf16x8 wf[2][4], xf[A][4];                 // 16 sum indexes each
     auto clear = [&]() {
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
+            for (int mt = 0; mt < A; ++mt)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[nt][mt][i] = 0.0f;
     };
-    // Where a lane reads sum indexes 0 .. of its wavefront's first 32 rows (columns) in an operand. Row
-    // by row: chunk 2 * j + half of row lane & 31 for those from 16 * j on. As it lies: rows half * 8 +
-    // 0 .. 3 (and, 4 rows further, the rest), its 16 lanes' half of a unit.
-    const int r32 = lane & 31, i16 = lane & 15;
+    // Where a lane reads sum indexes 0 .. of its wavefront's first 32 rows (columns) in a half. Row by row:
+    // chunk 2 * j + half of row lane & 31 for those from 16 * j on. As it lies: rows half * 8 + 0 .. 3
+    // (and, 4 rows further, the rest), its 16 lanes' part of a unit.
+    const int lane = lane_now(), half = lane >> 5, r32 = lane & 31, i16 = lane & 15;
     const int row_at = r32 * 128 + ((half ^ swizzle(r32)) << 4);
-    const int tr_sw = (i16 >> 2) | (half << 2);
-    const int tr_at = (half * 8 + (i16 >> 2)) * 512 + ((lane >> 4) & 1) * 32 + (i16 & 3) * 8;
-    const int x_at = kXTr ? tr_at + ((wm ^ tr_sw) << 6) : row_at + wm * 4096;
-    const int w_at = kOperand + (kWTr ? tr_at + (((wn * 2) ^ tr_sw) << 6) : row_at + wn * 8192);
+    const int tr_at = (half * 8 + (i16 >> 2)) * 256 + ((lane >> 4) & 1) * 32 + (i16 & 3) * 8;
+    const int x_at = kXTr ? tr_at + ((wm ^ (i16 >> 2)) << 6) : row_at + wm * 4096;
+    const int w_at = kWTr ? tr_at + ((wn ^ (i16 >> 2)) << 6) : row_at + wn * 4096;
     // worked out where it is used: kept for every j and unit it would take more registers than there are
     auto flip = [](int a, int bits) {
         if (bits) asm volatile("v_xor_b32 %0, %1, %2" : "=v"(a) : "s"(uniform(bits)), "0"(a));
@@ -354,57 +357,69 @@ __device__ __forceinline__ void run(const Product &p, const Stage &stage, const 
     // `unit`: how many 32 rows (columns) further on
     auto read = [&](auto tr, const uint8_t *from, int lane_at, int unit, int j) -> bf16x8 {
         if constexpr (decltype(tr)::value) {
-            const uint8_t *a = from + flip(lane_at, unit << 6) + j * 8192;
+            const uint8_t *a = from + flip(lane_at, unit << 6) + j * 4096;
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)a);
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(a + 2048));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(a + 1024));
             return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         } else {
             return *reinterpret_cast<const bf16x8 *>(from + flip(lane_at, j << 5) + unit * 4096);
         }
     };
-    auto read_x = [&](bf16x8 &to, const uint8_t *from, int mt, int j) {
-        to = read(std::bool_constant<kXTr>{}, from, x_at, mt * 2, j);
+    // rows (mt * 2 + wm) * 32 .. and columns (nt * 4 + wn) * 32 .. of the tile
+    auto read_x = [&](const uint8_t *from, int mt, int j) {
+        if (mt < A) xf[mt][j] = read(std::bool_constant<kXTr>{}, from + (mt >> 1) * kHalf, x_at, (mt & 1) * 2, j);
     };
-    auto read_w = [&](bf16x8 &to, const uint8_t *from, int nt, int j) {
-        to = read(std::bool_constant<kWTr>{}, from, w_at, nt, j);
+    auto read_w = [&](const uint8_t *from, int nt, int j) {
+        wf[nt][j] = read(std::bool_constant<kWTr>{}, from + (2 + nt) * kHalf, w_at, 0, j);
     };
 
-    // One block, in stage S, of a tile whose wavefronts have `parts` parts. The operands of the next 16
-    // sum indexes are read behind the products of these.
-    auto step = [&](auto at_s, int parts) {
-        constexpr int S = decltype(at_s)::value;
-        uint8_t *cur = stage(std::integral_constant<int, S>{});
-        const uint8_t *nxt = stage(std::integral_constant<int, S ^ 1>{});
+    constexpr int kLoads = A > 2 ? 8 : 6;      // of a block, by one wavefront
+    // The products of rows mt0, mt0 + 1 and columns nt, 16 sum indexes at a time, behind each `also(j)`.
+    auto multiply = [&](int mt0, int nt, auto also) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int b = j & 1;
-            if (j == 3) meet_loaded();         // this block is read, the next one is there
-            const uint8_t *from = j == 3 ? nxt : cur;
+            also(j);
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-                if (mt == 0) {
-                    read_w(wf[b ^ 1][0], from, 0, (j + 1) & 3);
-                    read_w(wf[b ^ 1][1], from, 1, (j + 1) & 3);
-                }
-                if (j == 3) {                  // the next tile may have more parts
-                    read_x(xf[b ^ 1][mt], from, mt, 0);
-                    load_some(cur, 2 * mt, 2 * mt + 2);
-                }
-                if (mt == 0 || parts > mt) {
-                    if (j < 3) read_x(xf[b ^ 1][mt], from, mt, j + 1);
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
-                        acc[nt][mt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf[b][nt], xf[b][mt],
-                                                                              acc[nt][mt], 0, 0, 0);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            }
+            for (int mt = mt0; mt < mt0 + 2; ++mt)
+                if (mt < A)
+                    acc[nt][mt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf[nt][j], xf[mt][j],
+                                                                          acc[nt][mt], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    // One block, in stage S. At each barrier what is read from then on has arrived, and what is loaded
+    // over has been read.
+    constexpr std::false_type x_half{};
+    constexpr std::true_type w_half{};
+    auto step = [&](auto at_s) {
+        constexpr int S = decltype(at_s)::value;
+        uint8_t *cur = stage(S);
+        const uint8_t *nxt = stage(S ^ 1);
+        meet_loaded<kLoads>();
+        multiply(0, 0, [&](int j) {
+            read_w(cur, 1, j);
+            read_x(cur, 2, j);
+            if (j == 1) load(cur, x_half, 0);
+        });
+        multiply(0, 1, [&](int j) {
+            read_x(cur, 3, j);
+            if (j == 1) load(cur, w_half, 0);
+        });
+        meet_loaded<kLoads>();
+        multiply(2, 0, [&](int j) {
+            read_x(nxt, 0, j);
+            if (j == 1) load(cur, w_half, 1);
+        });
+        multiply(2, 1, [&](int j) {
+            read_w(nxt, 0, j);
+            read_x(nxt, 1, j);
+            if (A > 2 && j == 1) load(cur, x_half, 1);
+        });
         advance();
     };
 
     // Eight consecutive columns of a row: the lanes' halves trade, so that a lane of half h has those of
-    // columns nt * 32 + (2 * g + h) * 8 of its wavefront's 64.
+    // columns (2 * g + h) * 8 .. of a product's 32.
     auto eight = [&](const f32x16 &v, int g, float (&to)[8]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -416,14 +431,14 @@ __device__ __forceinline__ void run(const Product &p, const Stage &stage, const 
     };
     auto finish = [&](int tile) {              // the tile's output
         const Tile t = at(tile);
-        const int m0 = F == Form::kWgrad ? t.mblk * kTile : 0;
-        const int rows = F == Form::kWgrad ? min(p.m - m0, kTile) : t.n;
-        const size_t first = F == Form::kWgrad ? (size_t)t.e * p.m + m0 : (size_t)t.row0;
+        const int m0 = F == form::kWgrad ? t.mblk * kTile : 0;
+        const int rows = F == form::kWgrad ? min(p.m - m0, kTile) : t.n;
+        const size_t first = F == form::kWgrad ? (size_t)t.e * p.m + m0 : (size_t)t.row0;
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-            const int r = (mt * 2 + wm) * 32 + r32;
+        for (int mt = 0; mt < A; ++mt) {
+            const int l = lane_now(), half = l >> 5, r = (mt * 2 + wm) * 32 + (l & 31);
             const size_t row = first + r;
-            if constexpr (O == Out::kSwiglu) {
+            if constexpr (O == to::kSwiglu) {
                 const int I = p.n / 2;
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
@@ -446,13 +461,13 @@ __device__ __forceinline__ void run(const Product &p, const Stage &stage, const 
                 for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
-                        const int c = t.nblk * kTile + wn * 64 + nt * 32 + (2 * g + half) * 8;
+                        const int c = t.nblk * kTile + nt * 128 + wn * 32 + (2 * g + half) * 8;
                         float v[8];
                         eight(acc[nt][mt], g, v);
                         if (r >= rows || c >= p.n) continue;
-                        if constexpr (O == Out::kBf16) {
+                        if constexpr (O == to::kBf16) {
                             *reinterpret_cast<u32x4 *>((uint16_t *)p.out + row * p.n + c) = pack8(v);
-                        } else if constexpr (O == Out::kF32) {
+                        } else if constexpr (O == to::kF32) {
                             f32x4 *o = reinterpret_cast<f32x4 *>((float *)p.out + row * p.n + c);
                             f32x4 a{v[0], v[1], v[2], v[3]}, b{v[4], v[5], v[6], v[7]};
                             if (p.accumulate) {
@@ -461,7 +476,7 @@ __device__ __forceinline__ void run(const Product &p, const Stage &stage, const 
                             }
                             o[0] = a;
                             o[1] = b;
-                        } else if constexpr (O == Out::kSwigluGrad) {
+                        } else if constexpr (O == to::kSwigluGrad) {
                             const uint16_t *gu = p.in + row * p.n * 2 + c;
                             float gate[8], up[8], dg[8], du[8];
                             unpack8(*reinterpret_cast<const u32x4 *>(gu), gate);
@@ -499,71 +514,88 @@ __device__ __forceinline__ void run(const Product &p, const Stage &stage, const 
     };
 
     enter(0);
-    load_some(stage(std::integral_constant<int, 0>{}), 0, 8);
-    advance();
-    meet_loaded();
-    const uint8_t *first = stage(std::integral_constant<int, 0>{});
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) read_w(wf[0][nt], first, nt, 0);
+    for (int b = 0; b < 2; ++b) {
+        load(stage(b), x_half, 0);
+        load(stage(b), w_half, 0);
+        load(stage(b), w_half, 1);
+        if constexpr (A > 2) load(stage(b), x_half, 1);
+        advance();
+    }
+    meet_loaded<2 * kLoads - 4>();             // the first block's first halves
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) read_x(xf[0][mt], first, mt, 0);
-    load_some(stage(std::integral_constant<int, 1>{}), 0, 8);
-    advance();
+    for (int j = 0; j < 4; ++j) {
+        read_w(stage(0), 0, j);
+        read_x(stage(0), 0, j);
+        read_x(stage(0), 1, j);
+    }
     clear();
-    int tile = 0, kb = 0, nkb, parts;
-    auto open = [&]() {
-        const Tile t = at(tile);
-        const int rows = F == Form::kWgrad ? min(p.m - t.mblk * kTile, kTile) : t.n;
-        parts = (rows + kPart - 1) / kPart;
-        nkb = blocks_of(t);
-        kb = 0;
-    };
+    int tile = 0, kb = 0, nkb = blocks_of(at(0));
     auto next = [&](auto at_s) {               // a block; false after the last one
-        step(at_s, parts);
+        step(at_s);
         if (++kb < nkb) return true;
         finish(tile);
         if (++tile == tiles) return false;
-        open();
+        kb = 0;
+        nkb = blocks_of(at(tile));
         return true;
     };
-    open();
     while (next(std::integral_constant<int, 0>{}) && next(std::integral_constant<int, 1>{})) {}
-    meet_loaded();                             // no direct load is left to write LDS
+    meet_loaded<0>();                           // no direct load is left to write LDS
 }
 #endif
 
-template <Form F, Out O>
+template <int F, int O>
 __global__ __launch_bounds__(kThreads) void product_kernel(Product p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
-    __shared__ __attribute__((aligned(16))) uint8_t s0[2 * kOperand];
-    __shared__ __attribute__((aligned(16))) uint8_t s1[2 * kOperand];
+    __shared__ __attribute__((aligned(1024))) uint8_t stages[2][4 * kHalf];
     __shared__ Tile list[kList];
-    static_assert(sizeof(TileTable) <= sizeof(s0), "the table is done with before the first block");
-    auto stage = [&](auto s) -> uint8_t * {
-        if constexpr (decltype(s)::value == 0) return s0;
-        else return s1;
-    };
-    TileTable &table = *reinterpret_cast<TileTable *>(s0);
+    static_assert(sizeof(TileTable) <= sizeof(stages), "the table is done with before the first block");
+    auto stage = [&](int s) -> uint8_t * { return stages[s]; };
+    TileTable &table = *reinterpret_cast<TileTable *>(stages);
     const int n_tiles = (p.n + kTile - 1) / kTile, m_tiles = (p.m + kTile - 1) / kTile;
     // Neighbours in the tiles' order share operands: of each gridDim.x tiles in a row an XCD takes one
     // eighth (its workgroups are blockIdx.x mod 8, gridDim.x is a multiple of 8)
-    const int place = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
-    for (int first = place;;) {                // kList tiles at a time
+    const int slot = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+    const int lane = threadIdx.x & (kWave - 1);
+    for (int first = slot;;) {                // kList tiles at a time
         int total;
-        if constexpr (F == Form::kWgrad) total = p.E * m_tiles * n_tiles;
+        if constexpr (F == form::kWgrad) total = p.E * m_tiles * n_tiles;
         else total = build_table(table, p) * n_tiles;
         if (first >= total) break;
         const int tiles = min((total - first + (int)gridDim.x - 1) / (int)gridDim.x, kList);
-        if ((int)threadIdx.x < tiles) {
-            const int at = first + threadIdx.x * gridDim.x;
+        // the tiles with the most parts first, so that those of one number of parts run together
+        Tile mine{};
+        int parts = 0;
+        if (lane < tiles) {
+            const int at = first + lane * gridDim.x;
             int columns;                       // nothing of its divisions stays in registers
             asm volatile("" : "=s"(columns) : "0"(uniform(n_tiles)));
-            if constexpr (F == Form::kWgrad) list[threadIdx.x] = locate_wgrad(p, at, m_tiles, columns);
-            else list[threadIdx.x] = locate(table, p, at, columns);
+            if constexpr (F == form::kWgrad) mine = locate_wgrad(p, at, m_tiles, columns);
+            else mine = locate(table, p, at, columns);
+            const int rows = F == form::kWgrad ? min(p.m - mine.mblk * kTile, kTile) : mine.n;
+            parts = (rows + kPart - 1) / kPart;
         }
-        __syncthreads();                       // the table is done with
-        run<F, O>(p, stage, list, tiles);
+        int count[5], place = 0;
+#pragma unroll
+        for (int a = 4; a >= 1; --a) {
+            const uint64_t these = __ballot(parts == a);
+            count[a] = __popcll(these);
+            place += parts < a ? count[a] : parts == a ? count_below(these) : 0;
+        }
+        if ((int)threadIdx.x < tiles) list[place] = mine;
+        __syncthreads();                       // the list is there, the table is done with
+        const Tile *these = list;
+        auto run_all = [&](auto a) {
+            constexpr int A = decltype(a)::value;
+            if (count[A]) run<F, O, A>(p, stage, these, count[A]);
+            these += count[A];
+        };
+        run_all(std::integral_constant<int, 4>{});
+        run_all(std::integral_constant<int, 3>{});
+        run_all(std::integral_constant<int, 2>{});
+        run_all(std::integral_constant<int, 1>{});
         first += tiles * gridDim.x;
     }
 #else
@@ -572,11 +604,11 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p)
 }
 
 // One workgroup per CU, or as many as there can be tiles.
-template <Form F, Out O>
+template <int F, int O>
 hipError_t launch_product(const Product &p, hipStream_t stream)
 {
     int64_t tiles = (p.n + kTile - 1) / kTile;
-    if (F == Form::kWgrad) {
+    if (F == form::kWgrad) {
         tiles *= (int64_t)p.E * ((p.m + kTile - 1) / kTile);
     } else {
         if (p.pairs == 0 || (p.offset && p.rows == 0)) return hipSuccess;
@@ -591,33 +623,33 @@ hipError_t launch_product(const Product &p, hipStream_t stream)
 
 hipError_t launch_expert_gemm(const Product &p, hipStream_t stream)
 {
-    return launch_product<Form::kForward, Out::kBf16>(p, stream);
+    return launch_product<form::kForward, to::kBf16>(p, stream);
 }
 
 hipError_t launch_expert_swiglu(const Product &p, hipStream_t stream)
 {
-    return launch_product<Form::kForward, Out::kSwiglu>(p, stream);
+    return launch_product<form::kForward, to::kSwiglu>(p, stream);
 }
 
 hipError_t launch_expert_dgrad(const Product &p, hipStream_t stream)
 {
-    return launch_product<Form::kDgrad, Out::kBf16>(p, stream);
+    return launch_product<form::kDgrad, to::kBf16>(p, stream);
 }
 
 hipError_t launch_expert_swiglu_dgrad(const Product &p, hipStream_t stream)
 {
-    return launch_product<Form::kDgrad, Out::kSwigluGrad>(p, stream);
+    return launch_product<form::kDgrad, to::kSwigluGrad>(p, stream);
 }
 
 hipError_t launch_expert_wgrad(const Product &p, bool f32, hipStream_t stream)
 {
-    return f32 ? launch_product<Form::kWgrad, Out::kF32>(p, stream)
-               : launch_product<Form::kWgrad, Out::kBf16>(p, stream);
+    return f32 ? launch_product<form::kWgrad, to::kF32>(p, stream)
+               : launch_product<form::kWgrad, to::kBf16>(p, stream);
 }
 
 hipError_t launch_linear(const Product &p, hipStream_t stream)
 {
-    return launch_product<Form::kForward, Out::kLinear>(p, stream);
+    return launch_product<form::kForward, to::kLinear>(p, stream);
 }
 
 }  // namespace ep
