@@ -921,8 +921,8 @@ int check_widths(int64_t H, int64_t N, const char *n_name, int64_t weights, cons
     if (N < 1) return fail(EP_ERR_INVALID, f + ": need " + n_name + " >= 1");
     if (H % 8 != 0 || N % 8 != 0)
         return fail(EP_ERR_UNSUPPORTED, f + ": H and " + n_name + " must be multiples of 8");
-    if (H >= 1 << 22 || N >= 1 << 22 || weights >= int64_t(1) << 30)
-        return fail(EP_ERR_UNSUPPORTED, f + ": a width reaches 2^22, or a weight matrix 2^30 elements");
+    if (H >= 1 << 20 || N >= 1 << 20 || weights >= int64_t(1) << 30)
+        return fail(EP_ERR_UNSUPPORTED, f + ": a width reaches 2^20, or a weight matrix 2^30 elements");
     return EP_OK;
 }
 

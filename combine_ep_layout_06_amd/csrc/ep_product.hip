@@ -198,18 +198,37 @@ __device__ __forceinline__ int lane_now()
     return l;
 }
 
-// Two values as bf16, NaN as 0x7FC0.
+// Two values as bf16, rounded to nearest even (a NaN stays one).
 __device__ __forceinline__ uint32_t pair(float a, float b)
 {
-    const uint32_t v = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
-    const uint32_t lo = a != a ? 0x7FC0u : v & 0xFFFFu, hi = b != b ? 0x7FC00000u : v & 0xFFFF0000u;
-    return lo | hi;
+    return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
 }
 
 __device__ __forceinline__ u32x4 pack8(const float (&v)[8])
 {
     return u32x4{pair(v[0], v[1]), pair(v[2], v[3]), pair(v[4], v[5]), pair(v[6], v[7])};
 }
+
+// Rows of an output (or of an epilogue's input) of a tile: `n` rows of `ld` values of `size` bytes. Lanes
+// address them by byte offsets; those of rows that are not there, and kNone, lie past the end, where
+// nothing is stored and loads give 0.
+constexpr uint32_t kNone = 0x80000000u;
+struct Rows {
+    __amdgpu_buffer_rsrc_t b;
+    __device__ __forceinline__ Rows(const void *p, size_t row0, int n, int ld, int size)
+    {
+        const uint8_t *at = reinterpret_cast<const uint8_t *>(p) + row0 * ld * size;
+        b = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(at), 0, n * ld * size, 0x00027000);
+    }
+    __device__ __forceinline__ void put(uint32_t off, u32x4 v) const
+    {
+        __builtin_amdgcn_raw_buffer_store_b128(v, b, off, 0, 0);
+    }
+    __device__ __forceinline__ u32x4 get(uint32_t off) const
+    {
+        return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0));
+    }
+};
 
 __device__ __forceinline__ void unpack8(u32x4 d, float (&v)[8])
 {
@@ -299,14 +318,16 @@ __device__ __forceinline__ void run(const Product &p, const Stage &stage, const 
         if constexpr (kWTr) ld.woff = (uint32_t)row4 * ldw * 2 + tr_byte;
         else ld.woff = (uint32_t)wrow * ldw * 2 + chunk * 16;
     };
-    const int tail = (p.k & (kBlock - 1)) ? (p.k & (kBlock - 1)) / 8 : 8;    // chunks of the last block
+    // lanes whose chunk of a row's last block is beyond the row
+    const int tail = (p.k & (kBlock - 1)) ? (p.k & (kBlock - 1)) / 8 : 8;
+    const uint64_t beyond = __ballot(chunk_of(lane_now()) >= tail);
     // One half of an operand of the block: past an operand's end the loads give 0.
     auto load = [&](uint8_t *to, auto is_w, int half_no) {
         constexpr bool W = decltype(is_w)::value, TR = W ? kWTr : kXTr;
         uint8_t *at = to + (2 * W + half_no) * kHalf + wave * 2048;
         const int ldm = W ? ldw : ldx;
         uint32_t off = W ? ld.woff : ld.xoff;
-        if (!TR && tail < 8 && ld.kb == ld.nkb - 1 && chunk_of(lane_now()) >= tail) off = 0x80000000u;
+        if (!TR && __builtin_amdgcn_inverse_ballot_w64(ld.kb == ld.nkb - 1 ? beyond : 0)) off = kNone;
         uint32_t soff = TR ? half_no * 256 : ld.kb * (kBlock * 2);
         if (!TR && half_no)                    // SwiGLU: the second half are the up rows
             soff += (W && O == to::kSwiglu ? (uint32_t)(p.n / 2) : 128u) * ldm * 2;
@@ -391,11 +412,21 @@ __device__ __forceinline__ void run(const Product &p, const Stage &stage, const 
     // over has been read.
     constexpr std::false_type x_half{};
     constexpr std::true_type w_half{};
+    constexpr int kStores = O == to::kSwiglu ? 2 * A : O == to::kSwigluGrad || O == to::kF32 ? 8 * A : 4 * A;
+    int stored = 0;                            // barriers to come whose loads are older than stores
+    auto meet = [&]() {
+        if (stored > 0) {
+            --stored;
+            meet_loaded<kLoads + kStores>();
+        } else {
+            meet_loaded<kLoads>();
+        }
+    };
     auto step = [&](auto at_s) {
         constexpr int S = decltype(at_s)::value;
         uint8_t *cur = stage(S);
         const uint8_t *nxt = stage(S ^ 1);
-        meet_loaded<kLoads>();
+        meet();
         multiply(0, 0, [&](int j) {
             read_w(cur, 1, j);
             read_x(cur, 2, j);
@@ -405,7 +436,7 @@ __device__ __forceinline__ void run(const Product &p, const Stage &stage, const 
             read_x(cur, 3, j);
             if (j == 1) load(cur, w_half, 0);
         });
-        meet_loaded<kLoads>();
+        meet();
         multiply(2, 0, [&](int j) {
             read_x(nxt, 0, j);
             if (j == 1) load(cur, w_half, 1);
@@ -418,9 +449,10 @@ __device__ __forceinline__ void run(const Product &p, const Stage &stage, const 
         advance();
     };
 
-    // Eight consecutive columns of a row: the lanes' halves trade, so that a lane of half h has those of
-    // columns (2 * g + h) * 8 .. of a product's 32.
-    auto eight = [&](const f32x16 &v, int g, float (&to)[8]) {
+    // A product's 32 x 32 results: element i of a lane is column (i >> 2) * 8 + (lane >> 5) * 4 + (i & 3) of
+    // row lane & 31. eight(): the lanes' halves trade, so that a lane has columns (2 * g + (lane >> 5)) * 8
+    // .. of its row.
+    auto eight = [](const f32x16 &v, int g, float (&to)[8]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[g * 8 + i]),
@@ -429,88 +461,160 @@ __device__ __forceinline__ void run(const Product &p, const Stage &stage, const 
             to[4 + i] = __uint_as_float(s[1]);
         }
     };
-    auto finish = [&](int tile) {              // the tile's output
+    auto eight_bf16 = [](const f32x16 &v, int g) {
+        const auto s = __builtin_amdgcn_permlane32_swap(pair(v[g * 8], v[g * 8 + 1]),
+                                                        pair(v[g * 8 + 4], v[g * 8 + 5]), false, false);
+        const auto t = __builtin_amdgcn_permlane32_swap(pair(v[g * 8 + 2], v[g * 8 + 3]),
+                                                        pair(v[g * 8 + 6], v[g * 8 + 7]), false, false);
+        return u32x4{s[0], t[0], s[1], t[1]};
+    };
+    // Neighbouring groups of 16 lanes trade, so that a and b are of rows lane & 15 and 16 more, 64 bytes of
+    // a row in four lanes; and back. (With 32 bytes of a row stored together L2 takes twice the
+    // requests.)
+    auto trade = [](u32x4 &a, u32x4 &b) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const auto s = __builtin_amdgcn_permlane16_swap(a[i], b[i], false, false);
+            a[i] = s[0];
+            b[i] = s[1];
+        }
+    };
+    // The tile's output. Every wavefront makes the same number of stores whatever the rows and columns
+    // that are there, kStores at least: the waits for loads count past them.
+    auto finish = [&](int tile) {
         const Tile t = at(tile);
         const int m0 = F == form::kWgrad ? t.mblk * kTile : 0;
         const int rows = F == form::kWgrad ? min(p.m - m0, kTile) : t.n;
-        const size_t first = F == form::kWgrad ? (size_t)t.e * p.m + m0 : (size_t)t.row0;
+        const size_t row0 = F == form::kWgrad ? (size_t)t.e * p.m + m0 : (size_t)t.row0;
+        const int l = lane_now();
+        const uint32_t r = wm * 32 + (l & 15);
+        // a lane's columns of 32: eight of 16 bits, or four and four more of 32
+        const uint32_t c16 = ((l >> 4) & 1) * 16 + (l >> 5) * 8, c32 = ((l >> 4) & 1) * 8 + (l >> 5) * 4;
+        const uint32_t n = p.n;
+        auto put_rows = [](const Rows &to, uint32_t off, uint32_t step, u32x4 a, u32x4 b) {
+            to.put(off, a);
+            to.put(off + step, b);
+        };
+        if constexpr (O == to::kSwiglu) {
+            const uint32_t I = n / 2, c = t.nblk * 128 + wn * 32 + c16;
+            const Rows h(p.out, row0, rows, I, 2);
 #pragma unroll
-        for (int mt = 0; mt < A; ++mt) {
-            const int l = lane_now(), half = l >> 5, r = (mt * 2 + wm) * 32 + (l & 31);
-            const size_t row = first + r;
-            if constexpr (O == to::kSwiglu) {
-                const int I = p.n / 2;
+            for (int mt = 0; mt < A; ++mt) {
+                const uint32_t row = r + mt * 64;
+                if (p.out2) {
+                    const Rows gu(p.out2, row0, rows, n, 2);
+                    const uint32_t off = c < I ? (row * n + c) * 2 : kNone;
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const int c = t.nblk * 128 + wn * 32 + (2 * g + half) * 8;
-                    float gate[8], up[8], h[8];
-                    eight(acc[0][mt], g, gate);
-                    eight(acc[1][mt], g, up);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) h[i] = swiglu(gate[i], up[i]);
-                    if (r < rows && c < I) {
-                        *reinterpret_cast<u32x4 *>((uint16_t *)p.out + row * I + c) = pack8(h);
-                        if (p.out2) {
-                            *reinterpret_cast<u32x4 *>(p.out2 + row * p.n + c) = pack8(gate);
-                            *reinterpret_cast<u32x4 *>(p.out2 + row * p.n + I + c) = pack8(up);
-                        }
+                    for (int nt = 0; nt < 2; ++nt) {
+                        u32x4 a = eight_bf16(acc[nt][mt], 0), b = eight_bf16(acc[nt][mt], 1);
+                        trade(a, b);
+                        put_rows(gu, off + nt * I * 2, n * 32, a, b);
                     }
                 }
-            } else {
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                for (int i = 0; i < 16; ++i) acc[0][mt][i] = swiglu(acc[0][mt][i], acc[1][mt][i]);
+                u32x4 a = eight_bf16(acc[0][mt], 0), b = eight_bf16(acc[0][mt], 1);
+                trade(a, b);
+                put_rows(h, c < I ? (row * I + c) * 2 : kNone, I * 32, a, b);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+            const Rows out(p.out, row0, rows, O == to::kSwigluGrad ? n * 2 : n, O == to::kF32 ? 4 : 2);
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const int c = t.nblk * kTile + nt * 128 + wn * 32 + (2 * g + half) * 8;
-                        float v[8];
-                        eight(acc[nt][mt], g, v);
-                        if (r >= rows || c >= p.n) continue;
-                        if constexpr (O == to::kBf16) {
-                            *reinterpret_cast<u32x4 *>((uint16_t *)p.out + row * p.n + c) = pack8(v);
-                        } else if constexpr (O == to::kF32) {
-                            f32x4 *o = reinterpret_cast<f32x4 *>((float *)p.out + row * p.n + c);
-                            f32x4 a{v[0], v[1], v[2], v[3]}, b{v[4], v[5], v[6], v[7]};
+            for (int mt = 0; mt < A; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const f32x16 &v = acc[nt][mt];
+                    const uint32_t row = r + mt * 64, c0 = t.nblk * kTile + nt * 128 + wn * 32, c = c0 + c16;
+                    const uint32_t off = c < n ? (row * n + c) * 2 : kNone;
+                    if constexpr (O == to::kBf16) {
+                        u32x4 a = eight_bf16(v, 0), b = eight_bf16(v, 1);
+                        trade(a, b);
+                        put_rows(out, off, n * 32, a, b);
+                    } else if constexpr (O == to::kF32) {
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            const uint32_t c = c0 + g * 16 + c32, at = c < n ? (row * n + c) * 4 : kNone;
+                            u32x4 a{__float_as_uint(v[g * 8]), __float_as_uint(v[g * 8 + 1]),
+                                    __float_as_uint(v[g * 8 + 2]), __float_as_uint(v[g * 8 + 3])};
+                            u32x4 b{__float_as_uint(v[g * 8 + 4]), __float_as_uint(v[g * 8 + 5]),
+                                    __float_as_uint(v[g * 8 + 6]), __float_as_uint(v[g * 8 + 7])};
+                            trade(a, b);
                             if (p.accumulate) {
-                                a += o[0];
-                                b += o[1];
+                                const f32x4 x = __builtin_bit_cast(f32x4, out.get(at));
+                                const f32x4 y = __builtin_bit_cast(f32x4, out.get(at + n * 64));
+                                a = __builtin_bit_cast(u32x4, __builtin_bit_cast(f32x4, a) + x);
+                                b = __builtin_bit_cast(u32x4, __builtin_bit_cast(f32x4, b) + y);
                             }
-                            o[0] = a;
-                            o[1] = b;
-                        } else if constexpr (O == to::kSwigluGrad) {
-                            const uint16_t *gu = p.in + row * p.n * 2 + c;
-                            float gate[8], up[8], dg[8], du[8];
-                            unpack8(*reinterpret_cast<const u32x4 *>(gu), gate);
-                            unpack8(*reinterpret_cast<const u32x4 *>(gu + p.n), up);
+                            put_rows(out, at, n * 64, a, b);
+                        }
+                    } else if constexpr (O == to::kSwigluGrad) {
+                        const Rows gu(p.in, row0, rows, n * 2, 2);
+                        const uint32_t at = off == kNone ? kNone : off + row * n * 2;
+                        u32x4 gate[2] = {gu.get(at), gu.get(at + n * 64)};
+                        u32x4 up[2] = {gu.get(at + n * 2), gu.get(at + n * 66)};
+                        trade(gate[0], gate[1]);
+                        trade(up[0], up[1]);
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            float d[8], a[8], b[8];
+                            eight(v, g, d);
+                            unpack8(gate[g], a);
+                            unpack8(up[g], b);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
-                                const float s = sigmoid(gate[i]);
-                                du[i] = v[i] * (gate[i] * s);
-                                dg[i] = v[i] * up[i] * (s * __builtin_fmaf(gate[i], 1.0f - s, 1.0f));
+                                const float s = sigmoid(a[i]), du = d[i] * (a[i] * s);
+                                a[i] = d[i] * b[i] * (s * __builtin_fmaf(a[i], 1.0f - s, 1.0f));
+                                b[i] = du;
                             }
-                            uint16_t *o = (uint16_t *)p.out + row * p.n * 2 + c;
-                            *reinterpret_cast<u32x4 *>(o) = pack8(dg);
-                            *reinterpret_cast<u32x4 *>(o + p.n) = pack8(du);
-                        } else {
-                            float b[8];
-                            if (p.bias) {
-                                unpack8(*reinterpret_cast<const u32x4 *>(p.bias + c), b);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) v[i] += b[i];
-                            }
-                            if (p.out2) *reinterpret_cast<u32x4 *>(p.out2 + row * p.n + c) = pack8(v);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) v[i] = activate(p.act, v[i]);
-                            if (p.in) {
-                                unpack8(*reinterpret_cast<const u32x4 *>(p.in + row * p.n + c), b);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) v[i] += b[i];
-                            }
-                            *reinterpret_cast<u32x4 *>((uint16_t *)p.out + row * p.n + c) = pack8(v);
+                            gate[g] = pack8(a);
+                            up[g] = pack8(b);
                         }
+                        trade(gate[0], gate[1]);
+                        trade(up[0], up[1]);
+                        put_rows(out, at, n * 64, gate[0], gate[1]);
+                        put_rows(out, at + n * 2, n * 64, up[0], up[1]);
+                    } else {
+                        const Rows bias(p.bias, 0, p.bias ? 1 : 0, n, 2);
+                        const Rows res(p.in, row0, p.in ? rows : 0, n, 2);
+                        u32x4 x[2], z[2];
+                        if (p.in) {
+                            x[0] = res.get(off);
+                            x[1] = res.get(off + n * 32);
+                            trade(x[0], x[1]);
+                        }
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            float d[8], b[8];
+                            eight(v, g, d);
+                            if (p.bias) {
+                                unpack8(bias.get((c0 + g * 16 + (l >> 5) * 8) * 2), b);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) d[i] += b[i];
+                            }
+                            if (p.out2) z[g] = pack8(d);
+                            if (p.act != EP_ACT_NONE)
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) d[i] = activate(p.act, d[i]);
+                            if (p.in) {
+                                unpack8(x[g], b);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) d[i] += b[i];
+                            }
+                            x[g] = pack8(d);
+                        }
+                        if (p.out2) {
+                            trade(z[0], z[1]);
+                            put_rows(Rows(p.out2, row0, rows, n, 2), off, n * 32, z[0], z[1]);
+                        }
+                        trade(x[0], x[1]);
+                        put_rows(out, off, n * 32, x[0], x[1]);
                     }
-            }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
         }
         clear();
+        stored = 3;
     };
 
     enter(0);

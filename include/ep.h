@@ -571,7 +571,7 @@ int ep_moe_layer_fp8(const ep_shape_t *shape, int32_t I, const uint16_t *x,
  * infinite values propagate to the elements they enter. Deterministic: the same inputs give the same
  * bits.
  *
- * Common requirements: all widths multiples of 8 and below 2^22, an expert's weights below 2^30
+ * Common requirements: all widths multiples of 8 and below 2^20, an expert's weights below 2^30
  * elements, E <= EP_MAX_EXPERTS (else EP_ERR_UNSUPPORTED); row buffers, weights and outputs 16-byte
  * aligned, counts and offsets 4-byte aligned (else EP_ERR_ALIGN). Outputs must not overlap inputs, and
  * no two experts' rows may overlap.
@@ -690,7 +690,7 @@ int ep_combine_grad_packed(const ep_shape_t *shape, int32_t rows, const uint16_t
  *   x [T*H], w [N*H], bias [N] or NULL, residual [T*N] or NULL: uint16 (bf16)
  *   pre [T*N] uint16 (bf16) out: bf16(z), which ep_linear_grad takes; NULL: not kept
  *   out [T*N] uint16 (bf16) out; may be residual itself
- * All 16-byte aligned. H and N multiples of 8 below 2^22, N*H < 2^30 (else EP_ERR_UNSUPPORTED). E, K, C
+ * All 16-byte aligned. H and N multiples of 8 below 2^20, N*H < 2^30 (else EP_ERR_UNSUPPORTED). E, K, C
  * and R are not used. T = 0 does nothing. Deterministic.
  */
 enum { EP_ACT_NONE = 0, EP_ACT_RELU = 1, EP_ACT_SILU = 2, EP_ACT_GELU = 3 };
