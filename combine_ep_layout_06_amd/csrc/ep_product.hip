@@ -41,16 +41,19 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kPart = 64;          // rows of a part
 constexpr int kBlock = 64;         // sum indexes of a block
 constexpr int kHalf = kTile / 2 * kBlock * 2;    // bytes of half an operand of a block
+constexpr int kStage = 4 * kHalf;  // of a block: x's halves, w's halves
+constexpr int kLoads = 8;          // of a block, by one wavefront
 constexpr int kList = kWave;       // tiles of a workgroup looked up together
 
 typedef __attribute__((address_space(3))) uint8_t *LdsBytes;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 *LdsTr;
+typedef __attribute__((address_space(3))) bf16x8 *LdsRows;
 
 using ep::uniform;
 
-// The experts' rows cut into row tiles: rows and first row of each expert, the running number of row
-// tiles, and the rows of a tile. An expert's tiles are of one height, a multiple of kPart.
+// The experts' rows cut into row tiles: rows and first row of each expert and the running number of row
+// tiles.
 struct TileTable {
     int32_t end[EP_MAX_EXPERTS], base[EP_MAX_EXPERTS], n[EP_MAX_EXPERTS];
     int32_t wave_sum[kWaves];
@@ -68,11 +71,10 @@ __device__ __forceinline__ void rows_of(const Product &p, int e, int &base, int 
 
 __device__ __forceinline__ int tiles_of(int n) { return (n + kTile - 1) / kTile; }
 
-// Rows of a tile of an expert with n rows: its rows spread evenly over its tiles.
-__device__ __forceinline__ int height_of(int n)
+// First part of tile i of an expert with n rows: its parts spread evenly over its tiles.
+__device__ __forceinline__ int first_part(int n, int i)
 {
-    const int tiles = max(tiles_of(n), 1);
-    return ((n + tiles - 1) / tiles + kPart - 1) / kPart * kPart;
+    return i * ((n + kPart - 1) / kPart) / max(tiles_of(n), 1);
 }
 
 __device__ __forceinline__ int build_table(TileTable &t, const Product &p)
@@ -131,16 +133,17 @@ __device__ __forceinline__ Tile locate(const TileTable &t, const Product &p, int
         if (t.end[mid] > m) hi = mid;
         else lo = mid + 1;
     }
-    const int n_e = t.n[lo], tiles = tiles_of(n_e), h = height_of(n_e);
+    const int n_e = t.n[lo], tiles = tiles_of(n_e);
     at -= (t.end[lo] - tiles) * n_tiles;
     const int group = at / (kGroup * n_tiles), in_group = min(tiles - group * kGroup, kGroup);
     at -= group * kGroup * n_tiles;
     Tile r;
     r.e = lo;
     r.nblk = at / in_group;
-    const int m0 = (group * kGroup + at - r.nblk * in_group) * h;
+    const int m_tile = group * kGroup + at - r.nblk * in_group;
+    const int m0 = first_part(n_e, m_tile) * kPart;
     r.row0 = t.base[lo] + m0;
-    r.n = min(max(n_e - m0, 0), h);
+    r.n = min(first_part(n_e, m_tile + 1) * kPart, n_e) - m0;
     r.mblk = 0;
     return r;
 }
@@ -261,96 +264,131 @@ __device__ __forceinline__ int swizzle(int r) { return (r & 7) ^ ((r >> 4) & 1);
 // In one kept as it lies the 64-byte unit u of row k's four is at place u ^ (k & 3): the four rows whose
 // units a transposing read of 32 lanes takes then lie in different banks.
 
-// The tiles of `list`, which all have A parts.
-template <int F, int O, int A, typename Stage>
-__device__ __forceinline__ void run(const Product &p, const Stage &stage, const Tile *list, int tiles)
-{
-    constexpr bool kXTr = F == form::kWgrad, kWTr = F != form::kForward;
-    const int wave = uniform(threadIdx.x / kWave);
-    const int wm = wave & 1, wn = wave >> 1;
-    const int ldx = F == form::kWgrad ? p.m : p.k;       // values of a row in memory
-    const int ldw = F == form::kForward ? p.k : p.n;
+// The stream of loads of a workgroup's tiles, kept up from tile to tile: the tile it is in and its next
+// block, and the stage that the products are in.
+template <int F, int O>
+struct Stream {
+    static constexpr bool kXTr = F == form::kWgrad, kWTr = F != form::kForward;
+    const Product &p;
+    const Tile *list;
+    int tiles;
+    uint32_t stage = 0;                        // byte offset
+    int stored = 0;                            // barriers to come whose loads are older than stores
+    int tile, kb, nkb;
+    const uint8_t *x, *w;
+    int64_t xleft, wleft;                      // bytes from x and w to the operands' ends
+    i32x4 xb, wb;
+    uint32_t xoff, woff;
+    uint64_t beyond;                           // lanes whose chunk of a row's last block is beyond the row
 
-    auto at = [&](int i) {
-        const Tile t = list[i];
-        return Tile{uniform(t.e), uniform(t.row0), uniform(t.n), uniform(t.nblk), uniform(t.mblk)};
-    };
-    auto blocks_of = [&](const Tile &t) {
-        return F == form::kWgrad ? max((t.n + kBlock - 1) / kBlock, 1) : (p.k + kBlock - 1) / kBlock;
-    };
-
-    // the stream of loads: the tile it is in and its next block
-    struct {
-        int tile, kb, nkb;
-        const uint8_t *x, *w;
-        int64_t xleft, wleft;              // bytes from x and w to the operands' ends
-        i32x4 xb, wb;
-        uint32_t xoff, woff;
-    } ld;
+    __device__ __forceinline__ int wave() const { return uniform(threadIdx.x / kWave); }
+    __device__ __forceinline__ int ldx() const { return F == form::kWgrad ? p.m : p.k; }
+    __device__ __forceinline__ int ldw() const { return F == form::kForward ? p.k : p.n; }
     // A load of an operand kept row by row fills 8 rows of 8 chunks, one of an operand kept as it lies 4
     // rows of 16; a wavefront makes two of each half.
-    auto chunk_of = [&](int l) { return (l & 7) ^ (l >> 3) ^ (wave & 1); };
-    auto enter = [&](int i) {
+    __device__ __forceinline__ int chunk_of(int l) const { return (l & 7) ^ (l >> 3) ^ (wave() & 1); }
+
+    __device__ __forceinline__ Stream(const Product &p, const Tile *list, int tiles)
+        : p(p), list(list), tiles(tiles)
+    {
+        const int tail = (p.k & (kBlock - 1)) ? (p.k & (kBlock - 1)) / 8 : 8;
+        beyond = __ballot(chunk_of(lane_now()) >= tail);
+        enter(0);
+    }
+    __device__ __forceinline__ Tile at(int i) const
+    {
+        const Tile t = list[i];
+        return Tile{uniform(t.e), uniform(t.row0), uniform(t.n), uniform(t.nblk), uniform(t.mblk)};
+    }
+    __device__ __forceinline__ int blocks_of(const Tile &t) const
+    {
+        return F == form::kWgrad ? max((t.n + kBlock - 1) / kBlock, 1) : (p.k + kBlock - 1) / kBlock;
+    }
+    __device__ __forceinline__ void enter(int i)
+    {
         const Tile t = at(i);
-        ld.tile = i;
-        ld.kb = 0;
-        ld.nkb = blocks_of(t);
+        tile = i;
+        kb = 0;
+        nkb = blocks_of(t);
         if constexpr (F == form::kForward) {
-            ld.w = reinterpret_cast<const uint8_t *>(p.w + (size_t)t.e * p.n * p.k);
-            ld.wleft = (int64_t)p.n * p.k * 2;
+            w = reinterpret_cast<const uint8_t *>(p.w + (size_t)t.e * p.n * p.k);
+            wleft = (int64_t)p.n * p.k * 2;
         } else if constexpr (F == form::kDgrad) {
-            ld.w = reinterpret_cast<const uint8_t *>(p.w + (size_t)t.e * p.n * p.k + t.nblk * kTile);
-            ld.wleft = ((int64_t)p.n * p.k - t.nblk * kTile) * 2;
+            w = reinterpret_cast<const uint8_t *>(p.w + (size_t)t.e * p.n * p.k + t.nblk * kTile);
+            wleft = ((int64_t)p.n * p.k - t.nblk * kTile) * 2;
         } else {
-            ld.w = reinterpret_cast<const uint8_t *>(p.w + (size_t)t.row0 * p.n + t.nblk * kTile);
-            ld.wleft = ((int64_t)t.n * p.n - t.nblk * kTile) * 2;
+            w = reinterpret_cast<const uint8_t *>(p.w + (size_t)t.row0 * p.n + t.nblk * kTile);
+            wleft = ((int64_t)t.n * p.n - t.nblk * kTile) * 2;
         }
-        ld.x = reinterpret_cast<const uint8_t *>(p.x + (size_t)t.row0 * ldx + t.mblk * kTile);
-        ld.xleft = ((int64_t)t.n * ldx - t.mblk * kTile) * 2;
-        ld.xb = buffer(ld.x, ld.xleft);
-        ld.wb = buffer(ld.w, ld.wleft);
+        x = reinterpret_cast<const uint8_t *>(p.x + (size_t)t.row0 * ldx() + t.mblk * kTile);
+        xleft = ((int64_t)t.n * ldx() - t.mblk * kTile) * 2;
+        xb = buffer(x, xleft);
+        wb = buffer(w, wleft);
         const int l = lane_now(), chunk = chunk_of(l);
-        const int row8 = wave * 16 + (l >> 3), row4 = wave * 8 + (l >> 4);
+        const int row8 = wave() * 16 + (l >> 3), row4 = wave() * 8 + (l >> 4);
         const int tr_byte = ((((l >> 2) ^ (l >> 4)) & 3) << 6) + (l & 3) * 16;
         const int wrow = t.nblk * (O == to::kSwiglu ? kTile / 2 : kTile) + row8;
-        if constexpr (kXTr) ld.xoff = (uint32_t)row4 * ldx * 2 + tr_byte;
-        else ld.xoff = (uint32_t)row8 * ldx * 2 + chunk * 16;
-        if constexpr (kWTr) ld.woff = (uint32_t)row4 * ldw * 2 + tr_byte;
-        else ld.woff = (uint32_t)wrow * ldw * 2 + chunk * 16;
-    };
-    // lanes whose chunk of a row's last block is beyond the row
-    const int tail = (p.k & (kBlock - 1)) ? (p.k & (kBlock - 1)) / 8 : 8;
-    const uint64_t beyond = __ballot(chunk_of(lane_now()) >= tail);
-    // One half of an operand of the block: past an operand's end the loads give 0.
-    auto load = [&](uint8_t *to, auto is_w, int half_no) {
-        constexpr bool W = decltype(is_w)::value, TR = W ? kWTr : kXTr;
-        uint8_t *at = to + (2 * W + half_no) * kHalf + wave * 2048;
-        const int ldm = W ? ldw : ldx;
-        uint32_t off = W ? ld.woff : ld.xoff;
-        if (!TR && __builtin_amdgcn_inverse_ballot_w64(ld.kb == ld.nkb - 1 ? beyond : 0)) off = kNone;
-        uint32_t soff = TR ? half_no * 256 : ld.kb * (kBlock * 2);
+        if constexpr (kXTr) xoff = (uint32_t)row4 * ldx() * 2 + tr_byte;
+        else xoff = (uint32_t)row8 * ldx() * 2 + chunk * 16;
+        if constexpr (kWTr) woff = (uint32_t)row4 * ldw() * 2 + tr_byte;
+        else woff = (uint32_t)wrow * ldw() * 2 + chunk * 16;
+    }
+    // One half of an operand of the block to the stage at byte offset `to`: past an operand's end the
+    // loads give 0.
+    template <bool W>
+    __device__ __forceinline__ void load(uint8_t *stages, uint32_t to, int half_no)
+    {
+        constexpr bool TR = W ? kWTr : kXTr;
+        uint8_t *at = stages + to + (2 * W + half_no) * kHalf + wave() * 2048;
+        const int ldm = W ? ldw() : ldx();
+        uint32_t off = W ? woff : xoff;
+        if (!TR && __builtin_amdgcn_inverse_ballot_w64(kb == nkb - 1 ? beyond : 0)) off = kNone;
+        uint32_t soff = TR ? half_no * 256 : kb * (kBlock * 2);
         if (!TR && half_no)                    // SwiGLU: the second half are the up rows
             soff += (W && O == to::kSwiglu ? (uint32_t)(p.n / 2) : 128u) * ldm * 2;
-        load_lds(W ? ld.wb : ld.xb, at, off, soff);
-        load_lds(W ? ld.wb : ld.xb, at + 1024, off, soff + (TR ? 8 : 16) * ldm);
-    };
-    auto advance = [&]() {                     // past the last block: that block again
-        if (ld.kb + 1 < ld.nkb) {
-            ++ld.kb;
+        load_lds(W ? wb : xb, at, off, soff);
+        load_lds(W ? wb : xb, at + 1024, off, soff + (TR ? 8 : 16) * ldm);
+    }
+    __device__ __forceinline__ void advance()  // past the last block: that block again
+    {
+        if (kb + 1 < nkb) {
+            ++kb;
             if constexpr (kXTr) {
-                ld.x += (size_t)kBlock * ldx * 2;
-                ld.xleft -= (int64_t)kBlock * ldx * 2;
-                ld.xb = buffer(ld.x, ld.xleft);
+                x += (size_t)kBlock * ldx() * 2;
+                xleft -= (int64_t)kBlock * ldx() * 2;
+                xb = buffer(x, xleft);
             }
             if constexpr (kWTr) {
-                ld.w += (size_t)kBlock * ldw * 2;
-                ld.wleft -= (int64_t)kBlock * ldw * 2;
-                ld.wb = buffer(ld.w, ld.wleft);
+                w += (size_t)kBlock * ldw() * 2;
+                wleft -= (int64_t)kBlock * ldw() * 2;
+                wb = buffer(w, wleft);
             }
-        } else if (ld.tile + 1 < tiles) {
-            enter(ld.tile + 1);
+        } else if (tile + 1 < tiles) {
+            enter(tile + 1);
         }
-    };
+    }
+    // The first two blocks; the first one's first halves are there when it returns.
+    __device__ __forceinline__ void start(uint8_t *stages)
+    {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            load<false>(stages, b * kStage, 0);
+            load<true>(stages, b * kStage, 0);
+            load<true>(stages, b * kStage, 1);
+            load<false>(stages, b * kStage, 1);
+            advance();
+        }
+        meet_loaded<2 * kLoads - 4>();
+    }
+};
+
+// Tiles `tile` .. `end` of the stream, which all have A parts.
+template <int F, int O, int A>
+__device__ __forceinline__ void run(Stream<F, O> &ld, uint8_t *stages, int tile, int end)
+{
+    constexpr bool kXTr = F == form::kWgrad, kWTr = F != form::kForward;
+    const Product &p = ld.p;
+    const int wave = ld.wave(), wm = wave & 1, wn = wave >> 1;
 
     f32x16 acc[2][A];
     bf16x8 wf[2][4], xf[A][4];                 // 16 sum indexes each
@@ -364,37 +402,39 @@ __device__ __forceinline__ void run(const Product &p, const Stage &stage, const 
     };
     // Where a lane reads sum indexes 0 .. of its wavefront's first 32 rows (columns) in a half. Row by row:
     // chunk 2 * j + half of row lane & 31 for those from 16 * j on. As it lies: rows half * 8 + 0 .. 3
-    // (and, 4 rows further, the rest), its 16 lanes' part of a unit.
-    const int lane = lane_now(), half = lane >> 5, r32 = lane & 31, i16 = lane & 15;
-    const int row_at = r32 * 128 + ((half ^ swizzle(r32)) << 4);
-    const int tr_at = (half * 8 + (i16 >> 2)) * 256 + ((lane >> 4) & 1) * 32 + (i16 & 3) * 8;
-    const int x_at = kXTr ? tr_at + ((wm ^ (i16 >> 2)) << 6) : row_at + wm * 4096;
-    const int w_at = kWTr ? tr_at + ((wn ^ (i16 >> 2)) << 6) : row_at + wn * 4096;
-    // worked out where it is used: kept for every j and unit it would take more registers than there are
-    auto flip = [](int a, int bits) {
-        if (bits) asm volatile("v_xor_b32 %0, %1, %2" : "=v"(a) : "s"(uniform(bits)), "0"(a));
-        return a;
+    // (and, 4 rows further, the rest), its 16 lanes' part of a unit. One address for each j, or for each
+    // of x's two units, that steps from stage to stage.
+    constexpr int kXAt = kXTr ? 2 : 4, kWAt = kWTr ? 1 : 4;
+    uint32_t x_at[kXAt], w_at[kWAt];
+    {
+        const int l = lane_now(), half = l >> 5, r32 = l & 31, i16 = l & 15;
+        const uint32_t base = (uint32_t)(uintptr_t)(LdsBytes)stages + ld.stage;
+        const uint32_t row_at = r32 * 128 + ((half ^ swizzle(r32)) << 4);
+        const uint32_t tr_at = (half * 8 + (i16 >> 2)) * 256 + ((l >> 4) & 1) * 32 + (i16 & 3) * 8;
+#pragma unroll
+        for (int i = 0; i < kXAt; ++i)
+            x_at[i] = base + (kXTr ? tr_at + ((wm ^ (i16 >> 2) ^ (i * 2)) << 6) : (row_at ^ (i << 5)) + wm * 4096);
+#pragma unroll
+        for (int i = 0; i < kWAt; ++i)
+            w_at[i] = base + (kWTr ? tr_at + ((wn ^ (i16 >> 2)) << 6) : (row_at ^ (i << 5)) + wn * 4096);
+    }
+    auto read_tr = [&](uint32_t at) -> bf16x8 {
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(uintptr_t)at);
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(uintptr_t)(at + 1024));
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     };
-    // `unit`: how many 32 rows (columns) further on
-    auto read = [&](auto tr, const uint8_t *from, int lane_at, int unit, int j) -> bf16x8 {
-        if constexpr (decltype(tr)::value) {
-            const uint8_t *a = from + flip(lane_at, unit << 6) + j * 4096;
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)a);
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(a + 1024));
-            return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        } else {
-            return *reinterpret_cast<const bf16x8 *>(from + flip(lane_at, j << 5) + unit * 4096);
-        }
-    };
+    auto read_rows = [&](uint32_t at) -> bf16x8 { return *(LdsRows)(uintptr_t)at; };
     // rows (mt * 2 + wm) * 32 .. and columns (nt * 4 + wn) * 32 .. of the tile
-    auto read_x = [&](const uint8_t *from, int mt, int j) {
-        if (mt < A) xf[mt][j] = read(std::bool_constant<kXTr>{}, from + (mt >> 1) * kHalf, x_at, (mt & 1) * 2, j);
+    auto read_x = [&](int mt, int j) {
+        if (mt >= A) return;
+        if constexpr (kXTr) xf[mt][j] = read_tr(x_at[mt & 1] + (mt >> 1) * kHalf + j * 4096);
+        else xf[mt][j] = read_rows(x_at[j] + (mt >> 1) * kHalf + (mt & 1) * 8192);
     };
-    auto read_w = [&](const uint8_t *from, int nt, int j) {
-        wf[nt][j] = read(std::bool_constant<kWTr>{}, from + (2 + nt) * kHalf, w_at, 0, j);
+    auto read_w = [&](int nt, int j) {
+        if constexpr (kWTr) wf[nt][j] = read_tr(w_at[0] + (2 + nt) * kHalf + j * 4096);
+        else wf[nt][j] = read_rows(w_at[j] + (2 + nt) * kHalf);
     };
 
-    constexpr int kLoads = A > 2 ? 8 : 6;      // of a block, by one wavefront
     // The products of rows mt0, mt0 + 1 and columns nt, 16 sum indexes at a time, behind each `also(j)`.
     auto multiply = [&](int mt0, int nt, auto also) {
 #pragma unroll
@@ -408,45 +448,45 @@ __device__ __forceinline__ void run(const Product &p, const Stage &stage, const 
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    // One block, in stage S. At each barrier what is read from then on has arrived, and what is loaded
-    // over has been read.
-    constexpr std::false_type x_half{};
-    constexpr std::true_type w_half{};
     constexpr int kStores = O == to::kSwiglu ? 2 * A : O == to::kSwigluGrad || O == to::kF32 ? 8 * A : 4 * A;
-    int stored = 0;                            // barriers to come whose loads are older than stores
     auto meet = [&]() {
-        if (stored > 0) {
-            --stored;
+        if (ld.stored > 0) {
+            --ld.stored;
             meet_loaded<kLoads + kStores>();
         } else {
             meet_loaded<kLoads>();
         }
     };
-    auto step = [&](auto at_s) {
-        constexpr int S = decltype(at_s)::value;
-        uint8_t *cur = stage(S);
-        const uint8_t *nxt = stage(S ^ 1);
+    // One block. At each barrier what is read from then on has arrived, and what is loaded over has been
+    // read.
+    auto step = [&]() {
+        const uint32_t cur = ld.stage;
         meet();
         multiply(0, 0, [&](int j) {
-            read_w(cur, 1, j);
-            read_x(cur, 2, j);
-            if (j == 1) load(cur, x_half, 0);
+            read_w(1, j);
+            read_x(2, j);
+            if (j == 1) ld.template load<false>(stages, cur, 0);
         });
         multiply(0, 1, [&](int j) {
-            read_x(cur, 3, j);
-            if (j == 1) load(cur, w_half, 0);
+            read_x(3, j);
+            if (j == 1) ld.template load<true>(stages, cur, 0);
         });
+        ld.stage ^= kStage;
+#pragma unroll
+        for (int i = 0; i < kXAt; ++i) x_at[i] ^= kStage;
+#pragma unroll
+        for (int i = 0; i < kWAt; ++i) w_at[i] ^= kStage;
         meet();
         multiply(2, 0, [&](int j) {
-            read_x(nxt, 0, j);
-            if (j == 1) load(cur, w_half, 1);
+            read_x(0, j);
+            if (j == 1) ld.template load<true>(stages, cur, 1);
         });
         multiply(2, 1, [&](int j) {
-            read_w(nxt, 0, j);
-            read_x(nxt, 1, j);
-            if (A > 2 && j == 1) load(cur, x_half, 1);
+            read_w(0, j);
+            read_x(1, j);
+            if (j == 1) ld.template load<false>(stages, cur, 1);
         });
-        advance();
+        ld.advance();
     };
 
     // A product's 32 x 32 results: element i of a lane is column (i >> 2) * 8 + (lane >> 5) * 4 + (i & 3) of
@@ -482,7 +522,7 @@ __device__ __forceinline__ void run(const Product &p, const Stage &stage, const 
     // The tile's output. Every wavefront makes the same number of stores whatever the rows and columns
     // that are there, kStores at least: the waits for loads count past them.
     auto finish = [&](int tile) {
-        const Tile t = at(tile);
+        const Tile t = ld.at(tile);
         const int m0 = F == form::kWgrad ? t.mblk * kTile : 0;
         const int rows = F == form::kWgrad ? min(p.m - m0, kTile) : t.n;
         const size_t row0 = F == form::kWgrad ? (size_t)t.e * p.m + m0 : (size_t)t.row0;
@@ -614,38 +654,20 @@ __device__ __forceinline__ void run(const Product &p, const Stage &stage, const 
                 }
         }
         clear();
-        stored = 3;
+        ld.stored = 3;
     };
 
-    enter(0);
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        load(stage(b), x_half, 0);
-        load(stage(b), w_half, 0);
-        load(stage(b), w_half, 1);
-        if constexpr (A > 2) load(stage(b), x_half, 1);
-        advance();
-    }
-    meet_loaded<2 * kLoads - 4>();             // the first block's first halves
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        read_w(stage(0), 0, j);
-        read_x(stage(0), 0, j);
-        read_x(stage(0), 1, j);
+        read_w(0, j);
+        read_x(0, j);
+        read_x(1, j);
     }
     clear();
-    int tile = 0, kb = 0, nkb = blocks_of(at(0));
-    auto next = [&](auto at_s) {               // a block; false after the last one
-        step(at_s);
-        if (++kb < nkb) return true;
+    for (; tile < end; ++tile) {
+        for (int kb = ld.blocks_of(ld.at(tile)); kb > 0; --kb) step();
         finish(tile);
-        if (++tile == tiles) return false;
-        kb = 0;
-        nkb = blocks_of(at(tile));
-        return true;
-    };
-    while (next(std::integral_constant<int, 0>{}) && next(std::integral_constant<int, 1>{})) {}
-    meet_loaded<0>();                           // no direct load is left to write LDS
+    }
 }
 #endif
 
@@ -653,10 +675,10 @@ template <int F, int O>
 __global__ __launch_bounds__(kThreads) void product_kernel(Product p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
-    __shared__ __attribute__((aligned(1024))) uint8_t stages[2][4 * kHalf];
+    // aligned so that the stage is one bit of an address
+    __shared__ __attribute__((aligned(kStage))) uint8_t stages[2 * kStage];
     __shared__ Tile list[kList];
     static_assert(sizeof(TileTable) <= sizeof(stages), "the table is done with before the first block");
-    auto stage = [&](int s) -> uint8_t * { return stages[s]; };
     TileTable &table = *reinterpret_cast<TileTable *>(stages);
     const int n_tiles = (p.n + kTile - 1) / kTile, m_tiles = (p.m + kTile - 1) / kTile;
     // Neighbours in the tiles' order share operands: of each gridDim.x tiles in a row an XCD takes one
@@ -690,16 +712,19 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p)
         }
         if ((int)threadIdx.x < tiles) list[place] = mine;
         __syncthreads();                       // the list is there, the table is done with
-        const Tile *these = list;
+        Stream<F, O> ld(p, list, tiles);
+        ld.start(stages);
+        int tile = 0;
         auto run_all = [&](auto a) {
             constexpr int A = decltype(a)::value;
-            if (count[A]) run<F, O, A>(p, stage, these, count[A]);
-            these += count[A];
+            if (count[A]) run<F, O, A>(ld, stages, tile, tile + count[A]);
+            tile += count[A];
         };
         run_all(std::integral_constant<int, 4>{});
         run_all(std::integral_constant<int, 3>{});
         run_all(std::integral_constant<int, 2>{});
         run_all(std::integral_constant<int, 1>{});
+        meet_loaded<0>();                      // no direct load is left to write LDS
         first += tiles * gridDim.x;
     }
 #else
