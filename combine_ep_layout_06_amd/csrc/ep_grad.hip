@@ -9,15 +9,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 
-__device__ __forceinline__ void unpack8(u32x4 d, float (&v)[8])
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16_lo(d[i]);
-        v[2 * i + 1] = bf16_hi(d[i]);
-    }
-}
-
 __device__ __forceinline__ u32x4 pack8(const float (&v)[8])
 {
     u32x4 d;
@@ -65,17 +56,7 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(
 
 // dz = bf16(dout * act'(z)) and, per kGradRows rows, the columns' sums of the unrounded dz.
 constexpr int kGradRows = kLinearGradRows;
-
-__device__ __forceinline__ float act_grad(int act, float z)
-{
-    if (act == EP_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
-    if (act == EP_ACT_SILU) {
-        const float s = __builtin_amdgcn_rcpf(__builtin_fmaf(__expf(-z), 0x1p-4f, 0x1p-4f)) * 0x1p-4f;
-        return s * __builtin_fmaf(z, 1.0f - s, 1.0f);
-    }
-    // Phi(z) + z phi(z)
-    return __builtin_fmaf(0.5f, erff(z * 0.70710678f), 0.5f) + z * __expf(-0.5f * z * z) * 0.39894228f;
-}
+constexpr int kGradAtOnce = 4;     // rows of a wavefront in flight
 
 __global__ __launch_bounds__(kThreads) void act_grad_kernel(
     const uint16_t *__restrict__ dout, const uint16_t *__restrict__ z, uint16_t *__restrict__ dz,
@@ -86,20 +67,31 @@ __global__ __launch_bounds__(kThreads) void act_grad_kernel(
     const int c = (blockIdx.x * kWave + lane) * 8;
     float sum[8] = {};
     if (c < N) {
-        const int end = min((int)(blockIdx.y + 1) * kGradRows, T);
-        for (int t = blockIdx.y * kGradRows + wave; t < end; t += kWaves) {
-            const size_t at = (size_t)t * N + c;
-            float d[8];
-            unpack8(*reinterpret_cast<const u32x4 *>(dout + at), d);
-            if (act != EP_ACT_NONE) {
-                float v[8];
-                unpack8(*reinterpret_cast<const u32x4 *>(z + at), v);
+        const int first = blockIdx.y * kGradRows + wave, end = min((int)(blockIdx.y + 1) * kGradRows, T);
+        for (int t0 = first; t0 < end; t0 += kGradAtOnce * kWaves) {
+            u32x4 d[kGradAtOnce], v[kGradAtOnce];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) d[k] *= act_grad(act, v[k]);
-                *reinterpret_cast<u32x4 *>(dz + at) = pack8(d);
+            for (int i = 0; i < kGradAtOnce; ++i) {    // a row that is not there: the last one again
+                const size_t at = (size_t)min(t0 + i * kWaves, end - 1) * N + c;
+                d[i] = *reinterpret_cast<const u32x4 *>(dout + at);
+                if (act != EP_ACT_NONE) v[i] = *reinterpret_cast<const u32x4 *>(z + at);
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sum[k] += d[k];
+            for (int i = 0; i < kGradAtOnce; ++i) {
+                const int t = t0 + i * kWaves;
+                if (t >= end) break;
+                float g[8];
+                unpack8(d[i], g);
+                if (act != EP_ACT_NONE) {
+                    float a[8];
+                    unpack8(v[i], a);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) g[k] *= act_grad(act, a[k]);
+                    *reinterpret_cast<u32x4 *>(dz + (size_t)t * N + c) = pack8(g);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum[k] += g[k];
+            }
         }
     }
 #pragma unroll
@@ -116,14 +108,21 @@ __global__ __launch_bounds__(kThreads) void act_grad_kernel(
     }
 }
 
+// The sums of the workgroups' sums: 64 columns a workgroup, a quarter of the rows a wavefront.
 __global__ __launch_bounds__(kThreads) void bias_grad_kernel(const float *__restrict__ part,
                                                              float *__restrict__ dbias, int chunks, int N)
 {
-    const int c = blockIdx.x * kThreads + threadIdx.x;
-    if (c >= N) return;
+    __shared__ float sums[kWaves][kWave];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int c = blockIdx.x * kWave + lane;
     float s = 0.0f;
-    for (int i = 0; i < chunks; ++i) s += part[(size_t)i * N + c];
-    dbias[c] = s;
+    if (c < N) {
+#pragma unroll 8
+        for (int i = wave; i < chunks; i += kWaves) s += part[(size_t)i * N + c];
+    }
+    sums[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && c < N) dbias[c] = (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
 }
 
 }  // namespace
@@ -148,8 +147,8 @@ hipError_t launch_act_grad(const uint16_t *dout, const uint16_t *z, uint16_t *dz
                                     dim3(kThreads), 0, stream, dout, z, dz, part, T, N, act);
         if (e != hipSuccess) return e;
     }
-    return launch(bias_grad_kernel, dim3((N + kThreads - 1) / kThreads), dim3(kThreads), 0, stream, part,
-                  dbias, chunks, N);
+    return launch(bias_grad_kernel, dim3((N + kWave - 1) / kWave), dim3(kThreads), 0, stream, part, dbias,
+                  chunks, N);
 }
 
 }  // namespace ep

@@ -48,4 +48,69 @@ constexpr int kLinearGradRows = 64;
 hipError_t launch_act_grad(const uint16_t *dout, const uint16_t *z, uint16_t *dz, float *part,
                            float *dbias, int T, int N, int act, hipStream_t stream);
 
+#if defined(__HIPCC__)
+
+__device__ __forceinline__ void unpack8(u32x4 d, float (&v)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(d[i]);
+        v[2 * i + 1] = bf16_hi(d[i]);
+    }
+}
+
+// 1 / (1 + exp(-g)), the reciprocal as in swiglu().
+__device__ __forceinline__ float sigmoid(float g)
+{
+    return __builtin_amdgcn_rcpf(__builtin_fmaf(__expf(-g), 0x1p-4f, 0x1p-4f)) * 0x1p-4f;
+}
+
+// A constant put into a register where it is used, and not kept in one through a kernel's loops.
+#define EP_HERE(value)                                                                          \
+    [] {                                                                                        \
+        float r;                                                                                \
+        asm volatile("v_mov_b32 %0, %1" : "=v"(r) : "i"(__builtin_bit_cast(int, value)));        \
+        return r;                                                                               \
+    }()
+
+// The normal distribution Phi(z) and, in `density`, exp(-z^2 / 2). With x = |z| / sqrt(2) and
+// t = 1 / (1 + 0.3275911 x), erfc(x) = exp(-x^2) times a polynomial of t (Abramowitz and Stegun,
+// Handbook of Mathematical Functions, 7.1.26: within 1.5e-7): half of it is the tail beyond |z|.
+__device__ __forceinline__ float normal_cdf(float z, float &density)
+{
+    const float x = __builtin_fabsf(z) * 0.70710678f;
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(EP_HERE(0.3275911f), x, 1.0f));
+    float y = __builtin_fmaf(EP_HERE(1.061405429f), t, EP_HERE(-1.453152027f));
+    y = __builtin_fmaf(y, t, EP_HERE(1.421413741f));
+    y = __builtin_fmaf(y, t, EP_HERE(-0.284496736f));
+    y = __builtin_fmaf(y, t, EP_HERE(0.254829592f));
+    density = __expf(-x * x);
+    y *= 0.5f * t * density;
+    return z < 0.0f ? y : 1.0f - y;
+}
+
+__device__ __forceinline__ float activate(int act, float z)
+{
+    float density;
+    if (act == EP_ACT_RELU) return z > 0.0f || z != z ? z : 0.0f;
+    if (act == EP_ACT_SILU) return z * sigmoid(z);
+    if (act == EP_ACT_GELU) return z * normal_cdf(z, density);
+    return z;
+}
+
+// The derivative of activate().
+__device__ __forceinline__ float act_grad(int act, float z)
+{
+    if (act == EP_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+    if (act == EP_ACT_SILU) {
+        const float s = sigmoid(z);
+        return s * __builtin_fmaf(z, 1.0f - s, 1.0f);
+    }
+    float density;                             // Phi(z) + z exp(-z^2 / 2) / sqrt(2 pi)
+    const float cdf = normal_cdf(z, density);
+    return __builtin_fmaf(z * 0.39894228f, density, cdf);
+}
+
+#endif
+
 }  // namespace ep

@@ -30,6 +30,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kTile = 256;         // rows and columns of a tile
+constexpr int kPart = 64;          // rows of a part
 constexpr int kCus = 256;
 
 namespace form { constexpr int kForward = 0, kDgrad = 1, kWgrad = 2; }
@@ -38,7 +39,6 @@ namespace to { constexpr int kBf16 = 0, kSwiglu = 1, kSwigluGrad = 2, kF32 = 3, 
 #if defined(__HIP_DEVICE_COMPILE__)            // buffer descriptors exist on the device only
 
 constexpr int kWaves = kThreads / kWave;
-constexpr int kPart = 64;          // rows of a part
 constexpr int kBlock = 64;         // sum indexes of a block
 constexpr int kHalf = kTile / 2 * kBlock * 2;    // bytes of half an operand of a block
 constexpr int kStage = 4 * kHalf;  // of a block: x's halves, w's halves
@@ -114,16 +114,15 @@ __device__ __forceinline__ int build_table(TileTable &t, const Product &p)
     return uniform(total);
 }
 
-// A tile. Forward and dgrad: rows row0 .. row0 + n of expert e. Wgrad: the sum is over these rows, and
-// `mblk` is the row tile of the output. nblk: column tile.
+// A tile: columns from nblk * kTile of the output, `rows` rows (0: no tile). Forward and dgrad: rows row0
+// .. row0 + n of expert e, n = rows. Wgrad: rows m0 .. of expert e's output, and the sum is over the
+// rows row0 .. row0 + n.
 struct Tile {
-    int e, row0, n, nblk, mblk;
+    int e, row0, n, nblk, m0, rows;
 };
 
-constexpr int kGroup = 8;
-
-// The tile at place `at` of the order: an expert's tiles in groups of kGroup row tiles, within a group
-// the row tile runs fastest, then the column tile.
+// The tile at place `at` of the order: an expert's tiles in groups of about 8 row tiles, within a group
+// the row tile runs fastest, then the column tile. Tiles side by side in this order share operands.
 __device__ __forceinline__ Tile locate(const TileTable &t, const Product &p, int at, int n_tiles)
 {
     const int m = at / n_tiles;
@@ -134,17 +133,18 @@ __device__ __forceinline__ Tile locate(const TileTable &t, const Product &p, int
         else lo = mid + 1;
     }
     const int n_e = t.n[lo], tiles = tiles_of(n_e);
+    const int groups = max((tiles + 4) / 8, 1), size = (tiles + groups - 1) / groups;
     at -= (t.end[lo] - tiles) * n_tiles;
-    const int group = at / (kGroup * n_tiles), in_group = min(tiles - group * kGroup, kGroup);
-    at -= group * kGroup * n_tiles;
+    const int group = at / (size * n_tiles), in_group = min(tiles - group * size, size);
+    at -= group * size * n_tiles;
     Tile r;
     r.e = lo;
     r.nblk = at / in_group;
-    const int m_tile = group * kGroup + at - r.nblk * in_group;
-    const int m0 = first_part(n_e, m_tile) * kPart;
-    r.row0 = t.base[lo] + m0;
-    r.n = min(first_part(n_e, m_tile + 1) * kPart, n_e) - m0;
-    r.mblk = 0;
+    const int m_tile = group * size + at - r.nblk * in_group;
+    const int first = first_part(n_e, m_tile) * kPart;
+    r.row0 = t.base[lo] + first;
+    r.n = r.rows = min(first_part(n_e, m_tile + 1) * kPart, n_e) - first;
+    r.m0 = 0;
     return r;
 }
 
@@ -154,9 +154,25 @@ __device__ __forceinline__ Tile locate_wgrad(const Product &p, int at, int m_til
     r.e = at / (m_tiles * n_tiles);
     at -= r.e * m_tiles * n_tiles;
     r.nblk = at / m_tiles;
-    r.mblk = at - r.nblk * m_tiles;
+    const int m_tile = at - r.nblk * m_tiles;
+    r.m0 = first_part(p.m, m_tile) * kPart;
+    r.rows = min(first_part(p.m, m_tile + 1) * kPart, p.m) - r.m0;
     rows_of(p, r.e, r.row0, r.n);
     return r;
+}
+
+// One of `cuts` pieces of a tile, whole parts of its rows.
+__device__ __forceinline__ void cut(Tile &t, int piece, int cuts, bool wgrad)
+{
+    const int parts = (t.rows + kPart - 1) / kPart;
+    const int first = piece * parts / cuts * kPart;
+    t.rows = min((piece + 1) * parts / cuts * kPart, t.rows) - first;
+    if (wgrad) {
+        t.m0 += first;
+    } else {
+        t.row0 += first;
+        t.n = t.rows;
+    }
 }
 
 // A buffer's descriptor, of `bytes` from p: loads past them give 0.
@@ -190,6 +206,16 @@ __device__ __forceinline__ void meet_loaded()
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+}
+
+// The kernel's argument, read anew: what only the epilogue uses takes no register through the products.
+__device__ __forceinline__ const __attribute__((address_space(4))) Product &argument()
+{
+    const auto at = reinterpret_cast<uint64_t>(__builtin_amdgcn_kernarg_segment_ptr());
+    uint32_t lo, hi;
+    asm volatile("" : "=s"(lo) : "0"(uniform((int)(uint32_t)at)));
+    asm volatile("" : "=s"(hi) : "0"(uniform((int)(uint32_t)(at >> 32))));
+    return *reinterpret_cast<const __attribute__((address_space(4))) Product *>((uint64_t)hi << 32 | lo);
 }
 
 // The lane, counted anew: what is computed from it is worked out where it is used, and takes no
@@ -233,29 +259,6 @@ struct Rows {
     }
 };
 
-__device__ __forceinline__ void unpack8(u32x4 d, float (&v)[8])
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16_lo(d[i]);
-        v[2 * i + 1] = bf16_hi(d[i]);
-    }
-}
-
-// 1 / (1 + exp(-g)), the reciprocal as in swiglu().
-__device__ __forceinline__ float sigmoid(float g)
-{
-    return __builtin_amdgcn_rcpf(__builtin_fmaf(__expf(-g), 0x1p-4f, 0x1p-4f)) * 0x1p-4f;
-}
-
-__device__ __forceinline__ float activate(int act, float z)
-{
-    if (act == EP_ACT_RELU) return z > 0.0f || z != z ? z : 0.0f;
-    if (act == EP_ACT_SILU) return z * sigmoid(z);
-    if (act == EP_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-    return z;
-}
-
 // Swizzle of row r of an operand kept row by row: chunk c (16 bytes) of the row's eight is at place
 // c ^ swizzle(r). LDS serves 16 lanes together, 8 consecutive rows and those 16 further on: they then
 // touch all banks once.
@@ -274,6 +277,7 @@ struct Stream {
     int tiles;
     uint32_t stage = 0;                        // byte offset
     int stored = 0;                            // barriers to come whose loads are older than stores
+    int parts = 0;                             // of the tile that made these
     int tile, kb, nkb;
     const uint8_t *x, *w;
     int64_t xleft, wleft;                      // bytes from x and w to the operands' ends
@@ -298,7 +302,7 @@ struct Stream {
     __device__ __forceinline__ Tile at(int i) const
     {
         const Tile t = list[i];
-        return Tile{uniform(t.e), uniform(t.row0), uniform(t.n), uniform(t.nblk), uniform(t.mblk)};
+        return Tile{uniform(t.e), uniform(t.row0), uniform(t.n), uniform(t.nblk), uniform(t.m0), uniform(t.rows)};
     }
     __device__ __forceinline__ int blocks_of(const Tile &t) const
     {
@@ -320,8 +324,8 @@ struct Stream {
             w = reinterpret_cast<const uint8_t *>(p.w + (size_t)t.row0 * p.n + t.nblk * kTile);
             wleft = ((int64_t)t.n * p.n - t.nblk * kTile) * 2;
         }
-        x = reinterpret_cast<const uint8_t *>(p.x + (size_t)t.row0 * ldx() + t.mblk * kTile);
-        xleft = ((int64_t)t.n * ldx() - t.mblk * kTile) * 2;
+        x = reinterpret_cast<const uint8_t *>(p.x + (size_t)t.row0 * ldx() + t.m0);
+        xleft = ((int64_t)t.n * ldx() - t.m0) * 2;
         xb = buffer(x, xleft);
         wb = buffer(w, wleft);
         const int l = lane_now(), chunk = chunk_of(l);
@@ -387,7 +391,6 @@ template <int F, int O, int A>
 __device__ __forceinline__ void run(Stream<F, O> &ld, uint8_t *stages, int tile, int end)
 {
     constexpr bool kXTr = F == form::kWgrad, kWTr = F != form::kForward;
-    const Product &p = ld.p;
     const int wave = ld.wave(), wm = wave & 1, wn = wave >> 1;
 
     f32x16 acc[2][A];
@@ -523,9 +526,9 @@ __device__ __forceinline__ void run(Stream<F, O> &ld, uint8_t *stages, int tile,
     // that are there, kStores at least: the waits for loads count past them.
     auto finish = [&](int tile) {
         const Tile t = ld.at(tile);
-        const int m0 = F == form::kWgrad ? t.mblk * kTile : 0;
-        const int rows = F == form::kWgrad ? min(p.m - m0, kTile) : t.n;
-        const size_t row0 = F == form::kWgrad ? (size_t)t.e * p.m + m0 : (size_t)t.row0;
+        const auto &p = argument();
+        const int rows = t.rows;
+        const size_t row0 = F == form::kWgrad ? (size_t)t.e * p.m + t.m0 : (size_t)t.row0;
         const int l = lane_now();
         const uint32_t r = wm * 32 + (l & 15);
         // a lane's columns of 32: eight of 16 bits, or four and four more of 32
@@ -615,37 +618,47 @@ __device__ __forceinline__ void run(Stream<F, O> &ld, uint8_t *stages, int tile,
                         put_rows(out, at, n * 64, gate[0], gate[1]);
                         put_rows(out, at + n * 2, n * 64, up[0], up[1]);
                     } else {
-                        const Rows bias(p.bias, 0, p.bias ? 1 : 0, n, 2);
-                        const Rows res(p.in, row0, p.in ? rows : 0, n, 2);
-                        u32x4 x[2], z[2];
+                        // z of eight columns, with the bias
+                        auto z8 = [&](int g, float (&d)[8]) {
+                            eight(v, g, d);
+                            if (p.bias) {
+                                float b[8];
+                                const uint32_t at = (c0 + g * 16 + (l >> 5) * 8) * 2;
+                                unpack8(Rows(p.bias, 0, 1, n, 2).get(at), b);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) d[i] += b[i];
+                            }
+                        };
+                        float d[8];
+                        u32x4 x[2];
+                        if (p.out2) {
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+                                z8(g, d);
+                                x[g] = pack8(d);
+                            }
+                            trade(x[0], x[1]);
+                            put_rows(Rows(p.out2, row0, rows, n, 2), off, n * 32, x[0], x[1]);
+                        }
                         if (p.in) {
+                            const Rows res(p.in, row0, rows, n, 2);
                             x[0] = res.get(off);
                             x[1] = res.get(off + n * 32);
                             trade(x[0], x[1]);
                         }
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
-                            float d[8], b[8];
-                            eight(v, g, d);
-                            if (p.bias) {
-                                unpack8(bias.get((c0 + g * 16 + (l >> 5) * 8) * 2), b);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) d[i] += b[i];
-                            }
-                            if (p.out2) z[g] = pack8(d);
+                            z8(g, d);
                             if (p.act != EP_ACT_NONE)
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) d[i] = activate(p.act, d[i]);
                             if (p.in) {
+                                float b[8];
                                 unpack8(x[g], b);
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) d[i] += b[i];
                             }
                             x[g] = pack8(d);
-                        }
-                        if (p.out2) {
-                            trade(z[0], z[1]);
-                            put_rows(Rows(p.out2, row0, rows, n, 2), off, n * 32, z[0], z[1]);
                         }
                         trade(x[0], x[1]);
                         put_rows(out, off, n * 32, x[0], x[1]);
@@ -664,6 +677,8 @@ __device__ __forceinline__ void run(Stream<F, O> &ld, uint8_t *stages, int tile,
         read_x(1, j);
     }
     clear();
+    if (ld.parts < A) ld.stored = 0;           // the last tile made fewer stores than its kStores here
+    ld.parts = A;
     for (; tile < end; ++tile) {
         for (int kb = ld.blocks_of(ld.at(tile)); kb > 0; --kb) step();
         finish(tile);
@@ -681,58 +696,70 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p)
     static_assert(sizeof(TileTable) <= sizeof(stages), "the table is done with before the first block");
     TileTable &table = *reinterpret_cast<TileTable *>(stages);
     const int n_tiles = (p.n + kTile - 1) / kTile, m_tiles = (p.m + kTile - 1) / kTile;
-    // Neighbours in the tiles' order share operands: of each gridDim.x tiles in a row an XCD takes one
-    // eighth (its workgroups are blockIdx.x mod 8, gridDim.x is a multiple of 8)
+    // of each gridDim.x tiles in a row an XCD takes one eighth (its workgroups are blockIdx.x mod 8,
+    // gridDim.x is a multiple of 8)
     const int slot = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
-    const int lane = threadIdx.x & (kWave - 1);
-    for (int first = slot;;) {                // kList tiles at a time
+    const int lane = threadIdx.x & (kWave - 1), grid = gridDim.x;
+    for (int first = slot;;) {                 // kList tiles at a time
         int total;
         if constexpr (F == form::kWgrad) total = p.E * m_tiles * n_tiles;
         else total = build_table(table, p) * n_tiles;
-        if (first >= total) break;
-        const int tiles = min((total - first + (int)gridDim.x - 1) / (int)gridDim.x, kList);
-        // the tiles with the most parts first, so that those of one number of parts run together
+        // The tiles of a last round that leaves at least half of the workgroups without one are cut, so
+        // that each of them gets a piece.
+        const int rest = total % grid, whole = total - rest;
+        const int cuts = rest ? min(grid / rest, kTile / kPart) : 1;
+        const int pieces = whole + rest * cuts;
+        if (first >= pieces) break;
+        const int tiles = min((pieces - first + grid - 1) / grid, kList);
         Tile mine{};
-        int parts = 0;
         if (lane < tiles) {
-            const int at = first + lane * gridDim.x;
+            int at = first + lane * grid, piece = 0;
+            if (at >= whole && cuts > 1) {
+                piece = (at - whole) % cuts;
+                at = whole + (at - whole) / cuts;
+            }
             int columns;                       // nothing of its divisions stays in registers
             asm volatile("" : "=s"(columns) : "0"(uniform(n_tiles)));
             if constexpr (F == form::kWgrad) mine = locate_wgrad(p, at, m_tiles, columns);
             else mine = locate(table, p, at, columns);
-            const int rows = F == form::kWgrad ? min(p.m - mine.mblk * kTile, kTile) : mine.n;
-            parts = (rows + kPart - 1) / kPart;
+            if (first + lane * grid >= whole && cuts > 1) cut(mine, piece, cuts, F == form::kWgrad);
         }
-        int count[5], place = 0;
+        const int parts = (mine.rows + kPart - 1) / kPart;
+        const uint64_t some = __ballot(parts > 0);
+        uint64_t with[5];
 #pragma unroll
-        for (int a = 4; a >= 1; --a) {
-            const uint64_t these = __ballot(parts == a);
-            count[a] = __popcll(these);
-            place += parts < a ? count[a] : parts == a ? count_below(these) : 0;
-        }
-        if ((int)threadIdx.x < tiles) list[place] = mine;
+        for (int a = 1; a <= 4; ++a) with[a] = __ballot(parts == a);
+        if ((int)threadIdx.x < tiles) list[threadIdx.x] = mine;
         __syncthreads();                       // the list is there, the table is done with
-        Stream<F, O> ld(p, list, tiles);
-        ld.start(stages);
-        int tile = 0;
-        auto run_all = [&](auto a) {
-            constexpr int A = decltype(a)::value;
-            if (count[A]) run<F, O, A>(ld, stages, tile, tile + count[A]);
-            tile += count[A];
-        };
-        run_all(std::integral_constant<int, 4>{});
-        run_all(std::integral_constant<int, 3>{});
-        run_all(std::integral_constant<int, 2>{});
-        run_all(std::integral_constant<int, 1>{});
-        meet_loaded<0>();                      // no direct load is left to write LDS
-        first += tiles * gridDim.x;
+        const int n_list = __popcll(some);     // a piece that is empty can only be the last
+        if (n_list > 0) {
+            Stream<F, O> ld(p, list, n_list);
+            ld.start(stages);
+            int tile = 0;
+            auto run_some = [&](auto a) {      // the tiles from here on that have A parts
+                constexpr int A = decltype(a)::value;
+                if (tile == n_list) return;
+                const uint64_t without = ~(with[A] >> tile);
+                const int n = min(without ? (int)__builtin_ctzll(without) : kWave, n_list - tile);
+                if (n > 0) run<F, O, A>(ld, stages, tile, tile + n);
+                tile += n;
+            };
+            while (tile < n_list) {
+                run_some(std::integral_constant<int, 4>{});
+                run_some(std::integral_constant<int, 3>{});
+                run_some(std::integral_constant<int, 2>{});
+                run_some(std::integral_constant<int, 1>{});
+            }
+            meet_loaded<0>();                  // no direct load is left to write LDS
+        }
+        first += tiles * grid;
     }
 #else
     (void)p;
 #endif
 }
 
-// One workgroup per CU, or as many as there can be tiles.
+// One workgroup per CU, or as many as there can be pieces of tiles.
 template <int F, int O>
 hipError_t launch_product(const Product &p, hipStream_t stream)
 {
@@ -744,6 +771,7 @@ hipError_t launch_product(const Product &p, hipStream_t stream)
         const int64_t experts = p.pairs < p.E ? p.pairs : p.E;
         tiles *= p.pairs / kTile + experts;
     }
+    tiles *= kTile / kPart;
     const dim3 grid((unsigned)(tiles < kCus ? (tiles + 7) / 8 * 8 : kCus));
     return launch(product_kernel<F, O>, grid, dim3(kThreads), 0, stream, p);
 }
