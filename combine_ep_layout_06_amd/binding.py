@@ -1099,11 +1099,15 @@ def ep_moe_layer_fp8(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tens
 # the experts in bf16, forward and backward
 # ------------------------------------------------------------------------------------------
 
-def _rows(t: torch.Tensor, name: str, width: int, lead: tuple, device):
-    """Checks that `t` is a bf16 row buffer of `width` channels with the leading sizes `lead`."""
-    if tuple(t.shape) != (*lead, width):
-        raise ValueError(f"{name}: expected {(*lead, width)}, got {tuple(t.shape)}")
-    _need(t, name, _bf16(t), t.numel(), device)
+_BF16_TYPES = (torch.bfloat16, torch.int16, torch.uint16)
+
+
+def _rows(t: torch.Tensor, name: str, shape: tuple, device):
+    """Checks that `t` holds bf16 values in this shape."""
+    if t.shape != shape or t.dtype not in _BF16_TYPES or t.device != device or not t.is_contiguous():
+        if t.shape != shape:
+            raise ValueError(f"{name}: expected {tuple(shape)}, got {tuple(t.shape)}")
+        _need(t, name, _bf16(t), t.numel(), device)
 
 
 def _weights3(w: torch.Tensor, name: str):
@@ -1112,19 +1116,25 @@ def _weights3(w: torch.Tensor, name: str):
     return w.shape
 
 
-def _expert_rows(x: torch.Tensor, name: str, E: int, expert_count: torch.Tensor, packed_offset,
-                 pairs: int):
-    """The leading sizes of a receive buffer and the shape's T (pairs) and C, with the counts and
-    offsets checked: [E, C, width], or [rows, width] with `packed_offset`."""
-    if x.dim() != (3 if packed_offset is None else 2):
+def _experts(expert_count: torch.Tensor) -> int:
+    if expert_count.dim() != 1:
+        raise ValueError(f"expert_count: expected [E], got {tuple(expert_count.shape)}")
+    return expert_count.shape[0]
+
+
+def _expert_rows(x: torch.Tensor, name: str, E: int, expert_count: torch.Tensor, packed_offset):
+    """The leading sizes of a receive buffer, [E, C, width] or with `packed_offset` [rows, width],
+    with the counts and offsets checked; and the buffer's device."""
+    shape, dev = x.shape, x.device
+    if len(shape) != (3 if packed_offset is None else 2):
         raise ValueError(f"{name}: expected {'[E, C, width]' if packed_offset is None else '[rows, width]'}"
-                         f", got {tuple(x.shape)}")
-    if packed_offset is None and x.shape[0] != E:
-        raise ValueError(f"{name}: {x.shape[0]} experts' rows for {E} experts")
-    _need(expert_count, "expert_count", torch.int32, E, x.device)
+                         f", got {tuple(shape)}")
+    if packed_offset is None and shape[0] != E:
+        raise ValueError(f"{name}: {shape[0]} experts' rows for {E} experts")
+    _need(expert_count, "expert_count", torch.int32, E, dev)
     if packed_offset is not None:
-        _need(packed_offset, "packed_offset", torch.int32, E + 1, x.device)
-    return tuple(x.shape[:-1])
+        _need(packed_offset, "packed_offset", torch.int32, E + 1, dev)
+    return shape[:-1], dev
 
 
 def _expert_call(fn: str, E, H, n, lead, packed_offset, pairs, head, count, tail, stream):
@@ -1138,12 +1148,11 @@ def _expert_call(fn: str, E, H, n, lead, packed_offset, pairs, head, count, tail
 
 def _expert_gemm(x, count, offset, w, pairs, y, stream):
     E, N, H = _weights3(w, "w")
-    lead = _expert_rows(x, "recv", E, count, offset, pairs)
-    dev = x.device
-    _rows(x, "recv", H, lead, dev)
-    _need(w, "w", _bf16(w), E * N * H, dev)
+    lead, dev = _expert_rows(x, "recv", E, count, offset)
+    _rows(x, "recv", (*lead, H), dev)
+    _rows(w, "w", w.shape, dev)
     y = _new((*lead, N), _bf16(x), dev, stream) if y is None else y
-    _rows(y, "y", N, lead, dev)
+    _rows(y, "y", (*lead, N), dev)
     _expert_call("ep_expert_gemm", E, H, N, lead, offset, pairs, (x,), count, (w, y), stream)
     return y
 
@@ -1169,14 +1178,13 @@ def _expert_swiglu(x, count, offset, w13, pairs, h, gu, stream):
     E, n, H = _weights3(w13, "w13")
     if n % 2:
         raise ValueError(f"w13: expected an even number of rows (gate, then up), got {n}")
-    lead = _expert_rows(x, "recv", E, count, offset, pairs)
-    dev = x.device
-    _rows(x, "recv", H, lead, dev)
-    _need(w13, "w13", _bf16(w13), E * n * H, dev)
+    lead, dev = _expert_rows(x, "recv", E, count, offset)
+    _rows(x, "recv", (*lead, H), dev)
+    _rows(w13, "w13", w13.shape, dev)
     h = _new((*lead, n // 2), _bf16(x), dev, stream) if h is None else h
-    _rows(h, "h", n // 2, lead, dev)
+    _rows(h, "h", (*lead, n // 2), dev)
     if gu is not None:
-        _rows(gu, "gu", n, lead, dev)
+        _rows(gu, "gu", (*lead, n), dev)
     _expert_call("ep_expert_swiglu", E, H, n // 2, lead, offset, pairs, (x,), count, (w13, gu, h),
                  stream)
     return h
@@ -1201,12 +1209,11 @@ def ep_expert_swiglu_packed(recv: torch.Tensor, expert_count: torch.Tensor,
 
 def _expert_dgrad(dy, count, offset, w, pairs, dx, stream):
     E, N, H = _weights3(w, "w")
-    lead = _expert_rows(dy, "dy", E, count, offset, pairs)
-    dev = dy.device
-    _rows(dy, "dy", N, lead, dev)
-    _need(w, "w", _bf16(w), E * N * H, dev)
+    lead, dev = _expert_rows(dy, "dy", E, count, offset)
+    _rows(dy, "dy", (*lead, N), dev)
+    _rows(w, "w", w.shape, dev)
     dx = _new((*lead, H), _bf16(dy), dev, stream) if dx is None else dx
-    _rows(dx, "dx", H, lead, dev)
+    _rows(dx, "dx", (*lead, H), dev)
     _expert_call("ep_expert_gemm_dgrad", E, H, N, lead, offset, pairs, (dy,), count, (w, dx), stream)
     return dx
 
@@ -1227,13 +1234,12 @@ def ep_expert_gemm_dgrad_packed(dy: torch.Tensor, expert_count: torch.Tensor,
 
 def _expert_swiglu_dgrad(dy, count, offset, w2, gu, pairs, dgu, stream):
     E, H, I = _weights3(w2, "w2")
-    lead = _expert_rows(dy, "dy", E, count, offset, pairs)
-    dev = dy.device
-    _rows(dy, "dy", H, lead, dev)
-    _need(w2, "w2", _bf16(w2), E * H * I, dev)
-    _rows(gu, "gu", 2 * I, lead, dev)
+    lead, dev = _expert_rows(dy, "dy", E, count, offset)
+    _rows(dy, "dy", (*lead, H), dev)
+    _rows(w2, "w2", w2.shape, dev)
+    _rows(gu, "gu", (*lead, 2 * I), dev)
     dgu = _new((*lead, 2 * I), _bf16(dy), dev, stream) if dgu is None else dgu
-    _rows(dgu, "dgu", 2 * I, lead, dev)
+    _rows(dgu, "dgu", (*lead, 2 * I), dev)
     _expert_call("ep_expert_swiglu_dgrad", E, H, I, lead, offset, pairs, (dy,), count, (w2, gu, dgu),
                  stream)
     return dgu
@@ -1257,11 +1263,10 @@ def ep_expert_swiglu_dgrad_packed(dy: torch.Tensor, expert_count: torch.Tensor,
 
 def _expert_wgrad(dy, x, count, offset, pairs, dw, accumulate, stream):
     E = _experts(count)
-    lead = _expert_rows(dy, "dy", E, count, offset, pairs)
-    dev = dy.device
+    lead, dev = _expert_rows(dy, "dy", E, count, offset)
     N, H = dy.shape[-1], x.shape[-1]
-    _rows(dy, "dy", N, lead, dev)
-    _rows(x, "recv", H, lead, dev)
+    _rows(dy, "dy", (*lead, N), dev)
+    _rows(x, "recv", (*lead, H), dev)
     if dw is None:
         if accumulate:
             raise ValueError("dw: accumulate adds to a float32 dw that the caller passes in")
@@ -1276,12 +1281,6 @@ def _expert_wgrad(dy, x, count, offset, pairs, dw, accumulate, stream):
     head = (int(bool(accumulate)), dy, x) if f32 else (dy, x)
     _expert_call(fn, E, H, N, lead, offset, pairs, head, count, (dw,), stream)
     return dw
-
-
-def _experts(expert_count: torch.Tensor) -> int:
-    if expert_count.dim() != 1:
-        raise ValueError(f"expert_count: expected [E], got {tuple(expert_count.shape)}")
-    return expert_count.shape[0]
 
 
 def ep_expert_gemm_wgrad(dy: torch.Tensor, recv: torch.Tensor, expert_count: torch.Tensor,
@@ -1305,9 +1304,9 @@ def _combine_grad(dout, y, idx, slot, topk_w, dy, dtopk_w, stream):
     lead = tuple(y.shape[:-1])
     dy = _new(y.shape, _bf16(y), dev, stream) if dy is None else dy
     dtopk_w = _new((T, K), torch.float32, dev, stream) if dtopk_w is None else dtopk_w
-    _rows(dout, "dout", H, (T,), dev)
-    _rows(y, "y", H, lead, dev)
-    _rows(dy, "dy", H, lead, dev)
+    _rows(dout, "dout", (T, H), dev)
+    _rows(y, "y", (*lead, H), dev)
+    _rows(dy, "dy", (*lead, H), dev)
     for name, t, dtype in (("topk_idx", idx, torch.int32), ("slot", slot, torch.int32),
                            ("topk_w", topk_w, torch.float32), ("dtopk_w", dtopk_w, torch.float32)):
         _need(t, name, dtype, T * K, dev)
@@ -1347,13 +1346,14 @@ def ep_combine_grad_packed(dout: torch.Tensor, y: torch.Tensor, topk_idx: torch.
 # ------------------------------------------------------------------------------------------
 
 def _linear_args(x, w, act):
-    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
-        raise ValueError(f"expected x [T, H] and w [N, H], got {tuple(x.shape)} and {tuple(w.shape)}")
+    xs, ws, dev = x.shape, w.shape, x.device
+    if len(xs) != 2 or len(ws) != 2 or xs[1] != ws[1]:
+        raise ValueError(f"expected x [T, H] and w [N, H], got {tuple(xs)} and {tuple(ws)}")
     if act not in ACTIVATIONS:
         raise ValueError(f"act: expected one of {sorted(ACTIVATIONS)}, got {act!r}")
-    _need(x, "x", _bf16(x), x.numel(), x.device)
-    _need(w, "w", _bf16(w), w.numel(), x.device)
-    return x.shape[0], x.shape[1], w.shape[0], ACTIVATIONS[act]
+    _rows(x, "x", xs, dev)
+    _rows(w, "w", ws, dev)
+    return xs[0], xs[1], ws[0], ACTIVATIONS[act], dev
 
 
 def ep_linear(x: torch.Tensor, w: torch.Tensor, *, bias=None, act="none", residual=None, pre=None,
@@ -1362,14 +1362,15 @@ def ep_linear(x: torch.Tensor, w: torch.Tensor, *, bias=None, act="none", residu
     and ``residual`` [T, N] (or None) bf16 -> ``out`` [T, N] bf16 (may be ``residual`` itself). ``act``:
     "none", "relu", "silu" or "gelu" (with the normal distribution). ``pre`` [T, N] bf16, if given,
     receives ``x @ w.T + bias``, which ep_linear_grad needs for an activation."""
-    T, H, N, a = _linear_args(x, w, act)
-    dev = x.device
+    T, H, N, a, dev = _linear_args(x, w, act)
     out = _new((T, N), _bf16(x), dev, stream) if out is None else out
     if bias is not None:
-        _need(bias, "bias", _bf16(bias), N, dev)
-    for name, t in (("residual", residual), ("pre", pre), ("out", out)):
-        if t is not None:
-            _rows(t, name, N, (T,), dev)
+        _rows(bias, "bias", (N,), dev)
+    _rows(out, "out", (T, N), dev)
+    if residual is not None:
+        _rows(residual, "residual", (T, N), dev)
+    if pre is not None:
+        _rows(pre, "pre", (T, N), dev)
     _call("ep_linear", _shape(T, H, 1, 1, 1, 1), N, a, x, w, bias, residual, pre, out, stream=stream)
     return out
 
@@ -1386,18 +1387,17 @@ def ep_linear_grad(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *, act=
     (with an activation) ``pre`` -> ``dx`` [T, H] bf16, ``dw`` [N, H] bf16, ``dbias`` [N] float32. The
     residual's gradient is ``dout``. ``workspace``: a device tensor of at least
     linear_grad_workspace_bytes(T, N, act) bytes (allocated here if not given)."""
-    T, H, N, a = _linear_args(x, w, act)
-    dev = x.device
-    _rows(dout, "dout", N, (T,), dev)
+    T, H, N, a, dev = _linear_args(x, w, act)
+    _rows(dout, "dout", (T, N), dev)
     if (pre is None) != (act == "none"):
         raise ValueError("pre: given exactly for an activation")
     if pre is not None:
-        _rows(pre, "pre", N, (T,), dev)
+        _rows(pre, "pre", (T, N), dev)
     dx = _new((T, H), _bf16(x), dev, stream) if dx is None else dx
     dw = _new((N, H), _bf16(x), dev, stream) if dw is None else dw
     dbias = _new((N,), torch.float32, dev, stream) if dbias is None else dbias
-    _rows(dx, "dx", H, (T,), dev)
-    _rows(dw, "dw", H, (N,), dev)
+    _rows(dx, "dx", (T, H), dev)
+    _rows(dw, "dw", (N, H), dev)
     _need(dbias, "dbias", torch.float32, N, dev)
     if workspace is None:
         workspace = _own_workspace(linear_grad_workspace_bytes(T, N, act), dev, stream)

@@ -36,6 +36,13 @@ hipError_t launch_expert_swiglu_dgrad(const Product &p, hipStream_t stream);
 hipError_t launch_expert_wgrad(const Product &p, bool f32, hipStream_t stream);
 hipError_t launch_linear(const Product &p, hipStream_t stream);
 
+// The forward products for few rows, and whether they are the better ones for these rows (some; of a
+// packed buffer with some).
+bool few_rows(const Product &p, bool swiglu);
+hipError_t launch_few_gemm(const Product &p, hipStream_t stream);
+hipError_t launch_few_swiglu(const Product &p, hipStream_t stream);
+hipError_t launch_few_linear(const Product &p, hipStream_t stream);
+
 hipError_t launch_combine_grad(const ep_shape_t &s, const uint16_t *dout, const uint16_t *y,
                                const int32_t *idx, const int32_t *slot, const float *w, uint16_t *dy,
                                float *dw, hipStream_t stream, RowMap map = RowMap());
@@ -49,6 +56,27 @@ hipError_t launch_act_grad(const uint16_t *dout, const uint16_t *z, uint16_t *dz
                            float *dbias, int T, int N, int act, hipStream_t stream);
 
 #if defined(__HIPCC__)
+
+#if defined(__HIP_DEVICE_COMPILE__)
+// The kernel's argument, a Product, read anew: what only the epilogue uses takes no register through the products.
+__device__ __forceinline__ const __attribute__((address_space(4))) Product &argument()
+{
+    const auto at = reinterpret_cast<uint64_t>(__builtin_amdgcn_kernarg_segment_ptr());
+    uint32_t lo, hi;
+    asm volatile("" : "=s"(lo) : "0"(__builtin_amdgcn_readfirstlane((int)(uint32_t)at)));
+    asm volatile("" : "=s"(hi) : "0"(__builtin_amdgcn_readfirstlane((int)(uint32_t)(at >> 32))));
+    return *reinterpret_cast<const __attribute__((address_space(4))) Product *>((uint64_t)hi << 32 | lo);
+}
+
+// The lane, counted anew: what is computed from it is worked out where it is used, and takes no
+// register through the products (which need them all).
+__device__ __forceinline__ int lane_now()
+{
+    int l;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(l));
+    return l;
+}
+#endif
 
 __device__ __forceinline__ void unpack8(u32x4 d, float (&v)[8])
 {

@@ -208,25 +208,6 @@ __device__ __forceinline__ void meet_loaded()
     asm volatile("" ::: "memory");
 }
 
-// The kernel's argument, read anew: what only the epilogue uses takes no register through the products.
-__device__ __forceinline__ const __attribute__((address_space(4))) Product &argument()
-{
-    const auto at = reinterpret_cast<uint64_t>(__builtin_amdgcn_kernarg_segment_ptr());
-    uint32_t lo, hi;
-    asm volatile("" : "=s"(lo) : "0"(uniform((int)(uint32_t)at)));
-    asm volatile("" : "=s"(hi) : "0"(uniform((int)(uint32_t)(at >> 32))));
-    return *reinterpret_cast<const __attribute__((address_space(4))) Product *>((uint64_t)hi << 32 | lo);
-}
-
-// The lane, counted anew: what is computed from it is worked out where it is used, and takes no
-// register through the products (which need them all).
-__device__ __forceinline__ int lane_now()
-{
-    int l;
-    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(l));
-    return l;
-}
-
 // Two values as bf16, rounded to nearest even (a NaN stays one).
 __device__ __forceinline__ uint32_t pair(float a, float b)
 {
@@ -759,15 +740,17 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p)
 #endif
 }
 
+bool no_rows(const Product &p) { return p.pairs == 0 || (p.offset && p.rows == 0); }
+
 // One workgroup per CU, or as many as there can be pieces of tiles.
 template <int F, int O>
 hipError_t launch_product(const Product &p, hipStream_t stream)
 {
     int64_t tiles = (p.n + kTile - 1) / kTile;
+    if (F != form::kWgrad && no_rows(p)) return hipSuccess;
     if (F == form::kWgrad) {
         tiles *= (int64_t)p.E * ((p.m + kTile - 1) / kTile);
     } else {
-        if (p.pairs == 0 || (p.offset && p.rows == 0)) return hipSuccess;
         const int64_t experts = p.pairs < p.E ? p.pairs : p.E;
         tiles *= p.pairs / kTile + experts;
     }
@@ -780,11 +763,13 @@ hipError_t launch_product(const Product &p, hipStream_t stream)
 
 hipError_t launch_expert_gemm(const Product &p, hipStream_t stream)
 {
+    if (!no_rows(p) && few_rows(p, false)) return launch_few_gemm(p, stream);
     return launch_product<form::kForward, to::kBf16>(p, stream);
 }
 
 hipError_t launch_expert_swiglu(const Product &p, hipStream_t stream)
 {
+    if (!no_rows(p) && few_rows(p, true)) return launch_few_swiglu(p, stream);
     return launch_product<form::kForward, to::kSwiglu>(p, stream);
 }
 
@@ -806,6 +791,7 @@ hipError_t launch_expert_wgrad(const Product &p, bool f32, hipStream_t stream)
 
 hipError_t launch_linear(const Product &p, hipStream_t stream)
 {
+    if (!no_rows(p) && few_rows(p, false)) return launch_few_linear(p, stream);
     return launch_product<form::kForward, to::kLinear>(p, stream);
 }
 
