@@ -1162,7 +1162,8 @@ def ep_expert_gemm(recv: torch.Tensor, expert_count: torch.Tensor, w: torch.Tens
     """The experts' product on a padded bf16 receive buffer ``recv`` [E, C, H] (as ep_dispatch
     writes it), the first ``expert_count[e]`` rows of each expert: weights ``w`` [E, N, H] ->
     ``y`` [E, C, N] bf16. Rows that hold no pair are neither read nor written. ``pairs``: T * K, the
-    pairs the layout placed (chooses the grid, never the result; 0: no rows)."""
+    pairs the layout placed (chooses the kernel and its grid, so that the order of the fp32 sums may
+    differ, but not the rows that are computed; 0: no rows)."""
     return _expert_gemm(recv, expert_count, None, w, pairs, y, stream)
 
 

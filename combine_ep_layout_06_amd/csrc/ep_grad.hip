@@ -27,8 +27,8 @@ constexpr int kManyPairs = 8192;   // 8 wavefronts for each SIMD
 
 template <int W>
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(
-    const u32x4 *__restrict__ dout, const u32x4 *__restrict__ y, const int32_t *__restrict__ idx,
-    const int32_t *__restrict__ slot, const float *__restrict__ topk_w, u32x4 *__restrict__ dy,
+    const u32x4 *__restrict__ dout, const u32x4 *y, const int32_t *__restrict__ idx,
+    const int32_t *__restrict__ slot, const float *__restrict__ topk_w, u32x4 *dy,
     float *__restrict__ dw, int pairs, int H8, int E, int C, int K, const int32_t *__restrict__ poff,
     int prows)
 {

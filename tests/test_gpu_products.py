@@ -183,3 +183,237 @@ def test_products(rows, H, N):
     check_swiglu_dgrad(x, H, N)
     for kind in ("bf16", "f32", "accumulate"):
         check_wgrad(x, H, N, kind)
+
+
+def kernels():
+    return [d["kernel"] for d in B.last_launches()]
+
+
+@pytest.mark.parametrize("mean,E", [(1, 9), (20, 4), (50, 3)])
+@pytest.mark.parametrize("A", [0, 8])
+def test_few_rows(mean, E, A):
+    """The kernel for few rows, each of its heights, with experts that have many more rows than the mean
+    and experts that have none."""
+    counts = [mean] * (E - 2) + [0, 2 * mean]
+    x = Experts(counts, A=A, seed=mean)
+    for H, N in ((200, 24), (520, 136), (1032, 40)):
+        check_forward(x, H, N)
+        assert all("few_rows_kernel" in k for k in kernels()), kernels()
+        check_swiglu(x, H, N, keep=True)
+        assert all("few_rows_kernel" in k for k in kernels()), kernels()
+    check_swiglu(x, 264, 72, keep=False)
+
+
+@pytest.mark.parametrize("pairs", [1, 10 ** 6])
+def test_pairs_do_not_choose_the_rows(pairs):
+    """Every row is computed whatever number of pairs the call is told."""
+    x = Experts([70, 0, 300, 5], A=0, seed=3)
+    x.pairs = pairs
+    check_forward(x, 136, 264)
+    check_swiglu(x, 136, 72, keep=False)
+    check_dgrad(x, 136, 264)
+    check_swiglu_dgrad(x, 136, 264)
+    check_wgrad(x, 136, 264)
+
+
+def test_counts_beyond_the_buffers():
+    """Counts below 0 and above the capacity, packed offsets outside the buffer."""
+    x = Experts([-3, 50, 7], C=20, seed=4)
+    for check in (check_forward, check_dgrad, check_swiglu_dgrad, check_wgrad):
+        check(x, 72, 136)
+    x = Experts([5, 9, 4], A=4, seed=5)
+    x.offset[0] = -1                           # no rows
+    x.offset[2] = x.rows - 2                   # two of its four
+    x.n, x.first = [0, 9, 2], [0, x.first[1], x.rows - 2]
+    x.held[:] = False
+    for e in range(3):
+        x.held[x.slice(e)] = True
+    for check in (check_forward, check_dgrad, check_swiglu_dgrad, check_wgrad):
+        check(x, 72, 136)
+
+
+def test_no_rows():
+    """No pairs: nothing is written, but the weights' gradient is zero; with pairs and no rows too."""
+    x = Experts([0, 0], C=4, seed=6)
+    for pairs in (0, 5):
+        x.pairs = pairs
+        check_forward(x, 64, 72)
+        check_swiglu(x, 64, 72, keep=True)
+        check_dgrad(x, 64, 72)
+        check_swiglu_dgrad(x, 64, 72)
+        for kind in ("bf16", "f32", "accumulate"):
+            check_wgrad(x, 64, 72, kind)
+
+
+def test_many_experts():
+    """1024 experts, most of them without rows."""
+    rng = np.random.default_rng(7)
+    counts = [int(v) for v in np.where(rng.random(1024) < 0.1, rng.integers(1, 40, 1024), 0)]
+    x = Experts(counts, A=1, seed=8)
+    check_forward(x, 72, 40)
+    check_dgrad(x, 72, 40)
+    check_wgrad(x, 40, 24)
+
+
+def test_parts_of_tiles():
+    """Tiles of one to four parts one after the other in a workgroup's list, over several rounds."""
+    rng = np.random.default_rng(9)
+    counts = [int(v) for v in rng.integers(0, 700, 120)]
+    x = Experts(counts, A=8, seed=10)
+    check_forward(x, 72, 776)
+    check_swiglu(x, 72, 392, keep=True)
+    check_dgrad(x, 776, 72)
+    check_swiglu_dgrad(x, 72, 776)
+    check_wgrad(x, 264, 520)
+    check_wgrad(x, 264, 520, "f32")
+
+
+def test_same_bits_twice():
+    x = Experts([300, 17, 0, 129], A=16, seed=11)
+    rows, w = x.dev(x.buffer(264)), x.random(x.E, 520, 264, scale=0.1).to(DEV)
+    dy = x.dev(x.buffer(520))
+    first = None
+    for _ in range(3):
+        y, dx = x.sentinel(520), x.sentinel(264)
+        B.ep_expert_gemm_packed(rows, *x.places, w, x.pairs, y=y)
+        B.ep_expert_gemm_dgrad_packed(dy, *x.places, w, x.pairs, dx=dx)
+        dw = B.ep_expert_gemm_wgrad_packed(dy, rows, *x.places, x.pairs).view(torch.int16)
+        if first is not None:
+            assert all(torch.equal(a, b) for a, b in zip(first, (y, dx, dw)))
+        first = (y, dx, dw)
+
+
+def test_swiglu_gradient_in_place():
+    check_swiglu_dgrad(Experts([70, 0, 300, 5], A=8, seed=12), 136, 264, in_place=True)
+
+
+def test_nan_and_infinity_stay_in_their_rows_and_columns():
+    """A NaN or an infinity reaches exactly the elements whose sums it is part of."""
+    x = Experts([5, 140], C=140, seed=13)
+    H, N = 200, 72
+    rows, w = x.buffer(H), x.random(2, N, H, scale=0.1)
+    rows[x.slice(1)][7, 3] = float("nan")
+    w[1, 9, 199] = float("inf")
+    y = x.sentinel(N)
+    B.ep_expert_gemm(x.dev(rows), x.count, w.to(DEV), x.pairs, y=y)
+    got = x.result(y)
+    for e, r in x.each():                      # which elements: on the CPU, row by row
+        ref = torch.stack([(rows[i].double() * w[e].double()).sum(1) for i in range(r.start, r.stop)])
+        assert torch.equal(torch.isnan(got[r]), torch.isnan(ref))
+        assert torch.equal(torch.isinf(got[r]), torch.isinf(ref))
+        assert torch.equal(got[r][torch.isinf(ref)], ref[torch.isinf(ref)])
+    # gradients: a NaN row of dy reaches its row of dx and every element of dw's columns it enters
+    dy = x.buffer(N)
+    dy[x.slice(0)][2, 5] = float("nan")
+    dx = x.sentinel(H)
+    w0 = x.random(2, N, H, scale=0.1)
+    B.ep_expert_gemm_dgrad(x.dev(dy), x.count, w0.to(DEV), x.pairs, dx=dx)
+    nan = torch.isnan(x.result(dx))[x.held]
+    assert nan[2].all() and not nan[torch.arange(len(nan)) != 2].any()
+    clean = rows.clone()
+    clean[x.slice(1)][7, 3] = 1.0
+    dw = torch.isnan(B.ep_expert_gemm_wgrad(x.dev(dy), x.dev(clean), x.count, x.pairs)).cpu()
+    assert dw[0, 5].all() and int(dw.sum()) == H
+
+
+def test_rows_beyond_4_gib():
+    """An expert whose rows begin beyond 4 GiB of the buffers, and the others' rows before them."""
+    H, N = 4096, 4096
+    first = [0, 200, 560_000]
+    counts = [130, 7, 90]
+    rows = 560_100
+    x = torch.empty(rows, H, dtype=torch.bfloat16, device=DEV)
+    y = torch.full((rows, N), SENTINEL, dtype=torch.int16, device=DEV)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    w = torch.empty(3, N, H, dtype=torch.bfloat16, device=DEV).normal_(0, 1 / 64, generator=g)
+    for f, n in zip(first, counts):
+        x[f:f + n].normal_(0, 1, generator=g)
+    count = torch.tensor(counts, dtype=torch.int32, device=DEV)
+    offset = torch.tensor(first + [rows], dtype=torch.int32, device=DEV)
+    for fn, out in ((B.ep_expert_gemm_packed, "y"), (B.ep_expert_gemm_dgrad_packed, "dx")):
+        y.fill_(SENTINEL)
+        print("[beyond 4 GiB]", out, flush=True)
+        fn(x, count, offset, w, sum(counts), **{out: y})
+        for e, (f, n) in enumerate(zip(first, counts)):
+            wide = w[e].double()
+            want, err = P.product64(x[f:f + n].double(), wide.T if out == "y" else wide)
+            close(y[f:f + n].view(torch.bfloat16).double(), want, P.rounded(want, err), (out, e))
+            end = first[e + 1] if e < 2 else rows
+            assert (y[f + n:min(end, f + n + 64)] == SENTINEL).all()
+    print("[beyond 4 GiB] dw", flush=True)
+    dw = B.ep_expert_gemm_wgrad_packed(y.view(torch.bfloat16), x, count, offset, sum(counts))
+    for e, (f, n) in enumerate(zip(first, counts)):
+        want, err = P.product64(y[f:f + n].view(torch.bfloat16).double().T, x[f:f + n].double())
+        close(dw[e].double(), want, P.rounded(want, err), ("dw", e))
+
+
+def test_more_tiles_than_one_list():
+    """More tiles than a workgroup looks up together (64 of 256 workgroups)."""
+    T = 64 * 256 * 256 + 3000
+    g = torch.Generator(device=DEV)
+    g.manual_seed(2)
+    x = torch.randn(T, 8, generator=g, device=DEV).to(torch.bfloat16)
+    w = torch.randn(8, 8, generator=g, device=DEV).to(torch.bfloat16)
+    print("[tiles] linear", T, flush=True)
+    out = B.ep_linear(x, w)
+    want, err = P.product64(x.double(), w.double().T)
+    close(out.double(), want, P.rounded(want, err), "out")
+    # weight gradients: 25 tiles for each of 700 experts, three of which have rows
+    E, N = 700, 1032
+    count = torch.zeros(E, dtype=torch.int32, device=DEV)
+    count[3], count[350], count[699] = 5, 70, 1
+    dy = torch.randn(E, 70, N, generator=g, device=DEV).to(torch.bfloat16)
+    rows = torch.randn(E, 70, N, generator=g, device=DEV).to(torch.bfloat16)
+    dw = torch.full((E, N, N), float("nan"), dtype=torch.bfloat16, device=DEV)
+    print("[tiles] dw", flush=True)
+    B.ep_expert_gemm_wgrad(dy, rows, count, 76, dw=dw)
+    held = []
+    for e, n in ((3, 5), (350, 70), (699, 1)):
+        want, err = P.product64(dy[e, :n].double().T, rows[e, :n].double())
+        close(dw[e].double(), want, P.rounded(want, err), ("dw", e))
+        held.append(e)
+    empty = torch.ones(E, dtype=torch.bool, device=DEV)
+    empty[held] = False
+    assert (dw[empty] == 0).all()
+
+
+def test_long_sum():
+    """A weights' gradient over rows whose bytes pass 2^31."""
+    T, H, N = 280_000, 4096, 8
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    x = torch.empty(T, H, dtype=torch.bfloat16, device=DEV).normal_(0, 1, generator=g)
+    dy = torch.randn(T, N, generator=g, device=DEV).to(torch.bfloat16)
+    dw = torch.zeros(1, N, H, device=DEV)
+    count = torch.tensor([T], dtype=torch.int32, device=DEV)
+    B.ep_expert_gemm_wgrad(dy[None], x[None], count, T, dw=dw)
+    want = torch.zeros(N, H, dtype=torch.float64, device=DEV)
+    size = torch.zeros(N, H, dtype=torch.float64, device=DEV)
+    for i in range(0, T, 20_000):
+        d, v = dy[i:i + 20_000].double(), x[i:i + 20_000].double()
+        want += d.T @ v
+        size += d.abs().T @ v.abs()
+    # the roundings of T additions, each at most half a step of a partial sum, are independent here: a
+    # partial sum is below size, and 280000 steps of random sign stay below 8 sqrt(T) half steps of it
+    close(dw[0].double(), want, 8 * T ** 0.5 * U32 * size, "dw")
+
+
+@pytest.mark.parametrize("T", [3, 300])
+def test_largest_weights(T):
+    """A weight matrix just below 2^30 elements, with the kernel for few rows and with tiles."""
+    H, N = 4096, 262_136
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    w = torch.empty(N, H, dtype=torch.bfloat16, device=DEV).normal_(0, 1 / 64, generator=g)
+    x = torch.randn(T, H, generator=g, device=DEV).to(torch.bfloat16)
+    out = B.ep_linear(x, w)
+    for c in (slice(0, 300), slice(131_000, 131_300), slice(N - 300, N)):
+        want, err = P.product64(x.double(), w[c].double().T)
+        close(out[:, c].double(), want, P.rounded(want, err), ("out", c))
+    dx, dw, _ = B.ep_linear_grad(out, x, w)
+    want, err = P.product64(out[:2].double(), w[:, :64].double())
+    close(dx[:2, :64].double(), want, P.rounded(want, err), "dx")
+    c = slice(N - 300, N)
+    want, err = P.product64(out[:, c].double().T, x.double())
+    close(dw[c].double(), want, P.rounded(want, err), "dw")
