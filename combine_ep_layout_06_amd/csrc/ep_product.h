@@ -36,12 +36,14 @@ hipError_t launch_expert_swiglu_dgrad(const Product &p, hipStream_t stream);
 hipError_t launch_expert_wgrad(const Product &p, bool f32, hipStream_t stream);
 hipError_t launch_linear(const Product &p, hipStream_t stream);
 
-// The forward products for few rows, and whether they are the better ones for these rows (some; of a
-// packed buffer with some).
+// The products for few rows, and whether they are the better ones for these rows (some; of a packed
+// buffer with some).
 bool few_rows(const Product &p, bool swiglu);
 hipError_t launch_few_gemm(const Product &p, hipStream_t stream);
 hipError_t launch_few_swiglu(const Product &p, hipStream_t stream);
 hipError_t launch_few_linear(const Product &p, hipStream_t stream);
+bool few_dgrad(const Product &p);
+hipError_t launch_few_dgrad(const Product &p, bool swiglu, hipStream_t stream);
 
 hipError_t launch_combine_grad(const ep_shape_t &s, const uint16_t *dout, const uint16_t *y,
                                const int32_t *idx, const int32_t *slot, const float *w, uint16_t *dy,
@@ -75,6 +77,45 @@ __device__ __forceinline__ int lane_now()
     int l;
     asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(l));
     return l;
+}
+
+// A lane's byte offset past every buffer's end: nothing is stored there, and loads give 0.
+constexpr uint32_t kNone = 0x80000000u;
+
+typedef __attribute__((address_space(3))) uint8_t *LdsBytes;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 *LdsTr;
+typedef __attribute__((address_space(3))) bf16x8 *LdsRows;
+
+// A buffer's descriptor, of `bytes` from p: loads past them give 0.
+__device__ __forceinline__ i32x4 buffer(const void *p, int64_t bytes)
+{
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    const int n = bytes <= 0 ? 0 : bytes > 0x7FFFFFFF ? 0x7FFFFFFF : (int)bytes;
+    return i32x4{(int)(uint32_t)a, (int)(uint32_t)(a >> 32), n, 0x00027000};
+}
+
+// 16 bytes a lane from buffer `b` to 1 KiB of LDS from `to` on, lane after lane. Written out, because
+// the compiler cannot tell which of the stages a load of the builtin's form fills once paths meet, and
+// then waits for all of them before the next LDS read. It has no register output: the waits for it are
+// the kernels' own, and the compiler's own waits for later loads are only stricter by it. Nothing
+// else in these kernels uses m0.
+__device__ __forceinline__ void load_lds(i32x4 b, uint8_t *to, uint32_t off, uint32_t soff)
+{
+    const uint32_t at = (uint32_t)(uintptr_t)(LdsBytes)to;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(uniform(at)), "v"(off),
+                    "s"(i32x4{uniform(b[0]), uniform(b[1]), uniform(b[2]), uniform(b[3])}),
+                    "s"(uniform(soff)) : "memory");
+}
+
+// Four consecutive sum indexes of one column from LDS: lane i of 16 gives the address of columns (i & 3) *
+// 4 .. of sum index i >> 2, and receives column i.
+__device__ __forceinline__ bf16x8 read_transposed(uint32_t at, uint32_t second)
+{
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(uintptr_t)at);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(uintptr_t)second);
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 #endif
 

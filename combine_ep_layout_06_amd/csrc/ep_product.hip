@@ -45,11 +45,6 @@ constexpr int kStage = 4 * kHalf;  // of a block: x's halves, w's halves
 constexpr int kLoads = 8;          // of a block, by one wavefront
 constexpr int kList = kWave;       // tiles of a workgroup looked up together
 
-typedef __attribute__((address_space(3))) uint8_t *LdsBytes;
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) s16x4 *LdsTr;
-typedef __attribute__((address_space(3))) bf16x8 *LdsRows;
-
 using ep::uniform;
 
 // The experts' rows cut into row tiles: rows and first row of each expert and the running number of row
@@ -175,28 +170,6 @@ __device__ __forceinline__ void cut(Tile &t, int piece, int cuts, bool wgrad)
     }
 }
 
-// A buffer's descriptor, of `bytes` from p: loads past them give 0.
-__device__ __forceinline__ i32x4 buffer(const void *p, int64_t bytes)
-{
-    const uint64_t a = reinterpret_cast<uint64_t>(p);
-    const int n = bytes <= 0 ? 0 : bytes > 0x7FFFFFFF ? 0x7FFFFFFF : (int)bytes;
-    return i32x4{(int)(uint32_t)a, (int)(uint32_t)(a >> 32), n, 0x00027000};
-}
-
-// 16 bytes a lane from buffer `b` to 1 KiB of LDS from `to` on, lane after lane. Written out, because
-// the compiler cannot tell which of the stages a load of the builtin's form fills once paths meet, and
-// then waits for all of them before the next LDS read. It has no register output: the waits for it are
-// those of meet_loaded, and the compiler's own waits for later loads are only stricter by it. Nothing
-// else in these kernels uses m0.
-__device__ __forceinline__ void load_lds(i32x4 b, uint8_t *to, uint32_t off, uint32_t soff)
-{
-    const uint32_t at = (uint32_t)(uintptr_t)(LdsBytes)to;
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "s"(uniform(at)), "v"(off),
-                    "s"(i32x4{uniform(b[0]), uniform(b[1]), uniform(b[2]), uniform(b[3])}),
-                    "s"(uniform(soff)) : "memory");
-}
-
 // Meet the other wavefronts with this one's LDS reads done, and all but its last N loads.
 template <int N>
 __device__ __forceinline__ void meet_loaded()
@@ -222,7 +195,6 @@ __device__ __forceinline__ u32x4 pack8(const float (&v)[8])
 // Rows of an output (or of an epilogue's input) of a tile: `n` rows of `ld` values of `size` bytes. Lanes
 // address them by byte offsets; those of rows that are not there, and kNone, lie past the end, where
 // nothing is stored and loads give 0.
-constexpr uint32_t kNone = 0x80000000u;
 struct Rows {
     __amdgpu_buffer_rsrc_t b;
     __device__ __forceinline__ Rows(const void *p, size_t row0, int n, int ld, int size)
@@ -402,11 +374,7 @@ __device__ __forceinline__ void run(Stream<F, O> &ld, uint8_t *stages, int tile,
         for (int i = 0; i < kWAt; ++i)
             w_at[i] = base + (kWTr ? tr_at + ((wn ^ (i16 >> 2)) << 6) : (row_at ^ (i << 5)) + wn * 4096);
     }
-    auto read_tr = [&](uint32_t at) -> bf16x8 {
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(uintptr_t)at);
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsTr)(uintptr_t)(at + 1024));
-        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-    };
+    auto read_tr = [&](uint32_t at) { return read_transposed(at, at + 1024); };
     auto read_rows = [&](uint32_t at) -> bf16x8 { return *(LdsRows)(uintptr_t)at; };
     // rows (mt * 2 + wm) * 32 .. and columns (nt * 4 + wn) * 32 .. of the tile
     auto read_x = [&](int mt, int j) {
@@ -775,11 +743,13 @@ hipError_t launch_expert_swiglu(const Product &p, hipStream_t stream)
 
 hipError_t launch_expert_dgrad(const Product &p, hipStream_t stream)
 {
+    if (!no_rows(p) && few_dgrad(p)) return launch_few_dgrad(p, false, stream);
     return launch_product<form::kDgrad, to::kBf16>(p, stream);
 }
 
 hipError_t launch_expert_swiglu_dgrad(const Product &p, hipStream_t stream)
 {
+    if (!no_rows(p) && few_dgrad(p)) return launch_few_dgrad(p, true, stream);
     return launch_product<form::kDgrad, to::kSwigluGrad>(p, stream);
 }
 

@@ -1,11 +1,16 @@
-// The forward products for few rows on gfx950 (a decode step, one token): bound by reading the weights
-// once, and by how soon enough of the read is under way.
+// The products for few rows on gfx950 (a decode step, one token), forward and dgrad: bound by reading the
+// weights once, and by how soon enough of the read is under way.
 //
 // A workgroup takes 16 columns of the output (SwiGLU: the same 16 gate and 16 up columns) for up to
 // 16 * MT rows of one expert, its 8 wavefronts an eighth of the sum each: so also a narrow product has
 // a workgroup for every CU, and all of them read at once. Weights and rows go from memory to registers
 // in the order of the 16 x 16 x 32 matrix instruction (16 rows, 64 bytes of each), kAhead steps ahead;
 // the wavefronts' sums meet in LDS, in ascending order.
+//
+// Of dgrad's weights [k][n] a column's sum indexes lie rows apart. Its workgroups take 64 columns, and
+// each wavefront loads 32 rows of them (128 bytes a row) at a time straight into a ring of LDS of its
+// own, from which the transposing read gives the matrix instruction its operand: 64 rows x 4096 x 4096
+// 48 -> 20 us, one row 47 -> 11 (the weights at 4.74 TB/s: 7).
 #include "ep_product.h"
 
 #include <algorithm>
@@ -19,7 +24,7 @@ constexpr int kThreads = 512;
 constexpr int kCols = 16;          // columns of a workgroup
 constexpr int kMostGroups = 32768; // workgroups of a column; they take more groups in turn
 
-namespace to { constexpr int kBf16 = 0, kSwiglu = 1, kLinear = 2; }
+namespace to { constexpr int kBf16 = 0, kSwiglu = 1, kLinear = 2, kSwigluGrad = 3; }
 
 #if defined(__HIP_DEVICE_COMPILE__)
 
@@ -66,6 +71,20 @@ __device__ __forceinline__ Group find_group(int group, int size)
     __syncthreads();
     // the number also where there is no such group
     return Group{uniform(found.e), uniform(found.row0), uniform(found.n), uniform(of)};
+}
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ void put_four(uint16_t *to, f32x4 v)
+{
+    *reinterpret_cast<u32x2 *>(to) = u32x2{__builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[0], (__bf16)v[1]}),
+                                           __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[2], (__bf16)v[3]})};
+}
+
+__device__ __forceinline__ void add_four(f32x4 &v, const uint16_t *from)
+{
+    const u32x2 d = *reinterpret_cast<const u32x2 *>(from);
+    v += f32x4{bf16_lo(d[0]), bf16_hi(d[0]), bf16_lo(d[1]), bf16_hi(d[1])};
 }
 
 template <int O, int MT>
@@ -132,33 +151,23 @@ __device__ __forceinline__ void few_rows(const Group &g, FewShared<O, MT> &sh)
 #pragma unroll
         for (int i = 1; i < kWaves; ++i) v[m] += sh.meet[i][m][t][lane];
     }
-    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    auto four = [](f32x4 f) {
-        return u32x2{__builtin_bit_cast(uint32_t, bf16x2{(__bf16)f[0], (__bf16)f[1]}),
-                     __builtin_bit_cast(uint32_t, bf16x2{(__bf16)f[2], (__bf16)f[3]})};
-    };
-    auto put = [](uint16_t *to, u32x2 d) { *reinterpret_cast<u32x2 *>(to) = d; };
-    auto add = [](f32x4 &f, const uint16_t *from) {
-        const u32x2 d = *reinterpret_cast<const u32x2 *>(from);
-        f += f32x4{bf16_lo(d[0]), bf16_hi(d[0]), bf16_lo(d[1]), bf16_hi(d[1])};
-    };
     const size_t row = (size_t)g.row0 + r;
     uint16_t *out = (uint16_t *)p.out + row * width + c;
     if constexpr (O == to::kSwiglu) {
         if (p.out2) {
-            put(p.out2 + row * p.n + c, four(v[0]));
-            put(p.out2 + row * p.n + width + c, four(v[1]));
+            put_four(p.out2 + row * p.n + c, v[0]);
+            put_four(p.out2 + row * p.n + width + c, v[1]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[0][i] = swiglu(v[0][i], v[1][i]);
     } else if constexpr (O == to::kLinear) {
-        if (p.bias) add(v[0], p.bias + c);
-        if (p.out2) put(p.out2 + row * p.n + c, four(v[0]));
+        if (p.bias) add_four(v[0], p.bias + c);
+        if (p.out2) put_four(p.out2 + row * p.n + c, v[0]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[0][i] = activate(p.act, v[0][i]);
-        if (p.in) add(v[0], p.in + row * p.n + c);
+        if (p.in) add_four(v[0], p.in + row * p.n + c);
     }
-    put(out, four(v[0]));
+    put_four(out, v[0]);
 }
 
 #endif
@@ -210,27 +219,219 @@ hipError_t launch_by_rows(const Product &p, hipStream_t stream)
     }
 }
 
+// ---- dgrad ----
+
+constexpr int kGradCols = 64;      // columns of a workgroup
+
+template <int MT> inline constexpr int kSlot = 4096 + MT * 1024;    // 32 rows of weights, 32 values of the rows
+template <int MT> inline constexpr int kRing = MT == 4 ? 2 : 3;     // slots of a wavefront
+
+#if defined(__HIP_DEVICE_COMPILE__)
+
+template <int N>
+__device__ __forceinline__ void wait_loaded()  // all but the wavefront's last N loads
+{
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));    // vmcnt(N)
+    asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ void wait_read()    // the wavefront's LDS reads
+{
+    __builtin_amdgcn_s_waitcnt(0xC07F);        // lgkmcnt(0)
+    asm volatile("" ::: "memory");
+}
+
+// In a slot, the 32-byte segment c of weight row r's four is at place c ^ (((r >> 1) & 1) | ((r >> 2) &
+// 2)), and 16-byte chunk c of row r's four at place c ^ ((r >> 2) & 3): the lanes that LDS serves
+// together then touch all banks.
+template <int O, int MT>
+__device__ __forceinline__ void few_dgrad_rows(const Group &g, uint8_t *lds)
+{
+    const auto &p = argument();
+    const int lane = lane_now(), wave = uniform(threadIdx.x / kWave), i16 = lane & 15, quarter = lane >> 4;
+    const int c0 = blockIdx.x * kGradCols;
+    const int steps = (p.k + kStep - 1) / kStep, per = (steps + kWaves - 1) / kWaves;
+    const int s0 = wave * per, s1 = min(s0 + per, steps);
+    const i32x4 wb = buffer(p.w + (size_t)g.e * p.n * p.k + c0, ((int64_t)p.n * p.k - c0) * 2);
+    const i32x4 xb = buffer(p.x + (size_t)g.row0 * p.k, (int64_t)g.n * p.k * 2);
+    uint32_t w_off[2];
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+        w_off[v] = (uint32_t)(lane >> 3) * p.n * 2 + (((lane & 7) ^ ((((lane >> 4) & 1) | v * 2) << 1)) << 4);
+    const int chunk = (lane & 3) ^ quarter;
+    const uint32_t x_off = ((uint32_t)(lane >> 2) * p.k + chunk * 8) * 2;
+    uint8_t *ring = lds + wave * (kRing<MT> * kSlot<MT>);
+    // the loads of a step; beyond the wavefront's last one they give 0 as well
+    auto load = [&](int slot, int s) {
+        const bool some = s < s1;
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+            load_lds(wb, ring + slot * kSlot<MT> + v * 1024, some ? w_off[v & 1] : kNone,
+                     some ? (uint32_t)(s * kStep + v * 8) * p.n * 2 : 0u);
+        const uint32_t off = some && s * kStep + chunk * 8 < p.k ? x_off : kNone;
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+            load_lds(xb, ring + slot * kSlot<MT> + 4096 + t * 1024, off + t * 16 * p.k * 2,
+                     some ? (uint32_t)s * (kStep * 2) : 0u);
+    };
+    constexpr int kLoads = 4 + MT;
+    const uint32_t base = (uint32_t)(uintptr_t)(LdsBytes)ring;
+    const uint32_t w_at = base + (quarter * 8 + (i16 >> 2)) * 128 + (((i16 >> 3) | ((quarter & 1) << 1)) << 5) +
+                          (i16 & 3) * 8;
+    const uint32_t x_at = base + 4096 + i16 * 64 + ((quarter ^ (i16 >> 2)) << 4);
+
+    f32x4 acc[4][MT] = {};
+#pragma unroll
+    for (int i = 0; i < kRing<MT>; ++i) load(i, s0 + i);
+    int slot = 0;
+    for (int s = s0; s < s1; ++s) {
+        wait_loaded<(kRing<MT> - 1) * kLoads>();
+        bf16x8 wf[4], xf[MT];
+        const uint32_t from = slot * kSlot<MT>;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t at = (w_at ^ (c << 5)) + from;
+            wf[c] = read_transposed(at, at + 512);
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t) xf[t] = *(LdsRows)(uintptr_t)(x_at + from + t * 1024);
+        wait_read();
+        load(slot, s + kRing<MT>);
+        slot = slot + 1 == kRing<MT> ? 0 : slot + 1;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+                acc[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[c], xf[t], acc[c][t], 0, 0, 0);
+    }
+    wait_loaded<0>();                          // the rings are free
+    __syncthreads();
+    f32x4 *meet = reinterpret_cast<f32x4 *>(lds);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) meet[((wave * 4 + c) * MT + t) * kWave + lane] = acc[c][t];
+    __syncthreads();
+    // a lane's four sums are columns quarter * 4 .. of row lane & 15
+    for (int q = wave; q < 4 * MT; q += kWaves) {
+        const int r = (q % MT) * 16 + i16, c = c0 + (q / MT) * 16 + quarter * 4;
+        f32x4 v = meet[q * kWave + lane];
+#pragma unroll
+        for (int i = 1; i < kWaves; ++i) v += meet[(i * 4 * MT + q) * kWave + lane];
+        if (r >= g.n || c >= p.n) continue;
+        const size_t row = (size_t)g.row0 + r;
+        if constexpr (O == to::kBf16) {
+            put_four((uint16_t *)p.out + row * p.n + c, v);
+        } else {
+            const uint16_t *gu = p.in + row * p.n * 2 + c;
+            uint16_t *out = (uint16_t *)p.out + row * p.n * 2 + c;
+            f32x4 gate{}, up{}, dg, du;
+            add_four(gate, gu);
+            add_four(up, gu + p.n);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float s = sigmoid(gate[i]);
+                du[i] = v[i] * (gate[i] * s);
+                dg[i] = v[i] * up[i] * (s * __builtin_fmaf(gate[i], 1.0f - s, 1.0f));
+            }
+            put_four(out, dg);
+            put_four(out + p.n, du);
+        }
+    }
+}
+
+#endif
+
+template <int O, int MT>
+__global__ __launch_bounds__(kThreads) void few_dgrad_kernel(Product p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kWaves * kRing<MT> * kSlot<MT>];
+    static_assert(sizeof(lds) >= kWaves * 4 * MT * kWave * sizeof(f32x4), "the sums' meeting place");
+    constexpr int kSize = kCols * MT;
+    for (int group = blockIdx.y;; group += gridDim.y) {
+        Group g;
+        if (p.count) g = find_group(group, kSize);
+        else g = Group{0, group * kSize, min(p.C - group * kSize, kSize), (p.C + kSize - 1) / kSize};
+        if (group >= g.of) break;
+        few_dgrad_rows<O, MT>(g, lds);
+        if (group + (int)gridDim.y >= g.of) break;
+        __syncthreads();                       // the meeting place is free again
+    }
+#else
+    (void)p;
+#endif
+}
+
+template <int O, int MT>
+hipError_t launch_dgrad(const Product &p, hipStream_t stream)
+{
+    const int size = kCols * MT;
+    const int groups = p.count ? p.pairs / size + (p.pairs < p.E ? p.pairs : p.E) : (p.C + size - 1) / size;
+    return launch(few_dgrad_kernel<O, MT>, dim3((p.n + kGradCols - 1) / kGradCols, std::min(groups, kMostGroups)),
+                  dim3(kThreads), 0, stream, p);
+}
+
+template <int O>
+hipError_t launch_dgrad_by_rows(const Product &p, hipStream_t stream)
+{
+    switch (row_tiles(p)) {
+    case 1: return launch_dgrad<O, 1>(p, stream);
+    case 2: return launch_dgrad<O, 2>(p, stream);
+    default: return launch_dgrad<O, 4>(p, stream);
+    }
+}
+
 }  // namespace
 
-// Both kernels' times in microseconds, from what they read, for rows spread evenly over the experts.
-// Tiles: a block of 64 of the sum takes 0.65 for 64 rows, a round of 256 workgroups at a time, and the
-// weights come at 4.9 TB/s. Few rows: every workgroup reads its weights and its rows, at 7.3 TB/s
-// together, and costs 0.0025. Measured (tiles, few rows): one matrix of 4096 x 4096, 1 row 42, 9, 64
-// rows 43, 24, 96 rows 43, 40, 128 rows 43, 46; 1024 x 2048, 256 rows 25, 12; 16384 x 4096, 16 rows 62,
-// 39, 64 rows 64, 94; 128 experts of 1536 x 2048, 8 rows 25, 12, 64 rows 80, 68, 256 rows 157, 149,
-// 1024 rows 180, 213; of 2048 x 768, 8 rows 13, 9, 32 rows 20, 27; 16 of 4096 x 4096, 32 rows 109, 73.
+// Experts that rows spread evenly over them reach.
+static double experts_reached(const Product &p)
+{
+    return p.count ? p.E * (1.0 - std::pow(1.0 - 1.0 / p.E, p.pairs)) : 1.0;
+}
+
+// The tiles' time in microseconds: a block of 64 of the sum takes 0.65 for 64 rows, a round of 256
+// workgroups at a time, and the weights come at `rate` MB/us.
+static double tiles_time(const Product &p, double experts, double rate)
+{
+    const double mean = p.pairs / experts;
+    const double rounds = std::ceil(experts * std::ceil(mean / 64) * std::ceil(p.n / 256.0) / 256);
+    return std::max(8.0 + rounds * std::ceil(p.k / 64.0) * 0.65, 4.0 + experts * p.n * p.k * 2e-6 / rate);
+}
+
+// Both kernels' times, from what they read, for rows spread evenly over the experts. Few rows: every
+// workgroup reads its weights and its rows, at 7.3 TB/s together, and costs 0.0025. Measured (tiles, few
+// rows): one matrix of 4096 x 4096, 1 row 42, 9, 64 rows 43, 24, 96 rows 43, 40, 128 rows 43, 46;
+// 1024 x 2048, 256 rows 25, 12; 16384 x 4096, 16 rows 62, 39, 64 rows 64, 94; 128 experts of 1536 x 2048,
+// 8 rows 25, 12, 64 rows 80, 68, 256 rows 157, 149, 1024 rows 180, 213; of 2048 x 768, 8 rows 13, 9, 32
+// rows 20, 27; 16 of 4096 x 4096, 32 rows 109, 73.
 bool few_rows(const Product &p, bool swiglu)
 {
-    const double experts = p.count ? p.E * (1.0 - std::pow(1.0 - 1.0 / p.E, p.pairs)) : 1.0;
-    const double mean = p.pairs / experts, k = p.k;
-    const int size = kCols * row_tiles(p);
-    const double weights = experts * p.n * k * 2.0;
-    const double rounds = std::ceil(experts * std::ceil(mean / 64) * std::ceil(p.n / 256.0) / 256);
-    const double tiles = std::max(8.0 + rounds * std::ceil(k / 64) * 0.65, 4.0 + weights / 4.9e6);
-    const double groups = std::ceil(mean / size), columns = std::ceil(p.n / 16.0) / (swiglu ? 2 : 1);
-    const double few = 8.0 + (groups * weights + columns * p.pairs * k * 2.0) / 7.3e6 +
+    const double experts = experts_reached(p), mean = p.pairs / experts, k = p.k;
+    const double groups = std::ceil(mean / (kCols * row_tiles(p)));
+    const double columns = std::ceil(p.n / 16.0) / (swiglu ? 2 : 1);
+    const double few = 8.0 + (groups * experts * p.n * k * 2.0 + columns * p.pairs * k * 2.0) / 7.3e6 +
                        experts * groups * columns * 0.0025;
-    return few < tiles;
+    return few < tiles_time(p, experts, 4.9);
+}
+
+// Both kernels' times again. Few rows: a workgroup a CU, that costs 1.7 and whose row of weights takes 2.2,
+// 2.7 or 3.6 ns for 16, 32 or 64 rows of the expert's; the weights come at 5.0 TB/s (tiles 5.2), and at 10
+// for an expert's next rows. Measured (tiles, few rows), sum x columns: 4096 x 4096, 1 row 47, 11, 64 rows
+// 48, 20, 512 rows 50, 39, 1024 rows 56, 74; 1024 x 2048, 512 rows 18, 10, 2048 rows 21, 30; 16384 x 4096,
+// 1 row 169, 36, 512 rows 173, 121, 1024 rows 184, 238; 8 experts of 4096 x 7168, 1 row 48, 15, 8 rows 50,
+// 78; 128 of 1536 x 2048, 8 rows 22, 11, 32 rows 33, 35, 256 rows 124, 150; of 2048 x 768, 32 rows 28, 20,
+// 128 rows 43, 43.
+bool few_dgrad(const Product &p)
+{
+    const double experts = experts_reached(p), mean = p.pairs / experts;
+    const int tiles = row_tiles(p);
+    const double groups = std::ceil(mean / (kCols * tiles));
+    const double rounds = std::ceil(experts * groups * std::ceil(p.n / (double)kGradCols) / 256);
+    const double row = tiles == 1 ? 0.0022 : tiles == 2 ? 0.0027 : 0.0036;
+    const double few = std::max(6.3 + rounds * (1.7 + p.k * row),
+                                4.0 + experts * p.n * p.k * 2e-6 * (1 / 5.0 + (groups - 1) / 10.0));
+    return few < tiles_time(p, experts, 5.2);
 }
 
 hipError_t launch_few_gemm(const Product &p, hipStream_t stream)
@@ -246,6 +447,12 @@ hipError_t launch_few_swiglu(const Product &p, hipStream_t stream)
 hipError_t launch_few_linear(const Product &p, hipStream_t stream)
 {
     return launch_by_rows<to::kLinear>(p, stream);
+}
+
+hipError_t launch_few_dgrad(const Product &p, bool swiglu, hipStream_t stream)
+{
+    return swiglu ? launch_dgrad_by_rows<to::kSwigluGrad>(p, stream)
+                  : launch_dgrad_by_rows<to::kBf16>(p, stream);
 }
 
 }  // namespace ep

@@ -204,6 +204,30 @@ def test_few_rows(mean, E, A):
     check_swiglu(x, 264, 72, keep=False)
 
 
+@pytest.mark.parametrize("mean,E", [(1, 9), (20, 4), (50, 3)])
+@pytest.mark.parametrize("A", [0, 8])
+def test_few_rows_dgrad(mean, E, A):
+    """The same of the gradient of the rows: sums that end inside a step, shorter than the eight
+    wavefronts' steps, as long as a ring of them and much longer; columns that end inside a workgroup's."""
+    x = Experts([mean] * (E - 2) + [0, 2 * mean], A=A, seed=mean)
+    for H, N in ((8, 8), (72, 24), (200, 264), (136, 1032), (64, 2056)):
+        check_dgrad(x, H, N)
+        assert all("few_dgrad_kernel" in k for k in kernels()), kernels()
+        check_swiglu_dgrad(x, N, H)
+        assert all("few_dgrad_kernel" in k for k in kernels()), kernels()
+    check_swiglu_dgrad(x, 136, 72, in_place=True)
+
+
+@pytest.mark.parametrize("H,N", [(8, 8), (264, 256), (72, 136), (200, 264), (136, 520), (328, 72)])
+def test_dgrad_of_tiles(H, N):
+    rng = np.random.default_rng(H)
+    x = Experts([int(v) for v in rng.integers(100, 500, 200)], A=8, seed=H + N)
+    check_dgrad(x, H, N)
+    assert all("product_kernel" in k for k in kernels()), kernels()
+    check_swiglu_dgrad(x, N, H, in_place=H == 200)
+    assert all("product_kernel" in k for k in kernels()), kernels()
+
+
 @pytest.mark.parametrize("pairs", [1, 10 ** 6])
 def test_pairs_do_not_choose_the_rows(pairs):
     """Every row is computed whatever number of pairs the call is told."""
