@@ -20,6 +20,15 @@
 // A block is four phases of a quarter of its products. In each a wavefront reads from LDS what the next
 // phase needs and starts loading one of the four halves of the block after the next into the place of
 // one that all have read: so the loads are spread evenly, and every one has six phases to arrive.
+//
+// 65536 rows x 4096 x 4096: a meeting of the wavefronts a block 1.86 ms, four phases 1.79, outputs stored
+// 64 bytes of a row together, which no later load waits for, 1.66, one stream of loads through tiles of
+// different heights 1.62 (1.36 PFLOP/s; matrix units 77% busy at the 1.6-1.75 GHz that the load leaves).
+// With short sums (768 to 2048) and about 340 rows an expert it is the outputs' stores and the operands'
+// way from L2 to LDS (9-12 TB/s) that bound it: cutting a last round's tiles and groups of about 8 row
+// tiles took 4096 tokens' gate and up products from 275 to 259 us and their down gradients from 308 to 286.
+// Blocks of 32 in four stages (64 bytes of a row, twice the L2 requests), other cache policies of loads or
+// stores (0-15% slower), groups of 4 or 16, a raised wave priority: slower or no gain.
 #include "ep_product.h"
 
 #include <type_traits>
@@ -64,12 +73,14 @@ __device__ __forceinline__ void rows_of(const Product &p, int e, int &base, int 
     }
 }
 
-__device__ __forceinline__ int tiles_of(int n) { return (n + kTile - 1) / kTile; }
+__device__ __forceinline__ int tiles_of(int n) { return ((uint32_t)n + kTile - 1) / kTile; }
 
-// First part of tile i of an expert with n rows: its parts spread evenly over its tiles.
+// First part of tile i of an expert with n rows: its parts spread evenly over its tiles, the larger ones
+// first.
 __device__ __forceinline__ int first_part(int n, int i)
 {
-    return i * ((n + kPart - 1) / kPart) / max(tiles_of(n), 1);
+    const int parts = ((uint32_t)n + kPart - 1) / kPart, tiles = max(tiles_of(n), 1), each = parts / tiles;
+    return i * each + min(i, parts - tiles * each);
 }
 
 __device__ __forceinline__ int build_table(TileTable &t, const Product &p)
@@ -138,7 +149,7 @@ __device__ __forceinline__ Tile locate(const TileTable &t, const Product &p, int
     const int m_tile = group * size + at - r.nblk * in_group;
     const int first = first_part(n_e, m_tile) * kPart;
     r.row0 = t.base[lo] + first;
-    r.n = r.rows = min(first_part(n_e, m_tile + 1) * kPart, n_e) - first;
+    r.n = r.rows = min((uint32_t)first_part(n_e, m_tile + 1) * kPart, (uint32_t)n_e) - first;
     r.m0 = 0;
     return r;
 }
@@ -259,7 +270,7 @@ struct Stream {
     }
     __device__ __forceinline__ int blocks_of(const Tile &t) const
     {
-        return F == form::kWgrad ? max((t.n + kBlock - 1) / kBlock, 1) : (p.k + kBlock - 1) / kBlock;
+        return F == form::kWgrad ? max((int)(((uint32_t)t.n + kBlock - 1) / kBlock), 1) : (p.k + kBlock - 1) / kBlock;
     }
     __device__ __forceinline__ void enter(int i)
     {

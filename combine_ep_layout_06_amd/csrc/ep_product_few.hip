@@ -26,6 +26,11 @@ constexpr int kMostGroups = 32768; // workgroups of a column; they take more gro
 
 namespace to { constexpr int kBf16 = 0, kSwiglu = 1, kLinear = 2, kSwigluGrad = 3; }
 
+__host__ __device__ __forceinline__ int groups_of(int rows, int size)
+{
+    return ((uint32_t)rows + size - 1) / size;
+}
+
 #if defined(__HIP_DEVICE_COMPILE__)
 
 constexpr int kWaves = kThreads / kWave;
@@ -51,7 +56,7 @@ __device__ __forceinline__ Group find_group(int group, int size)
     for (int i = 0; i < kPer; ++i) {
         base[i] = n[i] = 0;
         if (e0 + i < p.E) expert_rows(p.count, p.offset, e0 + i, p.C, p.rows, base[i], n[i]);
-        sum += (n[i] + size - 1) / size;
+        sum += groups_of(n[i], size);
     }
     const int incl = wave_inclusive_sum(sum);
     if (lane == kWave - 1) wave_sum[wave] = incl;
@@ -64,7 +69,7 @@ __device__ __forceinline__ Group find_group(int group, int size)
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int groups = (n[i] + size - 1) / size;
+        const int groups = groups_of(n[i], size);
         if (at >= 0 && at < groups) found = Group{e0 + i, base[i] + at * size, min(n[i] - at * size, size), of};
         at -= groups;
     }
@@ -181,7 +186,7 @@ __global__ __launch_bounds__(kThreads) void few_rows_kernel(Product p)
     for (int group = blockIdx.y;; group += gridDim.y) {
         Group g;
         if (p.count) g = find_group(group, kSize);
-        else g = Group{0, group * kSize, min(p.C - group * kSize, kSize), (p.C + kSize - 1) / kSize};
+        else g = Group{0, group * kSize, min(p.C - group * kSize, kSize), groups_of(p.C, kSize)};
         if (group >= g.of) break;
         few_rows<O, MT>(g, sh);
         if (group + (int)gridDim.y >= g.of) break;
@@ -196,7 +201,7 @@ template <int O, int MT>
 hipError_t launch_few(const Product &p, hipStream_t stream)
 {
     const int width = O == to::kSwiglu ? p.n / 2 : p.n, size = kCols * MT;
-    const int groups = p.count ? p.pairs / size + (p.pairs < p.E ? p.pairs : p.E) : (p.C + size - 1) / size;
+    const int groups = p.count ? p.pairs / size + (p.pairs < p.E ? p.pairs : p.E) : groups_of(p.C, size);
     return launch(few_rows_kernel<O, MT>, dim3((width + kCols - 1) / kCols, std::min(groups, kMostGroups)),
                   dim3(kThreads), 0, stream, p);
 }
@@ -352,7 +357,7 @@ __global__ __launch_bounds__(kThreads) void few_dgrad_kernel(Product p)
     for (int group = blockIdx.y;; group += gridDim.y) {
         Group g;
         if (p.count) g = find_group(group, kSize);
-        else g = Group{0, group * kSize, min(p.C - group * kSize, kSize), (p.C + kSize - 1) / kSize};
+        else g = Group{0, group * kSize, min(p.C - group * kSize, kSize), groups_of(p.C, kSize)};
         if (group >= g.of) break;
         few_dgrad_rows<O, MT>(g, lds);
         if (group + (int)gridDim.y >= g.of) break;
@@ -367,7 +372,7 @@ template <int O, int MT>
 hipError_t launch_dgrad(const Product &p, hipStream_t stream)
 {
     const int size = kCols * MT;
-    const int groups = p.count ? p.pairs / size + (p.pairs < p.E ? p.pairs : p.E) : (p.C + size - 1) / size;
+    const int groups = p.count ? p.pairs / size + (p.pairs < p.E ? p.pairs : p.E) : groups_of(p.C, size);
     return launch(few_dgrad_kernel<O, MT>, dim3((p.n + kGradCols - 1) / kGradCols, std::min(groups, kMostGroups)),
                   dim3(kThreads), 0, stream, p);
 }

@@ -402,6 +402,24 @@ def test_more_tiles_than_one_list():
     assert (dw[empty] == 0).all()
 
 
+def test_tiles_beyond_2_15():
+    """An expert of so many tiles that a tile's number times the parts of 64 rows passes 2^31."""
+    T = 12_000_001
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+    x = torch.randn(1, T, 8, generator=g, device=DEV).to(torch.bfloat16)
+    w = torch.randn(1, 8, 8, generator=g, device=DEV).to(torch.bfloat16)
+    count = torch.tensor([T - 70], dtype=torch.int32, device=DEV)
+    for fn, wide in ((B.ep_expert_gemm, w[0].double().T), (B.ep_expert_gemm_dgrad, w[0].double())):
+        out = torch.full((1, T, 8), SENTINEL, dtype=torch.int16, device=DEV)
+        print("[many tiles]", fn.__name__, flush=True)
+        fn(x, count, w, T, **{"y" if fn is B.ep_expert_gemm else "dx": out})
+        assert all("product_kernel" in k for k in kernels()), kernels()
+        want, err = P.product64(x[0, :T - 70].double(), wide)
+        close(out[0, :T - 70].view(torch.bfloat16).double(), want, P.rounded(want, err), fn.__name__)
+        assert (out[0, T - 70:] == SENTINEL).all()
+
+
 def test_long_sum():
     """A weights' gradient over rows whose bytes pass 2^31."""
     T, H, N = 280_000, 4096, 8
