@@ -36,9 +36,11 @@ def close(got, want, tol, what):
     assert not bad.any(), (what, int(bad.sum()), float((got - want).abs().max()), float(tol.max()))
 
 
-# T, H, E, K, C: one pair; odd widths; drops; K above a wavefront's pairs; rows longer than one pass
+# T, H, E, K, C: one pair; odd widths; drops; K above a wavefront's pairs; rows longer than one pass; the
+# last two with a wavefront for each pair
 COMBINE = [(1, 8, 1, 1, 1), (7, 72, 4, 3, 3), (65, 512, 16, 4, 9), (33, 1032, 128, 8, 33),
-           (5, 4104, 40, 33, 5), (129, 2056, 8, 2, 40)]
+           (5, 4104, 40, 33, 5), (129, 2056, 8, 2, 40), (1500, 264, 12, 6, 500),
+           (1100, 2056, 16, 8, 700)]
 
 
 @pytest.mark.parametrize("T,H,E,K,C", COMBINE)
