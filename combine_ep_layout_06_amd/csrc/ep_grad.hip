@@ -20,8 +20,9 @@ __device__ __forceinline__ u32x4 pack8(const float (&v)[8])
 // Combine's gradient: out[t] = sum_j w[t][j] y[row(t, j)] gives
 //   dy[row] = bf16(w[t][j] * dout[t]),  dw[t][j] = sum_h dout[t][h] y[row][h]
 // W wavefronts per pair: one where there are pairs enough for every CU, else the workgroup's four
-// (129 tokens, top-8, H = 2056: 10.9 -> 10.1 us, most of it the launch). A lane has kChunks 16-byte
-// chunks of both rows in flight. 4096 tokens, top-8, H = 2048: 57 us, the rate of a copy (4.9 TB/s).
+// (129 tokens, top-8, H = 2056: 10.9 -> 10.1 us with the launch). A lane has kChunks 16-byte chunks of
+// both rows in flight (one: 57 us). 4096 tokens, top-8, H = 2048: 49 us, bound by its bytes (268 MB, half
+// of them written: 5.6 TB/s, a copy has 4.7).
 constexpr int kChunks = 4;
 constexpr int kManyPairs = 8192;   // 8 wavefronts for each SIMD
 
@@ -78,31 +79,34 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(
     if (wave % W == 0 && lane == 0) dw[i] = sum;
 }
 
-// dz = bf16(dout * act'(z)) and, per kGradRows rows, the columns' sums of the unrounded dz.
+// dz = bf16(dout * act'(z)) and, per kGradRows rows, the columns' sums of the unrounded dz: bound by its
+// bytes, kGradAtOnce rows of both in flight. 4096 x 4096, silu: 256 threads 31 us, 512 28 (3.6 TB/s). dz is rounded because it
+// is the matrix instruction's operand twice.
 constexpr int kGradRows = kLinearGradRows;
+constexpr int kGradThreads = 512, kGradWaves = kGradThreads / kWave;
 constexpr int kGradAtOnce = 4;     // rows of a wavefront in flight
 
-__global__ __launch_bounds__(kThreads) void act_grad_kernel(
+__global__ __launch_bounds__(kGradThreads) void act_grad_kernel(
     const uint16_t *__restrict__ dout, const uint16_t *__restrict__ z, uint16_t *__restrict__ dz,
     float *__restrict__ part, int T, int N, int act)
 {
-    __shared__ float sums[kWaves][kWave][9];
+    __shared__ float sums[kGradWaves][kWave][9];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int c = (blockIdx.x * kWave + lane) * 8;
     float sum[8] = {};
     if (c < N) {
         const int first = blockIdx.y * kGradRows + wave, end = min((int)(blockIdx.y + 1) * kGradRows, T);
-        for (int t0 = first; t0 < end; t0 += kGradAtOnce * kWaves) {
+        for (int t0 = first; t0 < end; t0 += kGradAtOnce * kGradWaves) {
             u32x4 d[kGradAtOnce], v[kGradAtOnce];
 #pragma unroll
             for (int i = 0; i < kGradAtOnce; ++i) {    // a row that is not there: the last one again
-                const size_t at = (size_t)min(t0 + i * kWaves, end - 1) * N + c;
+                const size_t at = (size_t)min(t0 + i * kGradWaves, end - 1) * N + c;
                 d[i] = *reinterpret_cast<const u32x4 *>(dout + at);
                 if (act != EP_ACT_NONE) v[i] = *reinterpret_cast<const u32x4 *>(z + at);
             }
 #pragma unroll
             for (int i = 0; i < kGradAtOnce; ++i) {
-                const int t = t0 + i * kWaves;
+                const int t = t0 + i * kGradWaves;
                 if (t >= end) break;
                 float g[8];
                 unpack8(d[i], g);
@@ -121,18 +125,19 @@ __global__ __launch_bounds__(kThreads) void act_grad_kernel(
 #pragma unroll
     for (int k = 0; k < 8; ++k) sums[wave][lane][k] = sum[k];
     __syncthreads();
-    for (int i = threadIdx.x; i < kWave * 8; i += kThreads) {
+    for (int i = threadIdx.x; i < kWave * 8; i += kGradThreads) {
         const int col = blockIdx.x * kWave * 8 + i;
         if (col < N) {
             float s = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) s += sums[w][i >> 3][i & 7];
+            for (int w = 0; w < kGradWaves; ++w) s += sums[w][i >> 3][i & 7];
             part[(size_t)blockIdx.y * N + col] = s;
         }
     }
 }
 
-// The sums of the workgroups' sums: 64 columns a workgroup, a quarter of the rows a wavefront.
+// The sums of the workgroups' sums: 64 columns a workgroup, a quarter of the rows a wavefront (a column's
+// sums one after the other in one lane took 20 us for 4096 x 4096, this 5).
 __global__ __launch_bounds__(kThreads) void bias_grad_kernel(const float *__restrict__ part,
                                                              float *__restrict__ dbias, int chunks, int N)
 {
@@ -171,7 +176,7 @@ hipError_t launch_act_grad(const uint16_t *dout, const uint16_t *z, uint16_t *dz
     const int chunks = (T + kGradRows - 1) / kGradRows;
     if (chunks > 0) {
         const hipError_t e = launch(act_grad_kernel, dim3((N / 8 + kWave - 1) / kWave, chunks),
-                                    dim3(kThreads), 0, stream, dout, z, dz, part, T, N, act);
+                                    dim3(kGradThreads), 0, stream, dout, z, dz, part, T, N, act);
         if (e != hipSuccess) return e;
     }
     return launch(bias_grad_kernel, dim3((N + kWave - 1) / kWave), dim3(kThreads), 0, stream, part, dbias,
