@@ -80,8 +80,8 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(
 }
 
 // dz = bf16(dout * act'(z)) and, per kGradRows rows, the columns' sums of the unrounded dz: bound by its
-// bytes, kGradAtOnce rows of both in flight. 4096 x 4096, silu: 256 threads 31 us, 512 28 (3.6 TB/s). dz is rounded because it
-// is the matrix instruction's operand twice.
+// bytes, kGradAtOnce rows of both in flight. 4096 x 4096, silu: 256 threads 31 us, 512 28 (3.6 TB/s). dz
+// is rounded because it is the matrix instruction's operand twice.
 constexpr int kGradRows = kLinearGradRows;
 constexpr int kGradThreads = 512, kGradWaves = kGradThreads / kWave;
 constexpr int kGradAtOnce = 4;     // rows of a wavefront in flight

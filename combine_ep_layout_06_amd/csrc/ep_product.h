@@ -44,6 +44,9 @@ hipError_t launch_few_swiglu(const Product &p, hipStream_t stream);
 hipError_t launch_few_linear(const Product &p, hipStream_t stream);
 bool few_dgrad(const Product &p);
 hipError_t launch_few_dgrad(const Product &p, bool swiglu, hipStream_t stream);
+// And whether a weights' gradient is one of few tiles and long sums.
+bool few_wgrad(const Product &p);
+hipError_t launch_few_wgrad(const Product &p, bool f32, hipStream_t stream);
 
 hipError_t launch_combine_grad(const ep_shape_t &s, const uint16_t *dout, const uint16_t *y,
                                const int32_t *idx, const int32_t *slot, const float *w, uint16_t *dy,

@@ -766,6 +766,7 @@ hipError_t launch_expert_swiglu_dgrad(const Product &p, hipStream_t stream)
 
 hipError_t launch_expert_wgrad(const Product &p, bool f32, hipStream_t stream)
 {
+    if (few_wgrad(p)) return launch_few_wgrad(p, f32, stream);
     return f32 ? launch_product<form::kWgrad, to::kF32>(p, stream)
                : launch_product<form::kWgrad, to::kBf16>(p, stream);
 }

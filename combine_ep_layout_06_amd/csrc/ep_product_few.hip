@@ -1,5 +1,5 @@
-// The products for few rows on gfx950 (a decode step, one token), forward and dgrad: bound by reading the
-// weights once, and by how soon enough of the read is under way.
+// The products for few rows on gfx950 (a decode step, one token), forward and dgrad, bound by reading the
+// weights once, and by how soon enough of the read is under way; and weights' gradients with a long sum.
 //
 // A workgroup takes 16 columns of the output (SwiGLU: the same 16 gate and 16 up columns) for up to
 // 16 * MT rows of one expert, its 8 wavefronts an eighth of the sum each: so also a narrow product has
@@ -11,6 +11,9 @@
 // each wavefront loads 32 rows of them (128 bytes a row) at a time straight into a ring of LDS of its
 // own, from which the transposing read gives the matrix instruction its operand: 64 rows x 4096 x 4096
 // 48 -> 20 us, one row 47 -> 11 (the weights at 4.74 TB/s: 7).
+//
+// A weights' gradient whose few tiles have a long sum is made in squares of 64 x 64 in the same way, the
+// rows dealt out to the eight wavefronts: 8192 rows, 1024 x 1024 93 -> 35 us, 64 x 64 89 -> 22.
 #include "ep_product.h"
 
 #include <algorithm>
@@ -24,7 +27,7 @@ constexpr int kThreads = 512;
 constexpr int kCols = 16;          // columns of a workgroup
 constexpr int kMostGroups = 32768; // workgroups of a column; they take more groups in turn
 
-namespace to { constexpr int kBf16 = 0, kSwiglu = 1, kLinear = 2, kSwigluGrad = 3; }
+namespace to { constexpr int kBf16 = 0, kSwiglu = 1, kLinear = 2, kSwigluGrad = 3, kF32 = 4; }
 
 __host__ __device__ __forceinline__ int groups_of(int rows, int size)
 {
@@ -387,6 +390,103 @@ hipError_t launch_dgrad_by_rows(const Product &p, hipStream_t stream)
     }
 }
 
+// ---- wgrad of few columns and rows, with a long sum ----
+
+// 64 x 64 of an expert's output a workgroup, its rows dealt out to the eight wavefronts; both operands
+// lie in LDS as dgrad's weights do.
+template <int O>
+__global__ __launch_bounds__(kThreads) void few_wgrad_kernel(Product p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int kSumSlot = 8192;             // 32 rows of both operands, 64 columns of each
+    constexpr int kSumRing = 2;                // slots of a wavefront
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kWaves * kSumRing * kSumSlot];
+    static_assert(sizeof(lds) >= kWaves * 16 * kWave * sizeof(f32x4), "the sums' meeting place");
+    const int lane = lane_now(), wave = uniform(threadIdx.x / kWave), i16 = lane & 15, quarter = lane >> 4;
+    const int across = (p.n + kGradCols - 1) / kGradCols, down = (p.m + kGradCols - 1) / kGradCols;
+    const int e = blockIdx.x / (across * down), at = blockIdx.x - e * across * down;
+    const int m0 = at / across * kGradCols, c0 = (at - at / across * across) * kGradCols;
+    int base = 0, n = 0;
+    if (p.pairs > 0) {
+        if (p.count) expert_rows(p.count, p.offset, e, p.C, p.rows, base, n);
+        else n = p.C;
+    }
+    base = uniform(base);
+    n = uniform(n);
+    const int steps = ((uint32_t)n + kStep - 1) / kStep, per = (steps + kWaves - 1) / kWaves;
+    const int s0 = wave * per, s1 = min(s0 + per, steps);
+    uint32_t x_off[2], w_off[2];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        const int chunk = (lane & 7) ^ ((((lane >> 4) & 1) | v * 2) << 1);
+        x_off[v] = (uint32_t)(lane >> 3) * p.m * 2 + (chunk << 4);
+        w_off[v] = (uint32_t)(lane >> 3) * p.n * 2 + (chunk << 4);
+    }
+    uint8_t *ring = lds + wave * (kSumRing * kSumSlot);
+    // the loads of a step; past the expert's rows and the wavefront's last step they give 0
+    auto load = [&](int slot, int s) {
+        const int left = s < s1 ? n - s * kStep : 0;
+        const size_t row = (size_t)base + (left > 0 ? s * kStep : 0);
+        const i32x4 xb = buffer(p.x + row * p.m + m0, ((int64_t)left * p.m - m0) * 2);
+        const i32x4 wb = buffer(p.w + row * p.n + c0, ((int64_t)left * p.n - c0) * 2);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            load_lds(wb, ring + slot * kSumSlot + v * 1024, w_off[v & 1], (uint32_t)v * 16 * p.n);
+            load_lds(xb, ring + slot * kSumSlot + 4096 + v * 1024, x_off[v & 1], (uint32_t)v * 16 * p.m);
+        }
+    };
+    const uint32_t at0 = (uint32_t)(uintptr_t)(LdsBytes)ring + (quarter * 8 + (i16 >> 2)) * 128 +
+                         (((i16 >> 3) | ((quarter & 1) << 1)) << 5) + (i16 & 3) * 8;
+
+    f32x4 acc[4][4] = {};
+#pragma unroll
+    for (int i = 0; i < kSumRing; ++i) load(i, s0 + i);
+    int slot = 0;
+    for (int s = s0; s < s1; ++s) {
+        wait_loaded<(kSumRing - 1) * 8>();
+        bf16x8 wf[4], xf[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t from = (at0 ^ (c << 5)) + slot * kSumSlot;
+            wf[c] = read_transposed(from, from + 512);
+            xf[c] = read_transposed(from + 4096, from + 4096 + 512);
+        }
+        wait_read();
+        load(slot, s + kSumRing);
+        slot ^= 1;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                acc[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[c], xf[t], acc[c][t], 0, 0, 0);
+    }
+    wait_loaded<0>();                          // the rings are free
+    __syncthreads();
+    f32x4 *meet = reinterpret_cast<f32x4 *>(lds);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) meet[(wave * 16 + c * 4 + t) * kWave + lane] = acc[c][t];
+    __syncthreads();
+    for (int q = wave; q < 16; q += kWaves) {
+        const int r = m0 + (q & 3) * 16 + i16, c = c0 + (q >> 2) * 16 + quarter * 4;
+        f32x4 v = meet[q * kWave + lane];
+#pragma unroll
+        for (int i = 1; i < kWaves; ++i) v += meet[(i * 16 + q) * kWave + lane];
+        if (r >= p.m || c >= p.n) continue;
+        const size_t to = ((size_t)e * p.m + r) * p.n + c;
+        if constexpr (O == to::kBf16) {
+            put_four((uint16_t *)p.out + to, v);
+        } else {
+            f32x4 *out = reinterpret_cast<f32x4 *>((float *)p.out + to);
+            *out = p.accumulate ? *out + v : v;
+        }
+    }
+#else
+    (void)p;
+#endif
+}
+
 }  // namespace
 
 // Experts that rows spread evenly over them reach.
@@ -439,6 +539,22 @@ bool few_dgrad(const Product &p)
     return few < tiles_time(p, experts, 5.2);
 }
 
+static int64_t wgrad_squares(const Product &p)
+{
+    const int64_t across = (p.n + kGradCols - 1) / kGradCols, down = (p.m + kGradCols - 1) / kGradCols;
+    return p.E * across * down;
+}
+
+// The long sums: at most a square for each CU, and rows enough that the tiles' one wavefront a sum takes
+// longer. Measured (tiles, squares), experts of rows x columns, rows of an expert: one of 64 x 64, 512 10,
+// 10, 8192 89, 22; of 1024 x 1024 (256 squares), 512 12, 9, 4096 50, 20, 32768 352, 132; 8 of 256 x 512
+// (256), 256 10, 14, 512 12, 12, 1024 18, 11, 4096 50, 29; with two squares a CU, one of 2048 x 1024, 4096
+// 50, 38, of 4096 x 512 50, 59.
+bool few_wgrad(const Product &p)
+{
+    return wgrad_squares(p) <= 256 && p.pairs / p.E >= 512;
+}
+
 hipError_t launch_few_gemm(const Product &p, hipStream_t stream)
 {
     return launch_by_rows<to::kBf16>(p, stream);
@@ -458,6 +574,12 @@ hipError_t launch_few_dgrad(const Product &p, bool swiglu, hipStream_t stream)
 {
     return swiglu ? launch_dgrad_by_rows<to::kSwigluGrad>(p, stream)
                   : launch_dgrad_by_rows<to::kBf16>(p, stream);
+}
+
+hipError_t launch_few_wgrad(const Product &p, bool f32, hipStream_t stream)
+{
+    return launch(f32 ? few_wgrad_kernel<to::kF32> : few_wgrad_kernel<to::kBf16>, dim3((unsigned)wgrad_squares(p)),
+                  dim3(kThreads), 0, stream, p);
 }
 
 }  // namespace ep

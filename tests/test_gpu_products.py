@@ -402,6 +402,25 @@ def test_more_tiles_than_one_list():
     assert (dw[empty] == 0).all()
 
 
+@pytest.mark.parametrize("counts,A", [([600], 0), ([2000, 0, 1500, 31], 8), ([1, 1600], 24)])
+@pytest.mark.parametrize("H,N", [(8, 8), (72, 136), (200, 264), (520, 64)])
+def test_wgrad_of_long_sums(counts, A, H, N):
+    """Weights' gradients in squares, with sums that end inside a step and experts shorter than the eight
+    wavefronts' steps or without rows."""
+    x = Experts(counts, A=A, seed=H + N)
+    for kind in ("bf16", "f32", "accumulate"):
+        check_wgrad(x, H, N, kind)
+        assert all("few_wgrad_kernel" in k for k in kernels()), kernels()
+
+
+def test_wgrad_of_tiles_with_long_sums():
+    """Sums as long in the tiles' kernel: more squares than CUs."""
+    x = Experts([2000, 0, 1500, 31], A=8, seed=21)
+    for kind in ("bf16", "f32", "accumulate"):
+        check_wgrad(x, 584, 520, kind)
+        assert all("product_kernel" in k for k in kernels()), kernels()
+
+
 def test_tiles_beyond_2_15():
     """An expert of so many tiles that a tile's number times the parts of 64 rows passes 2^31."""
     T = 12_000_001
