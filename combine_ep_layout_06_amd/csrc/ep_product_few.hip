@@ -1,5 +1,5 @@
 // The products for few rows on gfx950 (a decode step, one token), forward and dgrad, bound by reading the
-// weights once, and by how soon enough of the read is under way; and weights' gradients with a long sum.
+// weights once, and by how soon enough of the read is under way; and products of few tiles with a long sum.
 //
 // A workgroup takes 16 columns of the output (SwiGLU: the same 16 gate and 16 up columns) for up to
 // 16 * MT rows of one expert, its 8 wavefronts an eighth of the sum each: so also a narrow product has
@@ -12,8 +12,9 @@
 // own, from which the transposing read gives the matrix instruction its operand: 64 rows x 4096 x 4096
 // 48 -> 20 us, one row 47 -> 11 (the weights at 4.74 TB/s: 7).
 //
-// A weights' gradient whose few tiles have a long sum is made in squares of 64 x 64 in the same way, the
-// rows dealt out to the eight wavefronts: 8192 rows, 1024 x 1024 93 -> 35 us, 64 x 64 89 -> 22.
+// Products of more rows whose few tiles have a long sum are made in squares of 64 x 64 in the same way:
+// 1024 rows x 1024 x 4096 43 -> 24 us. And weights' gradients, the rows dealt out to the eight wavefronts:
+// 8192 rows, 1024 x 1024 93 -> 35 us, 64 x 64 89 -> 22.
 #include "ep_product.h"
 
 #include <algorithm>
@@ -95,6 +96,20 @@ __device__ __forceinline__ void add_four(f32x4 &v, const uint16_t *from)
     v += f32x4{bf16_lo(d[0]), bf16_hi(d[0]), bf16_lo(d[1]), bf16_hi(d[1])};
 }
 
+// The output's columns c .. c + 3 of a row, from their sums.
+template <int O>
+__device__ __forceinline__ void put_linear(const Product &p, size_t row, int c, f32x4 v)
+{
+    if constexpr (O == to::kLinear) {
+        if (p.bias) add_four(v, p.bias + c);
+        if (p.out2) put_four(p.out2 + row * p.n + c, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = activate(p.act, v[i]);
+        if (p.in) add_four(v, p.in + row * p.n + c);
+    }
+    put_four((uint16_t *)p.out + row * p.n + c, v);
+}
+
 template <int O, int MT>
 struct FewShared {
     f32x4 meet[kWaves][O == to::kSwiglu ? 2 : 1][MT][kWave];
@@ -160,7 +175,6 @@ __device__ __forceinline__ void few_rows(const Group &g, FewShared<O, MT> &sh)
         for (int i = 1; i < kWaves; ++i) v[m] += sh.meet[i][m][t][lane];
     }
     const size_t row = (size_t)g.row0 + r;
-    uint16_t *out = (uint16_t *)p.out + row * width + c;
     if constexpr (O == to::kSwiglu) {
         if (p.out2) {
             put_four(p.out2 + row * p.n + c, v[0]);
@@ -168,14 +182,10 @@ __device__ __forceinline__ void few_rows(const Group &g, FewShared<O, MT> &sh)
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[0][i] = swiglu(v[0][i], v[1][i]);
-    } else if constexpr (O == to::kLinear) {
-        if (p.bias) add_four(v[0], p.bias + c);
-        if (p.out2) put_four(p.out2 + row * p.n + c, v[0]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[0][i] = activate(p.act, v[0][i]);
-        if (p.in) add_four(v[0], p.in + row * p.n + c);
+        put_four((uint16_t *)p.out + row * width + c, v[0]);
+    } else {
+        put_linear<O>(p, row, c, v[0]);
     }
-    put_four(out, v[0]);
 }
 
 #endif
@@ -487,6 +497,109 @@ __global__ __launch_bounds__(kThreads) void few_wgrad_kernel(Product p)
 #endif
 }
 
+// ---- forward with more rows, few tiles and a long sum ----
+
+#if defined(__HIP_DEVICE_COMPILE__)
+
+// 64 rows x 64 columns of the output a workgroup, the sum dealt out to the eight wavefronts: 32 of it at a
+// time, 64 bytes of each row, through rings in LDS.
+template <int O>
+__device__ __forceinline__ void square(const Group &g, uint8_t *lds)
+{
+    constexpr int kSlots = 2;
+    const auto &p = argument();
+    const int lane = lane_now(), wave = uniform(threadIdx.x / kWave), i16 = lane & 15, quarter = lane >> 4;
+    const int c0 = blockIdx.x * kGradCols;
+    const int steps = (p.k + kStep - 1) / kStep, per = (steps + kWaves - 1) / kWaves;
+    const int s0 = wave * per, s1 = min(s0 + per, steps);
+    const i32x4 wb = buffer(p.w + ((size_t)g.e * p.n + c0) * p.k, (int64_t)(p.n - c0) * p.k * 2);
+    const i32x4 xb = buffer(p.x + (size_t)g.row0 * p.k, (int64_t)g.n * p.k * 2);
+    const int chunk = (lane & 3) ^ quarter;
+    const uint32_t at = ((uint32_t)(lane >> 2) * p.k + chunk * 8) * 2;
+    uint8_t *ring = lds + wave * (kSlots * 8192);
+    // the loads of a step; beyond the row's end and the wavefront's last step they give 0
+    auto load = [&](int slot, int s) {
+        const bool some = s < s1;
+        const uint32_t off = some && s * kStep + chunk * 8 < p.k ? at : kNone;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const uint32_t soff = some ? (uint32_t)t * 32 * p.k + (uint32_t)s * (kStep * 2) : 0u;
+            load_lds(wb, ring + slot * 8192 + t * 1024, off, soff);
+            load_lds(xb, ring + slot * 8192 + 4096 + t * 1024, off, soff);
+        }
+    };
+    const uint32_t from = (uint32_t)(uintptr_t)(LdsBytes)ring + i16 * 64 + ((quarter ^ (i16 >> 2)) << 4);
+
+    f32x4 acc[4][4] = {};
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) load(i, s0 + i);
+    int slot = 0;
+    for (int s = s0; s < s1; ++s) {
+        wait_loaded<(kSlots - 1) * 8>();
+        bf16x8 wf[4], xf[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            wf[t] = *(LdsRows)(uintptr_t)(from + slot * 8192 + t * 1024);
+            xf[t] = *(LdsRows)(uintptr_t)(from + slot * 8192 + 4096 + t * 1024);
+        }
+        wait_read();
+        load(slot, s + kSlots);
+        slot ^= 1;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                acc[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[c], xf[t], acc[c][t], 0, 0, 0);
+    }
+    wait_loaded<0>();                          // the rings are free
+    __syncthreads();
+    f32x4 *meet = reinterpret_cast<f32x4 *>(lds);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) meet[(wave * 16 + c * 4 + t) * kWave + lane] = acc[c][t];
+    __syncthreads();
+    for (int q = wave; q < 16; q += kWaves) {
+        const int r = (q & 3) * 16 + i16, c = c0 + (q >> 2) * 16 + quarter * 4;
+        f32x4 v = meet[q * kWave + lane];
+#pragma unroll
+        for (int i = 1; i < kWaves; ++i) v += meet[(i * 16 + q) * kWave + lane];
+        if (r >= g.n || c >= p.n) continue;
+        put_linear<O>(p, (size_t)g.row0 + r, c, v);
+    }
+}
+
+#endif
+
+template <int O>
+__global__ __launch_bounds__(kThreads) void square_kernel(Product p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kWaves * 2 * 8192];
+    static_assert(sizeof(lds) >= kWaves * 16 * kWave * sizeof(f32x4), "the sums' meeting place");
+    for (int group = blockIdx.y;; group += gridDim.y) {
+        Group g;
+        if (p.count) g = find_group(group, kGradCols);
+        else g = Group{0, group * kGradCols, min(p.C - group * kGradCols, kGradCols), groups_of(p.C, kGradCols)};
+        if (group >= g.of) break;
+        square<O>(g, lds);
+        if (group + (int)gridDim.y >= g.of) break;
+        __syncthreads();                       // the meeting place is free again
+    }
+#else
+    (void)p;
+#endif
+}
+
+template <int O>
+hipError_t launch_squares(const Product &p, hipStream_t stream)
+{
+    const int size = kGradCols;
+    const int groups = p.count ? p.pairs / size + (p.pairs < p.E ? p.pairs : p.E) : groups_of(p.C, size);
+    return launch(square_kernel<O>, dim3((p.n + kGradCols - 1) / kGradCols, std::min(groups, kMostGroups)),
+                  dim3(kThreads), 0, stream, p);
+}
+
 }  // namespace
 
 // Experts that rows spread evenly over them reach.
@@ -504,6 +617,19 @@ static double tiles_time(const Product &p, double experts, double rate)
     return std::max(8.0 + rounds * std::ceil(p.k / 64.0) * 0.65, 4.0 + experts * p.n * p.k * 2e-6 / rate);
 }
 
+// A square for each CU at most, and more rows than few_rows reads in one go. Measured (the better of tiles
+// and few rows, squares), columns x sum: 64 x 4096, 64 rows 22, 13, 2048 rows 24, 13; 512 x 4096, 256 rows
+// 23, 13, 2048 rows (256 squares) 44, 28, 4096 rows 45, 52; 4096 x 4096, 32 rows 16, 19, 64 rows 24, 22,
+// 256 rows (256) 45, 24, 512 rows 47, 44; 512 x 16384, 2048 rows 150, 95; 8 experts of 512 x 4096, 512 rows
+// 47, 24, 1024 rows (160) 43, 26, 2048 rows (288) 44, 44.
+static bool squares(const Product &p)
+{
+    const double experts = experts_reached(p), mean = p.pairs / experts;
+    // an expert's last square is half empty on average
+    const double groups = p.count ? mean / kGradCols + 0.5 : std::ceil(mean / kGradCols);
+    return row_tiles(p) == 4 && experts * groups * std::ceil(p.n / (double)kGradCols) <= 256;
+}
+
 // Both kernels' times, from what they read, for rows spread evenly over the experts. Few rows: every
 // workgroup reads its weights and its rows, at 7.3 TB/s together, and costs 0.0025. Measured (tiles, few
 // rows): one matrix of 4096 x 4096, 1 row 42, 9, 64 rows 43, 24, 96 rows 43, 40, 128 rows 43, 46;
@@ -517,6 +643,7 @@ bool few_rows(const Product &p, bool swiglu)
     const double columns = std::ceil(p.n / 16.0) / (swiglu ? 2 : 1);
     const double few = 8.0 + (groups * experts * p.n * k * 2.0 + columns * p.pairs * k * 2.0) / 7.3e6 +
                        experts * groups * columns * 0.0025;
+    if (!swiglu && squares(p)) return true;
     return few < tiles_time(p, experts, 4.9);
 }
 
@@ -557,6 +684,7 @@ bool few_wgrad(const Product &p)
 
 hipError_t launch_few_gemm(const Product &p, hipStream_t stream)
 {
+    if (squares(p)) return launch_squares<to::kBf16>(p, stream);
     return launch_by_rows<to::kBf16>(p, stream);
 }
 
@@ -567,6 +695,7 @@ hipError_t launch_few_swiglu(const Product &p, hipStream_t stream)
 
 hipError_t launch_few_linear(const Product &p, hipStream_t stream)
 {
+    if (squares(p)) return launch_squares<to::kLinear>(p, stream);
     return launch_by_rows<to::kLinear>(p, stream);
 }
 

@@ -84,7 +84,7 @@ def test_combine_grad(T, H, E, K, C, packed):
 
 
 LINEAR = [(1, 8, 8), (1, 4096, 520), (3, 264, 72), (17, 72, 136), (64, 512, 256), (130, 200, 1032),
-          (300, 1096, 264), (513, 64, 8)]
+          (300, 1096, 264), (513, 64, 8), (2100, 136, 520), (20000, 520, 8)]
 
 
 def linear_inputs(T, H, N):

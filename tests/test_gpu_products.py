@@ -192,16 +192,43 @@ def kernels():
 @pytest.mark.parametrize("mean,E", [(1, 9), (20, 4), (50, 3)])
 @pytest.mark.parametrize("A", [0, 8])
 def test_few_rows(mean, E, A):
-    """The kernel for few rows, each of its heights, with experts that have many more rows than the mean
-    and experts that have none."""
+    """The kernel for few rows, with experts that have many more rows than the mean and experts that have
+    none; the squares from 33 rows on."""
     counts = [mean] * (E - 2) + [0, 2 * mean]
     x = Experts(counts, A=A, seed=mean)
     for H, N in ((200, 24), (520, 136), (1032, 40)):
         check_forward(x, H, N)
-        assert all("few_rows_kernel" in k for k in kernels()), kernels()
+        assert all(("few_rows" if mean <= 32 else "square") + "_kernel" in k for k in kernels()), kernels()
         check_swiglu(x, H, N, keep=True)
         assert all("few_rows_kernel" in k for k in kernels()), kernels()
     check_swiglu(x, 264, 72, keep=False)
+
+
+def test_few_rows_of_many_experts():
+    """Its largest height, where there are more squares than CUs."""
+    rng = np.random.default_rng(13)
+    x = Experts([int(v) for v in rng.integers(0, 100, 300)], A=8, seed=14)
+    check_forward(x, 520, 24)
+    assert all("few_rows_kernel" in k for k in kernels()), kernels()
+
+
+@pytest.mark.parametrize("counts,A", [([300], 0), ([90, 0, 130, 1, 64], 8)])
+@pytest.mark.parametrize("H,N", WIDTHS + [(264, 64), (1032, 200), (2056, 8)])
+def test_squares(counts, A, H, N):
+    """Sums that end inside a step, shorter than the eight wavefronts' steps and longer than a ring."""
+    x = Experts(counts, A=A, seed=H + N)
+    check_forward(x, H, N)
+    assert all("square_kernel" in k for k in kernels()), kernels()
+
+
+@pytest.mark.parametrize("H,N", [(264, 256), (72, 136), (200, 264), (136, 520), (328, 72)])
+def test_forward_of_tiles(H, N):
+    rng = np.random.default_rng(H)
+    x = Experts([int(v) for v in rng.integers(100, 500, 200)], A=8, seed=H + N)
+    check_forward(x, H, N)
+    assert all("product_kernel" in k for k in kernels()), kernels()
+    check_swiglu(x, H, N, keep=True)
+    assert all("product_kernel" in k for k in kernels()), kernels()
 
 
 @pytest.mark.parametrize("mean,E", [(1, 9), (20, 4), (50, 3)])
