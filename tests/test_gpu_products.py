@@ -255,7 +255,7 @@ def test_dgrad_of_tiles(H, N):
     assert all("product_kernel" in k for k in kernels()), kernels()
 
 
-@pytest.mark.parametrize("pairs", [1, 10 ** 6])
+@pytest.mark.parametrize("pairs", [1, 140, 4096, 10 ** 6])
 def test_pairs_do_not_choose_the_rows(pairs):
     """Every row is computed whatever number of pairs the call is told."""
     x = Experts([70, 0, 300, 5], A=0, seed=3)
