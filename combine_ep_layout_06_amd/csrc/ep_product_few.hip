@@ -40,6 +40,8 @@ __host__ __device__ __forceinline__ int groups_of(int rows, int size)
 constexpr int kWaves = kThreads / kWave;
 constexpr int kStep = 32;          // sum indexes of a matrix instruction
 constexpr int kAhead = 8;          // of them loaded together
+constexpr int kSquareSlot = 8192;  // a step of both operands of a square
+constexpr int kSquareRing = 2;     // such slots of a wavefront
 
 // The group of rows number `group` of all experts' groups of at most `size` rows: expert, first row, rows,
 // and how many groups there are.
@@ -400,7 +402,7 @@ hipError_t launch_dgrad_by_rows(const Product &p, hipStream_t stream)
     }
 }
 
-// ---- wgrad of few columns and rows, with a long sum ----
+// ---- wgrad with few tiles and a long sum ----
 
 // 64 x 64 of an expert's output a workgroup, its rows dealt out to the eight wavefronts; both operands
 // lie in LDS as dgrad's weights do.
@@ -408,9 +410,7 @@ template <int O>
 __global__ __launch_bounds__(kThreads) void few_wgrad_kernel(Product p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
-    constexpr int kSumSlot = 8192;             // 32 rows of both operands, 64 columns of each
-    constexpr int kSumRing = 2;                // slots of a wavefront
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kWaves * kSumRing * kSumSlot];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kWaves * kSquareRing * kSquareSlot];
     static_assert(sizeof(lds) >= kWaves * 16 * kWave * sizeof(f32x4), "the sums' meeting place");
     const int lane = lane_now(), wave = uniform(threadIdx.x / kWave), i16 = lane & 15, quarter = lane >> 4;
     const int across = (p.n + kGradCols - 1) / kGradCols, down = (p.m + kGradCols - 1) / kGradCols;
@@ -432,7 +432,7 @@ __global__ __launch_bounds__(kThreads) void few_wgrad_kernel(Product p)
         x_off[v] = (uint32_t)(lane >> 3) * p.m * 2 + (chunk << 4);
         w_off[v] = (uint32_t)(lane >> 3) * p.n * 2 + (chunk << 4);
     }
-    uint8_t *ring = lds + wave * (kSumRing * kSumSlot);
+    uint8_t *ring = lds + wave * (kSquareRing * kSquareSlot);
     // the loads of a step; past the expert's rows and the wavefront's last step they give 0
     auto load = [&](int slot, int s) {
         const int left = s < s1 ? n - s * kStep : 0;
@@ -441,8 +441,8 @@ __global__ __launch_bounds__(kThreads) void few_wgrad_kernel(Product p)
         const i32x4 wb = buffer(p.w + row * p.n + c0, ((int64_t)left * p.n - c0) * 2);
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-            load_lds(wb, ring + slot * kSumSlot + v * 1024, w_off[v & 1], (uint32_t)v * 16 * p.n);
-            load_lds(xb, ring + slot * kSumSlot + 4096 + v * 1024, x_off[v & 1], (uint32_t)v * 16 * p.m);
+            load_lds(wb, ring + slot * kSquareSlot + v * 1024, w_off[v & 1], (uint32_t)v * 16 * p.n);
+            load_lds(xb, ring + slot * kSquareSlot + 4096 + v * 1024, x_off[v & 1], (uint32_t)v * 16 * p.m);
         }
     };
     const uint32_t at0 = (uint32_t)(uintptr_t)(LdsBytes)ring + (quarter * 8 + (i16 >> 2)) * 128 +
@@ -450,19 +450,19 @@ __global__ __launch_bounds__(kThreads) void few_wgrad_kernel(Product p)
 
     f32x4 acc[4][4] = {};
 #pragma unroll
-    for (int i = 0; i < kSumRing; ++i) load(i, s0 + i);
+    for (int i = 0; i < kSquareRing; ++i) load(i, s0 + i);
     int slot = 0;
     for (int s = s0; s < s1; ++s) {
-        wait_loaded<(kSumRing - 1) * 8>();
+        wait_loaded<(kSquareRing - 1) * 8>();
         bf16x8 wf[4], xf[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const uint32_t from = (at0 ^ (c << 5)) + slot * kSumSlot;
+            const uint32_t from = (at0 ^ (c << 5)) + slot * kSquareSlot;
             wf[c] = read_transposed(from, from + 512);
             xf[c] = read_transposed(from + 4096, from + 4096 + 512);
         }
         wait_read();
-        load(slot, s + kSumRing);
+        load(slot, s + kSquareRing);
         slot ^= 1;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -506,7 +506,6 @@ __global__ __launch_bounds__(kThreads) void few_wgrad_kernel(Product p)
 template <int O>
 __device__ __forceinline__ void square(const Group &g, uint8_t *lds)
 {
-    constexpr int kSlots = 2;
     const auto &p = argument();
     const int lane = lane_now(), wave = uniform(threadIdx.x / kWave), i16 = lane & 15, quarter = lane >> 4;
     const int c0 = blockIdx.x * kGradCols;
@@ -516,7 +515,7 @@ __device__ __forceinline__ void square(const Group &g, uint8_t *lds)
     const i32x4 xb = buffer(p.x + (size_t)g.row0 * p.k, (int64_t)g.n * p.k * 2);
     const int chunk = (lane & 3) ^ quarter;
     const uint32_t at = ((uint32_t)(lane >> 2) * p.k + chunk * 8) * 2;
-    uint8_t *ring = lds + wave * (kSlots * 8192);
+    uint8_t *ring = lds + wave * (kSquareRing * kSquareSlot);
     // the loads of a step; beyond the row's end and the wavefront's last step they give 0
     auto load = [&](int slot, int s) {
         const bool some = s < s1;
@@ -524,26 +523,26 @@ __device__ __forceinline__ void square(const Group &g, uint8_t *lds)
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const uint32_t soff = some ? (uint32_t)t * 32 * p.k + (uint32_t)s * (kStep * 2) : 0u;
-            load_lds(wb, ring + slot * 8192 + t * 1024, off, soff);
-            load_lds(xb, ring + slot * 8192 + 4096 + t * 1024, off, soff);
+            load_lds(wb, ring + slot * kSquareSlot + t * 1024, off, soff);
+            load_lds(xb, ring + slot * kSquareSlot + 4096 + t * 1024, off, soff);
         }
     };
     const uint32_t from = (uint32_t)(uintptr_t)(LdsBytes)ring + i16 * 64 + ((quarter ^ (i16 >> 2)) << 4);
 
     f32x4 acc[4][4] = {};
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i) load(i, s0 + i);
+    for (int i = 0; i < kSquareRing; ++i) load(i, s0 + i);
     int slot = 0;
     for (int s = s0; s < s1; ++s) {
-        wait_loaded<(kSlots - 1) * 8>();
+        wait_loaded<(kSquareRing - 1) * 8>();
         bf16x8 wf[4], xf[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            wf[t] = *(LdsRows)(uintptr_t)(from + slot * 8192 + t * 1024);
-            xf[t] = *(LdsRows)(uintptr_t)(from + slot * 8192 + 4096 + t * 1024);
+            wf[t] = *(LdsRows)(uintptr_t)(from + slot * kSquareSlot + t * 1024);
+            xf[t] = *(LdsRows)(uintptr_t)(from + slot * kSquareSlot + 4096 + t * 1024);
         }
         wait_read();
-        load(slot, s + kSlots);
+        load(slot, s + kSquareRing);
         slot ^= 1;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -575,7 +574,7 @@ template <int O>
 __global__ __launch_bounds__(kThreads) void square_kernel(Product p)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kWaves * 2 * 8192];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kWaves * kSquareRing * kSquareSlot];
     static_assert(sizeof(lds) >= kWaves * 16 * kWave * sizeof(f32x4), "the sums' meeting place");
     for (int group = blockIdx.y;; group += gridDim.y) {
         Group g;
