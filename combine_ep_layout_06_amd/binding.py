@@ -1346,15 +1346,20 @@ def ep_combine_grad_packed(dout: torch.Tensor, y: torch.Tensor, topk_idx: torch.
 # the dense product beside the experts
 # ------------------------------------------------------------------------------------------
 
+def _activation(act):
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act: expected one of {sorted(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
 def _linear_args(x, w, act):
     xs, ws, dev = x.shape, w.shape, x.device
     if len(xs) != 2 or len(ws) != 2 or xs[1] != ws[1]:
         raise ValueError(f"expected x [T, H] and w [N, H], got {tuple(xs)} and {tuple(ws)}")
-    if act not in ACTIVATIONS:
-        raise ValueError(f"act: expected one of {sorted(ACTIVATIONS)}, got {act!r}")
+    a = _activation(act)
     _rows(x, "x", xs, dev)
     _rows(w, "w", ws, dev)
-    return xs[0], xs[1], ws[0], ACTIVATIONS[act], dev
+    return xs[0], xs[1], ws[0], a, dev
 
 
 def ep_linear(x: torch.Tensor, w: torch.Tensor, *, bias=None, act="none", residual=None, pre=None,
@@ -1379,7 +1384,7 @@ def ep_linear(x: torch.Tensor, w: torch.Tensor, *, bias=None, act="none", residu
 def linear_grad_workspace_bytes(T: int, N: int, act: str) -> int:
     """Bytes of workspace ep_linear_grad needs for T rows, N outputs and an activation."""
     return int(load_library().ep_linear_grad_workspace_bytes(
-        ctypes.byref(_shape(T, 8, 1, 1, 1, 1)), N, ACTIVATIONS[act]))
+        ctypes.byref(_shape(T, 8, 1, 1, 1, 1)), N, _activation(act)))
 
 
 def ep_linear_grad(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *, act="none", pre=None,

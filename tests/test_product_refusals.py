@@ -156,6 +156,7 @@ def test_binding_refuses_what_does_not_fit():
                                   torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2), C + 1),
         lambda: B.ep_linear(z(4, H), z(N, H + 8)),
         lambda: B.ep_linear(z(4, H), z(N, H), act="tanh"),
+        lambda: B.linear_grad_workspace_bytes(4, N, "tanh"),
         lambda: B.ep_linear(z(4, H), z(N, H), residual=z(4, N + 8)),
         lambda: B.ep_linear(z(4, H), z(N, H), bias=z(N + 8)),
         lambda: B.ep_linear_grad(z(4, N), z(4, H), z(N, H), act="silu"),
