@@ -687,7 +687,9 @@ int ep_combine_grad_packed(const ep_shape_t *shape, int32_t rows, const uint16_t
  * expert, a projection; with the combined rows as the residual it adds itself to them):
  *   z[t][c] = sum_k x[t][k] * w[c][k] + bias[c],  out[t][c] = bf16(act(z[t][c]) + residual[t][c])
  * in fp32, one rounding. act: EP_ACT_NONE z, EP_ACT_RELU max(z, 0), EP_ACT_SILU z / (1 + exp(-z)),
- * EP_ACT_GELU z * Phi(z) with the normal distribution Phi.
+ * within (1.5 |z| + 8) * 2^-24 of its value for z above -88.7 (a zero below), EP_ACT_GELU z * Phi(z)
+ * with the normal distribution Phi, itself within 2^-21 and, for z < 0, within (1 + z^2) * 2^-19 of its
+ * value down to z = -13.1 (a zero or a value below 2^-126 from there on).
  *   x [T*H], w [N*H], bias [N] or NULL, residual [T*N] or NULL: uint16 (bf16)
  *   pre [T*N] uint16 (bf16) out: bf16(z), which ep_linear_grad takes; NULL: not kept
  *   out [T*N] uint16 (bf16) out; may be residual itself
