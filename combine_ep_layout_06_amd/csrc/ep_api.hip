@@ -1159,20 +1159,21 @@ namespace {
 
 int check_linear(const ep_shape_t *shape, int32_t N, int32_t act, const char *fn)
 {
-    if (int rc = check_shape(shape, fn)) return rc;
+    ep::launch_log().n = 0;
+    const std::string f(fn);
+    if (!shape) return fail(EP_ERR_INVALID, f + ": shape is NULL");
+    if (shape->T < 0 || shape->H < 1) return fail(EP_ERR_INVALID, f + ": need T >= 0 and H >= 1");
     if (int rc = check_widths(shape->H, N, "N", (int64_t)N * shape->H, fn)) return rc;
     if (act < EP_ACT_NONE || act > EP_ACT_GELU)
-        return fail(EP_ERR_INVALID, std::string(fn) + ": act is no EP_ACT_ value");
+        return fail(EP_ERR_INVALID, f + ": act is no EP_ACT_ value");
     return EP_OK;
 }
 
 // A product over the T rows of dense matrices.
 ep::Product dense(const ep_shape_t *s, const uint16_t *x, const uint16_t *w, int k, int n, void *out)
 {
-    ep::Product p = bf16_product(s, x, w, nullptr, k, n, out);
-    p.E = 1;
-    p.C = p.pairs = s->T;
-    return p;
+    const ep_shape_t rows{s->T, s->H, 1, 1, s->T, 1};      // the caller's E, K, C and R may be anything
+    return bf16_product(&rows, x, w, nullptr, k, n, out);
 }
 
 }  // namespace

@@ -197,3 +197,14 @@ def test_formulas_against_differences():
     dg, du, _, _ = P.swiglu_grad64(dh, torch.zeros_like(dh), z, u)
     assert (dg - dh * (h(z + d, u) - h(z - d, u)) / (2 * d)).abs().max() < 1e-7
     assert (du - dh * (h(z, u + d) - h(z, u - d)) / (2 * d)).abs().max() < 1e-7
+
+
+@pytest.mark.parametrize("kw", [dict(E=0, K=0, C=0, R=0), dict(E=-1, K=-1, C=-1, R=-1), dict(E=5, R=2),
+                                dict(K=1 << 20), dict(E=1 << 16, C=1 << 16)])
+def test_linear_takes_no_part_of_the_shape_but_its_rows(lib, kw):
+    """E, K, C and R are not used: whatever they hold, the call gets as far as its next check, and one of
+    no rows does nothing."""
+    p = [A16 + 8, *[A16] * 5]
+    assert lib.ep_linear(shape(T=1 << 20, **kw), 768, 0, *p, None) == ALIGN
+    assert lib.ep_linear_grad(shape(T=1 << 20, **kw), 768, 2, A16 + 8, *[A16] * 7, 1 << 40, None) == ALIGN
+    assert lib.ep_linear(shape(T=0, **kw), 768, 0, *[A16] * 6, None) == 0
