@@ -913,15 +913,24 @@ int ep_moe_layer_fp8(const ep_shape_t *shape, int32_t I, const uint16_t *x,
 
 namespace {
 
+constexpr int32_t kLinearGradMostRows = 1 << 21;    // half the chunks of rows that grid.y holds
+
 // Widths and weights of the bf16 products: rows in 16-byte chunks; lane offsets inside one matrix and
 // inside one tile of rows are 32 bits wide.
+bool whole_chunks(int64_t H, int64_t N) { return H % 8 == 0 && N % 8 == 0; }
+
+bool widths_fit(int64_t H, int64_t N, int64_t weights)
+{
+    return H < 1 << 20 && N < 1 << 20 && weights < int64_t(1) << 30;
+}
+
 int check_widths(int64_t H, int64_t N, const char *n_name, int64_t weights, const char *fn)
 {
     const std::string f(fn);
     if (N < 1) return fail(EP_ERR_INVALID, f + ": need " + n_name + " >= 1");
-    if (H % 8 != 0 || N % 8 != 0)
+    if (!whole_chunks(H, N))
         return fail(EP_ERR_UNSUPPORTED, f + ": H and " + n_name + " must be multiples of 8");
-    if (H >= 1 << 20 || N >= 1 << 20 || weights >= int64_t(1) << 30)
+    if (!widths_fit(H, N, weights))
         return fail(EP_ERR_UNSUPPORTED, f + ": a width reaches 2^20, or a weight matrix 2^30 elements");
     return EP_OK;
 }
@@ -1199,7 +1208,10 @@ int ep_linear(const ep_shape_t *shape, int32_t N, int32_t act, const uint16_t *x
 
 size_t ep_linear_grad_workspace_bytes(const ep_shape_t *shape, int32_t N, int32_t act)
 {
-    if (!shape || shape->T < 0 || N < 1 || act < EP_ACT_NONE || act > EP_ACT_GELU) return 0;
+    if (!shape || shape->T < 0 || shape->T > kLinearGradMostRows || shape->H < 1 || N < 1 ||
+        act < EP_ACT_NONE || act > EP_ACT_GELU)
+        return 0;
+    if (!whole_chunks(shape->H, N) || !widths_fit(shape->H, N, (int64_t)N * shape->H)) return 0;
     const size_t T = shape->T, chunks = (T + ep::kLinearGradRows - 1) / ep::kLinearGradRows;
     return (size_t)N * (4 * chunks + (act == EP_ACT_NONE ? 0 : 2 * T));
 }
@@ -1212,7 +1224,7 @@ int ep_linear_grad(const ep_shape_t *shape, int32_t N, int32_t act, const uint16
     const char *fn = "ep_linear_grad";
     const std::string f(fn);
     if (int rc = check_linear(shape, N, act, fn)) return rc;
-    if (shape->T > 1 << 21) return fail(EP_ERR_UNSUPPORTED, f + ": T exceeds 2^21");
+    if (shape->T > kLinearGradMostRows) return fail(EP_ERR_UNSUPPORTED, f + ": T exceeds 2^21");
     const bool some = shape->T > 0;
     if ((some && (!dout || !x || !w || !dx || (act != EP_ACT_NONE && !pre))) || !dw || !dbias)
         return fail(EP_ERR_INVALID, f + ": NULL required pointer");

@@ -714,8 +714,8 @@ int ep_linear(const ep_shape_t *shape, int32_t N, int32_t act, const uint16_t *x
  *            EP_ERR_INVALID), 16-byte aligned; overwritten. Two calls in flight at once need two.
  * The requirements of ep_linear; T <= 2^21.
  *
- * ep_linear_grad_workspace_bytes: 4*N * ceil(T / 64), and with an activation 2*T*N more (0 for an
- * invalid shape, N or act). Host only.
+ * ep_linear_grad_workspace_bytes: 4*N * ceil(T / 64), and with an activation 2*T*N more (0 for sizes
+ * or an act that ep_linear_grad refuses). Host only.
  */
 size_t ep_linear_grad_workspace_bytes(const ep_shape_t *shape, int32_t N, int32_t act);
 

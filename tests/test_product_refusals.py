@@ -208,3 +208,16 @@ def test_linear_takes_no_part_of_the_shape_but_its_rows(lib, kw):
     assert lib.ep_linear(shape(T=1 << 20, **kw), 768, 0, *p, None) == ALIGN
     assert lib.ep_linear_grad(shape(T=1 << 20, **kw), 768, 2, A16 + 8, *[A16] * 7, 1 << 40, None) == ALIGN
     assert lib.ep_linear(shape(T=0, **kw), 768, 0, *[A16] * 6, None) == 0
+
+
+def test_workspace_of_sizes_that_are_refused(lib):
+    """0 wherever ep_linear_grad refuses the sizes."""
+    f, g = lib.ep_linear_grad_workspace_bytes, lib.ep_linear_grad
+    for kw, n, act in ((dict(T=-1), 768, 2), (dict(H=0), 768, 2), (dict(H=-8), 768, 2), (dict(H=2044), 768, 2),
+                       (dict(), 764, 2), (dict(), 0, 2), (dict(), -8, 0), (dict(H=1 << 20), 768, 0),
+                       (dict(H=8), 1 << 20, 0), (dict(), 524_288, 2), (dict(T=(1 << 21) + 1), 768, 2),
+                       (dict(), 768, 4)):
+        assert g(shape(**kw), n, act, *[A16] * 8, 1 << 40, None) in (INVALID, UNSUPPORTED), (kw, n)
+        assert f(shape(**kw), n, act) == 0, (kw, n, act)
+    assert f(shape(T=1 << 21), 520, 3) == 520 * (4 * (1 << 15) + (2 << 21))
+    assert f(shape(T=0), 520, 3) == 0
