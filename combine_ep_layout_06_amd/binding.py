@@ -73,6 +73,7 @@ class EpError(RuntimeError):
 
 
 _lib = None
+_int_places = {}       # per C call: where its 32-bit integers are among its arguments after the shape
 
 
 def library_path() -> str:
@@ -149,6 +150,9 @@ def load_library():
                                                    "ep_moe_layer_workspace_bytes",
                                                    "ep_linear_grad_workspace_bytes"):
                 getattr(L, fn).restype = ctypes.c_int
+        for fn in EXPORTED:
+            types = getattr(L, fn).argtypes or ()
+            _int_places[fn] = [i for i, t in enumerate(types[1:]) if t is i32]
         L.ep_layout_workspace_bytes.argtypes = [sp]
         L.ep_layout_workspace_bytes.restype = ctypes.c_size_t
         L.ep_linear_grad_workspace_bytes.restype = ctypes.c_size_t
@@ -261,9 +265,17 @@ def _require_current(name: str, dev):
                      f"HIP device ({cur}); move them there or call under torch.cuda.device()")
 
 
+def _fits32(name: str, value: int):
+    if not -2147483648 <= value <= 2147483647:     # ctypes would pass its low half
+        raise ValueError(f"{name}: a size of {value} does not fit 32 bits")
+
+
 def _call(name: str, sh: EpShape, *args, stream=None):
     """Issue (or record) one C call; tensor arguments are passed as their data pointers."""
     fn = getattr(load_library(), name)
+    for i in _int_places[name]:
+        if not -2147483648 <= args[i] <= 2147483647:
+            _fits32(name, args[i])
     cargs = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
     dev = next((a.device for a in args if isinstance(a, torch.Tensor)), None)
     cl = getattr(_recording, "calls", None)
@@ -1383,6 +1395,7 @@ def ep_linear(x: torch.Tensor, w: torch.Tensor, *, bias=None, act="none", residu
 
 def linear_grad_workspace_bytes(T: int, N: int, act: str) -> int:
     """Bytes of workspace ep_linear_grad needs for T rows, N outputs and an activation."""
+    _fits32("ep_linear_grad_workspace_bytes", N)
     return int(load_library().ep_linear_grad_workspace_bytes(
         ctypes.byref(_shape(T, 8, 1, 1, 1, 1)), N, _activation(act)))
 

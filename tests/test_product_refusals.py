@@ -221,3 +221,23 @@ def test_workspace_of_sizes_that_are_refused(lib):
         assert f(shape(**kw), n, act) == 0, (kw, n, act)
     assert f(shape(T=1 << 21), 520, 3) == 520 * (4 * (1 << 15) + (2 << 21))
     assert f(shape(T=0), 520, 3) == 0
+
+
+def test_binding_refuses_sizes_beyond_32_bits(lib):
+    """A width or a number of rows that the C call would see as its low half (2^32 + 8 as 8)."""
+    z = lambda *s, t=torch.bfloat16: torch.empty(s, dtype=t, device="meta")  # noqa: E731
+    many, E = 2 ** 32 + 8, 3
+    count, offset = z(E, t=torch.int32), z(E + 1, t=torch.int32)
+    idx, w = z(4, 2, t=torch.int32), z(4, 2, t=torch.float32)
+    for f in (lambda: B.ep_linear(z(4, 8), z(many, 8)),
+              lambda: B.ep_linear_grad(z(4, many), z(4, 8), z(many, 8), workspace=z(64)),
+              lambda: B.linear_grad_workspace_bytes(4, many, "none"),
+              lambda: B.ep_expert_gemm(z(E, 4, 8), count, z(E, many, 8), 4),
+              lambda: B.ep_expert_gemm_packed(z(many, 8), count, offset, z(E, 16, 8), 4),
+              lambda: B.ep_expert_swiglu(z(E, 4, 8), count, z(E, 2 * many, 8), 4),
+              lambda: B.ep_expert_gemm_dgrad(z(E, 4, many), count, z(E, many, 8), 4),
+              lambda: B.ep_expert_swiglu_dgrad_packed(z(many, 8), count, offset, z(E, 8, 16), z(many, 32), 4),
+              lambda: B.ep_expert_gemm_wgrad_packed(z(many, 16), z(many, 8), count, offset, 4),
+              lambda: B.ep_combine_grad_packed(z(4, 8), z(many, 8), idx, idx, offset, w, E, 4)):
+        with pytest.raises(ValueError, match="32 bits"):
+            f()
