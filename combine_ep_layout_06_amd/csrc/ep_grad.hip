@@ -2,6 +2,8 @@
 // activation and bias.
 #include "ep_product.h"
 
+#include <algorithm>
+
 namespace ep {
 
 namespace {
@@ -25,6 +27,7 @@ __device__ __forceinline__ u32x4 pack8(const float (&v)[8])
 // of them written: 5.6 TB/s, a copy has 4.7).
 constexpr int kChunks = 4;
 constexpr int kManyPairs = 8192;   // 8 wavefronts for each SIMD
+constexpr int64_t kMostGroups = 1 << 23;       // of a row of the grid, which holds fewer than 2^32 threads
 
 template <int W>
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(
@@ -35,7 +38,7 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(
 {
     __shared__ float sums[kWaves];
     const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int64_t i = (int64_t)blockIdx.x * (kWaves / W) + wave / W;
+    const int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (kWaves / W) + wave / W;
     if (i >= pairs) return;                    // W > 1: the whole workgroup
     const int row = __builtin_amdgcn_readfirstlane(pair_row(idx[i], slot[i], E, C, poff, prows));
     if (row < 0) {
@@ -163,9 +166,11 @@ hipError_t launch_combine_grad(const ep_shape_t &s, const uint16_t *dout, const 
     const int pairs = s.T * s.K;
     if (pairs == 0) return hipSuccess;
     auto go = [&](auto kernel, int per) {
-        return launch(kernel, dim3((unsigned)(((int64_t)pairs + per - 1) / per)), dim3(kThreads), 0, stream,
-                      reinterpret_cast<const u32x4 *>(dout), reinterpret_cast<const u32x4 *>(y), idx, slot, w,
-                      reinterpret_cast<u32x4 *>(dy), dw, pairs, s.H / 8, s.E, s.C, s.K, map.offset, map.rows);
+        const int64_t groups = ((int64_t)pairs + per - 1) / per;
+        const dim3 grid((unsigned)std::min(groups, kMostGroups), (unsigned)((groups + kMostGroups - 1) / kMostGroups));
+        return launch(kernel, grid, dim3(kThreads), 0, stream, reinterpret_cast<const u32x4 *>(dout),
+                      reinterpret_cast<const u32x4 *>(y), idx, slot, w, reinterpret_cast<u32x4 *>(dy), dw, pairs,
+                      s.H / 8, s.E, s.C, s.K, map.offset, map.rows);
     };
     return pairs >= kManyPairs ? go(combine_grad_kernel<1>, kWaves) : go(combine_grad_kernel<kWaves>, 1);
 }

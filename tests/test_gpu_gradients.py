@@ -150,3 +150,30 @@ def test_linear_grad(T, H, N, act):
     want = dz.T @ x.double()
     tol = op.T @ x.double().abs() + (T + 8) * U32 * (top.T @ x.double().abs())
     close(dw.cpu().double(), want, P.rounded(want, tol), "dw")
+
+
+def test_combine_grad_of_more_pairs_than_a_grid_row_holds():
+    """A wavefront for each of 67.2 million pairs is more than 2^32 threads."""
+    T, H, K = 8_400_000, 8, 8
+    g = torch.Generator(device=DEV)
+    g.manual_seed(6)
+    dout = torch.randn(T, H, generator=g, device=DEV).to(BF16)
+    w = torch.randn(T, K, generator=g, device=DEV)
+    y = torch.randn(K, T, H, generator=g, device=DEV).to(BF16)
+    idx = torch.arange(K, dtype=torch.int32, device=DEV).repeat(T, 1)
+    slot = torch.arange(T, dtype=torch.int32, device=DEV)[:, None].repeat(1, K)
+    drop = torch.rand(T, K, generator=g, device=DEV) < 0.05
+    slot[drop] = -1
+    dy = torch.full((K, T, H), SENTINEL, dtype=torch.int16, device=DEV).view(BF16)
+    dw = torch.full((T, K), float("nan"), device=DEV)
+    print("[combine_grad]", T * K, "pairs", flush=True)
+    B.ep_combine_grad(dout, y, idx, slot, w, T, dy=dy, dtopk_w=dw)
+    for j in range(K):
+        d, v = dout.double(), y[j].double()
+        want = w[:, j].double()[:, None] * d
+        got = dy[j].double()
+        off = (got - want).abs() - P.rounded(want, U32 * want.abs())
+        assert (off[~drop[:, j]] <= 0).all(), j
+        assert (dy[j].view(torch.int16)[drop[:, j]] == SENTINEL).all(), j
+        off = (dw[:, j].double() - (d * v).sum(1)).abs() - (H + 8) * U32 * (d * v).abs().sum(1)
+        assert (off[~drop[:, j]] <= 0).all() and (dw[:, j][drop[:, j]] == 0).all(), j
