@@ -39,6 +39,10 @@ inline hipError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t
                          hipStream_t stream, Args... args)
 {
     static_assert(sizeof...(KArgs) == sizeof...(Args), "kernel argument count");
+    // a dimension of 2^32 threads or more would wrap without an error
+    if ((uint64_t)grid.x * block.x > UINT32_MAX || (uint64_t)grid.y * block.y > UINT32_MAX ||
+        (uint64_t)grid.z * block.z > UINT32_MAX)
+        return hipErrorInvalidConfiguration;
     LaunchLog &log = launch_log();
     if (log.n < kLaunchLogCap)
         log.e[log.n] = LaunchEntry{reinterpret_cast<const void *>(kernel), grid, block, shmem};

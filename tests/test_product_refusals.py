@@ -241,3 +241,11 @@ def test_binding_refuses_sizes_beyond_32_bits(lib):
               lambda: B.ep_combine_grad_packed(z(4, 8), z(many, 8), idx, idx, offset, w, E, 4)):
         with pytest.raises(ValueError, match="32 bits"):
             f()
+
+
+def test_grid_of_too_many_threads_is_refused(lib):
+    """A launch whose grid has 2^32 threads or more in a dimension, which would wrap, is an error instead:
+    combine of 2^27 tokens."""
+    s = shape(T=1 << 27, H=8, E=1, K=1, C=1 << 27)
+    assert lib.ep_combine(s, *[A16] * 5, None) == B.EP_ERR_HIP
+    assert "hipErrorInvalidConfiguration" in lib.ep_last_error().decode()
