@@ -936,10 +936,10 @@ int check_widths(int64_t H, int64_t N, const char *n_name, int64_t weights, cons
 }
 
 // Checks shared by the experts' bf16 products: `n` channels beside H, n * halves rows or columns of an
-// expert's weights; `extra` is a third row buffer.
+// expert's weights; `extra` is a third row buffer. A packed buffer may have no rows, and be NULL.
 int check_bf16_product(const ep_shape_t *shape, int32_t n, int halves, const char *n_name,
                        const void *x, const void *w, const int32_t *expert_count, const void *extra,
-                       const void *out, const char *fn)
+                       const void *out, const char *fn, bool rows = true)
 {
     const std::string f(fn);
     if (int rc = check_shape(shape, fn)) return rc;
@@ -948,7 +948,7 @@ int check_bf16_product(const ep_shape_t *shape, int32_t n, int halves, const cha
         return rc;
     if (n % 8 != 0)
         return fail(EP_ERR_UNSUPPORTED, f + ": H and " + n_name + " must be multiples of 8");
-    if (shape->T > 0 && (!x || !w || !expert_count || !out))
+    if (shape->T > 0 && rows && (!x || !w || !expert_count || !out))
         return fail(EP_ERR_INVALID, f + ": NULL required pointer");
     if (!aligned(x, 16) || !aligned(w, 16) || !aligned(extra, 16) || !aligned(out, 16))
         return fail(EP_ERR_ALIGN, f + ": row buffers, weights and outputs must be 16-byte aligned");
@@ -978,13 +978,16 @@ void pack(ep::Product &p, const int32_t *packed_offset, int32_t rows)
 {
     p.offset = packed_offset;
     p.rows = p.C = rows;
+    if (rows == 0) p.pairs = 0;
 }
 
 int expert_wgrad(const ep_shape_t *shape, int32_t N, const uint16_t *dy, const uint16_t *recv,
                  const int32_t *expert_count, const int32_t *packed_offset, bool packed, int32_t rows,
                  bool f32, int32_t accumulate, void *dw, hipStream_t stream, const char *fn)
 {
-    if (int rc = check_bf16_product(shape, N, 1, "N", dy, recv, expert_count, nullptr, dw, fn)) return rc;
+    if (int rc = check_bf16_product(shape, N, 1, "N", dy, recv, expert_count, nullptr, dw, fn,
+                                    !packed || rows != 0))
+        return rc;
     if (packed)
         if (int rc = check_packed_rows(shape, rows, packed_offset, fn)) return rc;
     if (!dw) return fail(EP_ERR_INVALID, std::string(fn) + ": NULL required pointer");
@@ -1011,7 +1014,7 @@ int ep_expert_gemm_packed(const ep_shape_t *shape, int32_t rows, int32_t N, cons
                           const uint16_t *w, uint16_t *y, hipStream_t stream)
 {
     const char *fn = "ep_expert_gemm_packed";
-    if (int rc = check_bf16_product(shape, N, 1, "N", recv, w, expert_count, nullptr, y, fn)) return rc;
+    if (int rc = check_bf16_product(shape, N, 1, "N", recv, w, expert_count, nullptr, y, fn, rows != 0)) return rc;
     if (int rc = check_packed_rows(shape, rows, packed_offset, fn)) return rc;
     ep::Product p = bf16_product(shape, recv, w, expert_count, shape->H, N, y);
     pack(p, packed_offset, rows);
@@ -1034,7 +1037,7 @@ int ep_expert_swiglu_packed(const ep_shape_t *shape, int32_t rows, int32_t I, co
                             const uint16_t *w13, uint16_t *gu, uint16_t *h, hipStream_t stream)
 {
     const char *fn = "ep_expert_swiglu_packed";
-    if (int rc = check_bf16_product(shape, I, 2, "I", recv, w13, expert_count, gu, h, fn)) return rc;
+    if (int rc = check_bf16_product(shape, I, 2, "I", recv, w13, expert_count, gu, h, fn, rows != 0)) return rc;
     if (int rc = check_packed_rows(shape, rows, packed_offset, fn)) return rc;
     ep::Product p = bf16_product(shape, recv, w13, expert_count, shape->H, 2 * I, h);
     p.out2 = gu;
@@ -1057,7 +1060,7 @@ int ep_expert_gemm_dgrad_packed(const ep_shape_t *shape, int32_t rows, int32_t N
                                 const uint16_t *w, uint16_t *dx, hipStream_t stream)
 {
     const char *fn = "ep_expert_gemm_dgrad_packed";
-    if (int rc = check_bf16_product(shape, N, 1, "N", dy, w, expert_count, nullptr, dx, fn)) return rc;
+    if (int rc = check_bf16_product(shape, N, 1, "N", dy, w, expert_count, nullptr, dx, fn, rows != 0)) return rc;
     if (int rc = check_packed_rows(shape, rows, packed_offset, fn)) return rc;
     ep::Product p = bf16_product(shape, dy, w, expert_count, N, shape->H, dx);
     pack(p, packed_offset, rows);
@@ -1082,8 +1085,8 @@ int ep_expert_swiglu_dgrad_packed(const ep_shape_t *shape, int32_t rows, int32_t
                                   const uint16_t *gu, uint16_t *dgu, hipStream_t stream)
 {
     const char *fn = "ep_expert_swiglu_dgrad_packed";
-    if (int rc = check_bf16_product(shape, I, 1, "I", dy, w2, expert_count, gu, dgu, fn)) return rc;
-    if (shape->T > 0 && !gu) return fail(EP_ERR_INVALID, std::string(fn) + ": NULL required pointer");
+    if (int rc = check_bf16_product(shape, I, 1, "I", dy, w2, expert_count, gu, dgu, fn, rows != 0)) return rc;
+    if (shape->T > 0 && rows != 0 && !gu) return fail(EP_ERR_INVALID, std::string(fn) + ": NULL required pointer");
     if (int rc = check_packed_rows(shape, rows, packed_offset, fn)) return rc;
     ep::Product p = bf16_product(shape, dy, w2, expert_count, shape->H, I, dgu);
     p.in = gu;
@@ -1130,7 +1133,8 @@ int combine_grad(const ep_shape_t *shape, const uint16_t *dout, const uint16_t *
                  float *dtopk_w, ep::RowMap map, hipStream_t stream, const char *fn)
 {
     const std::string f(fn);
-    if (shape->T > 0 && (!dout || !y || !topk_idx || !slot || !topk_w || !dy || !dtopk_w))
+    const bool rows = !map.offset || map.rows != 0;
+    if (shape->T > 0 && (!dout || !topk_idx || !slot || !topk_w || !dtopk_w || (rows && (!y || !dy))))
         return fail(EP_ERR_INVALID, f + ": NULL required pointer");
     if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(dy, 16))
         return fail(EP_ERR_ALIGN, f + ": dout, y and dy must be 16-byte aligned");

@@ -562,8 +562,8 @@ int ep_moe_layer_fp8(const ep_shape_t *shape, int32_t I, const uint16_t *x,
  *
  * Rows are as in the FP8 products: each expert e holds n = expert_count[e] rows from row e*C of a padded
  * buffer [E][C] (n taken as min(max(n, 0), C)), or from row packed_offset[e] of a packed buffer of
- * `rows` rows (rows outside the buffer are left out; C is not used). Only these rows are read and
- * written; other rows of the outputs keep what they hold. shape->T * shape->K is the number of pairs
+ * `rows` rows (rows outside the buffer are left out; C is not used; with rows = 0 its pointers may be
+ * NULL). Only these rows are read and written; other rows of the outputs keep what they hold. shape->T * shape->K is the number of pairs
  * laid out; it chooses the kernel and its grid, not which rows are computed (the order of the fp32 sums
  * may differ), except that T = 0 means no rows. R is not used. H is the width of the rows that the
  * forward product takes, in its gradients too.
@@ -668,7 +668,8 @@ int ep_expert_gemm_wgrad_f32_packed(const ep_shape_t *shape, int32_t rows, int32
  * ep_combine_grad / ep_combine_grad_packed -- the gradient of ep_combine (ep_combine_packed): for each
  * kept pair i = t*K + j, with its row r as in the forward call,
  *   dy[r][h] = bf16(topk_w[i] * dout[t][h]),  dtopk_w[i] = sum_h dout[t][h] * y[r][h]  (fp32)
- * A pair that is not kept gets dtopk_w = 0; rows of dy that hold no pair keep what they hold.
+ * A pair that is not kept gets dtopk_w = 0; rows of dy that hold no pair keep what they hold. y and dy
+ * of no packed rows may be NULL.
  *   dout [T*H] uint16 (bf16), y and dy [E*C*H] (packed: [rows*H]) uint16 (bf16), 16-byte aligned;
  *   topk_idx, slot [T*K] int32, topk_w and dtopk_w [T*K] float, 4-byte aligned. dy may be y itself.
  * K <= EP_MAX_TOPK, H % 8 == 0 (else EP_ERR_UNSUPPORTED).

@@ -505,3 +505,34 @@ def test_largest_weights(T):
     c = slice(N - 300, N)
     want, err = P.product64(out[:, c].double().T, x.double())
     close(dw[c].double(), want, P.rounded(want, err), "dw")
+
+
+def test_packed_buffers_of_no_rows():
+    """Pairs laid out, but a packed buffer of no rows (a tensor without memory): the weights' gradients are
+    zero, the rest does nothing. The same of a dense product of no rows."""
+    E, H, N = 5, 72, 144
+    z = lambda *s: torch.empty(s, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    count = torch.full((E,), 3, dtype=torch.int32, device=DEV)
+    offset = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    at, w = (count, offset), torch.ones(E, N, H, device=DEV).to(torch.bfloat16)
+    for pairs in (7, 5000):
+        print("[no rows]", pairs, flush=True)
+        assert B.ep_expert_gemm_packed(z(0, H), *at, w, pairs).shape == (0, N)
+        assert B.ep_expert_swiglu_packed(z(0, H), *at, w, pairs, gu=z(0, N)).shape == (0, N // 2)
+        assert B.ep_expert_gemm_dgrad_packed(z(0, N), *at, w, pairs).shape == (0, H)
+        assert B.ep_expert_swiglu_dgrad_packed(z(0, N), *at, w, z(0, 2 * H), pairs).shape == (0, 2 * H)
+        for kind in ("bf16", "f32", "accumulate"):
+            dw = torch.full((E, N, H), 2.0, dtype=torch.bfloat16 if kind == "bf16" else torch.float32,
+                            device=DEV)
+            B.ep_expert_gemm_wgrad_packed(z(0, N), z(0, H), *at, pairs, dw=dw,
+                                          accumulate=kind == "accumulate")
+            assert (dw == (2 if kind == "accumulate" else 0)).all(), kind
+    idx = torch.zeros(4, 2, dtype=torch.int32, device=DEV)
+    dw = torch.full((4, 2), float("nan"), device=DEV)
+    B.ep_combine_grad_packed(torch.ones(4, H, device=DEV).to(torch.bfloat16), z(0, H), idx, idx, offset,
+                             torch.ones(4, 2, device=DEV), E, 8, dtopk_w=dw)
+    assert (dw == 0).all()
+    out = B.ep_linear(z(0, H), w[0], bias=w[0, :, 0].contiguous(), act="gelu", pre=z(0, N))
+    assert out.shape == (0, N)
+    dx, dw, dbias = B.ep_linear_grad(z(0, N), z(0, H), w[0], act="gelu", pre=z(0, N))
+    assert dx.shape == (0, H) and (dw == 0).all() and (dbias == 0).all()

@@ -249,3 +249,15 @@ def test_grid_of_too_many_threads_is_refused(lib):
     s = shape(T=1 << 27, H=8, E=1, K=1, C=1 << 27)
     assert lib.ep_combine(s, *[A16] * 5, None) == B.EP_ERR_HIP
     assert "hipErrorInvalidConfiguration" in lib.ep_last_error().decode()
+
+
+@pytest.mark.parametrize("name,ints,n,wide,optional", PRODUCTS[:4])
+def test_packed_buffers_of_no_rows(lib, name, ints, n, wide, optional):
+    """A packed buffer of no rows may be NULL, whatever number of pairs was laid out: nothing to do."""
+    p = [A16] * (n + 1)
+    for k in range(n):
+        if k in wide:
+            p[k + (k > 1)] = None
+    assert getattr(lib, name + "_packed")(shape(), 0, *ints, *p, None) == 0
+    p[2] = None                                # packed_offset
+    assert getattr(lib, name + "_packed")(shape(), 0, *ints, *p, None) == INVALID
