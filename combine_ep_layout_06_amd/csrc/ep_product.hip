@@ -24,9 +24,14 @@
 // 65536 rows x 4096 x 4096: a meeting of the wavefronts a block 1.86 ms, four phases 1.79, outputs stored
 // 64 bytes of a row together, which no later load waits for, 1.66, one stream of loads through tiles of
 // different heights 1.62 (1.36 PFLOP/s; matrix units 77% busy at the 1.6-1.75 GHz that the load leaves).
-// With short sums (768 to 2048) and about 340 rows an expert it is the outputs' stores and the operands'
-// way from L2 to LDS (9-12 TB/s) that bound it: cutting a last round's tiles and groups of about 8 row
-// tiles took 4096 tokens' gate and up products from 275 to 259 us and their down gradients from 308 to 286.
+// With short sums and some 340 rows an expert (two row tiles of 192) a round of tiles is its blocks and then
+// its output, beside which nothing runs. 96 experts of 2048 columns, sums of 256 to 4096 (kernel times): a
+// block 1.4-1.55 us (10 TB/s into LDS, 1.1 PFLOP/s, 3.3 TB/s from HBM if all is read once), the output of
+// a round 4 us, with gu 7, SwiGLU's gradient 22 (100 MB of gu and dgu: a copy's rate). Of experts
+// with one row tile a block takes 1.6-2.4, the weights' read (4.4 TB/s of 64 rows); of one matrix that the
+// caches hold 0.65 for 64 rows (16 TB/s into LDS, which is not what bounds the others). Cutting a last
+// round's tiles and groups of about 8 row tiles took 4096 tokens' gate and up products from 275 to 259 us and
+// their down gradients from 308 to 286.
 // Blocks of 32 in four stages (64 bytes of a row, twice the L2 requests), other cache policies of loads or
 // stores (0-15% slower), groups of 4 or 16, a raised wave priority: slower or no gain.
 #include "ep_product.h"

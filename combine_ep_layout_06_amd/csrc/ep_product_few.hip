@@ -1,5 +1,5 @@
 // The products for few rows on gfx950 (a decode step, one token), forward and dgrad, bound by reading the
-// weights once, and by how soon enough of the read is under way; and products of few tiles with a long sum.
+// weights once, and by how soon enough of the read is under way; and products of few tiles.
 //
 // A workgroup takes 16 columns of the output (SwiGLU: the same 16 gate and 16 up columns) for up to
 // 16 * MT rows of one expert, its 8 wavefronts an eighth of the sum each: so also a narrow product has
@@ -12,9 +12,10 @@
 // own, from which the transposing read gives the matrix instruction its operand: 64 rows x 4096 x 4096
 // 48 -> 20 us, one row 47 -> 11 (the weights at 4.74 TB/s: 7).
 //
-// Products of more rows whose few tiles have a long sum are made in squares of 64 x 64 in the same way:
-// 1024 rows x 1024 x 4096 43 -> 24 us. And weights' gradients, the rows dealt out to the eight wavefronts:
-// 8192 rows, 1024 x 1024 93 -> 35 us, 64 x 64 89 -> 22.
+// Products of more rows with few tiles are made in squares of 64 x 64 in the same way: 1024 rows x 1024 x
+// 4096 43 -> 24 us. And weights' gradients of few tiles with long sums, an expert's rows dealt out to the eight
+// wavefronts of one workgroup: 8192 rows, 1024 x 1024 93 -> 35 us, 64 x 64 (one workgroup, one CU busy) 89 -> 22,
+// in proportion to the rows from there on.
 #include "ep_product.h"
 
 #include <algorithm>
@@ -620,7 +621,10 @@ static double tiles_time(const Product &p, double experts, double rate)
 // and few rows, squares), columns x sum: 64 x 4096, 64 rows 22, 13, 2048 rows 24, 13; 512 x 4096, 256 rows
 // 23, 13, 2048 rows (256 squares) 44, 28, 4096 rows 45, 52; 4096 x 4096, 32 rows 16, 19, 64 rows 24, 22,
 // 256 rows (256) 45, 24, 512 rows 47, 44; 512 x 16384, 2048 rows 150, 95; 8 experts of 512 x 4096, 512 rows
-// 47, 24, 1024 rows (160) 43, 26, 2048 rows (288) 44, 44.
+// 47, 24, 1024 rows (160) 43, 26, 2048 rows (288) 44, 44. The sum's length does not enter, though with sums of
+// up to 256 the eight wavefronts have few steps or none: kernel times there, 64 to 2048 rows x 64 to 2048, few
+// rows 3.5-4.1, squares 4.7-5.9, tiles 7.6-9.5 (a call on its own takes 8 on the host); 512 5.3, 5.8, 11.6;
+// 1024 7.3, 6.8, 16.
 static bool squares(const Product &p)
 {
     const double experts = experts_reached(p), mean = p.pairs / experts;
@@ -634,7 +638,9 @@ static bool squares(const Product &p)
 // rows): one matrix of 4096 x 4096, 1 row 42, 9, 64 rows 43, 24, 96 rows 43, 40, 128 rows 43, 46;
 // 1024 x 2048, 256 rows 25, 12; 16384 x 4096, 16 rows 62, 39, 64 rows 64, 94; 128 experts of 1536 x 2048,
 // 8 rows 25, 12, 64 rows 80, 68, 256 rows 157, 149, 1024 rows 180, 213; of 2048 x 768, 8 rows 13, 9, 32
-// rows 20, 27; 16 of 4096 x 4096, 32 rows 109, 73.
+// rows 20, 27; 16 of 4096 x 4096, 32 rows 109, 73. Where most rows are one expert's the rule does not see it, and
+// this kernel reads that expert's weights once for each of its groups: 256 rows of 128 experts of 1536 x 2048
+// spread evenly 180, all of one expert 43 (tiles 28).
 bool few_rows(const Product &p, bool swiglu)
 {
     const double experts = experts_reached(p), mean = p.pairs / experts, k = p.k;
