@@ -38,7 +38,8 @@ extern "C" {
 #endif
 
 /* Problem shape. Requirements (else EP_ERR_INVALID): T >= 0, H >= 1, 1 <= K, 1 <= E,
- * 1 <= C, 1 <= R, E % R == 0, T*K <= INT32_MAX, E*C <= INT32_MAX. */
+ * 1 <= C, 1 <= R, E % R == 0, T*K <= INT32_MAX, E*C <= INT32_MAX (ep_linear and its gradient: of T and
+ * H alone). */
 typedef struct ep_shape {
     int32_t T;   /* tokens on this GPU */
     int32_t H;   /* hidden size (channels per row) */
