@@ -147,9 +147,9 @@ __device__ __forceinline__ float sigmoid(float g)
 
 // The normal distribution Phi(z) and, in `density`, exp(-z^2 / 2). With x = |z| / sqrt(2) and t = 1 / (1 +
 // 0.41 x) the tail beyond |z| is erfc(x) / 2 = exp(-x^2) t q(t). q is fitted to it for x up to 9.6 with an
-// error of 2.3e-7 (1 + 8 x^2) of the tail at most: as large a share of it as the rounding of exp's argument
-// far out, and near 0, where it shows beside 1, the least. So the tail keeps its relative accuracy,
-// which a value of z far below 0 needs: with fp32's roundings Phi is within 2^-21, and for z < 0 within
+// error of 2.3e-7 (1 + 8 x^2) of the tail at most: near 0, where it shows beside 1, the least, and far out a few
+// times what the rounding of exp's argument makes. So the tail keeps its relative accuracy, which a value of z
+// far below 0 needs: with fp32's roundings Phi is within 2^-21, and for z < 0 within
 // (1 + z^2) 2^-19 of its own size down to z = -13.1 (below it the tail ends as a zero).
 __device__ __forceinline__ float normal_cdf(float z, float &density)
 {

@@ -564,10 +564,10 @@ int ep_moe_layer_fp8(const ep_shape_t *shape, int32_t I, const uint16_t *x,
  * Rows are as in the FP8 products: each expert e holds n = expert_count[e] rows from row e*C of a padded
  * buffer [E][C] (n taken as min(max(n, 0), C)), or from row packed_offset[e] of a packed buffer of
  * `rows` rows (rows outside the buffer are left out; C is not used; with rows = 0 its pointers may be
- * NULL). Only these rows are read and written; other rows of the outputs keep what they hold. shape->T * shape->K is the number of pairs
- * laid out; it chooses the kernel and its grid, not which rows are computed (the order of the fp32 sums
- * may differ), except that T = 0 means no rows. R is not used. H is the width of the rows that the
- * forward product takes, in its gradients too.
+ * NULL). Only these rows are read and written; other rows of the outputs keep what they hold.
+ * shape->T * shape->K is the number of pairs laid out; it chooses the kernel and its grid, not which rows
+ * are computed (the order of the fp32 sums may differ), except that T = 0 means no rows. R is not used. H
+ * is the width of the rows that the forward product takes, in its gradients too.
  *
  * Sums are fp32 (of exact products of bf16 values), rounded once to the output's type. NaN and
  * infinite values propagate to the elements they enter. Deterministic: the same inputs give the same
